@@ -269,6 +269,125 @@ q8_status q8_dot_f32(const float *A, const float *B, float *C, int64_t M, int64_
 q8_status q8_dot_t_f32(const float *A, const float *B, float *C, int64_t M, int64_t K, int64_t N,
                        const q8_epilogue *epilogue, void *stream);
 
+/*
+ * The Q8_0 cache: keys and values of an attention layer in pages, in the
+ * weights' own format (i8 codes, one f32 scale per 32 values; value = code *
+ * scale), what goes in and out of it, and the attention that reads it.
+ *
+ * A page holds page_size tokens of every head.  Codes of a token's row of dim
+ * channels lie in pair order: channel d = 32 b + 2 j + i (j < 16, i < 2) is
+ * byte j * (dim / 16) + 2 b + i of the row; block b's scale is scale b.
+ */
+typedef struct q8_cache {
+  int8_t *K;         /* i8  [pages, heads, page_size, dim], device, 16-byte aligned */
+  float *KS;         /* f32 [pages, heads, page_size, dim / 32], device */
+  int8_t *V;         /* as K */
+  float *VS;         /* as KS */
+  int64_t pages;     /* below 2^31; the arrays themselves may be of any size */
+  int32_t heads;     /* 1 .. 65535 */
+  int32_t page_size; /* a power of two, 16 .. 1024 */
+  int32_t dim;       /* 64, 128 or 256 */
+} q8_cache;
+
+/*
+ * The sequences of a call (device arrays, read when the work runs, so a
+ * captured graph follows their contents).  Sequence b owns the pages
+ * table[b, 0], table[b, 1], ... and holds lengths[b] tokens, the new ones
+ * among them: its newest n = offsets[b+1] - offsets[b] tokens are rows
+ * offsets[b] .. offsets[b+1]-1 of the call's row tensors.  Rows before
+ * offsets[0] and from offsets[seqs] on belong to no sequence and are neither
+ * read nor written.  Sequences must not share pages that a call writes.
+ *
+ * The contents are checked where they are used: a sequence whose offsets do
+ * not ascend within the rows has no rows; one with lengths[b] < n, or with more
+ * tokens than its table row holds, and a position whose page is not one of
+ * the cache's (0 .. pages-1), is skipped by a write or keep, and gives NaN in
+ * the rows of a read or an attention that would need it.  A row that the
+ * offsets give to two sequences holds either one's result.
+ */
+typedef struct q8_cache_seqs {
+  const int32_t *table;   /* [seqs, max_pages], rows table_stride apart; entries past a sequence's tokens are not read */
+  const int32_t *lengths; /* [seqs] */
+  const int32_t *offsets; /* [seqs + 1], ascending */
+  int64_t seqs;
+  int64_t max_pages;      /* max_pages * page_size below 2^30 */
+  int64_t table_stride;
+} q8_cache_seqs;
+
+/* Element types of the rows outside the cache. */
+typedef enum q8_type { Q8_F32 = 0, Q8_BF16 = 1, Q8_F16 = 2 } q8_type;
+
+/*
+ * q8_cache_write -- quantises the new tokens' keys and values into the cache.
+ *   k, v  [rows, heads, dim] of `type`, rows k_stride / v_stride elements apart
+ *         (at least heads * dim), aligned to their elements
+ * Per 32 channels x: scale = f32(max|x| / 127), code = x / scale rounded to
+ * the nearest, ties to even, both correctly rounded (a scale of zero gives
+ * zeros).  A block that holds an infinity or a NaN is stored so that it reads
+ * back as NaN.  Everything else in the cache is left as it was.
+ * q8_cache_read -- the reverse: k, v = code * scale, rounded once to `type`, for
+ * the newest tokens of each sequence (offsets that count all of its tokens
+ * read the whole sequence).
+ * Errors of both: Q8_ERR_INVALID, Q8_ERR_TOO_LARGE, Q8_ERR_UNSUPPORTED_DEVICE,
+ * Q8_ERR_HIP.
+ */
+q8_status q8_cache_write(const q8_cache *cache, const void *k, const void *v, q8_type type,
+                         int64_t rows, int64_t k_stride, int64_t v_stride,
+                         const q8_cache_seqs *seqs, void *stream);
+q8_status q8_cache_read(const q8_cache *cache, void *k, void *v, q8_type type, int64_t rows,
+                        int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs,
+                        void *stream);
+
+/*
+ * q8_cache_keep -- after a tree of drafted tokens has been verified, moves the
+ * accepted ones to the front of the sequence's new tokens: for a = 0, 1, ...
+ * the codes and scales of new token keep[b, a] go to the place of new token a.
+ *   keep  i32 [seqs, width], device: indexes among sequence b's new tokens in
+ *         strictly ascending order; the first entry that is negative, not
+ *         below n or not above the one before it ends the list
+ *   rows  of the row tensors that the offsets refer to
+ * Places past the kept ones hold what they held or were moved from; the caller
+ * shortens lengths[b].
+ */
+q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs *seqs,
+                        const int32_t *keep, int64_t width, void *stream);
+
+/*
+ * q8_cache_attention -- attention of the new tokens' queries over the cache
+ * (their own keys and values included: write them first):
+ *   out[t, h] = sum_j softmax_j(alpha * q[t, h] . K[j, h / g]) V[j, h / g]
+ * with g = q_heads / heads, over the tokens j that row t sees: all tokens
+ * before the new ones, and of the new ones
+ *   tree == NULL  those up to the row's own (one new token per sequence is
+ *                 plain decoding, many are a piece of a prompt)
+ *   tree != NULL  those whose bit is set: bit j % 64 of word j / 64 of the
+ *                 row's tree_words words (u64 [rows, tree_words], 8-byte
+ *                 aligned) for new token j; tokens past the words are not seen
+ * A row that sees nothing gives zeros.  What a token that no row sees holds
+ * (NaN among it) changes nothing.
+ *   q, out  [rows, q_heads, dim] of `type`, rows q_stride / out_stride elements
+ *           apart; out must not overlap anything else
+ *   workspace  device memory of at least the size that
+ *           q8_cache_attention_workspace gives for the same cache, rows,
+ *           q_heads, seqs and max_pages, 16-byte aligned; its contents need no
+ *           preparation and are free again when the call's work is done.  Calls that may
+ *           overlap in time (and graphs whose replays may) need one each
+ * f32 accuracy for f32 rows: codes are exact in the bf16 matrix operands, q and
+ * the scaled weights are cut into enough bf16 parts to lose nothing (weights
+ * for bf16 and f16 rows: 16 bits), sums, maxima and scales are f32.  Products
+ * of q and the codes must stay finite before they are scaled: |q| below
+ * 2^115.  Deterministic: the order of the sums depends on the extents, the lengths and
+ * offsets, never on timing.
+ * Errors: as q8_cache_write; Q8_ERR_INVALID also for q_heads that is no multiple
+ * of heads and for a missing, misaligned or small workspace.
+ */
+q8_status q8_cache_attention_workspace(const q8_cache *cache, int64_t rows, int32_t q_heads,
+                                       const q8_cache_seqs *seqs, int64_t *bytes);
+q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8_type type,
+                             int64_t rows, int32_t q_heads, int64_t q_stride, int64_t out_stride,
+                             const q8_cache_seqs *seqs, const uint64_t *tree, int64_t tree_words,
+                             float alpha, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *q8_status_string(q8_status s);
 

@@ -7,7 +7,12 @@ Importing this package loads nothing; the library is loaded on first use.
 
 from .binding import (  # noqa: F401
     EXPORTED,
+    Q8Cache,
     Q8Error,
+    q8_cache_attention,
+    q8_cache_keep,
+    q8_cache_read,
+    q8_cache_write,
     q8_dot_f32,
     q8_dot_t,
     q8_dot_t_f32,

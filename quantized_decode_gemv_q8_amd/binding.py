@@ -33,6 +33,11 @@ EXPORTED = (
     "q8_dot_t",
     "q8_dot_f32",
     "q8_dot_t_f32",
+    "q8_cache_write",
+    "q8_cache_read",
+    "q8_cache_keep",
+    "q8_cache_attention_workspace",
+    "q8_cache_attention",
     "q8_status_string",
     "q8_last_hip_error",
     "q8_release",
@@ -54,6 +59,17 @@ class Q8Sibling(ctypes.Structure):
 
 class Q8Epilogue(ctypes.Structure):
     _fields_ = [("alpha", ctypes.c_float), ("corr", ctypes.c_void_p)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("KS", ctypes.c_void_p), ("V", ctypes.c_void_p), ("VS", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
+class _SeqsStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
 
 
 class Q8Error(RuntimeError):
@@ -94,6 +110,18 @@ def load():
         fn = getattr(L, name)
         fn.argtypes = [p, p, p, i64, i64, i64, ctypes.POINTER(Q8Epilogue), p]
         fn.restype = ctypes.c_int
+    cache, seqs = ctypes.POINTER(_CacheStruct), ctypes.POINTER(_SeqsStruct)
+    for name in ("q8_cache_write", "q8_cache_read"):
+        fn = getattr(L, name)
+        fn.argtypes = [cache, p, p, ctypes.c_int, i64, i64, i64, seqs, p]
+        fn.restype = ctypes.c_int
+    L.q8_cache_keep.argtypes = [cache, i64, seqs, p, i64, p]
+    L.q8_cache_keep.restype = ctypes.c_int
+    L.q8_cache_attention_workspace.argtypes = [cache, i64, i32, seqs, ctypes.POINTER(i64)]
+    L.q8_cache_attention_workspace.restype = ctypes.c_int
+    L.q8_cache_attention.argtypes = [cache, p, p, ctypes.c_int, i64, i32, i64, i64, seqs, p, i64, ctypes.c_float,
+                                     p, i64, p]
+    L.q8_cache_attention.restype = ctypes.c_int
     L.q8_status_string.argtypes = [ctypes.c_int]
     L.q8_status_string.restype = ctypes.c_char_p
     L.q8_last_hip_error.argtypes = []
@@ -323,3 +351,265 @@ def q8_dot_f32(A, B, out=None, alpha=1.0, corr=None, stream=None):
 def q8_dot_t_f32(A, B, out=None, alpha=1.0, corr=None, stream=None):
     """C = alpha * (A @ B^T) (+ corr[m] * C) for f32 A [M,K], B [N,K]; returns C (f32 [M,N])."""
     return _dense("q8_dot_t_f32", A, B, True, out, alpha, corr, stream)
+
+
+# ------------------------------------------------------------------ the Q8_0 cache
+
+#: Element types of the rows outside the cache.
+_ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class Q8Cache:
+    """Keys and values of an attention layer in pages, in Q8_0.
+
+    k, v              i8  [pages, heads, page_size, dim], codes
+    k_scale, v_scale  f32 [pages, heads, page_size, dim // 32]
+
+    A token's value is code * scale.  Codes of a row lie in pair order: the
+    natural order [dim // 32, 16, 2] is stored as [16, dim // 32, 2].  The tensors
+    stay the caller's; the handle only checks them once.
+    """
+
+    __slots__ = ("k", "k_scale", "v", "v_scale", "pages", "heads", "page_size", "dim", "device", "_struct")
+
+    def __init__(self, k, k_scale, v, v_scale):
+        if not isinstance(k, torch.Tensor):
+            raise TypeError("k must be a torch.Tensor")
+        if k.dim() != 4:
+            raise ValueError(f"k must be rank 4, got {k.dim()} dimensions")
+        pages, heads, page_size, dim = k.shape
+        if dim not in (64, 128, 256):
+            raise ValueError(f"dim must be 64, 128 or 256, got {dim}")
+        if page_size not in (16, 32, 64, 128, 256, 512, 1024):
+            raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
+        for name, t, dtype, last in (("k", k, torch.int8, dim), ("k_scale", k_scale, torch.float32, dim // BLOCK),
+                                     ("v", v, torch.int8, dim), ("v_scale", v_scale, torch.float32, dim // BLOCK)):
+            _check_tensor(name, t, dtype, (pages, heads, page_size, last))
+            if t.device != k.device:
+                raise ValueError("all tensors must be on one device")
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        for i, a in enumerate(("k", "k_scale", "v", "v_scale")):
+            _check_disjoint(a, getattr(self, a),
+                            [(b, getattr(self, b)) for b in ("k", "k_scale", "v", "v_scale")[:i]])
+        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
+        self.device = k.device
+        self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
+                                    pages, heads, page_size, dim)
+
+    @classmethod
+    def empty(cls, pages, heads, page_size, dim, device="cuda"):
+        """A cache with new tensors; what it holds is undefined until it is written."""
+        def new(last, dtype):
+            return torch.empty((pages, heads, page_size, last), dtype=dtype, device=device)
+        return cls(new(dim, torch.int8), new(dim // BLOCK, torch.float32),
+                   new(dim, torch.int8), new(dim // BLOCK, torch.float32))
+
+
+def _cache_seqs(cache, table, lengths, offsets):
+    """The checked descriptor of a call's sequences."""
+    if not isinstance(cache, Q8Cache):
+        raise TypeError("cache must be a Q8Cache")
+    for name, t, rank in (("table", table, 2), ("lengths", lengths, 1), ("offsets", offsets, 1)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
+        if t.device != cache.device:
+            raise ValueError("all tensors must be on one device")
+        if t.dim() != rank:
+            raise ValueError(f"{name} must be rank {rank}, got {t.dim()} dimensions")
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    n, pages = table.shape
+    if lengths.shape[0] != n or offsets.shape[0] != n + 1:
+        raise ValueError(f"{n} rows of table need {n} lengths and {n + 1} offsets, got "
+                         f"{lengths.shape[0]} and {offsets.shape[0]}")
+    stride = table.stride(0) if n > 1 else pages
+    if stride < pages:
+        raise ValueError("rows of table must not overlap")
+    return _SeqsStruct(table.data_ptr(), lengths.data_ptr(), offsets.data_ptr(), n, pages, stride)
+
+
+def _cache_rows(name, t, rows, heads, cache, dtype=None):
+    """Checks a row tensor [rows, heads, dim]: rows may be apart, a row is dense.  Returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
+        want = dtype if dtype is not None else "float32, bfloat16 or float16"
+        raise ValueError(f"{name} must be {want}, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError("all tensors must be on one device")
+    if t.dim() != 3 or t.shape[2] != cache.dim or (rows is not None and t.shape[0] != rows) or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, "
+                         f"{'heads' if heads is None else heads}, {cache.dim}), got {tuple(t.shape)}")
+    s = t.stride()
+    if t.numel() == 0:
+        return t.shape[1] * t.shape[2]
+    if s[2] != 1 or (t.shape[1] > 1 and s[1] != cache.dim):
+        raise ValueError(f"{name} must be dense in its last two dimensions")
+    if t.shape[0] > 1 and s[0] < t.shape[1] * t.shape[2]:
+        raise ValueError(f"rows of {name} must not overlap")
+    return s[0]
+
+
+def _span(t):
+    """First byte and one past the last byte of a tensor with non-negative strides."""
+    if t.numel() == 0:
+        return 0, 0
+    a = t.data_ptr()
+    return a, a + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _check_apart(out_name, out, others):
+    """_check_disjoint for row tensors, whose rows may be apart."""
+    a0, a1 = _span(out)
+    for name, t in others:
+        if t is None:
+            continue
+        b0, b1 = _span(t)
+        if a0 < b1 and b0 < a1 and not _interleaved(out, t):
+            raise ValueError(f"{out_name} overlaps {name}")
+
+
+def _interleaved(a, b):
+    """Whether two row tensors are views of one wide one, side by side: rows
+    equally far apart, and apart from each other within that distance."""
+    if a.dim() != 3 or b.dim() != 3:
+        return False
+    pitch = a.stride(0) * a.element_size()
+    if pitch != b.stride(0) * b.element_size():
+        return False
+    between = (b.data_ptr() - a.data_ptr()) % pitch
+    return between >= _span(a[0])[1] - _span(a[0])[0] and pitch - between >= _span(b[0])[1] - _span(b[0])[0]
+
+
+def _empty_on(stream, shape, dtype, device):
+    """A new tensor whose memory is ordered with the work of `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cache_tensors(cache):
+    return (("the cache", cache.k), ("the cache", cache.k_scale), ("the cache", cache.v), ("the cache", cache.v_scale))
+
+
+def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
+    """Quantises rows k and v ([rows, heads, dim]) into the cache: sequence b's
+    newest offsets[b+1] - offsets[b] tokens of lengths[b] are rows offsets[b]
+    .. of k and v, and live in the pages table[b]."""
+    seqs = _cache_seqs(cache, table, lengths, offsets)
+    ks = _cache_rows("k", k, None, cache.heads, cache)
+    vs = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
+    for name, c in _cache_tensors(cache):
+        _check_apart(name, c, (("k", k), ("v", v), ("table", table), ("lengths", lengths), ("offsets", offsets)))
+    with torch.cuda.device(cache.device):
+        st = load().q8_cache_write(cache._struct, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], k.shape[0], ks, vs,
+                                   seqs, _stream_handle(stream, cache.device))
+    if st != Q8_OK:
+        raise Q8Error(st, "q8_cache_write")
+
+
+def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
+    """The newest offsets[b+1] - offsets[b] tokens of each sequence as rows
+    [rows, heads, dim] of dtype; returns (k, v).  Rows of no sequence keep what
+    the given k and v hold (new tensors: undefined)."""
+    seqs = _cache_seqs(cache, table, lengths, offsets)
+    shape = (int(rows), cache.heads, cache.dim)
+    new = [t is None for t in (k, v)]
+    if any(new):
+        if dtype not in _ROW_TYPES:
+            raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        if k is None:
+            k = _empty_on(stream, shape, dtype, cache.device)
+        if v is None:
+            v = _empty_on(stream, shape, dtype, cache.device)
+    ks = _cache_rows("k", k, shape[0], cache.heads, cache)
+    vs = _cache_rows("v", v, shape[0], cache.heads, cache, k.dtype)
+    inputs = _cache_tensors(cache) + (("table", table), ("lengths", lengths), ("offsets", offsets))
+    _check_apart("k", k, inputs)
+    _check_apart("v", v, inputs + (("k", k),))
+    with torch.cuda.device(cache.device):
+        st = load().q8_cache_read(cache._struct, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], shape[0], ks, vs,
+                                  seqs, _stream_handle(stream, cache.device))
+    if st != Q8_OK:
+        raise Q8Error(st, "q8_cache_read")
+    return k, v
+
+
+def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
+    """Moves new token keep[b, a] of sequence b to the place of its new token a,
+    a = 0, 1, ...; keep is i32 [sequences, width], strictly ascending until its
+    first negative entry."""
+    seqs = _cache_seqs(cache, table, lengths, offsets)
+    if not isinstance(keep, torch.Tensor):
+        raise TypeError("keep must be a torch.Tensor")
+    if keep.dim() != 2:
+        raise ValueError(f"keep must be rank 2, got {keep.dim()} dimensions")
+    _check_tensor("keep", keep, torch.int32, (table.shape[0], keep.shape[1]))
+    if keep.device != cache.device:
+        raise ValueError("all tensors must be on one device")
+    for name, c in _cache_tensors(cache):
+        _check_apart(name, c, (("keep", keep), ("table", table), ("lengths", lengths), ("offsets", offsets)))
+    with torch.cuda.device(cache.device):
+        st = load().q8_cache_keep(cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(), keep.shape[1],
+                                  _stream_handle(stream, cache.device))
+    if st != Q8_OK:
+        raise Q8Error(st, "q8_cache_keep")
+
+
+#: Most rows a call's offsets may refer to.
+MAX_CACHE_ROWS = (1 << 31) - 1
+
+
+def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None, out=None, stream=None):
+    """Attention of the new tokens' queries q ([rows, q_heads, dim]) over the
+    cache, their own keys and values included; returns out, shaped like q.
+
+    Row offsets[b] + i (new token i of sequence b) sees every token before the
+    new ones and, of the new ones, those up to i; or with tree (i64 [rows, words])
+    those j whose bit j % 64 of word j // 64 of the row is set.  alpha: scale of
+    the scores, 1 / sqrt(dim) if None.  Rows of no sequence keep what out holds
+    (a new out: undefined); rows that see nothing are zeros.
+    """
+    seqs = _cache_seqs(cache, table, lengths, offsets)
+    qs = _cache_rows("q", q, None, None, cache)
+    rows, q_heads = q.shape[0], q.shape[1]
+    if q_heads == 0 or q_heads % cache.heads:
+        raise ValueError(f"the heads of q must be a multiple of the cache's {cache.heads}, got {q_heads}")
+    words = 0
+    if tree is not None:
+        if not isinstance(tree, torch.Tensor):
+            raise TypeError("tree must be a torch.Tensor")
+        if tree.dim() != 2:
+            raise ValueError(f"tree must be rank 2, got {tree.dim()} dimensions")
+        words = tree.shape[1]
+        _check_tensor("tree", tree, torch.int64, (rows, words))
+        if tree.device != cache.device:
+            raise ValueError("all tensors must be on one device")
+    if alpha is None:
+        alpha = cache.dim ** -0.5
+    L = load()
+    with torch.cuda.device(cache.device):
+        if out is None:
+            out = _empty_on(stream, (rows, q_heads, cache.dim), q.dtype, cache.device)
+            os_ = q_heads * cache.dim
+        else:
+            os_ = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
+            _check_apart("out", out, _cache_tensors(cache) + (("q", q), ("table", table), ("lengths", lengths),
+                                                              ("offsets", offsets), ("tree", tree)))
+        need = ctypes.c_int64(0)
+        st = L.q8_cache_attention_workspace(cache._struct, rows, q_heads, seqs, need)
+        if st == Q8_OK:
+            work = _empty_on(stream, (max(16, need.value),), torch.uint8, cache.device)
+            mask = None
+            if tree is not None:  # an empty tree still is one: no new token is seen
+                mask = tree.data_ptr() if tree.numel() else work.data_ptr()
+            st = L.q8_cache_attention(cache._struct, q.data_ptr(), out.data_ptr(), _ROW_TYPES[q.dtype], rows, q_heads,
+                                      qs, os_, seqs, mask, words, alpha, work.data_ptr(), need.value,
+                                      _stream_handle(stream, cache.device))
+    if st != Q8_OK:
+        raise Q8Error(st, "q8_cache_attention")
+    return out

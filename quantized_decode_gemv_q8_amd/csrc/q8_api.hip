@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "q8_attention.h"
 #include "q8_common.h"
 #include "q8_gemv.h"
 
@@ -717,6 +718,104 @@ q8_status dense_impl(const float *A, const float *B, float *C, int64_t M, int64_
   return hip_status(q8::launch_dense_f32(a, trans_b, wide ? 4 : 1, 2 * info.cus, stream));
 }
 
+
+// ---------------------------------------------------------------- the Q8_0 cache
+
+// The cache and the sequences of a call, checked; what the kernels take.
+// Device arrays (table, lengths, offsets) are checked by the kernels.
+q8_status cache_args(const q8_cache *c, const q8_cache_seqs *s, int64_t rows, q8::Cache *cache, q8::Seqs *seqs) {
+  if (c == nullptr || s == nullptr) return Q8_ERR_INVALID;
+  if (c->pages < 0 || c->heads < 1 || rows < 0 || s->seqs < 0 || s->max_pages < 0) return Q8_ERR_INVALID;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return Q8_ERR_INVALID;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return Q8_ERR_INVALID;
+  if (s->seqs > 1 && s->table_stride < s->max_pages) return Q8_ERR_INVALID;
+  if (c->pages >= kIndexLimit || c->heads > 65535 || rows >= kIndexLimit || s->seqs >= kIndexLimit / 2)
+    return Q8_ERR_TOO_LARGE;
+  // Positions are 32-bit with one unit of overhang.
+  if (s->max_pages >= kIndexLimit / 2 / c->page_size) return Q8_ERR_TOO_LARGE;
+  if (rows > 0 && s->seqs > 0) {
+    if (s->lengths == nullptr || s->offsets == nullptr || (s->max_pages > 0 && s->table == nullptr)) return Q8_ERR_INVALID;
+    if (c->pages > 0 && (c->K == nullptr || c->KS == nullptr || c->V == nullptr || c->VS == nullptr)) return Q8_ERR_INVALID;
+    if (address_alignment(c->K) < 16 || address_alignment(c->V) < 16 || address_alignment(c->KS) < 4 ||
+        address_alignment(c->VS) < 4 || address_alignment(s->table) < 4 || address_alignment(s->lengths) < 4 ||
+        address_alignment(s->offsets) < 4)
+      return Q8_ERR_INVALID;
+  }
+  cache->K = c->K;
+  cache->KS = c->KS;
+  cache->V = c->V;
+  cache->VS = c->VS;
+  cache->pages = c->pages;
+  cache->heads = c->heads;
+  cache->dim = c->dim;
+  cache->page_shift = __builtin_ctz((unsigned)c->page_size);
+  seqs->table = s->table;
+  seqs->lengths = s->lengths;
+  seqs->offsets = s->offsets;
+  seqs->table_stride = s->table_stride;
+  seqs->max_tokens = s->max_pages * c->page_size;
+  seqs->seqs = (int)s->seqs;
+  seqs->rows = (int)rows;
+  return Q8_OK;
+}
+
+bool row_type(q8_type type, int64_t *bytes) {
+  if (type != Q8_F32 && type != Q8_BF16 && type != Q8_F16) return false;
+  *bytes = type == Q8_F32 ? 4 : 2;
+  return true;
+}
+
+q8_status cache_rows_impl(const q8_cache *c, const void *k, const void *v, q8_type type, int64_t rows,
+                          int64_t k_stride, int64_t v_stride, const q8_cache_seqs *s, bool write, void *stream_v) {
+  q8::CacheRowsArgs a;
+  int64_t bytes = 0;
+  q8_status st = cache_args(c, s, rows, &a.c, &a.s);
+  if (st != Q8_OK) return st;
+  if (!row_type(type, &bytes)) return Q8_ERR_INVALID;
+  if (rows == 0 || s->seqs == 0) return Q8_OK;
+  const int64_t width = (int64_t)c->heads * c->dim;
+  if (k == nullptr || v == nullptr || address_alignment(k) < bytes || address_alignment(v) < bytes) return Q8_ERR_INVALID;
+  if (rows > 1 && (k_stride < width || v_stride < width)) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.k = const_cast<void *>(k);
+  a.v = const_cast<void *>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  if (log_debug())
+    log_line("cache_%s rows=%lld heads=%d dim=%d seqs=%lld", write ? "write" : "read", (long long)rows, c->heads, c->dim,
+             (long long)s->seqs);
+  return hip_status((write ? q8::launch_cache_write : q8::launch_cache_read)(a, (q8::RowType)type, (hipStream_t)stream_v));
+}
+
+// How the rows of an attention call are cut: items of up to 16 * row_tiles
+// rows (tokens x heads of a group), and the workgroups the units are dealt to.
+struct AttnPlan {
+  int row_tiles, subs, sub_heads, tile_tokens;
+  int64_t wgs, bytes;  // workgroups; workspace
+};
+
+AttnPlan attn_plan(int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens, int cus) {
+  AttnPlan p;
+  const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
+  p.row_tiles = 1;
+  while (p.row_tiles < q8::attn_max_row_tiles(dim) && 16 * p.row_tiles < mean) p.row_tiles *= 2;
+  const int tile = 16 * p.row_tiles;
+  p.subs = (int)ceil_div(group, tile);
+  p.sub_heads = (int)ceil_div(group, p.subs);
+  p.subs = (int)ceil_div(group, p.sub_heads);  // no empty sub-group
+  p.tile_tokens = tile / p.sub_heads;
+  const int64_t items = (rows / p.tile_tokens + seqs) * heads * p.subs;
+  const int64_t units = ceil_div(max_tokens, q8::kAttnUnit);
+  p.wgs = (int64_t)cus * q8::kAttnWgsPerCu;
+  if (items < p.wgs && items * (units < 1 ? 1 : units) < p.wgs) p.wgs = items * (units < 1 ? 1 : units);
+  p.bytes = 2 * p.wgs * q8::attn_slot_floats(tile, dim) * 4;
+  p.bytes = ceil_div(p.bytes, 256) * 256 + p.wgs * (int64_t)sizeof(q8::AttnItem);
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -806,6 +905,102 @@ q8_status q8_dot_f32(const float *A, const float *B, float *C, int64_t M, int64_
 q8_status q8_dot_t_f32(const float *A, const float *B, float *C, int64_t M, int64_t K, int64_t N,
                        const q8_epilogue *epilogue, void *stream) {
   return dense_impl(A, B, C, M, K, N, true, epilogue, stream);
+}
+
+q8_status q8_cache_write(const q8_cache *cache, const void *k, const void *v, q8_type type, int64_t rows,
+                         int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, true, stream);
+}
+
+q8_status q8_cache_read(const q8_cache *cache, void *k, void *v, q8_type type, int64_t rows, int64_t k_stride,
+                        int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, false, stream);
+}
+
+q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs *seqs, const int32_t *keep,
+                        int64_t width, void *stream) {
+  q8::CacheKeepArgs a;
+  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
+  if (st != Q8_OK) return st;
+  if (width < 0) return Q8_ERR_INVALID;
+  if (width >= kIndexLimit / 2) return Q8_ERR_TOO_LARGE;
+  if (rows == 0 || seqs->seqs == 0 || width == 0) return Q8_OK;
+  if (keep == nullptr || address_alignment(keep) < 4) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.keep = keep;
+  a.width = (int)width;
+  if (log_debug()) log_line("cache_keep seqs=%lld width=%lld", (long long)seqs->seqs, (long long)width);
+  return hip_status(q8::launch_cache_keep(a, (hipStream_t)stream));
+}
+
+q8_status q8_cache_attention_workspace(const q8_cache *cache, int64_t rows, int32_t q_heads, const q8_cache_seqs *seqs,
+                                       int64_t *bytes) {
+  q8::Cache c;
+  q8::Seqs s;
+  if (bytes == nullptr) return Q8_ERR_INVALID;
+  q8_status st = cache_args(cache, seqs, rows, &c, &s);
+  if (st != Q8_OK) return st;
+  if (q_heads < 1 || q_heads % cache->heads != 0) return Q8_ERR_INVALID;
+  *bytes = 0;
+  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  *bytes = attn_plan(c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens, info.cus).bytes;
+  return Q8_OK;
+}
+
+q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8_type type, int64_t rows,
+                             int32_t q_heads, int64_t q_stride, int64_t out_stride, const q8_cache_seqs *seqs,
+                             const uint64_t *tree, int64_t tree_words, float alpha, void *workspace,
+                             int64_t workspace_bytes, void *stream_v) {
+  q8::AttnArgs a;
+  int64_t bytes = 0;
+  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
+  if (st != Q8_OK) return st;
+  if (!row_type(type, &bytes) || q_heads < 1 || q_heads % cache->heads != 0 || tree_words < 0) return Q8_ERR_INVALID;
+  if (q_heads > (1 << 24) || tree_words >= kIndexLimit / 64) return Q8_ERR_TOO_LARGE;
+  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
+  const int64_t width = (int64_t)q_heads * cache->dim;
+  if (q == nullptr || out == nullptr || address_alignment(q) < bytes || address_alignment(out) < bytes) return Q8_ERR_INVALID;
+  if (rows > 1 && (q_stride < width || out_stride < width)) return Q8_ERR_INVALID;
+  if (address_alignment(tree) < 8) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  const AttnPlan pl =
+      attn_plan(a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens, info.cus);
+  if (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes) return Q8_ERR_INVALID;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.tree = tree;
+  a.tree_words = (int)tree_words;
+  a.group = q_heads / a.c.heads;
+  a.subs = pl.subs;
+  a.sub_heads = pl.sub_heads;
+  a.tile_tokens = pl.tile_tokens;
+  a.alpha = alpha;
+  a.partial = static_cast<float *>(workspace);
+  const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(16 * pl.row_tiles, a.c.dim) * 4;
+  a.items = reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256);
+  if (log_debug())
+    log_line("cache_attention rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", (long long)rows,
+             q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", 16 * pl.row_tiles,
+             (long long)pl.wgs);
+  hipStream_t stream = (hipStream_t)stream_v;
+  switch (type) {
+    case Q8_F32: return hip_status(q8::launch_attention_f32(a, pl.row_tiles, (int)pl.wgs, stream));
+    case Q8_BF16: return hip_status(q8::launch_attention_bf16(a, pl.row_tiles, (int)pl.wgs, stream));
+    case Q8_F16: return hip_status(q8::launch_attention_f16(a, pl.row_tiles, (int)pl.wgs, stream));
+  }
+  return Q8_ERR_INVALID;
 }
 
 const char *q8_status_string(q8_status s) {

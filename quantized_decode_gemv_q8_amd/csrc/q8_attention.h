@@ -1,0 +1,56 @@
+// Internal declarations of the attention over the Q8_0 cache.
+#pragma once
+
+#include "q8_cache.h"
+
+namespace q8 {
+
+// Keys per unit of work: one 32-key tile for each of a workgroup's four waves.
+constexpr int kAttnTile = 32;
+constexpr int kAttnUnit = kAttnTile * kWaves;
+
+// One split item: rows whose keys several workgroups share.  Workgroup w is
+// the first contributor of at most one, so the descriptors are indexed by it.
+struct AttnItem {
+  int valid;
+  int last;    // last contributing workgroup
+  int row0;    // first row of the row tensors
+  int tokens;  // rows of the item
+  int head0;   // first query head
+  int heads;   // query heads per row
+  int seq_row0, seq_new;  // of the sequence, for rows that see nothing
+  int context;            // tokens before the new ones
+};
+
+struct AttnArgs {
+  Cache c;
+  Seqs s;
+  const void *q;
+  void *out;
+  int64_t q_stride, out_stride;  // elements between rows
+  const uint64_t *tree;          // [rows, tree_words] or null: causal
+  int tree_words;
+  int group;       // query heads per head of the cache
+  int subs;        // a group's heads are taken in `subs` items of sub_heads
+  int sub_heads;
+  int tile_tokens;  // tokens (rows of q) per item
+  float alpha;
+  float *partial;   // 2 * gridDim.x slots of attn_slot_floats(rows, dim)
+  AttnItem *items;  // gridDim.x
+};
+
+// Floats of one partial: rows x dim sums, then the rows' maxima and weights.
+__host__ __device__ constexpr int64_t attn_slot_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
+
+// Row tiles of 16 an instance holds at most: the sums (rows * dim / 64
+// registers) and the query parts must leave room for the tiles in flight.
+constexpr int attn_max_row_tiles(int dim) { return dim <= 128 ? 2 : 1; }
+
+// Workgroups per CU of an instance.
+constexpr int kAttnWgsPerCu = 2;
+
+hipError_t launch_attention_f32(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
+hipError_t launch_attention_bf16(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
+hipError_t launch_attention_f16(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
+
+}  // namespace q8

@@ -1,0 +1,360 @@
+// The Q8_0 cache: quantising rows as they are written, reading them back, and
+// moving accepted drafts to the front of a sequence's new tokens.
+//
+// Q8_0 per 32 channels x of a row: s = f32(max|x| / 127), code = x / s rounded
+// to the nearest (ties to even), value = code * s.  Every step is exact or
+// correctly rounded, so codes and scales do not depend on how the work is
+// split:
+//   * the scale is one correctly rounded division;
+//   * the code is the rounded f32 quotient, corrected by at most one step with
+//     the exact remainder x - code * s (a multiple of ulp(s) / 2 no larger
+//     than 2 s, so the fused multiply-add that forms it does not round).
+// A block that holds an infinity or a NaN has no scale; it is stored as s =
+// NaN and reads back as NaN.
+//
+// All three are bound by memory: they touch each byte once.  A row of dim
+// channels belongs to 16 lanes; lane j holds channel pair j of every block,
+// which is the cache's pair order, so codes leave (or come) in one access of
+// dim / 16 bytes and the row outside in dim / 32 accesses, each of 16
+// neighbouring pairs.
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include "q8_cache.h"
+
+namespace q8 {
+namespace {
+
+template <RowType T>
+struct Elem;
+template <>
+struct Elem<kRowF32> {
+  typedef float type;
+  static __device__ __forceinline__ float to_float(float x) { return x; }
+  static __device__ __forceinline__ float from_float(float x) { return x; }
+};
+template <>
+struct Elem<kRowBf16> {
+  typedef __bf16 type;
+  static __device__ __forceinline__ float to_float(__bf16 x) { return (float)x; }
+  static __device__ __forceinline__ __bf16 from_float(float x) { return (__bf16)x; }
+};
+template <>
+struct Elem<kRowF16> {
+  typedef _Float16 type;
+  static __device__ __forceinline__ float to_float(_Float16 x) { return (float)x; }
+  static __device__ __forceinline__ _Float16 from_float(float x) { return (_Float16)x; }
+};
+
+// Two neighbouring elements, aligned as one: a row may start at any element.
+template <typename E>
+struct __attribute__((packed, aligned(sizeof(E)))) Pair {
+  E x, y;
+};
+
+// Largest |x| of a 16-lane group, NaN if any lane's is.
+__device__ __forceinline__ float group_max(float m) {
+#define Q8_STEP(ctrl)                                                                                    \
+  {                                                                                                      \
+    const float o = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), ctrl, 0xf, 0xf, false)); \
+    m = (o > m || o != o) ? o : m;                                                                       \
+  }
+  Q8_STEP(0x128) Q8_STEP(0x124) Q8_STEP(0x122) Q8_STEP(0x121)  // row_ror:8, 4, 2, 1
+#undef Q8_STEP
+  return m;
+}
+
+// Where row t of the row tensors lives: found by the whole wave (t is the same
+// in all lanes).  64 sequences are looked at per step, so up to 64 sequences
+// take one round of loads, and 4096 take two.
+struct Place {
+  bool found;
+  Seq seq;
+  int index;  // among the sequence's new tokens
+  int b;
+};
+
+__device__ __forceinline__ Place find_row(const Seqs &s, int t, int lane) {
+  int lo = 0, n = s.seqs;
+  while (n > 64) {
+    const int step = (n + 63) / 64;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && s.offsets[at] <= t;
+    int k = __popcll(__ballot(below)) - 1;
+    if (k < 0) k = 0;  // rows before the first sequence
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  const bool in = lane < n;
+  const int b = lo + (in ? lane : 0);
+  const int start = s.offsets[b], end = s.offsets[b + 1], length = s.lengths[b];
+  const uint64_t hit = __ballot(in && start <= t && t < end);
+  Place p;
+  p.found = hit != 0;
+  const int from = p.found ? __builtin_ctzll(hit) : 0;
+  p.b = __builtin_amdgcn_readfirstlane(lo + from);
+  p.seq = seq_of(s, __builtin_amdgcn_readlane(start, from), __builtin_amdgcn_readlane(end, from),
+                 __builtin_amdgcn_readlane(length, from));
+  p.found = p.found && p.seq.n > 0;
+  p.index = t - p.seq.start;
+  return p;
+}
+
+// First element, among the page's token rows of head 0, of position `pos` of
+// sequence b; -1 where the table holds no page of the cache.
+__device__ __forceinline__ int64_t token_row(const Cache &c, const Seqs &s, int b, int pos) {
+  const int page = s.table[(int64_t)b * s.table_stride + (pos >> c.page_shift)];
+  if (page < 0 || (int64_t)page >= c.pages) return -1;
+  return (((int64_t)page * c.heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+template <int DIM>
+struct CodeWord;  // the dim / 16 bytes of one lane
+template <>
+struct CodeWord<64> { typedef uint32_t type; };
+template <>
+struct CodeWord<128> { typedef uint2 type; };
+template <>
+struct CodeWord<256> { typedef uint4 type; };
+
+constexpr int kRowsPerGroup = 2;                              // (head, K or V) rows per 16-lane group
+constexpr int kRowsPerWave = kRowsPerGroup * 4;
+
+// A wave takes one token's rows r = kRowsPerWave * blockIdx.y ..: row r is
+// head r / 2, K for even r and V for odd.
+template <RowType T, int DIM>
+__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) {
+  typedef typename Elem<T>::type E;
+  typedef typename CodeWord<DIM>::type Word;
+  constexpr int NB = DIM / 32;
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (t >= p.s.rows) return;
+  const int group = lane >> 4, j = lane & 15;
+  const int nrows = 2 * p.c.heads;
+  const int r0 = blockIdx.y * kRowsPerWave + group;
+
+  float x[kRowsPerGroup][NB][2];
+#pragma unroll
+  for (int q = 0; q < kRowsPerGroup; ++q) {
+    const int r = r0 + 4 * q;
+    const int rr = r < nrows ? r : 0;
+    const E *row = static_cast<const E *>((rr & 1) ? p.v : p.k) + (int64_t)t * ((rr & 1) ? p.v_stride : p.k_stride) +
+                   (int64_t)(rr >> 1) * DIM;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Pair<E> v = *reinterpret_cast<const Pair<E> *>(row + 32 * b + 2 * j);
+      x[q][b][0] = Elem<T>::to_float(v.x);
+      x[q][b][1] = Elem<T>::to_float(v.y);
+    }
+  }
+  const Place at = find_row(p.s, t, lane);
+  if (!at.found || at.seq.bad) return;
+  const int64_t base = token_row(p.c, p.s, at.b, at.seq.length - at.seq.n + at.index);
+  if (base < 0) return;
+#pragma unroll
+  for (int q = 0; q < kRowsPerGroup; ++q) {
+    const int r = r0 + 4 * q;
+    union {
+      Word w;
+      int8_t c[2 * NB];
+    } out;
+    float mine = 0.f;  // lane b keeps block b's scale
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float a0 = fabsf(x[q][b][0]), a1 = fabsf(x[q][b][1]);
+      const float top = group_max((a1 > a0 || a1 != a1) ? a1 : a0);
+      const bool fine = top < INFINITY;  // not for NaN either
+      const float s = fine ? top / 127.f : NAN;
+      if (j == b) mine = s;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float c = 0.f;
+        if (fine && s > 0.f) {
+          c = rintf(x[q][b][i] / s);
+          const float rest = fmaf(-c, s, x[q][b][i]);
+          const float half = 0.5f * s;
+          // Past half a step the next code is nearer; at half a step the even one is.
+          const bool odd = ((int)c & 1) != 0;
+          if (rest > half || (rest == half && odd)) c += 1.f;
+          if (rest < -half || (rest == -half && odd)) c -= 1.f;
+          c = fminf(fmaxf(c, -127.f), 127.f);
+        }
+        out.c[2 * b + i] = (int8_t)(int)c;
+      }
+    }
+    if (r < nrows) {
+      const int64_t row = base + ((int64_t)(r >> 1) << p.c.page_shift);
+      int8_t *codes = (r & 1) ? p.c.V : p.c.K;
+      float *scales = (r & 1) ? p.c.VS : p.c.KS;
+      *reinterpret_cast<Word *>(codes + row * DIM + j * (DIM / 16)) = out.w;
+      if (j < NB) scales[row * NB + j] = mine;
+    }
+  }
+}
+
+template <RowType T, int DIM>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
+  typedef typename Elem<T>::type E;
+  typedef typename CodeWord<DIM>::type Word;
+  constexpr int NB = DIM / 32;
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (t >= p.s.rows) return;
+  const int group = lane >> 4, j = lane & 15;
+  const int nrows = 2 * p.c.heads;
+  const int r0 = blockIdx.y * kRowsPerWave + group;
+  const Place at = find_row(p.s, t, lane);
+  if (!at.found) return;  // no sequence's row: left as it was
+  int64_t base = -1;
+  if (!at.seq.bad) base = token_row(p.c, p.s, at.b, at.seq.length - at.seq.n + at.index);
+#pragma unroll
+  for (int q = 0; q < kRowsPerGroup; ++q) {
+    const int r = r0 + 4 * q;
+    if (r >= nrows) continue;
+    union {
+      Word w;
+      int8_t c[2 * NB];
+    } in;
+    float s[NB];
+    if (base >= 0) {
+      const int64_t row = base + ((int64_t)(r >> 1) << p.c.page_shift);
+      in.w = *reinterpret_cast<const Word *>(((r & 1) ? p.c.V : p.c.K) + row * DIM + j * (DIM / 16));
+      const float *scales = ((r & 1) ? p.c.VS : p.c.KS) + row * NB;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) s[b] = scales[b];
+    } else {  // no such token: NaN, never a wrong value
+      in.w = Word{};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) s[b] = NAN;
+    }
+    E *row = static_cast<E *>((r & 1) ? p.v : p.k) + (int64_t)t * ((r & 1) ? p.v_stride : p.k_stride) +
+             (int64_t)(r >> 1) * DIM;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      Pair<E> v;
+      v.x = Elem<T>::from_float((float)in.c[2 * b] * s[b]);
+      v.y = Elem<T>::from_float((float)in.c[2 * b + 1] * s[b]);
+      *reinterpret_cast<Pair<E> *>(row + 32 * b + 2 * j) = v;
+    }
+  }
+}
+
+// keep: one workgroup per (sequence, head).  The kept indexes ascend strictly,
+// so place a is at or before the place of keep[a], and never one that a later
+// step reads (keep[a'] > keep[a] >= a for a' > a).  It may be one that an
+// earlier step reads, so a chunk's rows are all read before any is written.
+template <int DIM>
+__global__ __launch_bounds__(kThreads) void cache_keep_kernel(CacheKeepArgs p) {
+  typedef typename CodeWord<DIM>::type Word;
+  constexpr int NB = DIM / 32;
+  constexpr int kChunk = kThreads / 16;  // 16-lane groups: one kept token each
+  const int b = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int group = tid >> 4, j = tid & 15;
+  const Seq seq = seq_at(p.s, b);
+  if (seq.n == 0 || seq.bad) return;
+  const int first = seq.length - seq.n;
+  const int *keep = p.keep + (int64_t)b * p.width;
+
+  for (int a0 = 0; a0 < p.width; a0 += kChunk) {
+    // How many of this chunk's entries are kept: up to the first that is not
+    // an index of a new token or does not ascend.
+    const int a = a0 + group;
+    int from = -1, before = -1;
+    if (a < p.width) {
+      from = keep[a];
+      if (a > 0) before = keep[a - 1];
+    }
+    const bool ok = a < p.width && from > before && from < seq.n && from >= 0;
+    __shared__ int good[kChunk];
+    if (j == 0) good[group] = ok;
+    __syncthreads();
+    int count = 0;
+    while (count < kChunk && good[count]) ++count;
+    const bool mine = group < count;
+    int64_t src = -1, dst = -1;
+    if (mine) {
+      src = token_row(p.c, p.s, b, first + from);
+      dst = token_row(p.c, p.s, b, first + a);
+    }
+    const bool move = mine && src >= 0 && dst >= 0 && src != dst;
+    for (int h = blockIdx.y; h < p.c.heads; h += gridDim.y) {
+      const int64_t head = (int64_t)h << p.c.page_shift;
+      Word kw{}, vw{};
+      float ks = 0.f, vs = 0.f;
+      if (move) {
+        kw = *reinterpret_cast<const Word *>(p.c.K + (src + head) * DIM + j * (DIM / 16));
+        vw = *reinterpret_cast<const Word *>(p.c.V + (src + head) * DIM + j * (DIM / 16));
+        if (j < NB) {
+          ks = p.c.KS[(src + head) * NB + j];
+          vs = p.c.VS[(src + head) * NB + j];
+        }
+      }
+      // Every wave's rows of this chunk have arrived before any is written.
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (move) {
+        *reinterpret_cast<Word *>(p.c.K + (dst + head) * DIM + j * (DIM / 16)) = kw;
+        *reinterpret_cast<Word *>(p.c.V + (dst + head) * DIM + j * (DIM / 16)) = vw;
+        if (j < NB) {
+          p.c.KS[(dst + head) * NB + j] = ks;
+          p.c.VS[(dst + head) * NB + j] = vs;
+        }
+      }
+    }
+    if (count < kChunk) return;  // the same in every thread
+    __syncthreads();             // `good` is written again
+  }
+}
+
+template <RowType T>
+hipError_t launch_rows(const CacheRowsArgs &a, bool write, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.s.rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kRowsPerWave - 1) / kRowsPerWave));
+#define Q8_LAUNCH(DIM)                                                                                   \
+  case DIM:                                                                                              \
+    if (write)                                                                                           \
+      hipLaunchKernelGGL((cache_write_kernel<T, DIM>), grid, dim3(kThreads), 0, stream, a);              \
+    else                                                                                                 \
+      hipLaunchKernelGGL((cache_read_kernel<T, DIM>), grid, dim3(kThreads), 0, stream, a);               \
+    return hipGetLastError();
+  switch (a.c.dim) {
+    Q8_LAUNCH(64)
+    Q8_LAUNCH(128)
+    Q8_LAUNCH(256)
+  }
+#undef Q8_LAUNCH
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_typed(const CacheRowsArgs &a, RowType type, bool write, hipStream_t stream) {
+  switch (type) {
+    case kRowF32: return launch_rows<kRowF32>(a, write, stream);
+    case kRowBf16: return launch_rows<kRowBf16>(a, write, stream);
+    case kRowF16: return launch_rows<kRowF16>(a, write, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const CacheRowsArgs &a, RowType type, hipStream_t stream) {
+  return launch_typed(a, type, true, stream);
+}
+
+hipError_t launch_cache_read(const CacheRowsArgs &a, RowType type, hipStream_t stream) {
+  return launch_typed(a, type, false, stream);
+}
+
+hipError_t launch_cache_keep(const CacheKeepArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.s.seqs, (unsigned)(a.c.heads < 65535 ? a.c.heads : 65535));
+  switch (a.c.dim) {
+    case 64: hipLaunchKernelGGL((cache_keep_kernel<64>), grid, dim3(kThreads), 0, stream, a); break;
+    case 128: hipLaunchKernelGGL((cache_keep_kernel<128>), grid, dim3(kThreads), 0, stream, a); break;
+    case 256: hipLaunchKernelGGL((cache_keep_kernel<256>), grid, dim3(kThreads), 0, stream, a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace q8

@@ -1,0 +1,406 @@
+"""Attention over the Q8_0 cache on the GPU, against the f64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import cache_cases as cc
+from oracle import cache as oc
+from quantized_decode_gemv_q8_amd import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def handle(c):
+    return binding.Q8Cache(*(dev(c[n]) for n in ("k", "k_scale", "v", "v_scale")))
+
+
+class Case:
+    """Random sequences and queries of one call, and its outputs in f64."""
+
+    def __init__(self, seed, lengths, news, heads, group, dim, page_size, dtype, tree=False, first=0, pad=0,
+                 alpha=None, q_scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.table, pages = cc.layout(rng, lengths, page_size)
+        self.c = cc.random_cache(rng, pages, heads, page_size, dim)
+        self.lengths = np.array(lengths, np.int32)
+        self.offsets = cc.offsets_of(news, first)
+        self.rows = int(self.offsets[-1]) + pad
+        self.q, self.qf = cc.rows_of(rng, (self.rows, heads * group, dim), dtype, q_scale)
+        self.alpha = dim ** -0.5 if alpha is None else alpha
+        self.trees = [cc.random_tree(rng, n) for n in news] if tree else None
+        self.words = -(-max(list(news) + [1]) // 64)
+        self.dtype = dtype
+
+    def bits(self):
+        if self.trees is None:
+            return None
+        return dev(cc.tree_words(self.trees, self.rows, self.words, int(self.offsets[0])))
+
+    def held(self):
+        return dev(self.table), dev(self.lengths), dev(self.offsets)
+
+    def run(self, cache=None, **kw):
+        return binding.q8_cache_attention(self.q.to(DEV), cache or handle(self.c), *self.held(), tree=self.bits(),
+                                          alpha=self.alpha, **kw)
+
+    def want(self):
+        return oc.attention(self.qf, self.c, self.table, self.lengths, self.offsets, self.alpha, self.trees)
+
+    def check(self, out):
+        ref, spread, size = self.want()
+        own = slice(int(self.offsets[0]), int(self.offsets[-1]))
+        got = out.float().cpu().numpy().astype(np.float64)
+        far = np.abs(got - ref)[own] / cc.attention_bound(ref, spread, size, self.dtype)[own]
+        assert far.size == 0 or far.max() <= 1, f"{far.max():.3f} of the bound at {np.unravel_index(far.argmax(), far.shape)}"
+
+
+# lengths, new tokens: one token alone; the last key at and beside the ends of
+# tiles, units and pages; ragged, with sequences that bring nothing; pieces of prompts
+LENGTHS = [
+    ([1], [1]),
+    ([31, 32, 33, 127, 128, 129], [1, 1, 1, 1, 1, 1]),
+    ([40, 0, 333, 7, 90], [3, 0, 33, 1, 0]),
+    ([150, 64], [70, 64]),
+    ([1500], [2]),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("which", range(len(LENGTHS)))
+def test_attention(which, tree, dim, dtype):
+    lengths, news = LENGTHS[which]
+    heads, group, page = [(1, 1, 16), (2, 4, 64), (3, 7, 16), (1, 5, 128), (2, 8, 32)][which]
+    c = Case((21, which, dim, tree), lengths, news, heads, group, dim, page, dtype, tree)
+    print(f"[attention] {which} tree {tree} dim {dim} {dtype}", flush=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 16, 17, 31, 33, 40, 64])
+def test_groups(group):
+    """Groups that fill an item, leave rows over, or are cut into sub-groups."""
+    for dim, news in ((128, [1, 1]), (128, [9, 2]), (256, [5, 1])):
+        c = Case((22, group, dim), [70, 200], news, 2, group, dim, 16, torch.float32, tree=group % 2 == 0)
+        print(f"[attention] group {group} dim {dim} new {news}", flush=True)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("seqs", [255, 256, 257, 700])
+def test_many_sequences(seqs):
+    """More sequences than a workgroup has threads; some bring nothing."""
+    rng = np.random.default_rng(seqs)
+    news = rng.integers(0, 3, seqs).tolist()
+    lengths = [n + int(x) if n else 0 for n, x in zip(news, rng.integers(0, 200, seqs))]
+    c = Case((23, seqs), lengths, news, 2, 2, 64, 16, torch.float16)
+    print(f"[attention] {seqs} sequences", flush=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_split_over_many_workgroups(dtype):
+    """Few rows over long sequences: every item is joined from many parts."""
+    for lengths, news, heads, group, dim in (([40000], [1], 1, 1, 128), ([9000, 30, 20011], [1, 1, 2], 1, 8, 64),
+                                             ([17001], [1], 2, 4, 256)):
+        c = Case((24, len(lengths), dim), lengths, news, heads, group, dim, 64, dtype)
+        print(f"[attention] long {lengths} {dtype}", flush=True)
+        c.check(c.run())
+
+
+def test_long_pieces_of_prompts():
+    """Many items per sequence: the first ones see fewer keys than the last."""
+    for news, lengths in (([300, 129], [300, 200]), ([257], [1000])):
+        c = Case((25, len(news)), lengths, news, 2, 3, 64, 32, torch.float32)
+        print(f"[attention] pieces {news}", flush=True)
+        c.check(c.run())
+
+
+def test_wide_tree():
+    """Trees over several words, beside sequences with fewer tokens than the words hold."""
+    c = Case(26, [400, 130, 65], [200, 130, 1], 1, 2, 64, 16, torch.float32, tree=True)
+    c.check(c.run())
+
+
+def test_rows_that_see_nothing():
+    """No token before the new ones and an empty mask: zeros, not NaN; also with
+    a mask of no words, and where the key the row does not see holds NaN."""
+    c = Case(27, [5, 40, 3], [5, 3, 3], 2, 2, 128, 16, torch.float32, tree=True)
+    c.trees[0][1] = 0
+    c.trees[0][4] = 0b00010
+    c.trees[1][0] = 0
+    c.trees[2] = [0, 0, 0]
+    c.check(c.run())
+    assert c.run()[1].abs().max() == 0
+    c.trees[2] = [0b010, 0b010, 0b010]
+    page, at = oc.slot_of(c.table, 16, 2, 0)
+    c.c["k_scale"][page, :, at] = np.nan       # new token 0 of sequence 2: seen by none
+    c.c["v_scale"][page, :, at] = np.nan
+    page, at = oc.slot_of(c.table, 16, 0, 3)
+    c.c["v_scale"][page, :, at] = np.nan       # new token 3 of sequence 0: seen by those whose bit says so
+    c.c["k_scale"][page, :, at, 0] = np.inf
+    out = c.run().cpu()
+    ref = torch.from_numpy(c.want()[0])
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    seen3 = [t >> 3 & 1 for t in c.trees[0]]
+    assert any(seen3) and not all(seen3)
+    c.c["v_scale"][page, :, at] = 1.0
+    empty = c.held()
+    none = binding.q8_cache_attention(c.q.to(DEV), handle(c.c), *empty,
+                                      tree=torch.zeros((c.rows, 0), dtype=torch.int64, device=DEV))
+    assert bool((none[:5] == 0).all()) and bool((none[8:] == 0).all()) and bool((none[5:8] != 0).any())
+
+
+def test_garbage_behind_the_last_token():
+    """What a page holds behind its sequence's last token changes no bit."""
+    c = Case(28, [37, 129], [1, 5], 2, 4, 128, 64, torch.bfloat16)
+    want = c.run()
+    for b, n in enumerate(c.lengths):
+        page, at = oc.slot_of(c.table, 64, b, int(n))
+        for name in ("k", "v"):
+            c.c[name][page, :, at:] = 127
+            c.c[name + "_scale"][page, :, at:] = [np.nan, np.inf][b]
+    assert torch.equal(c.run(), want)
+
+
+def test_rows_of_no_sequence_and_rows_apart():
+    """Padded rows keep what out holds; q and out may be views with rows apart, at any element."""
+    c = Case(29, [50, 20], [3, 4], 2, 3, 64, 16, torch.float16, first=2, pad=3)
+    width = 6 * 64
+    wide = torch.zeros((c.rows, width + 9), dtype=torch.float16, device=DEV)
+    q = wide[:, 3:3 + width].unflatten(1, (6, 64))
+    q.copy_(c.q)
+    room = torch.full((c.rows, width + 5), 7.0, dtype=torch.float16, device=DEV)
+    out = room[:, 1:1 + width].unflatten(1, (6, 64))
+    got = binding.q8_cache_attention(q, handle(c.c), *c.held(), alpha=c.alpha, out=out)
+    assert got is out
+    c.check(out)
+    assert bool((room[:2] == 7).all()) and bool((room[-3:] == 7).all())
+    assert bool((room[:, 0] == 7).all()) and bool((room[:, 1 + width:] == 7).all())
+    assert torch.equal(out[2:-3], c.run()[2:-3])
+
+
+@pytest.mark.parametrize("alpha", [0.0, -0.3, 1.0, 4.0])
+def test_alpha(alpha):
+    c = Case(30, [300, 5], [2, 1], 1, 4, 128, 16, torch.float32, alpha=alpha)
+    c.check(c.run())
+
+
+def test_large_scores():
+    """Scores of hundreds: one key takes nearly all the weight; q of 1e30 still makes finite ones with a small alpha."""
+    c = Case(31, [500, 77], [1, 2], 2, 2, 64, 16, torch.float32, q_scale=60.0)
+    c.check(c.run())
+    c = Case(32, [500], [1], 2, 2, 64, 16, torch.float32, q_scale=1e30, alpha=1e-31)
+    c.check(c.run())
+
+
+def test_infinite_and_nan_queries():
+    """A row whose query is not finite gives NaN; its neighbours are as without it."""
+    c = Case(33, [80, 40], [4, 1], 1, 4, 128, 16, torch.bfloat16)
+    cache = handle(c.c)
+    want = c.run(cache)
+    c.q[1, 2, 5] = float("nan")
+    c.q[3, 0, 100] = float("inf")
+    got = c.run(cache)
+    hit = torch.zeros(got.shape[:2], dtype=torch.bool)
+    hit[1, 2] = hit[3, 0] = True
+    assert bool(torch.isnan(got.cpu()[hit]).all()) and torch.equal(got.cpu()[~hit], want.cpu()[~hit])
+
+
+def test_bad_descriptions():
+    """A sequence with a wrong length or a page that is not the cache's gives
+    NaN; the others are as without it; one whose offsets are wrong has no rows."""
+    c = Case(34, [90, 200, 64], [2, 3, 1], 2, 2, 64, 16, torch.float32)
+    cache, q = handle(c.c), c.q.to(DEV)
+    want = c.run(cache).cpu()
+    c.check(want)
+    cases = [("page below", 0, 1, -1), ("page above", 0, 4, len(c.c["k"])), ("page far above", 0, 12, 2 ** 31 - 1),
+             ("length negative", 1, 1, -7), ("length below its new tokens", 1, 1, 2),
+             ("length past the table", 1, 1, 2 ** 31 - 1), ("offsets past the rows", 2, 2, 2 ** 31 - 1),
+             ("offsets descend", 2, 2, 0)]
+    for name, where, at, value in cases:
+        t, n, o = c.table.copy(), c.lengths.copy(), c.offsets.copy()
+        print(f"[attention] {name}", flush=True)
+        if where == 0:
+            t[1, at] = value
+        else:
+            (n if where == 1 else o)[at] = value
+        out = torch.full(q.shape, 5.0, device=DEV)
+        binding.q8_cache_attention(q, cache, dev(t), dev(n), dev(o), alpha=c.alpha, out=out)
+        got = out.cpu()
+        if name == "offsets descend":  # sequence 2 now claims rows 0 .. 5, sequence 0's among them
+            assert bool(torch.isfinite(got).all())
+            continue
+        assert torch.equal(got[:2], want[:2]), name
+        if where == 2:     # sequence 1 has no rows, and 2 none either
+            assert bool((got[2:] == 5).all()), name
+        else:
+            assert bool(torch.isnan(got[2:5]).all()) and torch.equal(got[5], want[5]), name
+
+
+def test_table_entries_past_the_tokens_are_not_read():
+    c = Case(35, [20, 65], [1, 2], 1, 2, 128, 16, torch.float32)
+    want = c.run()
+    for b, n in enumerate(c.lengths):
+        c.table[b, -(-n // 16):] = 2 ** 31 - 1
+    assert torch.equal(c.run(), want)
+
+
+def test_same_call_gives_the_same_bits():
+    c = Case(36, [5000, 300, 9], [1, 4, 9], 2, 4, 128, 64, torch.float32, tree=True)
+    cache = handle(c.c)
+    first = c.run(cache)
+    for _ in range(5):
+        assert torch.equal(c.run(cache), first)
+
+
+def test_empty_calls():
+    c = Case(37, [20], [1], 1, 1, 64, 16, torch.float32)
+    cache = handle(c.c)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = binding.q8_cache_attention(c.q[:0].to(DEV), cache, *c.held())
+    assert out.shape == (0, 1, 64)
+    keepsake = torch.full(c.q.shape, 5.0, device=DEV)
+    binding.q8_cache_attention(c.q.to(DEV), cache, none.reshape(0, 4), none, torch.zeros(1, dtype=torch.int32, device=DEV),
+                               out=keepsake)
+    binding.q8_cache_attention(c.q.to(DEV), cache, c.held()[0], c.held()[1], torch.zeros(2, dtype=torch.int32, device=DEV),
+                               out=keepsake)
+    assert bool((keepsake == 5).all())
+
+
+def test_captured_and_replayed():
+    """A captured step follows the lengths, pages, offsets and rows that its
+    tensors hold at each replay; eager work of another shape runs between."""
+    lengths, news = [700, 30, 129], [1, 1, 1]
+    c = Case(38, [900, 900, 900], news, 2, 4, 128, 64, torch.float32)
+    c.lengths = np.array(lengths, np.int32)
+    cache = handle(c.c)
+    table, n, offsets = c.held()
+    q, k, v = c.q.to(DEV), torch.randn((3, 2, 128), device=DEV), torch.randn((3, 2, 128), device=DEV)
+    out = torch.empty_like(q)
+
+    def step():
+        binding.q8_cache_write(cache, k, v, table, n, offsets)
+        binding.q8_cache_attention(q, cache, table, n, offsets, alpha=c.alpha, out=out)
+
+    step()
+    oc.write(c.c, k.cpu().numpy(), v.cpu().numpy(), c.table, c.lengths, c.offsets)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    other = Case(39, [3000], [5], 1, 4, 128, 64, torch.float32, tree=True)
+    for turn in range(4):
+        n += 1
+        q.normal_()
+        k.normal_()
+        v.normal_()
+        other.check(other.run())
+        out.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = out.clone()
+        oc.write(c.c, k.cpu().numpy(), v.cpu().numpy(), c.table, n.cpu().numpy(), c.offsets)
+        c.lengths, c.qf = n.cpu().numpy(), q.cpu().numpy()
+        c.check(replayed)
+        out.fill_(0)
+        step()
+        assert torch.equal(out, replayed)
+
+
+def test_two_graphs_replayed_at_once():
+    """Two captured calls have workspaces of their own."""
+    cases = [Case((40, i), [6000 + 500 * i], [1], 1, 8, 128, 64, torch.float32) for i in range(2)]
+    caches, runs, graphs, outs = [], [], [], []
+    for c in cases:
+        cache, held, q = handle(c.c), c.held(), c.q.to(DEV)
+        out = torch.empty_like(q)
+        binding.q8_cache_attention(q, cache, *held, out=out)
+        torch.cuda.synchronize()
+        runs.append(out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.q8_cache_attention(q, cache, *held, out=out)
+        caches.append((cache, held, q))
+        graphs.append(g)
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, out, first in zip(cases, outs, runs):
+        assert torch.equal(out, first)
+        c.check(out)
+
+
+def test_streams():
+    """A stream given by name, and calls on several streams at once."""
+    cases = [Case((41, i), [2000 + 300 * i, 90], [1, 2], 2, 4, 64, 16, torch.bfloat16) for i in range(3)]
+    caches = [handle(c.c) for c in cases]
+    helds, qs = [c.held() for c in cases], [c.q.to(DEV) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(4):
+        outs = [binding.q8_cache_attention(q, cache, *h, alpha=c.alpha, stream=s)
+                for c, cache, h, q, s in zip(cases, caches, helds, qs, streams)]
+    torch.cuda.synchronize()
+    for c, out in zip(cases, outs):
+        c.check(out)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_drafting_step(dtype):
+    """As a serving loop runs it: prompts in pieces, then a tree of drafts
+    written and attended to, the accepted ones kept, and the next token's
+    attention over what is left; the cache read back at the end."""
+    heads, group, dim, page = 2, 4, 64, 16
+    rng = np.random.default_rng(42)
+    table = rng.permutation(20).reshape(2, 10).astype(np.int32)
+    c = cc.random_cache(rng, 20, heads, page, dim)
+    cache, dtable = handle(c), dev(table)
+    lengths = np.array([0, 0], np.int32)
+
+    def step(news, trees=None):
+        nonlocal lengths
+        lengths = lengths + np.array(news, np.int32)
+        offsets = cc.offsets_of(news)
+        rows = int(offsets[-1])
+        held = (dtable, dev(lengths), dev(offsets))
+        k, kf = cc.rows_of(rng, (rows, heads, dim), dtype)
+        v, vf = cc.rows_of(rng, (rows, heads, dim), dtype)
+        q, qf = cc.rows_of(rng, (rows, heads * group, dim), dtype)
+        binding.q8_cache_write(cache, k.to(DEV), v.to(DEV), *held)
+        oc.write(c, kf, vf, table, lengths, offsets)
+        bits = None if trees is None else dev(cc.tree_words(trees, rows, 1))
+        out = binding.q8_cache_attention(q.to(DEV), cache, *held, tree=bits)
+        ref, spread, size = oc.attention(qf, c, table, lengths, offsets, dim ** -0.5, trees)
+        far = np.abs(out.float().cpu().numpy() - ref) / cc.attention_bound(ref, spread, size, dtype)
+        assert far.max() <= 1
+        return held, offsets
+
+    step([50, 3])
+    step([17, 40])
+    held, offsets = step([12, 9], [cc.random_tree(rng, 12), cc.random_tree(rng, 9)])
+    kept = [[0, 3, 7, 11], [2]]
+    keep = np.full((2, 4), -1, np.int32)
+    for b, x in enumerate(kept):
+        keep[b, :len(x)] = x
+    binding.q8_cache_keep(cache, *held, dev(keep))
+    oc.keep(c, table, lengths, offsets, kept)
+    lengths = lengths - np.array([12 - 4, 9 - 1], np.int32)
+    step([1, 1])
+    offsets = cc.offsets_of(lengths)
+    k, v = binding.q8_cache_read(cache, dtable, dev(lengths), dev(offsets), int(offsets[-1]), dtype=dtype)
+    ek, ev = oc.read(c, table, lengths, offsets)
+    for got, want in ((k, ek), (v, ev)):
+        assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(dtype))
