@@ -370,7 +370,7 @@ class Q8Cache:
     stay the caller's; the handle only checks them once.
     """
 
-    __slots__ = ("k", "k_scale", "v", "v_scale", "pages", "heads", "page_size", "dim", "device", "_struct")
+    __slots__ = ("k", "k_scale", "v", "v_scale", "pages", "heads", "page_size", "dim", "device", "_struct", "_spans")
 
     def __init__(self, k, k_scale, v, v_scale):
         if not isinstance(k, torch.Tensor):
@@ -393,6 +393,7 @@ class Q8Cache:
                             [(b, getattr(self, b)) for b in ("k", "k_scale", "v", "v_scale")[:i]])
         self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
         self.device = k.device
+        self._spans = tuple(("the cache", *_span(t)) for t in (k, k_scale, v, v_scale))
         self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
                                     pages, heads, page_size, dim)
 
@@ -418,7 +419,7 @@ def _cache_seqs(cache, table, lengths, offsets):
             raise ValueError("all tensors must be on one device")
         if t.dim() != rank:
             raise ValueError(f"{name} must be rank {rank}, got {t.dim()} dimensions")
-        if t.numel() and t.stride(-1) != 1:
+        if t.stride(-1) != 1 and t.numel():
             raise ValueError(f"{name} must be contiguous in its last dimension")
     n, pages = table.shape
     if lengths.shape[0] != n or offsets.shape[0] != n + 1:
@@ -439,18 +440,20 @@ def _cache_rows(name, t, rows, heads, cache, dtype=None):
         raise ValueError(f"{name} must be {want}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError("all tensors must be on one device")
-    if t.dim() != 3 or t.shape[2] != cache.dim or (rows is not None and t.shape[0] != rows) or \
-            (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.dim or (rows is not None and shape[0] != rows) or \
+            (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, "
-                         f"{'heads' if heads is None else heads}, {cache.dim}), got {tuple(t.shape)}")
-    s = t.stride()
-    if t.numel() == 0:
-        return t.shape[1] * t.shape[2]
-    if s[2] != 1 or (t.shape[1] > 1 and s[1] != cache.dim):
+                         f"{'heads' if heads is None else heads}, {cache.dim}), got {tuple(shape)}")
+    n, h, dim = shape
+    if n == 0 or h == 0:
+        return h * dim
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != dim):
         raise ValueError(f"{name} must be dense in its last two dimensions")
-    if t.shape[0] > 1 and s[0] < t.shape[1] * t.shape[2]:
+    if n > 1 and s0 < h * dim:
         raise ValueError(f"rows of {name} must not overlap")
-    return s[0]
+    return s0
 
 
 def _span(t):
@@ -458,6 +461,8 @@ def _span(t):
     if t.numel() == 0:
         return 0, 0
     a = t.data_ptr()
+    if t.is_contiguous():
+        return a, a + t.numel() * t.element_size()
     return a, a + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
@@ -470,6 +475,17 @@ def _check_apart(out_name, out, others):
         b0, b1 = _span(t)
         if a0 < b1 and b0 < a1 and not _interleaved(out, t):
             raise ValueError(f"{out_name} overlaps {name}")
+
+
+def _check_outside(cache, **tensors):
+    """No tensor of a call shares a byte with the cache."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        b0, b1 = _span(t)
+        for what, a0, a1 in cache._spans:
+            if a0 < b1 and b0 < a1:
+                raise ValueError(f"{name} overlaps {what}")
 
 
 def _interleaved(a, b):
@@ -492,8 +508,16 @@ def _empty_on(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _cache_tensors(cache):
-    return (("the cache", cache.k), ("the cache", cache.k_scale), ("the cache", cache.v), ("the cache", cache.v_scale))
+def _call(cache, stream, what, fn, *args):
+    """fn(*args, stream) on the cache's device; an error status raises."""
+    device = cache.device
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(stream, device))
+    if st != Q8_OK:
+        raise Q8Error(st, what)
 
 
 def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
@@ -503,13 +527,9 @@ def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
     seqs = _cache_seqs(cache, table, lengths, offsets)
     ks = _cache_rows("k", k, None, cache.heads, cache)
     vs = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
-    for name, c in _cache_tensors(cache):
-        _check_apart(name, c, (("k", k), ("v", v), ("table", table), ("lengths", lengths), ("offsets", offsets)))
-    with torch.cuda.device(cache.device):
-        st = load().q8_cache_write(cache._struct, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], k.shape[0], ks, vs,
-                                   seqs, _stream_handle(stream, cache.device))
-    if st != Q8_OK:
-        raise Q8Error(st, "q8_cache_write")
+    _check_outside(cache, k=k, v=v, table=table, lengths=lengths, offsets=offsets)
+    _call(cache, stream, "q8_cache_write", load().q8_cache_write, cache._struct, k.data_ptr(), v.data_ptr(),
+          _ROW_TYPES[k.dtype], k.shape[0], ks, vs, seqs)
 
 
 def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
@@ -518,24 +538,24 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
     the given k and v hold (new tensors: undefined)."""
     seqs = _cache_seqs(cache, table, lengths, offsets)
     shape = (int(rows), cache.heads, cache.dim)
-    new = [t is None for t in (k, v)]
-    if any(new):
+    given = k is not None or v is not None
+    if not given or k is None or v is None:
         if dtype not in _ROW_TYPES:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
         if k is None:
             k = _empty_on(stream, shape, dtype, cache.device)
         if v is None:
             v = _empty_on(stream, shape, dtype, cache.device)
-    ks = _cache_rows("k", k, shape[0], cache.heads, cache)
-    vs = _cache_rows("v", v, shape[0], cache.heads, cache, k.dtype)
-    inputs = _cache_tensors(cache) + (("table", table), ("lengths", lengths), ("offsets", offsets))
-    _check_apart("k", k, inputs)
-    _check_apart("v", v, inputs + (("k", k),))
-    with torch.cuda.device(cache.device):
-        st = load().q8_cache_read(cache._struct, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], shape[0], ks, vs,
-                                  seqs, _stream_handle(stream, cache.device))
-    if st != Q8_OK:
-        raise Q8Error(st, "q8_cache_read")
+    ks = vs = cache.heads * cache.dim
+    if given:
+        ks = _cache_rows("k", k, shape[0], cache.heads, cache)
+        vs = _cache_rows("v", v, shape[0], cache.heads, cache, k.dtype)
+        _check_outside(cache, k=k, v=v)
+        inputs = (("table", table), ("lengths", lengths), ("offsets", offsets))
+        _check_apart("k", k, inputs)
+        _check_apart("v", v, inputs + (("k", k),))
+    _call(cache, stream, "q8_cache_read", load().q8_cache_read, cache._struct, k.data_ptr(), v.data_ptr(),
+          _ROW_TYPES[k.dtype], shape[0], ks, vs, seqs)
     return k, v
 
 
@@ -551,13 +571,9 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
     _check_tensor("keep", keep, torch.int32, (table.shape[0], keep.shape[1]))
     if keep.device != cache.device:
         raise ValueError("all tensors must be on one device")
-    for name, c in _cache_tensors(cache):
-        _check_apart(name, c, (("keep", keep), ("table", table), ("lengths", lengths), ("offsets", offsets)))
-    with torch.cuda.device(cache.device):
-        st = load().q8_cache_keep(cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(), keep.shape[1],
-                                  _stream_handle(stream, cache.device))
-    if st != Q8_OK:
-        raise Q8Error(st, "q8_cache_keep")
+    _check_outside(cache, keep=keep, table=table, lengths=lengths, offsets=offsets)
+    _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(),
+          keep.shape[1])
 
 
 #: Most rows a call's offsets may refer to.
@@ -591,25 +607,38 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
             raise ValueError("all tensors must be on one device")
     if alpha is None:
         alpha = cache.dim ** -0.5
-    L = load()
-    with torch.cuda.device(cache.device):
-        if out is None:
-            out = _empty_on(stream, (rows, q_heads, cache.dim), q.dtype, cache.device)
-            os_ = q_heads * cache.dim
-        else:
-            os_ = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
-            _check_apart("out", out, _cache_tensors(cache) + (("q", q), ("table", table), ("lengths", lengths),
-                                                              ("offsets", offsets), ("tree", tree)))
-        need = ctypes.c_int64(0)
-        st = L.q8_cache_attention_workspace(cache._struct, rows, q_heads, seqs, need)
-        if st == Q8_OK:
-            work = _empty_on(stream, (max(16, need.value),), torch.uint8, cache.device)
-            mask = None
-            if tree is not None:  # an empty tree still is one: no new token is seen
-                mask = tree.data_ptr() if tree.numel() else work.data_ptr()
-            st = L.q8_cache_attention(cache._struct, q.data_ptr(), out.data_ptr(), _ROW_TYPES[q.dtype], rows, q_heads,
-                                      qs, os_, seqs, mask, words, alpha, work.data_ptr(), need.value,
-                                      _stream_handle(stream, cache.device))
-    if st != Q8_OK:
-        raise Q8Error(st, "q8_cache_attention")
+    if out is None:
+        out = _empty_on(stream, (rows, q_heads, cache.dim), q.dtype, cache.device)
+        os_ = q_heads * cache.dim
+    else:
+        os_ = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
+        _check_outside(cache, out=out)
+        _check_apart("out", out, (("q", q), ("table", table), ("lengths", lengths), ("offsets", offsets),
+                                  ("tree", tree)))
+    need = _attention_workspace(cache, rows, q_heads, seqs)
+    work = _empty_on(stream, (max(16, need),), torch.uint8, cache.device)
+    mask = None
+    if tree is not None:  # an empty tree still is one: no new token is seen
+        mask = tree.data_ptr() if tree.numel() else work.data_ptr()
+    _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q.data_ptr(), out.data_ptr(),
+          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha), work.data_ptr(), need)
     return out
+
+
+#: Workspace sizes by the extents that they follow from.
+_WORKSPACE = {}
+
+
+def _attention_workspace(cache, rows, q_heads, seqs):
+    key = (cache.device.index, cache.heads, cache.page_size, cache.dim, rows, q_heads, seqs.seqs, seqs.max_pages)
+    need = _WORKSPACE.get(key)
+    if need is None:
+        size = ctypes.c_int64(0)
+        with torch.cuda.device(cache.device):
+            st = load().q8_cache_attention_workspace(cache._struct, rows, q_heads, seqs, size)
+        if st != Q8_OK:
+            raise Q8Error(st, "q8_cache_attention")
+        if len(_WORKSPACE) >= 4096:
+            _WORKSPACE.clear()
+        need = _WORKSPACE[key] = size.value
+    return need

@@ -745,7 +745,7 @@ q8_status cache_args(const q8_cache *c, const q8_cache_seqs *s, int64_t rows, q8
   cache->KS = c->KS;
   cache->V = c->V;
   cache->VS = c->VS;
-  cache->pages = c->pages;
+  cache->pages = (uint32_t)c->pages;
   cache->heads = c->heads;
   cache->dim = c->dim;
   cache->page_shift = __builtin_ctz((unsigned)c->page_size);

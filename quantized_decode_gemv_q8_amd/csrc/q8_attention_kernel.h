@@ -182,7 +182,7 @@ __device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int
     __syncthreads();
   }
   Run0 r;
-  r.total = sums[kThreads - 1];
+  r.total = uniform(sums[kThreads - 1]);
   r.wgs = (int)(r.total < wgs ? r.total : wgs);
   r.begin = r.end = r.rest = 0;
   r.b = 0;
@@ -202,7 +202,7 @@ __device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int
     }
     __syncthreads();
     r.b = __builtin_amdgcn_readfirstlane(found_b);
-    r.rest = found_rest;
+    r.rest = uniform(found_rest);
   }
   return r;
 }
@@ -277,36 +277,37 @@ struct Attn {
   const AttnArgs *p;
   int lane, row, c;  // row = lane % 16, c = lane / 16
 
-  // Row 16 h + .. of the tile at `pos`: first token row of its page, and
-  // whether the table holds a page there.
-  __device__ __forceinline__ int64_t half_base(const int *pages, int pos, int last, int kvh, bool &ok) const {
+  // The token row, of head kvh, where the 16 keys at `pos` begin.  poison: NaN,
+  // to be added to the scales, where the table holds no page of the cache.
+  __device__ __forceinline__ int64_t half_base(const int *pages, int pos, int last, int kvh, float &poison) const {
     const int at = min(pos, last);
-    int page = pages[at >> p->c.page_shift];
-    ok = page >= 0 && (int64_t)page < p->c.pages;
+    int page = uniform_load(pages + (at >> p->c.page_shift));
+    const bool ok = (uint32_t)page < p->c.pages;
     page = ok ? page : 0;
+    poison = ok ? 0.f : NAN;
     // 16-key halves lie within a page (pages hold 16 tokens or more); one past
     // the last key reads the last key's half instead.
     const int in = at & ((1 << p->c.page_shift) - 1) & ~15;
     return ((((int64_t)page * p->c.heads + kvh) << p->c.page_shift)) + in;
   }
 
-  __device__ __forceinline__ void load_k(const int64_t (&base)[2], const bool (&ok)[2]) {
+  __device__ __forceinline__ void load_k(const int64_t (&base)[2], const float (&poison)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       load_words<KW>(p->c.K + base[h] * DIM + row * DIM + c * (DIM / 4), kw[h]);
       const float *s = p->c.KS + (base[h] + 4 * c) * NB;
 #pragma unroll
-      for (int w = 0; w < SW; ++w) ks[h][w] = ok[h] ? s[(16 * w + row) % (4 * NB)] : NAN;
+      for (int w = 0; w < SW; ++w) ks[h][w] = s[(16 * w + row) % (4 * NB)] + poison[h];
     }
   }
-  __device__ __forceinline__ void load_v(const int64_t (&base)[2], const bool (&ok)[2]) {
+  __device__ __forceinline__ void load_v(const int64_t (&base)[2], const float (&poison)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_words<VW>(p->c.V + (base[h] + 4 * c + i) * DIM + row * (DIM / 16), vw[4 * h + i]);
       const float *s = p->c.VS + (base[h] + 4 * c) * NB;
 #pragma unroll
-      for (int w = 0; w < SW; ++w) vs[h][w] = ok[h] ? s[(16 * w + row) % (4 * NB)] : NAN;
+      for (int w = 0; w < SW; ++w) vs[h][w] = s[(16 * w + row) % (4 * NB)] + poison[h];
     }
   }
 
@@ -338,6 +339,7 @@ struct Attn {
           });
         }
       });
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -410,6 +412,7 @@ struct Attn {
 #pragma unroll
           for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     });
   }
 };
@@ -464,7 +467,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
 
   // Where the run begins: sequence b, head vh (with its sub-group), row item r, unit k0.
   int b = run.b;
-  Seq seq = seq_at(p.s, b);
+  Seq seq = uniform_seq_at(p.s, b);
   int vh, r, k0;
   {
     const int64_t per_head = head_units(p, seq);
@@ -528,35 +531,37 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
       const int end = min(k1 * kAttnUnit, keys);
       if (begin < end) {
         int64_t base[2];
-        bool ok[2];
+        float poison[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, begin + 16 * h, last, kvh, ok[h]);
-        a.load_k(base, ok);
-        a.load_v(base, ok);
-        for (int at = begin; at < end; at += kAttnUnit) {
+        for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, begin + 16 * h, last, kvh, poison[h]);
+        a.load_k(base, poison);
+        a.load_v(base, poison);
+        // Two loops, not a branch in one: the compiler would move what both
+        // sides begin with (128 conversions) above the branch and run out of registers.
+        auto step = [&](auto masked_, int at) {
+          constexpr bool MASKED = decltype(masked_)::value;
           const int next = at + kAttnUnit;
           const bool more = next < end;
           if (more) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, next + 16 * h, last, kvh, ok[h]);
+            for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, next + 16 * h, last, kvh, poison[h]);
           }
           float s[RT][8];
           a.scores(s);
-          if (more) a.load_k(base, ok);
+          if (more) a.load_k(base, poison);
           uint32_t sees[RT];
-          const bool masked = at + kAttnTile > all;
-          if (masked) {
+          if constexpr (MASKED) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
               sees[rt] = seen_bits(p, at, context, seq.n, seq.length, index[rt], seq.start + index[rt]);
-            a.template softmax<true>(s, sees);
-            a.template values<true>(s, sees);
-          } else {
-            a.template softmax<false>(s, sees);
-            a.template values<false>(s, sees);
           }
-          if (more) a.load_v(base, ok);
-        }
+          a.template softmax<MASKED>(s, sees);
+          a.template values<MASKED>(s, sees);
+          if (more) a.load_v(base, poison);
+        };
+        int at = begin;
+        for (; at < end && at + kAttnTile <= all; at += kAttnUnit) step(std::false_type{}, at);
+        for (; at < end; at += kAttnUnit) step(std::true_type{}, at);
       }
     }
 
@@ -642,7 +647,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
       if (++vh == p.c.heads * p.subs) {
         vh = 0;
         do {
-          seq = seq_at(p.s, ++b);
+          seq = uniform_seq_at(p.s, ++b);
         } while (seq.n == 0);
       }
     }

@@ -24,7 +24,7 @@ struct Cache {
   float *KS;
   int8_t *V;
   float *VS;
-  int64_t pages;
+  uint32_t pages;
   int heads, dim;
   int page_shift;  // log2 of page_size
 };
@@ -75,6 +75,20 @@ __device__ __forceinline__ Seq seq_of(const Seqs &s, int start, int end, int len
   q.length = length;
   q.bad = length < q.n || (int64_t)length > s.max_tokens;
   return q;
+}
+
+// A word whose address is the same in all lanes, through the scalar cache.
+__device__ __forceinline__ int uniform_load(const int *p) {
+  return *(const __attribute__((address_space(4))) int *)p;
+}
+__device__ __forceinline__ Seq uniform_seq_at(const Seqs &s, int b) {
+  return seq_of(s, uniform_load(s.offsets + b), uniform_load(s.offsets + b + 1), uniform_load(s.lengths + b));
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 __device__ __forceinline__ Seq seq_at(const Seqs &s, int b) {

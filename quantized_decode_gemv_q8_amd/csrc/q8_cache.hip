@@ -104,7 +104,7 @@ __device__ __forceinline__ Place find_row(const Seqs &s, int t, int lane) {
 // sequence b; -1 where the table holds no page of the cache.
 __device__ __forceinline__ int64_t token_row(const Cache &c, const Seqs &s, int b, int pos) {
   const int page = s.table[(int64_t)b * s.table_stride + (pos >> c.page_shift)];
-  if (page < 0 || (int64_t)page >= c.pages) return -1;
+  if ((uint32_t)page >= c.pages) return -1;
   return (((int64_t)page * c.heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
