@@ -368,7 +368,7 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  *   q, out  [rows, q_heads, dim] of `type`, rows q_stride / out_stride elements
  *           apart; out must not overlap anything else
  *   workspace  device memory of at least the size that
- *           q8_cache_attention_workspace gives for the same cache, rows,
+ *           q8_cache_attention_workspace gives for the same cache, type, rows,
  *           q_heads, seqs and max_pages, 16-byte aligned; its contents need no
  *           preparation and are free again when the call's work is done.  Calls that may
  *           overlap in time (and graphs whose replays may) need one each
@@ -381,8 +381,8 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  * Errors: as q8_cache_write; Q8_ERR_INVALID also for q_heads that is no multiple
  * of heads and for a missing, misaligned or small workspace.
  */
-q8_status q8_cache_attention_workspace(const q8_cache *cache, int64_t rows, int32_t q_heads,
-                                       const q8_cache_seqs *seqs, int64_t *bytes);
+q8_status q8_cache_attention_workspace(const q8_cache *cache, q8_type type, int64_t rows,
+                                       int32_t q_heads, const q8_cache_seqs *seqs, int64_t *bytes);
 q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8_type type,
                              int64_t rows, int32_t q_heads, int64_t q_stride, int64_t out_stride,
                              const q8_cache_seqs *seqs, const uint64_t *tree, int64_t tree_words,

@@ -117,7 +117,7 @@ def load():
         fn.restype = ctypes.c_int
     L.q8_cache_keep.argtypes = [cache, i64, seqs, p, i64, p]
     L.q8_cache_keep.restype = ctypes.c_int
-    L.q8_cache_attention_workspace.argtypes = [cache, i64, i32, seqs, ctypes.POINTER(i64)]
+    L.q8_cache_attention_workspace.argtypes = [cache, ctypes.c_int, i64, i32, seqs, ctypes.POINTER(i64)]
     L.q8_cache_attention_workspace.restype = ctypes.c_int
     L.q8_cache_attention.argtypes = [cache, p, p, ctypes.c_int, i64, i32, i64, i64, seqs, p, i64, ctypes.c_float,
                                      p, i64, p]
@@ -615,7 +615,7 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
         _check_outside(cache, out=out)
         _check_apart("out", out, (("q", q), ("table", table), ("lengths", lengths), ("offsets", offsets),
                                   ("tree", tree)))
-    need = _attention_workspace(cache, rows, q_heads, seqs)
+    need = _attention_workspace(cache, _ROW_TYPES[q.dtype], rows, q_heads, seqs)
     work = _empty_on(stream, (max(16, need),), torch.uint8, cache.device)
     mask = None
     if tree is not None:  # an empty tree still is one: no new token is seen
@@ -629,13 +629,13 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
 _WORKSPACE = {}
 
 
-def _attention_workspace(cache, rows, q_heads, seqs):
-    key = (cache.device.index, cache.heads, cache.page_size, cache.dim, rows, q_heads, seqs.seqs, seqs.max_pages)
+def _attention_workspace(cache, type_, rows, q_heads, seqs):
+    key = (cache.device.index, cache.heads, cache.page_size, cache.dim, type_, rows, q_heads, seqs.seqs, seqs.max_pages)
     need = _WORKSPACE.get(key)
     if need is None:
         size = ctypes.c_int64(0)
         with torch.cuda.device(cache.device):
-            st = load().q8_cache_attention_workspace(cache._struct, rows, q_heads, seqs, size)
+            st = load().q8_cache_attention_workspace(cache._struct, type_, rows, q_heads, seqs, size)
         if st != Q8_OK:
             raise Q8Error(st, "q8_cache_attention")
         if len(_WORKSPACE) >= 4096:

@@ -790,19 +790,19 @@ q8_status cache_rows_impl(const q8_cache *c, const void *k, const void *v, q8_ty
   return hip_status((write ? q8::launch_cache_write : q8::launch_cache_read)(a, (q8::RowType)type, (hipStream_t)stream_v));
 }
 
-// How the rows of an attention call are cut: items of up to 16 * row_tiles
-// rows (tokens x heads of a group), and the workgroups the units are dealt to.
+// How the rows of an attention call are cut: items of up to `tile` rows
+// (tokens x heads of a group), and the workgroups the units are dealt to.
 struct AttnPlan {
-  int row_tiles, subs, sub_heads, tile_tokens;
+  int tile, subs, sub_heads, tile_tokens;
   int64_t wgs, bytes;  // workgroups; workspace
 };
 
-AttnPlan attn_plan(int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens, int cus) {
+AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens,
+                   int cus) {
   AttnPlan p;
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
-  p.row_tiles = 1;
-  while (p.row_tiles < q8::attn_max_row_tiles(dim) && 16 * p.row_tiles < mean) p.row_tiles *= 2;
-  const int tile = 16 * p.row_tiles;
+  p.tile = mean <= 16 ? 16 : mean <= q8::attn_direct_rows(dim) ? 32 : mean <= 64 ? 64 : q8::attn_max_rows(type, dim);
+  const int tile = p.tile;
   p.subs = (int)ceil_div(group, tile);
   p.sub_heads = (int)ceil_div(group, p.subs);
   p.subs = (int)ceil_div(group, p.sub_heads);  // no empty sub-group
@@ -936,11 +936,12 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
   return hip_status(q8::launch_cache_keep(a, (hipStream_t)stream));
 }
 
-q8_status q8_cache_attention_workspace(const q8_cache *cache, int64_t rows, int32_t q_heads, const q8_cache_seqs *seqs,
-                                       int64_t *bytes) {
+q8_status q8_cache_attention_workspace(const q8_cache *cache, q8_type type, int64_t rows, int32_t q_heads,
+                                       const q8_cache_seqs *seqs, int64_t *bytes) {
   q8::Cache c;
   q8::Seqs s;
-  if (bytes == nullptr) return Q8_ERR_INVALID;
+  int64_t elem = 0;
+  if (bytes == nullptr || !row_type(type, &elem)) return Q8_ERR_INVALID;
   q8_status st = cache_args(cache, seqs, rows, &c, &s);
   if (st != Q8_OK) return st;
   if (q_heads < 1 || q_heads % cache->heads != 0) return Q8_ERR_INVALID;
@@ -950,7 +951,7 @@ q8_status q8_cache_attention_workspace(const q8_cache *cache, int64_t rows, int3
   DevInfo info;
   st = current_device(&dev, &info);
   if (st != Q8_OK) return st;
-  *bytes = attn_plan(c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens, info.cus).bytes;
+  *bytes = attn_plan((q8::RowType)type, c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens, info.cus).bytes;
   return Q8_OK;
 }
 
@@ -974,7 +975,7 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   st = current_device(&dev, &info);
   if (st != Q8_OK) return st;
   const AttnPlan pl =
-      attn_plan(a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens, info.cus);
+      attn_plan((q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens, info.cus);
   if (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes) return Q8_ERR_INVALID;
   a.q = q;
   a.out = out;
@@ -988,17 +989,17 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   a.tile_tokens = pl.tile_tokens;
   a.alpha = alpha;
   a.partial = static_cast<float *>(workspace);
-  const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(16 * pl.row_tiles, a.c.dim) * 4;
+  const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
   a.items = reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256);
   if (log_debug())
     log_line("cache_attention rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", (long long)rows,
-             q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", 16 * pl.row_tiles,
+             q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", pl.tile,
              (long long)pl.wgs);
   hipStream_t stream = (hipStream_t)stream_v;
   switch (type) {
-    case Q8_F32: return hip_status(q8::launch_attention_f32(a, pl.row_tiles, (int)pl.wgs, stream));
-    case Q8_BF16: return hip_status(q8::launch_attention_bf16(a, pl.row_tiles, (int)pl.wgs, stream));
-    case Q8_F16: return hip_status(q8::launch_attention_f16(a, pl.row_tiles, (int)pl.wgs, stream));
+    case Q8_F32: return hip_status(q8::launch_attention_f32(a, pl.tile, (int)pl.wgs, stream));
+    case Q8_BF16: return hip_status(q8::launch_attention_bf16(a, pl.tile, (int)pl.wgs, stream));
+    case Q8_F16: return hip_status(q8::launch_attention_f16(a, pl.tile, (int)pl.wgs, stream));
   }
   return Q8_ERR_INVALID;
 }

@@ -18,7 +18,7 @@ struct AttnItem {
   int tokens;  // rows of the item
   int head0;   // first query head
   int heads;   // query heads per row
-  int seq_row0, seq_new;  // of the sequence, for rows that see nothing
+  int seq_new;            // new tokens of the sequence, for rows that see nothing
   int context;            // tokens before the new ones
 };
 
@@ -42,15 +42,17 @@ struct AttnArgs {
 // Floats of one partial: rows x dim sums, then the rows' maxima and weights.
 __host__ __device__ constexpr int64_t attn_slot_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
 
-// Row tiles of 16 an instance holds at most: the sums (rows * dim / 64
-// registers) and the query parts must leave room for the tiles in flight.
-constexpr int attn_max_row_tiles(int dim) { return dim <= 128 ? 2 : 1; }
+// Rows of an item of the kernel whose waves take different keys (16, and 32
+// where the sums and the query parts still leave room for a tile in flight).
+constexpr int attn_direct_rows(int dim) { return dim <= 128 ? 32 : 16; }
+// Rows of an item of the other kernel: 64 or 128, as far as a wave's registers hold.
+constexpr int attn_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
 
 // Workgroups per CU of an instance.
 constexpr int kAttnWgsPerCu = 2;
 
-hipError_t launch_attention_f32(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
-hipError_t launch_attention_bf16(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
-hipError_t launch_attention_f16(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream);
+hipError_t launch_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
+hipError_t launch_attention_bf16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
+hipError_t launch_attention_f16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
 
 }  // namespace q8

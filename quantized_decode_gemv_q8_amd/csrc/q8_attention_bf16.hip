@@ -3,8 +3,8 @@
 
 namespace q8 {
 
-hipError_t launch_attention_bf16(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream) {
-  return launch_attention<kRowBf16>(a, row_tiles, wgs, stream);
+hipError_t launch_attention_bf16(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
+  return launch_attention<kRowBf16>(a, rows, wgs, stream);
 }
 
 }  // namespace q8

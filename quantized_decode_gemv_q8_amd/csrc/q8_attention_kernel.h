@@ -43,6 +43,9 @@ namespace q8 {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
@@ -53,16 +56,19 @@ template <>
 struct AttnElem<kRowF32> {
   typedef float type;
   static constexpr int kQParts = 3, kPParts = 3;
+  static constexpr bool kQHalf = false;
 };
 template <>
 struct AttnElem<kRowBf16> {
   typedef __bf16 type;
   static constexpr int kQParts = 1, kPParts = 2;
+  static constexpr bool kQHalf = false;
 };
 template <>
 struct AttnElem<kRowF16> {
   typedef _Float16 type;
-  static constexpr int kQParts = 2, kPParts = 2;
+  static constexpr int kQParts = 1, kPParts = 2;
+  static constexpr bool kQHalf = true;  // scores in f16 operands, which hold q and the codes exactly
 };
 
 template <typename E, int N>
@@ -76,7 +82,6 @@ __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ uint32_t pack_hi(float lo, float hi) {
   return __builtin_amdgcn_perm(bits(hi), bits(lo), 0x07060302u);
 }
-__device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(bits(x) & 0xffff0000u); }
 
 // Codes at byte pair `half` of a word, as two bf16.
 __device__ __forceinline__ uint32_t pair_bf16(uint32_t w, int half) {
@@ -85,7 +90,29 @@ __device__ __forceinline__ uint32_t pair_bf16(uint32_t w, int half) {
   return pack_hi(a, b);
 }
 
-// Parts of eight floats as matrix operands.
+// The same as two f16: 1024 + (code + 128) by its bits, less 1152.
+__device__ __forceinline__ uint32_t pair_f16(uint32_t w, int half) {
+  const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w ^ 0x80808080u, half ? 0x04030402u : 0x04010400u);
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, u) - v2h{(_Float16)1152.f, (_Float16)1152.f});
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t pair_q(uint32_t w, int half) {
+  return HALF ? pair_f16(w, half) : pair_bf16(w, half);
+}
+
+// x less half `half` of a packed pair of bf16, in one instruction: exact where
+// that half is x cut to bf16.
+template <int HALF>
+__device__ __forceinline__ float less(uint32_t pair, float x) {
+  // The pair (-1, 0) must not become the inline constant -1.0: the compiler
+  // takes that for the lower half, the hardware for the upper one.
+  uint32_t minus_one = 0xbf800000u;
+  if constexpr (HALF == 0) asm("s_mov_b32 %0, 0xbf80" : "=s"(minus_one));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, pair), __builtin_bit_cast(v2bf, minus_one), x, false);
+}
+
+// Parts of eight floats as matrix operands, each the first 8 bits of what the
+// ones before left.
 template <int PARTS>
 __device__ __forceinline__ void split8(const float (&x)[8], v4u (&out)[PARTS]) {
   float r[8];
@@ -94,16 +121,27 @@ __device__ __forceinline__ void split8(const float (&x)[8], v4u (&out)[PARTS]) {
 #pragma unroll
   for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[p][i] = pack_hi(r[2 * i], r[2 * i + 1]);
-    if (p + 1 < PARTS) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] -= cut_bf16(r[i]);
+    for (int i = 0; i < 4; ++i) {
+      out[p][i] = pack_hi(r[2 * i], r[2 * i + 1]);
+      if (p + 1 < PARTS) {
+        r[2 * i] = less<0>(out[p][i], r[2 * i]);
+        r[2 * i + 1] = less<1>(out[p][i], r[2 * i + 1]);
+      }
     }
   }
 }
 
 __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// The product for scores: f16 operands or bf16 ones.
+template <bool HALF>
+__device__ __forceinline__ v4f mfma_q(v4u a, v4u b, v4f c) {
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  else
+    return mfma(a, b, c);
 }
 
 // Lane N of each 16-lane group, to all of them (row_newbcast).
@@ -126,6 +164,28 @@ __device__ __forceinline__ float across_groups_max(float x) {
 __device__ __forceinline__ float across_groups_sum(float x) {
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
+}
+
+// Query parts of one row, as lane group c holds them: channels 32 b + 8 c + 0..7
+// of every block.  A row that is not `in` is zeros.
+template <RowType T, int DIM>
+__device__ __forceinline__ void load_query(const AttnArgs &p, int t, int head, int c, bool in,
+                                           v4u (&qf)[DIM / 32][AttnElem<T>::kQParts]) {
+  typedef typename AttnElem<T>::type E;
+  const E *q = static_cast<const E *>(p.q) + (int64_t)t * p.q_stride + (int64_t)head * DIM + 8 * c;
+#pragma unroll
+  for (int b = 0; b < DIM / 32; ++b) {
+    const Run<E, 8> v = *reinterpret_cast<const Run<E, 8> *>(q + 32 * b);
+    if constexpr (AttnElem<T>::kQHalf) {
+      const v4u x = __builtin_bit_cast(v4u, v);
+      qf[b][0] = in ? x : v4u{0, 0, 0, 0};
+    } else {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = in ? (float)v.x[i] : 0.f;
+      split8<AttnElem<T>::kQParts>(x, qf[b]);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- the work list
@@ -233,24 +293,92 @@ __device__ __forceinline__ void store_run(E *to, const float (&x)[N]) {
 
 // ---------------------------------------------------------------- the main kernel
 
-// VB-byte pieces of codes.
+// A buffer of `bytes` bytes: loads past its end return zeros without touching
+// memory, so a missing tile (0 bytes) needs no branch around its loads.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
+}
 template <int WORDS>
-__device__ __forceinline__ void load_words(const int8_t *p, uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int offset, uint32_t (&w)[WORDS]) {
   if constexpr (WORDS == 1) {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, 0);
   } else if constexpr (WORDS == 2) {
-    const v2u v = *reinterpret_cast<const v2u *>(p);
+    const v2u v = __builtin_amdgcn_raw_buffer_load_b64(rs, offset, 0, 0);
     w[0] = v[0];
     w[1] = v[1];
   } else {
 #pragma unroll
     for (int i = 0; i < WORDS / 4; ++i) {
-      const v4u v = reinterpret_cast<const v4u *>(p)[i];
+      const v4u v = __builtin_amdgcn_raw_buffer_load_b128(rs, offset + 16 * i, 0, 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
     }
   }
 }
+__device__ __forceinline__ float load_scale(__amdgpu_buffer_rsrc_t rs, int offset) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, 0));
+}
+
+// The token row, of head kvh, where the 16 keys at `pos` begin.  poison: NaN,
+// to be added to the scales, where the table holds no page of the cache.
+__device__ __forceinline__ int64_t half_base(const AttnArgs &p, const int *pages, int pos, int last, int kvh,
+                                             float &poison) {
+  const int at = min(pos, last);
+  int page = uniform_load(pages + (at >> p.c.page_shift));
+  const bool ok = (uint32_t)page < p.c.pages;
+  page = ok ? page : 0;
+  poison = ok ? 0.f : NAN;
+  // 16 keys lie within a page (pages hold 16 tokens or more); a half past the
+  // last key reads the last key's instead.
+  const int in = at & ((1 << p.c.page_shift) - 1) & ~15;
+  return (((int64_t)page * p.c.heads + kvh) << p.c.page_shift) + in;
+}
+
+// How much larger (as a power of two) a score may be than the maximum its row
+// keeps before the row's sums are scaled down to it: weights stay below 2^8, and
+// most tiles leave the sums as they are.
+constexpr float kMaxSlack = 8.f;
+
+// Scores (already times alpha log2 e) to weights, against the rows' kept maxima.
+template <int NRT, int NK, int NB>
+__device__ __forceinline__ void weigh(float (&s)[NRT][NK], float *m, float *l, v4f (*acc)[NB][2]) {
+  float top[NRT];
+  bool above = false;
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    top[rt] = s[rt][0];
+#pragma unroll
+    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
+    top[rt] = across_groups_max(top[rt]);
+    above |= top[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
+  }
+  if (__ballot(above) != 0) {
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
+      const float to = fmaxf(m[rt], top[rt]);
+      const float f = __builtin_amdgcn_exp2f(m[rt] - (to == -INFINITY ? 0.f : to));
+      m[rt] = to;
+      l[rt] *= f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[rt][b][i] *= f;
+    }
+  }
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    const float from = m[rt] == -INFINITY ? 0.f : m[rt];  // nothing seen yet: weights are exp2(-inf) = 0
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k] - from);
+      sum += s[rt][k];
+    }
+    l[rt] += sum;
+  }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 template <RowType T, int DIM, int RT>
 struct Attn {
@@ -258,6 +386,7 @@ struct Attn {
   static constexpr int NB = DIM / 32;             // blocks
   static constexpr int QP = AttnElem<T>::kQParts;
   static constexpr int PP = AttnElem<T>::kPParts;
+  static constexpr bool QHALF = AttnElem<T>::kQHalf;
   static constexpr int KW = DIM / 16;             // words of a lane's quarter row of K
   static constexpr int VW = DIM / 64;             // words of a lane's pairs of V
   static constexpr int SW = (4 * NB + 15) / 16;   // scale words per lane for 4 keys
@@ -275,39 +404,28 @@ struct Attn {
   float m[RT], l[RT];
 
   const AttnArgs *p;
+  float scale;       // alpha log2 e, multiplied into the key scales
   int lane, row, c;  // row = lane % 16, c = lane / 16
 
-  // The token row, of head kvh, where the 16 keys at `pos` begin.  poison: NaN,
-  // to be added to the scales, where the table holds no page of the cache.
-  __device__ __forceinline__ int64_t half_base(const int *pages, int pos, int last, int kvh, float &poison) const {
-    const int at = min(pos, last);
-    int page = uniform_load(pages + (at >> p->c.page_shift));
-    const bool ok = (uint32_t)page < p->c.pages;
-    page = ok ? page : 0;
-    poison = ok ? 0.f : NAN;
-    // 16-key halves lie within a page (pages hold 16 tokens or more); one past
-    // the last key reads the last key's half instead.
-    const int in = at & ((1 << p->c.page_shift) - 1) & ~15;
-    return ((((int64_t)page * p->c.heads + kvh) << p->c.page_shift)) + in;
-  }
-
-  __device__ __forceinline__ void load_k(const int64_t (&base)[2], const float (&poison)[2]) {
+  // live: 0 for a tile that does not exist (nothing is read), 1 otherwise.
+  __device__ __forceinline__ void load_k(const int64_t (&base)[2], const float (&poison)[2], int live) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load_words<KW>(p->c.K + base[h] * DIM + row * DIM + c * (DIM / 4), kw[h]);
-      const float *s = p->c.KS + (base[h] + 4 * c) * NB;
+      load_words<KW>(buffer_of(p->c.K + base[h] * DIM, 16 * DIM * live), row * DIM + c * (DIM / 4), kw[h]);
+      const __amdgpu_buffer_rsrc_t rs = buffer_of(p->c.KS + base[h] * NB, 64 * NB * live);
 #pragma unroll
-      for (int w = 0; w < SW; ++w) ks[h][w] = s[(16 * w + row) % (4 * NB)] + poison[h];
+      for (int w = 0; w < SW; ++w) ks[h][w] = fmaf(load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB))), scale, poison[h]);
     }
   }
-  __device__ __forceinline__ void load_v(const int64_t (&base)[2], const float (&poison)[2]) {
+  __device__ __forceinline__ void load_v(const int64_t (&base)[2], const float (&poison)[2], int live) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const __amdgpu_buffer_rsrc_t codes = buffer_of(p->c.V + base[h] * DIM, 16 * DIM * live);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_words<VW>(p->c.V + (base[h] + 4 * c + i) * DIM + row * (DIM / 16), vw[4 * h + i]);
-      const float *s = p->c.VS + (base[h] + 4 * c) * NB;
+      for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), vw[4 * h + i]);
+      const __amdgpu_buffer_rsrc_t rs = buffer_of(p->c.VS + base[h] * NB, 64 * NB * live);
 #pragma unroll
-      for (int w = 0; w < SW; ++w) vs[h][w] = s[(16 * w + row) % (4 * NB)] + poison[h];
+      for (int w = 0; w < SW; ++w) vs[h][w] = load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB))) + poison[h];
     }
   }
 
@@ -325,13 +443,13 @@ struct Attn {
 #pragma unroll
         for (int jl = 0; jl < 4; ++jl) {
           constexpr int byte = 2 * b;  // within the pair's NB * 2 bytes
-          a[jl] = pair_bf16(kw[h][jl * VW + byte / 4], (byte / 2) % 2);
+          a[jl] = pair_q<QHALF>(kw[h][jl * VW + byte / 4], (byte / 2) % 2);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = QP - 1; q >= 0; --q) x = mfma(a, qf[rt][b][q], x);  // small parts first
+          for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a, qf[rt][b][q], x);  // small parts first
           static_for<0, 4>([&](auto i_) {
             constexpr int i = decltype(i_)::value;
             constexpr int e = i * NB + b;
@@ -343,43 +461,46 @@ struct Attn {
     }
   }
 
-  // Weights of the tile (running maximum, sums), then the second product.
-  // sees[rt]: bit k of it for key k of the tile (MASKED only).
-  template <bool MASKED>
-  __device__ __forceinline__ void softmax(float (&s)[RT][8], const uint32_t (&sees)[RT]) {
-    const float scale = p->alpha * 1.4426950408889634f;
+  // sees[rt]: bit k for key k of the tile.  Keys a row does not see get the
+  // score of no weight.  Their value scales may be anything: a scale that is
+  // not finite is taken out, and the rows that do see it are remembered in
+  // lost[rt], bit b for block b.  Returns whether there is any such scale.
+  __device__ __forceinline__ bool mask(float (&s)[RT][8], const uint32_t (&sees)[RT], uint32_t (&lost)[RT]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (!((sees[rt] >> (16 * (k / 4) + 4 * c + k % 4)) & 1)) s[rt][k] = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < SW; ++w) bad |= !finite(vs[h][w]);
+    if (__ballot(bad) == 0) return false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) lost[rt] = 0;
+    static_for<0, 8>([&](auto k_) {
+      static_for<0, NB>([&](auto b_) {
+        constexpr int k = decltype(k_)::value, b = decltype(b_)::value, e = (k % 4) * NB + b;
+        const bool gone = !finite(bcast<e % 16>(vs[k / 4][e / 16]));
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          if (gone && ((sees[rt] >> (16 * (k / 4) + 4 * c + k % 4)) & 1)) lost[rt] |= 1u << b;
+      });
+    });
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s[rt][k] *= scale;
-        if constexpr (MASKED)
-          if (!((sees[rt] >> (16 * (k / 4) + 4 * c + k % 4)) & 1)) s[rt][k] = -INFINITY;
-      }
-      float top = s[rt][0];
-#pragma unroll
-      for (int k = 1; k < 8; ++k) top = fmaxf(top, s[rt][k]);
-      top = across_groups_max(top);
-      const float to = fmaxf(m[rt], top);
-      const float from = to == -INFINITY ? 0.f : to;  // nothing seen yet: all weights are exp2(-inf) = 0
-      const float f = __builtin_amdgcn_exp2f(m[rt] - from);
-      m[rt] = to;
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k] - from);
-        sum += s[rt][k];
-      }
-      l[rt] = l[rt] * f + sum;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[rt][b][i] *= f;
+      lost[rt] |= __shfl_xor(lost[rt], 16);
+      lost[rt] |= __shfl_xor(lost[rt], 32);
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < SW; ++w) vs[h][w] = finite(vs[h][w]) ? vs[h][w] : 0.f;
+    return true;
   }
 
-  template <bool MASKED>
-  __device__ __forceinline__ void values(const float (&s)[RT][8], const uint32_t (&sees)[RT]) {
+  __device__ __forceinline__ void values(const float (&s)[RT][8]) {
     static_for<0, NB>([&](auto b_) {
       constexpr int b = decltype(b_)::value;
       // Lane: codes of keys (k index 4 h + i) at channels 32 b + 2 row + 0, 1.
@@ -401,9 +522,6 @@ struct Attn {
           constexpr int k = decltype(k_)::value;
           constexpr int e = (k % 4) * NB + b;
           w[k] = bcast<e % 16>(vs[k / 4][e / 16]) * s[rt][k];
-          // A key the row does not see may hold anything, a NaN scale too.
-          if constexpr (MASKED)
-            if (!((sees[rt] >> (16 * (k / 4) + 4 * c + k % 4)) & 1)) w[k] = 0.f;
         });
         v4u parts[PP];
         split8<PP>(w, parts);
@@ -419,8 +537,7 @@ struct Attn {
 
 // Bit k: whether the row at index `i` among its sequence's new tokens (row t
 // of q) sees key base + k.
-__device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int base, int context, int n, int length, int i,
-                                              int64_t t) {
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int base, int context, int length, int i, int64_t t) {
   const int left = length - base;  // keys that exist; more than 0
   uint32_t seen = left >= 32 ? 0xffffffffu : (1u << left) - 1;
   if (p.tree == nullptr) {
@@ -442,6 +559,109 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs &p, int base, int c
   return seen & tree;
 }
 
+// One workgroup's share of one item: units k0 .. k1 - 1 of its keys.
+struct Share {
+  Seq seq;
+  const int *pages;  // the sequence's table row
+  int kvh, head0, sub_heads;
+  int i0, tokens, rows;  // the item's first token among the new ones, its tokens, tokens x heads
+  int context;           // tokens before the new ones
+  int keys;              // keys the item's rows may see
+  int all;               // keys that all of its rows see
+  int k0, k1;
+  bool whole;            // all of the item's units
+  float *slot;           // where the sums go otherwise
+};
+
+// Walks through the shares of this workgroup's run.  slot_rows: rows of a slot.
+template <int DIM, typename F>
+__device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, int tid, F work) {
+  // Neighbouring runs, which may share keys or an item, on one XCD.
+  const int per_xcd = gridDim.x / kXcds;
+  const int wg = gridDim.x % kXcds == 0 ? (int)(blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds : (int)blockIdx.x;
+  const Run0 run = find_run(p, wg, gridDim.x, tid);
+  if (tid == 0) p.items[wg].valid = 0;
+  if (wg >= run.wgs) return;
+
+  // Where the run begins: sequence b, head vh (with its sub-group), row item r, unit k0.
+  Share h;
+  int b = run.b;
+  h.seq = uniform_seq_at(p.s, b);
+  int vh, r;
+  {
+    const int64_t per_head = head_units(p, h.seq);
+    vh = (int)(run.rest / per_head);
+    int64_t rest = run.rest - vh * per_head;
+    if (p.tree != nullptr || h.seq.bad) {
+      const int u = item_units(p, h.seq, 0);
+      r = (int)(rest / u);
+      h.k0 = (int)(rest - (int64_t)r * u);
+    } else {
+      r = 0;
+      while (rest >= item_units(p, h.seq, r)) rest -= item_units(p, h.seq, r++);
+      h.k0 = (int)rest;
+    }
+  }
+
+  for (int64_t unit = run.begin;;) {
+    const int units = item_units(p, h.seq, r);
+    const int64_t left = run.end - unit;
+    h.k1 = left < units - h.k0 ? h.k0 + (int)left : units;
+    h.whole = h.k0 == 0 && h.k1 == units;
+    h.kvh = vh / p.subs;
+    const int sub = vh - h.kvh * p.subs;
+    h.sub_heads = min(p.sub_heads, p.group - sub * p.sub_heads);
+    h.head0 = h.kvh * p.group + sub * p.sub_heads;
+    h.i0 = r * p.tile_tokens;
+    h.tokens = min(p.tile_tokens, h.seq.n - h.i0);
+    h.rows = h.tokens * h.sub_heads;
+    h.context = h.seq.length - h.seq.n;
+    h.keys = item_keys(p, h.seq, r);
+    h.all = p.tree != nullptr ? h.context : h.context + h.i0 + 1;
+    h.pages = p.s.table + (int64_t)b * p.s.table_stride;
+    // Slot 1 holds the run's last item, cut short at its end; slot 0 an item
+    // that an earlier run began.
+    h.slot = p.partial + (2 * (int64_t)wg + (h.k0 == 0 ? 1 : 0)) * attn_slot_floats(slot_rows, DIM);
+    work(h);
+    if (tid == 0 && h.k0 == 0 && !h.whole) {
+      AttnItem it;
+      it.valid = 1;
+      it.last = wg_of(unit + units - 1, run);
+      it.row0 = h.seq.start + h.i0;
+      it.tokens = h.tokens;
+      it.head0 = h.head0;
+      it.heads = h.sub_heads;
+      it.seq_new = h.seq.n;
+      it.context = h.context;
+      p.items[wg] = it;
+    }
+    unit += h.k1 - h.k0;
+    if (unit >= run.end) return;
+    // The next item.
+    h.k0 = 0;
+    if (++r == row_items(p, h.seq)) {
+      r = 0;
+      if (++vh == p.c.heads * p.subs) {
+        vh = 0;
+        do {
+          h.seq = uniform_seq_at(p.s, ++b);
+        } while (h.seq.n == 0);
+      }
+    }
+  }
+}
+
+// Channels of one finished row: sums over weight; zeros for a row that sees
+// nothing, NaN for one of a sequence that is described wrongly.
+template <int N>
+__device__ __forceinline__ void finish_row(const AttnArgs &p, const Share &h, int64_t t, float weight, float (&x)[N]) {
+  const float scale = h.seq.bad ? NAN : 1.f / weight;
+  bool nothing = false;
+  if (weight == 0.f && !h.seq.bad) nothing = !sees_any(p.tree, p.tree_words, h.context, h.seq.n, t);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = nothing ? 0.f : x[i] * scale;
+}
+
 template <RowType T, int DIM, int RT>
 __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(AttnArgs p) {
   typedef Attn<T, DIM, RT> A;
@@ -452,116 +672,67 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Neighbouring runs, which may share keys or an item, on one XCD.
-  const int per_xcd = gridDim.x / kXcds;
-  const int wg = gridDim.x % kXcds == 0 ? (int)(blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds : (int)blockIdx.x;
-  const Run0 run = find_run(p, wg, gridDim.x, tid);
-  if (tid == 0) p.items[wg].valid = 0;
-  if (wg >= run.wgs) return;
-
   A a;
   a.p = &p;
+  a.scale = p.alpha * 1.4426950408889634f;
   a.lane = tid & 63;
   a.row = a.lane & 15;
   a.c = a.lane >> 4;
 
-  // Where the run begins: sequence b, head vh (with its sub-group), row item r, unit k0.
-  int b = run.b;
-  Seq seq = uniform_seq_at(p.s, b);
-  int vh, r, k0;
-  {
-    const int64_t per_head = head_units(p, seq);
-    vh = (int)(run.rest / per_head);
-    int64_t rest = run.rest - vh * per_head;
-    if (p.tree != nullptr || seq.bad) {
-      const int u = item_units(p, seq, 0);
-      r = (int)(rest / u);
-      k0 = (int)(rest - (int64_t)r * u);
-    } else {
-      r = 0;
-      while (rest >= item_units(p, seq, r)) rest -= item_units(p, seq, r++);
-      k0 = (int)rest;
-    }
-  }
-
-  for (int64_t unit = run.begin; unit < run.end;) {
-    const int units = item_units(p, seq, r);
-    const int64_t left = run.end - unit;
-    const int k1 = left < units - k0 ? k0 + (int)left : units;
-    const int kvh = vh / p.subs, sub = vh - kvh * p.subs;
-    const int sub_heads = min(p.sub_heads, p.group - sub * p.sub_heads);
-    const int head0 = kvh * p.group + sub * p.sub_heads;
-    const int i0 = r * p.tile_tokens;
-    const int tokens = min(p.tile_tokens, seq.n - i0);
-    const int context = seq.length - seq.n;
-    const int rows = tokens * sub_heads;
-
-    int index[RT], head[RT];
+  walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
+    int index[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int rho = 16 * rt + a.row;
-      const int tok = rho / sub_heads;
-      index[rt] = i0 + min(tok, tokens - 1);
-      head[rt] = head0 + rho - tok * sub_heads;
-      // the query's parts; rows past the item's are zeros
-      const bool in = rho < rows;
-      const E *q = static_cast<const E *>(p.q) + (int64_t)(seq.start + index[rt]) * p.q_stride +
-                   (int64_t)(in ? head[rt] : head0) * DIM + 8 * a.c;
-#pragma unroll
-      for (int bb = 0; bb < NB; ++bb) {
-        const Run<E, 8> v = *reinterpret_cast<const Run<E, 8> *>(q + 32 * bb);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = in ? (float)v.x[i] : 0.f;
-        split8<A::QP>(x, a.qf[rt][bb]);
-      }
+      const int tok = rho / h.sub_heads;
+      const bool in = rho < h.rows;
+      index[rt] = h.i0 + min(tok, h.tokens - 1);
+      load_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, a.c, in, a.qf[rt]);
       a.m[rt] = -INFINITY;
       a.l[rt] = 0.f;
 #pragma unroll
       for (int bb = 0; bb < NB; ++bb) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    if (!seq.bad) {
-      const int keys = item_keys(p, seq, r);
-      const int last = keys - 1;
-      // Keys that every row of the item sees.
-      const int all = p.tree != nullptr ? context : context + i0 + 1;
-      const int *pages = p.s.table + (int64_t)b * p.s.table_stride;
-      const int begin = k0 * kAttnUnit + wave * kAttnTile;
-      const int end = min(k1 * kAttnUnit, keys);
+    if (!h.seq.bad) {
+      const int last = h.keys - 1;
+      const int begin = h.k0 * kAttnUnit + wave * kAttnTile;
+      const int end = min(h.k1 * kAttnUnit, h.keys);
       if (begin < end) {
         int64_t base[2];
         float poison[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, begin + 16 * h, last, kvh, poison[h]);
-        a.load_k(base, poison);
-        a.load_v(base, poison);
-        // Two loops, not a branch in one: the compiler would move what both
-        // sides begin with (128 conversions) above the branch and run out of registers.
-        auto step = [&](auto masked_, int at) {
-          constexpr bool MASKED = decltype(masked_)::value;
+        for (int k = 0; k < 2; ++k) base[k] = half_base(p, h.pages, begin + 16 * k, last, h.kvh, poison[k]);
+        a.load_k(base, poison, 1);
+        a.load_v(base, poison, 1);
+        for (int at = begin; at < end; at += kAttnUnit) {
           const int next = at + kAttnUnit;
-          const bool more = next < end;
-          if (more) {
+          const int more = next < end;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) base[h] = a.half_base(pages, next + 16 * h, last, kvh, poison[h]);
-          }
+          for (int k = 0; k < 2; ++k) base[k] = half_base(p, h.pages, next + 16 * k, last, h.kvh, poison[k]);
           float s[RT][8];
           a.scores(s);
-          if (more) a.load_k(base, poison);
-          uint32_t sees[RT];
-          if constexpr (MASKED) {
+          a.load_k(base, poison, more);
+          bool some_lost = false;
+          uint32_t lost[RT];
+          if (at + kAttnTile > h.all) {
+            uint32_t sees[RT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-              sees[rt] = seen_bits(p, at, context, seq.n, seq.length, index[rt], seq.start + index[rt]);
+              sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], h.seq.start + index[rt]);
+            some_lost = a.mask(s, sees, lost);
           }
-          a.template softmax<MASKED>(s, sees);
-          a.template values<MASKED>(s, sees);
-          if (more) a.load_v(base, poison);
-        };
-        int at = begin;
-        for (; at < end && at + kAttnTile <= all; at += kAttnUnit) step(std::false_type{}, at);
-        for (; at < end; at += kAttnUnit) step(std::true_type{}, at);
+          weigh<RT, 8, NB>(s, a.m, a.l, a.acc);
+          a.values(s);
+          if (some_lost) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int bb = 0; bb < NB; ++bb)
+                if (lost[rt] >> bb & 1) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{NAN, NAN, NAN, NAN};
+          }
+          a.load_v(base, poison, more);
+        }
       }
     }
 
@@ -582,11 +753,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
       }
     }
     __syncthreads();
-    const bool whole = k0 == 0 && k1 == units;
-    // Slot 1 holds the run's last item, cut short at its end; slot 0 an item
-    // that an earlier run began.
-    float *slot = p.partial + (2 * (int64_t)wg + (k0 == 0 ? 1 : 0)) * attn_slot_floats(ROWS, DIM);
-    for (int e = tid; e < rows * (DIM / 8); e += kThreads) {
+    for (int e = tid; e < h.rows * (DIM / 8); e += kThreads) {
       const int rho = e / (DIM / 8), d = 8 * (e % (DIM / 8));
       float top = tops[0][rho];
 #pragma unroll
@@ -600,58 +767,288 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(Attn
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] += f * sums[w][rho][d + i];
       }
-      if (whole) {
-        const int tok = rho / sub_heads;
-        const int64_t t = seq.start + i0 + tok;
-        float scale = 1.f / weight;
-        bool nothing = false;
-        if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, context, seq.n, t);
-        if (seq.bad) {
-          scale = NAN;
-          nothing = false;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = nothing ? 0.f : seq.bad ? NAN : x[i] * scale;
-        store_run<E, 8>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(head0 + rho - tok * sub_heads) * DIM + d, x);
+      if (h.whole) {
+        const int tok = rho / h.sub_heads;
+        const int64_t t = h.seq.start + h.i0 + tok;
+        finish_row(p, h, t, weight, x);
+        store_run<E, 8>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(h.head0 + rho - tok * h.sub_heads) * DIM + d, x);
       } else {
-        v4f *to = reinterpret_cast<v4f *>(slot + (int64_t)rho * DIM + d);
+        v4f *to = reinterpret_cast<v4f *>(h.slot + (int64_t)rho * DIM + d);
         to[0] = v4f{x[0], x[1], x[2], x[3]};
         to[1] = v4f{x[4], x[5], x[6], x[7]};
         if (d == 0) {
-          slot[(int64_t)ROWS * DIM + rho] = top;
-          slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
+          h.slot[(int64_t)ROWS * DIM + rho] = top;
+          h.slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
         }
       }
     }
-    if (tid == 0 && k0 == 0 && !whole) {
-      AttnItem it;
-      it.valid = 1;
-      it.last = wg_of(unit + units - 1, run);
-      it.row0 = seq.start + i0;
-      it.tokens = tokens;
-      it.head0 = head0;
-      it.heads = sub_heads;
-      it.seq_row0 = seq.start;
-      it.seq_new = seq.n;
-      it.context = context;
-      p.items[wg] = it;
-    }
     __syncthreads();  // the sums are read before the next item's are written
+  });
+}
 
-    unit += k1 - k0;
-    if (unit >= run.end) break;
-    // The next item.
-    k0 = 0;
-    if (++r == row_items(p, seq)) {
-      r = 0;
-      if (++vh == p.c.heads * p.subs) {
-        vh = 0;
-        do {
-          seq = uniform_seq_at(p.s, ++b);
-        } while (seq.n == 0);
+// ---------------------------------------------------------------- many rows
+
+// The same for items of more rows (trees, prompts): up to 64 * RT rows, 16 * RT
+// for each wave, and all four waves take the same keys.  Converting the codes
+// costs as much as the rest of the work on 32 rows, so a workgroup does it
+// once: per step of 64 keys each wave loads 16 keys' codes, converts them and
+// lays them into LDS as the matrix operands that all waves read (16 bytes per
+// lane, conflict-free).  The next step's codes are in flight meanwhile.  Row
+// tiles are dealt to the waves in turn, so a short item still uses all four.
+constexpr int kWideKeys = 64;
+
+template <int DIM>
+struct WideLds {
+  static constexpr int NB = DIM / 32;
+  static constexpr int BUFS = DIM == 256 ? 1 : 2;  // two workgroups must fit a CU
+  v4u k[BUFS][4][NB][64];     // 16-key tile, block, lane
+  v2u v[BUFS][2][NB][2][64][2];  // 32-key group, block, pair element, lane, half
+  float ks[BUFS][4][NB][16], vs[BUFS][4][NB][16];  // 16-key tile, block, key: a lane reads its four keys at once
+};
+
+template <RowType T, int DIM, int RT>
+__global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel(AttnArgs p) {
+  typedef typename AttnElem<T>::type E;
+  constexpr int NB = DIM / 32, QP = AttnElem<T>::kQParts, PP = AttnElem<T>::kPParts;
+  constexpr bool QHALF = AttnElem<T>::kQHalf;
+  constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;
+  constexpr int ROWS = 64 * RT, BUFS = WideLds<DIM>::BUFS;
+  constexpr int SPL = (16 * NB + 63) / 64;  // scale words a lane stages
+  __shared__ WideLds<DIM> lds;
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, row = lane & 15, c = lane >> 4;
+
+  const float scale = p.alpha * 1.4426950408889634f;  // multiplied into the key scales
+
+  // This wave's 16 keys of a step, on their way to LDS.
+  uint32_t kw[KW], vw[4][VW];
+  float ksw[SPL], vsw[SPL];
+  auto load = [&](int64_t base, float poison) {
+    load_words<KW>(buffer_of(p.c.K + base * DIM, 16 * DIM), row * DIM + c * (DIM / 4), kw);
+    const __amdgpu_buffer_rsrc_t codes = buffer_of(p.c.V + base * DIM, 16 * DIM);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), vw[i]);
+#pragma unroll
+    for (int w = 0; w < SPL; ++w) {
+      const int e = (64 * w + lane) % (16 * NB);
+      ksw[w] = fmaf(p.c.KS[base * NB + e], scale, poison);
+      vsw[w] = p.c.VS[base * NB + e] + poison;
+    }
+  };
+  auto lay = [&](int buf) {
+    static_for<0, NB>([&](auto b_) {
+      constexpr int b = decltype(b_)::value;
+      v4u x;
+#pragma unroll
+      for (int jl = 0; jl < 4; ++jl) x[jl] = pair_q<QHALF>(kw[jl * VW + b / 2], b % 2);
+      lds.k[buf][wave][b][lane] = x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = (float)(int8_t)(vw[k][b / 2] >> (16 * (b % 2) + 8 * i));
+        lds.v[buf][wave / 2][b][i][lane][wave % 2] = v2u{pack_hi(y[0], y[1]), pack_hi(y[2], y[3])};
+      }
+    });
+#pragma unroll
+    for (int w = 0; w < SPL; ++w)
+      if (64 * w + lane < 16 * NB) {
+        const int e = 64 * w + lane;  // key e / NB, block e % NB
+        lds.ks[buf][wave][e % NB][e / NB] = ksw[w];
+        lds.vs[buf][wave][e % NB][e / NB] = vsw[w];
+      }
+  };
+
+  walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
+    // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
+    v4u qf[RT][NB][QP];
+    v4f acc[RT][NB][2];
+    float m[RT], l[RT];
+    int index[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rho = 16 * (4 * rt + wave) + row;
+      const int tok = rho / h.sub_heads;
+      const bool in = rho < h.rows;
+      index[rt] = h.i0 + min(tok, h.tokens - 1);
+      load_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, c, in, qf[rt]);
+      m[rt] = -INFINITY;
+      l[rt] = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[rt][b][0] = acc[rt][b][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    const int tiles = (h.rows + 15) / 16;
+    const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has
+
+    // One step over the 64 keys from `at` on, for the wave's first NRT row tiles.
+    auto compute = [&](auto nrt_, int at, int buf) {
+      constexpr int NRT = decltype(nrt_)::value;
+      float s[NRT][16];
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[rt][4 * kt + i] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const v4u a = lds.k[buf][kt][b][lane];
+          const v4f ks = *reinterpret_cast<const v4f *>(&lds.ks[buf][kt][b][4 * c]);
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) {
+            v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a, qf[rt][b][q], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[rt][4 * kt + i] = fmaf(ks[i], x[i], s[rt][4 * kt + i]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one tile's operands in registers, not all
+      }
+
+      // Keys not seen: no weight.  Their value scales may be anything, as in
+      // the other kernel: one that is not finite is taken out of the products
+      // and its rows' blocks are remembered.
+      bool some_lost = false;
+      uint32_t lost[NRT];
+      if (at + kWideKeys > h.all) {
+        uint64_t sees[NRT];
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt) {
+          const int64_t t = h.seq.start + index[rt];
+          sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], t);
+          if (at + 32 < h.seq.length)
+            sees[rt] |= (uint64_t)seen_bits(p, at + 32, h.context, h.seq.length, index[rt], t) << 32;
+          sees[rt] >>= 4 * c;  // bit 16 kt + i is this lane's
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
+          lost[rt] = 0;
+        }
+        bool bad = false;
+        const float *all_vs = &lds.vs[buf][0][0][0];
+#pragma unroll
+        for (int w = 0; w < NB; ++w) bad |= !finite(all_vs[64 * w + lane]);
+        some_lost = __ballot(bad) != 0;
+        if (some_lost) {
+          for (int kt = 0; kt < 4; ++kt)
+            for (int b = 0; b < NB; ++b)
+              for (int i = 0; i < 4; ++i)
+                if (!finite(lds.vs[buf][kt][b][4 * c + i]))
+#pragma unroll
+                  for (int rt = 0; rt < NRT; ++rt) lost[rt] |= (uint32_t)(sees[rt] >> (16 * kt + i) & 1) << b;
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) {
+            lost[rt] |= __shfl_xor(lost[rt], 16);
+            lost[rt] |= __shfl_xor(lost[rt], 32);
+          }
+        }
+      }
+      weigh<NRT, 16, NB>(s, m, l, acc);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          v4u a[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
+          v4f vs[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) vs[k] = *reinterpret_cast<const v4f *>(&lds.vs[buf][2 * g + k][b][4 * c]);
+          if (some_lost) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (!finite(vs[k / 4][k % 4])) vs[k / 4][k % 4] = 0.f;
+          }
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) {
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = vs[k / 4][k % 4] * s[rt][8 * g + k];
+            v4u parts[PP];
+            split8<PP>(w, parts);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (some_lost) {
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (lost[rt] >> b & 1) acc[rt][b][0] = acc[rt][b][1] = v4f{NAN, NAN, NAN, NAN};
+      }
+    };
+
+    if (!h.seq.bad) {
+      const int last = h.keys - 1;
+      const int begin = h.k0 * kAttnUnit;
+      const int end = min(h.k1 * kAttnUnit, h.keys);
+      float poison;
+      int64_t base = half_base(p, h.pages, begin + 16 * wave, last, h.kvh, poison);
+      load(base, poison);
+      lay(0);
+      if (begin + kWideKeys < end) {
+        base = half_base(p, h.pages, begin + kWideKeys + 16 * wave, last, h.kvh, poison);
+        load(base, poison);
+      }
+      __syncthreads();
+      auto steps = [&](auto nrt_) {
+        for (int at = begin; at < end; at += kWideKeys) {
+          const int buf = BUFS == 2 ? (at - begin) / kWideKeys % 2 : 0;
+          if constexpr (decltype(nrt_)::value > 0) compute(nrt_, at, buf);
+          if constexpr (BUFS == 1) __syncthreads();
+          if (at + kWideKeys < end) {
+            lay(BUFS == 2 ? buf ^ 1 : 0);
+            if (at + 2 * kWideKeys < end) {
+              base = half_base(p, h.pages, at + 2 * kWideKeys + 16 * wave, last, h.kvh, poison);
+              load(base, poison);
+            }
+          }
+          __syncthreads();
+        }
+      };
+      if (RT == 2 && mine == 2)
+        steps(std::integral_constant<int, RT>{});
+      else if (mine >= 1)
+        steps(std::integral_constant<int, 1>{});
+      else
+        steps(std::integral_constant<int, 0>{});
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rho = 16 * (4 * rt + wave) + row;
+      const float weight = across_groups_sum(l[rt]);
+      if (rho >= h.rows) continue;
+      const int tok = rho / h.sub_heads;
+      const int64_t t = h.seq.start + h.i0 + tok;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const v4f u = acc[rt][b][0], v = acc[rt][b][1];
+        float x[8] = {u[0], v[0], u[1], v[1], u[2], v[2], u[3], v[3]};
+        const int d = 32 * b + 8 * c;
+        if (h.whole) {
+          finish_row(p, h, t, weight, x);
+          store_run<E, 8>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(h.head0 + rho - tok * h.sub_heads) * DIM + d, x);
+        } else {
+          v4f *to = reinterpret_cast<v4f *>(h.slot + (int64_t)rho * DIM + d);
+          to[0] = v4f{x[0], x[1], x[2], x[3]};
+          to[1] = v4f{x[4], x[5], x[6], x[7]};
+        }
+      }
+      if (!h.whole && c == 0) {
+        h.slot[(int64_t)ROWS * DIM + rho] = m[rt];
+        h.slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
       }
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------- joining the parts
@@ -705,25 +1102,39 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, in
   store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
 }
 
-template <RowType T, int DIM, int RT>
+template <RowType T, int DIM, int RT, bool WIDE>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
-  hipLaunchKernelGGL((attention_kernel<T, DIM, RT>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  if constexpr (WIDE)
+    hipLaunchKernelGGL((attention_wide_kernel<T, DIM, RT>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attention_kernel<T, DIM, RT>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, 16 * RT / kWaves), dim3(kThreads), 0, stream,
-                     a, 16 * RT);
+  constexpr int rows = (WIDE ? 64 : 16) * RT;
+  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, rows / kWaves), dim3(kThreads), 0, stream, a,
+                     rows);
   return hipGetLastError();
 }
 
+template <RowType T, int DIM>
+hipError_t launch_rows(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
+  constexpr int most = attn_max_rows(T, DIM);
+  if (rows == 16) return launch_instance<T, DIM, 1, false>(a, wgs, stream);
+  if constexpr (attn_direct_rows(DIM) == 32)
+    if (rows == 32) return launch_instance<T, DIM, 2, false>(a, wgs, stream);
+  if (rows == 64) return launch_instance<T, DIM, 1, true>(a, wgs, stream);
+  if constexpr (most == 128)
+    if (rows == 128) return launch_instance<T, DIM, 2, true>(a, wgs, stream);
+  return hipErrorInvalidValue;
+}
+
+// rows: of an item, 16, 32, 64 or 128.
 template <RowType T>
-hipError_t launch_attention(const AttnArgs &a, int row_tiles, int wgs, hipStream_t stream) {
-  if (row_tiles == 1) {
-    if (a.c.dim == 64) return launch_instance<T, 64, 1>(a, wgs, stream);
-    if (a.c.dim == 128) return launch_instance<T, 128, 1>(a, wgs, stream);
-    if (a.c.dim == 256) return launch_instance<T, 256, 1>(a, wgs, stream);
-  } else if (row_tiles == 2) {
-    if (a.c.dim == 64) return launch_instance<T, 64, 2>(a, wgs, stream);
-    if (a.c.dim == 128) return launch_instance<T, 128, 2>(a, wgs, stream);
+hipError_t launch_attention(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
+  switch (a.c.dim) {
+    case 64: return launch_rows<T, 64>(a, rows, wgs, stream);
+    case 128: return launch_rows<T, 128>(a, rows, wgs, stream);
+    case 256: return launch_rows<T, 256>(a, rows, wgs, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -34,7 +34,7 @@ def calls(c, s, rows=5, k=FAKE, type_=0, stride=128, q_heads=4, q_stride=256, ke
     return (L.q8_cache_write(c, k, k, type_, rows, stride, stride, s, None),
             L.q8_cache_read(c, k, k, type_, rows, stride, stride, s, None),
             L.q8_cache_keep(c, rows, s, keep, width, None),
-            L.q8_cache_attention_workspace(c, rows, q_heads, s, need),
+            L.q8_cache_attention_workspace(c, type_, rows, q_heads, s, need),
             L.q8_cache_attention(c, k, k, type_, rows, q_heads, q_stride, q_stride, s, tree, words, 1.0, work,
                                  work_bytes, None))
 
@@ -93,7 +93,7 @@ def test_bad_attention():
         assert calls(cache(), seqs(), **kw)[3:] == INVALID[:2], kw
     assert calls(cache(), seqs(), words=-1)[4] == binding.Q8_ERR_INVALID
     assert calls(cache(), seqs(), tree=FAKE + 4, words=1)[4] == binding.Q8_ERR_INVALID
-    assert binding.load().q8_cache_attention_workspace(cache(), 5, 4, seqs(), None) == binding.Q8_ERR_INVALID
+    assert binding.load().q8_cache_attention_workspace(cache(), 0, 5, 4, seqs(), None) == binding.Q8_ERR_INVALID
 
 
 def test_nothing_to_do_touches_nothing():
