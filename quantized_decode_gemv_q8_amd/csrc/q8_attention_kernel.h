@@ -378,6 +378,11 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], float *m, float *l, v
   }
 }
 
+// Keeps the arithmetic behind x on this side of what follows: otherwise the
+// compiler spreads one step's operands over all steps and runs out of registers.
+__device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
+
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 template <RowType T, int DIM, int RT>
@@ -804,6 +809,9 @@ struct WideLds {
   v4u k[BUFS][4][NB][64];     // 16-key tile, block, lane
   v2u v[BUFS][2][NB][2][64][2];  // 32-key group, block, pair element, lane, half
   float ks[BUFS][4][NB][16], vs[BUFS][4][NB][16];  // 16-key tile, block, key: a lane reads its four keys at once
+  // Value scales that are not finite are zeros in vs; bit e % 64 of word e / 64
+  // marks the one of key e / NB and block e % NB of a 16-key tile.
+  uint64_t gone[BUFS][4][(16 * NB + 63) / 64];
 };
 
 template <RowType T, int DIM, int RT>
@@ -853,12 +861,15 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       }
     });
 #pragma unroll
-    for (int w = 0; w < SPL; ++w)
+    for (int w = 0; w < SPL; ++w) {
+      const uint64_t gone = __ballot(64 * w + lane < 16 * NB && !finite(vsw[w]));
+      if (lane == 0) lds.gone[buf][wave][w] = gone;
       if (64 * w + lane < 16 * NB) {
         const int e = 64 * w + lane;  // key e / NB, block e % NB
         lds.ks[buf][wave][e % NB][e / NB] = ksw[w];
-        lds.vs[buf][wave][e % NB][e / NB] = vsw[w];
+        lds.vs[buf][wave][e % NB][e / NB] = finite(vsw[w]) ? vsw[w] : 0.f;
       }
+    }
   };
 
   walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
@@ -886,103 +897,111 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
     auto compute = [&](auto nrt_, int at, int buf) {
       constexpr int NRT = decltype(nrt_)::value;
       float s[NRT][16];
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-#pragma unroll
-        for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[rt][4 * kt + i] = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const v4u a = lds.k[buf][kt][b][lane];
-          const v4f ks = *reinterpret_cast<const v4f *>(&lds.ks[buf][kt][b][4 * c]);
+      {
+        // Operands of product n + 1 are on their way while product n runs.
+        v4u a[2];
+        v4f ks[2];
+        a[0] = lds.k[buf][0][0][lane];
+        ks[0] = *reinterpret_cast<const v4f *>(&lds.ks[buf][0][0][4 * c]);
+        static_for<0, 4 * NB>([&](auto n_) {
+          constexpr int n = decltype(n_)::value, kt = n / NB, b = n % NB;
+          if constexpr (n + 1 < 4 * NB) {
+            a[(n + 1) % 2] = lds.k[buf][(n + 1) / NB][(n + 1) % NB][lane];
+            ks[(n + 1) % 2] = *reinterpret_cast<const v4f *>(&lds.ks[buf][(n + 1) / NB][(n + 1) % NB][4 * c]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int rt = 0; rt < NRT; ++rt) {
             v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a, qf[rt][b][q], x);
+            for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a[n % 2], qf[rt][b][q], x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[rt][4 * kt + i] = fmaf(ks[i], x[i], s[rt][4 * kt + i]);
+            for (int i = 0; i < 4; ++i)
+              s[rt][4 * kt + i] = b == 0 ? ks[n % 2][i] * x[i] : fmaf(ks[n % 2][i], x[i], s[rt][4 * kt + i]);
           }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // one tile's operands in registers, not all
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pin(s[rt][4 * kt + i]);
+        });
       }
 
-      // Keys not seen: no weight.  Their value scales may be anything, as in
-      // the other kernel: one that is not finite is taken out of the products
-      // and its rows' blocks are remembered.
-      bool some_lost = false;
-      uint32_t lost[NRT];
+      uint64_t sees[NRT];  // shifted: bit 16 kt + i is this lane's key i of tile kt
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt) sees[rt] = ~0ull;
       if (at + kWideKeys > h.all) {
-        uint64_t sees[NRT];
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt) {
           const int64_t t = h.seq.start + index[rt];
           sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], t);
           if (at + 32 < h.seq.length)
             sees[rt] |= (uint64_t)seen_bits(p, at + 32, h.context, h.seq.length, index[rt], t) << 32;
-          sees[rt] >>= 4 * c;  // bit 16 kt + i is this lane's
+          sees[rt] >>= 4 * c;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
-          lost[rt] = 0;
-        }
-        bool bad = false;
-        const float *all_vs = &lds.vs[buf][0][0][0];
-#pragma unroll
-        for (int w = 0; w < NB; ++w) bad |= !finite(all_vs[64 * w + lane]);
-        some_lost = __ballot(bad) != 0;
-        if (some_lost) {
-          for (int kt = 0; kt < 4; ++kt)
-            for (int b = 0; b < NB; ++b)
-              for (int i = 0; i < 4; ++i)
-                if (!finite(lds.vs[buf][kt][b][4 * c + i]))
-#pragma unroll
-                  for (int rt = 0; rt < NRT; ++rt) lost[rt] |= (uint32_t)(sees[rt] >> (16 * kt + i) & 1) << b;
-#pragma unroll
-          for (int rt = 0; rt < NRT; ++rt) {
-            lost[rt] |= __shfl_xor(lost[rt], 16);
-            lost[rt] |= __shfl_xor(lost[rt], 32);
-          }
         }
       }
       weigh<NRT, 16, NB>(s, m, l, acc);
+      {
+        v4u a[2][2];
+        v4f vs[2][2];
+        auto fetch = [&](auto n_) {
+          constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          v4u a[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
-          v4f vs[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) vs[k] = *reinterpret_cast<const v4f *>(&lds.vs[buf][2 * g + k][b][4 * c]);
-          if (some_lost) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (!finite(vs[k / 4][k % 4])) vs[k / 4][k % 4] = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            a[n % 2][i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
+            vs[n % 2][i] = *reinterpret_cast<const v4f *>(&lds.vs[buf][2 * g + i][b][4 * c]);
           }
+        };
+        fetch(std::integral_constant<int, 0>{});
+        static_for<0, 2 * NB>([&](auto n_) {
+          constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
+          if constexpr (n + 1 < 2 * NB) fetch(std::integral_constant<int, n + 1>{});
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int rt = 0; rt < NRT; ++rt) {
             float w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = vs[k / 4][k % 4] * s[rt][8 * g + k];
+            for (int k = 0; k < 8; ++k) w[k] = vs[n % 2][k / 4][k % 4] * s[rt][8 * g + k];
             v4u parts[PP];
             split8<PP>(w, parts);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
+              for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[n % 2][i], parts[q], acc[rt][b][i]);
           }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      if (some_lost) {
 #pragma unroll
-        for (int rt = 0; rt < NRT; ++rt)
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pin(acc[rt][b][i]);
+        });
+      }
+      // Blocks of rows that see a value scale that is not finite are lost.
+      uint64_t any = 0;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int w = 0; w < SPL; ++w) any |= lds.gone[buf][kt][w];
+      if (uniform((int64_t)any) != 0) {
+        uint32_t lost[NRT] = {};
+#pragma unroll 1
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll 1
+          for (int e = 0; e < 4 * NB; ++e) {
+            const int at_e = 4 * NB * c + e;  // key 4 c + e / NB, block e % NB
+            if (lds.gone[buf][kt][at_e / 64] >> (at_e % 64) & 1)
+#pragma unroll
+              for (int rt = 0; rt < NRT; ++rt) lost[rt] |= (uint32_t)(sees[rt] >> (16 * kt + e / NB) & 1) << (e % NB);
+          }
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt) {
+          lost[rt] |= __shfl_xor(lost[rt], 16);
+          lost[rt] |= __shfl_xor(lost[rt], 32);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
             if (lost[rt] >> b & 1) acc[rt][b][0] = acc[rt][b][1] = v4f{NAN, NAN, NAN, NAN};
+        }
       }
     };
 
