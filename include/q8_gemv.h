@@ -369,7 +369,7 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  *           apart; out must not overlap anything else
  *   workspace  device memory of at least the size that
  *           q8_cache_attention_workspace gives for the same cache, type, rows,
- *           q_heads, seqs and max_pages, 16-byte aligned; its contents need no
+ *           q_heads, seqs and max_pages (which may be none), 16-byte aligned; its contents need no
  *           preparation and are free again when the call's work is done.  Calls that may
  *           overlap in time (and graphs whose replays may) need one each
  * f32 accuracy for f32 rows: codes are exact in the bf16 matrix operands, q and

@@ -157,7 +157,7 @@ def _check_tensor(name, t, dtype, shape):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (dense row-major)")
@@ -382,20 +382,23 @@ class Q8Cache:
             raise ValueError(f"dim must be 64, 128 or 256, got {dim}")
         if page_size not in (16, 32, 64, 128, 256, 512, 1024):
             raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
-        for name, t, dtype, last in (("k", k, torch.int8, dim), ("k_scale", k_scale, torch.float32, dim // BLOCK),
-                                     ("v", v, torch.int8, dim), ("v_scale", v_scale, torch.float32, dim // BLOCK)):
-            _check_tensor(name, t, dtype, (pages, heads, page_size, last))
-            if t.device != k.device:
+        device, scales = k.device, (pages, heads, page_size, dim // BLOCK)
+        for name, t, dtype, shape in (("k", k, torch.int8, k.shape), ("k_scale", k_scale, torch.float32, scales),
+                                      ("v", v, torch.int8, k.shape), ("v_scale", v_scale, torch.float32, scales)):
+            _check_tensor(name, t, dtype, shape)
+            if t.device != device:
                 raise ValueError("all tensors must be on one device")
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
-        for i, a in enumerate(("k", "k_scale", "v", "v_scale")):
-            _check_disjoint(a, getattr(self, a),
-                            [(b, getattr(self, b)) for b in ("k", "k_scale", "v", "v_scale")[:i]])
-        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
-        self.device = k.device
-        self._spans = tuple(("the cache", *_span(t)) for t in (k, k_scale, v, v_scale))
-        self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
-                                    pages, heads, page_size, dim)
+        self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, dim, device
+        at = k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr()
+        codes = pages * heads * page_size * dim
+        self._spans = tuple((a, a + n) for a, n in zip(at, (codes, codes // 8) * 2))
+        edge = 0
+        for a, b in sorted(self._spans):
+            if a < edge and codes:
+                raise ValueError("the cache's tensors overlap")
+            edge = b
+        self._struct = _CacheStruct(*at, pages, heads, page_size, dim)
 
     @classmethod
     def empty(cls, pages, heads, page_size, dim, device="cuda"):
@@ -477,15 +480,13 @@ def _check_apart(out_name, out, others):
             raise ValueError(f"{out_name} overlaps {name}")
 
 
-def _check_outside(cache, **tensors):
-    """No tensor of a call shares a byte with the cache."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        b0, b1 = _span(t)
-        for what, a0, a1 in cache._spans:
-            if a0 < b1 and b0 < a1:
-                raise ValueError(f"{name} overlaps {what}")
+def _check_outside(cache, *tensors):
+    """No tensor (pairs of a name and a tensor) of a call shares a byte with the cache."""
+    (a0, a1), (b0, b1), (c0, c1), (d0, d1) = cache._spans
+    for name, t in tensors:
+        p, q = _span(t)
+        if (p < a1 and a0 < q) or (p < b1 and b0 < q) or (p < c1 and c0 < q) or (p < d1 and d0 < q):
+            raise ValueError(f"{name} overlaps the cache")
 
 
 def _interleaved(a, b):
@@ -527,7 +528,7 @@ def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
     seqs = _cache_seqs(cache, table, lengths, offsets)
     ks = _cache_rows("k", k, None, cache.heads, cache)
     vs = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
-    _check_outside(cache, k=k, v=v, table=table, lengths=lengths, offsets=offsets)
+    _check_outside(cache, ("k", k), ("v", v), ("table", table), ("lengths", lengths), ("offsets", offsets))
     _call(cache, stream, "q8_cache_write", load().q8_cache_write, cache._struct, k.data_ptr(), v.data_ptr(),
           _ROW_TYPES[k.dtype], k.shape[0], ks, vs, seqs)
 
@@ -550,7 +551,7 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
     if given:
         ks = _cache_rows("k", k, shape[0], cache.heads, cache)
         vs = _cache_rows("v", v, shape[0], cache.heads, cache, k.dtype)
-        _check_outside(cache, k=k, v=v)
+        _check_outside(cache, ("k", k), ("v", v))
         inputs = (("table", table), ("lengths", lengths), ("offsets", offsets))
         _check_apart("k", k, inputs)
         _check_apart("v", v, inputs + (("k", k),))
@@ -571,7 +572,7 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
     _check_tensor("keep", keep, torch.int32, (table.shape[0], keep.shape[1]))
     if keep.device != cache.device:
         raise ValueError("all tensors must be on one device")
-    _check_outside(cache, keep=keep, table=table, lengths=lengths, offsets=offsets)
+    _check_outside(cache, ("keep", keep), ("table", table), ("lengths", lengths), ("offsets", offsets))
     _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(),
           keep.shape[1])
 
@@ -612,16 +613,16 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
         os_ = q_heads * cache.dim
     else:
         os_ = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
-        _check_outside(cache, out=out)
+        _check_outside(cache, ("out", out))
         _check_apart("out", out, (("q", q), ("table", table), ("lengths", lengths), ("offsets", offsets),
                                   ("tree", tree)))
     need = _attention_workspace(cache, _ROW_TYPES[q.dtype], rows, q_heads, seqs)
-    work = _empty_on(stream, (max(16, need),), torch.uint8, cache.device)
+    work = _empty_on(stream, (need,), torch.uint8, cache.device).data_ptr() if need else None
     mask = None
     if tree is not None:  # an empty tree still is one: no new token is seen
-        mask = tree.data_ptr() if tree.numel() else work.data_ptr()
+        mask = tree.data_ptr() if words and rows else offsets.data_ptr() & -8
     _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q.data_ptr(), out.data_ptr(),
-          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha), work.data_ptr(), need)
+          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha), work, need)
     return out
 
 

@@ -794,25 +794,48 @@ q8_status cache_rows_impl(const q8_cache *c, const void *k, const void *v, q8_ty
 // (tokens x heads of a group), and the workgroups the units are dealt to.
 struct AttnPlan {
   int tile, subs, sub_heads, tile_tokens;
+  int unit_shift;      // log2 of the keys of a unit
+  int item_cost;       // units that an item is charged besides its keys
+  bool few_units;      // the units of all items are sure to stay below 2^31
+  bool split;          // an item may have several units
   int64_t wgs, bytes;  // workgroups; workspace
 };
+
+// Sequences that the table bounds to this many tokens are not split: one
+// workgroup takes all keys of an item, and the second launch that joins parts
+// is saved.
+constexpr int64_t kAttnWholeTokens = 1024;
+// What an item costs besides its keys (its query, its first loads' latency and
+// its sums' way out), in units of kAttnStep keys, when work is dealt out.
+constexpr int kAttnItemCost = 2;
 
 AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens,
                    int cus) {
   AttnPlan p;
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
-  p.tile = mean <= 16 ? 16 : mean <= q8::attn_direct_rows(dim) ? 32 : mean <= 64 ? 64 : q8::attn_max_rows(type, dim);
+  // The instances for 4 and 8 rows do not fit the registers at dim 256.
+  p.tile = mean <= 4 && dim <= 128                 ? 4
+           : mean <= 8 && dim <= 128               ? 8
+           : mean <= 16                            ? 16
+           : mean <= q8::attn_direct_rows(dim)     ? 32
+           : mean <= 64                            ? 64
+                                                   : q8::attn_max_rows(type, dim);
   const int tile = p.tile;
   p.subs = (int)ceil_div(group, tile);
   p.sub_heads = (int)ceil_div(group, p.subs);
   p.subs = (int)ceil_div(group, p.sub_heads);  // no empty sub-group
   p.tile_tokens = tile / p.sub_heads;
   const int64_t items = (rows / p.tile_tokens + seqs) * heads * p.subs;
-  const int64_t units = ceil_div(max_tokens, q8::kAttnUnit);
-  p.wgs = (int64_t)cus * q8::kAttnWgsPerCu;
-  if (items < p.wgs && items * (units < 1 ? 1 : units) < p.wgs) p.wgs = items * (units < 1 ? 1 : units);
-  p.bytes = 2 * p.wgs * q8::attn_slot_floats(tile, dim) * 4;
-  p.bytes = ceil_div(p.bytes, 256) * 256 + p.wgs * (int64_t)sizeof(q8::AttnItem);
+  p.split = max_tokens > kAttnWholeTokens || tile > 16;
+  p.unit_shift = __builtin_ctz((unsigned)(p.split ? q8::kAttnStep : kAttnWholeTokens));
+  const int64_t units = p.split ? ceil_div(max_tokens, q8::kAttnStep) : 1;
+  p.item_cost = p.split ? kAttnItemCost : 0;
+  p.few_units = items <= (kIndexLimit - 1) / (units + p.item_cost);
+  p.wgs = (int64_t)cus * q8::attn_wgs_per_cu(type, dim, tile);
+  if (items < p.wgs && items * units < p.wgs) p.wgs = items * units;
+  p.bytes = 0;
+  if (p.split)
+    p.bytes = ceil_div(2 * p.wgs * q8::attn_slot_floats(tile, dim) * 4, 256) * 256 + p.wgs * (int64_t)sizeof(q8::AttnItem);
   return p;
 }
 
@@ -976,7 +999,8 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   if (st != Q8_OK) return st;
   const AttnPlan pl =
       attn_plan((q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens, info.cus);
-  if (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes) return Q8_ERR_INVALID;
+  if (pl.split && (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes))
+    return Q8_ERR_INVALID;
   a.q = q;
   a.out = out;
   a.q_stride = q_stride;
@@ -990,7 +1014,10 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   a.alpha = alpha;
   a.partial = static_cast<float *>(workspace);
   const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
-  a.items = reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256);
+  a.items = pl.split ? reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256) : nullptr;
+  a.unit_shift = pl.unit_shift;
+  a.item_cost = pl.item_cost;
+  a.few_units = pl.few_units;
   if (log_debug())
     log_line("cache_attention rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", (long long)rows,
              q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", pl.tile,

@@ -5,9 +5,9 @@
 
 namespace q8 {
 
-// Keys per unit of work: one 32-key tile for each of a workgroup's four waves.
+// Keys a workgroup takes at a time: one 32-key tile for each of its four waves.
 constexpr int kAttnTile = 32;
-constexpr int kAttnUnit = kAttnTile * kWaves;
+constexpr int kAttnStep = kAttnTile * kWaves;
 
 // One split item: rows whose keys several workgroups share.  Workgroup w is
 // the first contributor of at most one, so the descriptors are indexed by it.
@@ -35,8 +35,11 @@ struct AttnArgs {
   int sub_heads;
   int tile_tokens;  // tokens (rows of q) per item
   float alpha;
-  float *partial;   // 2 * gridDim.x slots of attn_slot_floats(rows, dim)
-  AttnItem *items;  // gridDim.x
+  int unit_shift;    // log2 of the keys of a unit of work, a multiple of kAttnStep
+  int item_cost;     // units that an item is charged besides its keys
+  int few_units;     // the units of all items are sure to stay below 2^31
+  float *partial;    // 2 * gridDim.x slots of attn_slot_floats(rows, dim)
+  AttnItem *items;   // gridDim.x; null where every item is one unit
 };
 
 // Floats of one partial: rows x dim sums, then the rows' maxima and weights.
@@ -48,8 +51,10 @@ constexpr int attn_direct_rows(int dim) { return dim <= 128 ? 32 : 16; }
 // Rows of an item of the other kernel: 64 or 128, as far as a wave's registers hold.
 constexpr int attn_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
 
-// Workgroups per CU of an instance.
-constexpr int kAttnWgsPerCu = 2;
+// Workgroups per CU of an instance (items of `rows` rows).
+constexpr int attn_wgs_per_cu(RowType type, int dim, int rows) {
+  return 2;
+}
 
 hipError_t launch_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
 hipError_t launch_attention_bf16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);

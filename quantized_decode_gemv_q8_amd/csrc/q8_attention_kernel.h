@@ -26,7 +26,8 @@
 // the 16-lane group by DPP.
 //
 // Work.  An item is a sequence's tile of rows for one head of the cache; its
-// keys are cut into units of 128 (32 for each wave).  The units of all items
+// keys are cut into units (of 128, 32 for each wave, or one unit with all of a
+// short sequence).  The units of all items
 // form one list that is dealt to the workgroups in equal contiguous runs, so
 // sequences of all lengths load the device evenly.  A workgroup that has all
 // of an item's units writes the rows; otherwise it leaves sums, maxima and
@@ -52,23 +53,21 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 template <RowType T>
 struct AttnElem;
+// kQParts f16 parts of a query, kPParts bf16 parts of a weight.
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
-  static constexpr int kQParts = 3, kPParts = 3;
-  static constexpr bool kQHalf = false;
+  static constexpr int kQParts = 2, kPParts = 3;
 };
 template <>
 struct AttnElem<kRowBf16> {
   typedef __bf16 type;
   static constexpr int kQParts = 1, kPParts = 2;
-  static constexpr bool kQHalf = false;
 };
 template <>
 struct AttnElem<kRowF16> {
   typedef _Float16 type;
   static constexpr int kQParts = 1, kPParts = 2;
-  static constexpr bool kQHalf = true;  // scores in f16 operands, which hold q and the codes exactly
 };
 
 template <typename E, int N>
@@ -83,21 +82,17 @@ __device__ __forceinline__ uint32_t pack_hi(float lo, float hi) {
   return __builtin_amdgcn_perm(bits(hi), bits(lo), 0x07060302u);
 }
 
-// Codes at byte pair `half` of a word, as two bf16.
-__device__ __forceinline__ uint32_t pair_bf16(uint32_t w, int half) {
-  const float a = (float)(int8_t)(w >> (16 * half));
-  const float b = (float)(int8_t)(w >> (16 * half + 8));
-  return pack_hi(a, b);
-}
-
-// The same as two f16: 1024 + (code + 128) by its bits, less 1152.
+// Codes at byte pair `half` of a word as two f16: 1024 + (code + 128) by its
+// bits, less 1152.
 __device__ __forceinline__ uint32_t pair_f16(uint32_t w, int half) {
   const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w ^ 0x80808080u, half ? 0x04030402u : 0x04010400u);
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, u) - v2h{(_Float16)1152.f, (_Float16)1152.f});
 }
-template <bool HALF>
-__device__ __forceinline__ uint32_t pair_q(uint32_t w, int half) {
-  return HALF ? pair_f16(w, half) : pair_bf16(w, half);
+// The same as code + 128 in units of 2^-24, the f16 numbers whose bits are the
+// biased code: one instruction, and the matrix cores take them as they are.
+constexpr float kBiasedUnit = 1.f / 16777216.f;
+__device__ __forceinline__ uint32_t pair_biased(uint32_t biased, int half) {
+  return __builtin_amdgcn_perm(0u, biased, half ? 0x0c030c02u : 0x0c010c00u);
 }
 
 // x less half `half` of a packed pair of bf16, in one instruction: exact where
@@ -135,19 +130,18 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// The product for scores: f16 operands or bf16 ones.
-template <bool HALF>
-__device__ __forceinline__ v4f mfma_q(v4u a, v4u b, v4f c) {
-  if constexpr (HALF)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
-  else
-    return mfma(a, b, c);
+__device__ __forceinline__ v4f mfma_f16(v4u a, v4u b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
 // Lane N of each 16-lane group, to all of them (row_newbcast).
 template <int N>
 __device__ __forceinline__ float bcast(float x) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
 }
 template <int I, int N, typename F>
 __device__ __forceinline__ void static_for(F f) {
@@ -166,26 +160,52 @@ __device__ __forceinline__ float across_groups_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// Query parts of one row, as lane group c holds them: channels 32 b + 8 c + 0..7
-// of every block.  A row that is not `in` is zeros.
+// Channels 32 b + 8 c + 0..7 of every block of one row of q, as they come.
 template <RowType T, int DIM>
-__device__ __forceinline__ void load_query(const AttnArgs &p, int t, int head, int c, bool in,
-                                           v4u (&qf)[DIM / 32][AttnElem<T>::kQParts]) {
+struct QueryRow {
+  Run<typename AttnElem<T>::type, 8> x[DIM / 32];
+};
+template <RowType T, int DIM>
+__device__ __forceinline__ void fetch_query(const AttnArgs &p, int t, int head, int c, QueryRow<T, DIM> &to) {
   typedef typename AttnElem<T>::type E;
   const E *q = static_cast<const E *>(p.q) + (int64_t)t * p.q_stride + (int64_t)head * DIM + 8 * c;
 #pragma unroll
-  for (int b = 0; b < DIM / 32; ++b) {
-    const Run<E, 8> v = *reinterpret_cast<const Run<E, 8> *>(q + 32 * b);
-    if constexpr (AttnElem<T>::kQHalf) {
-      const v4u x = __builtin_bit_cast(v4u, v);
-      qf[b][0] = in ? x : v4u{0, 0, 0, 0};
-    } else {
-      float x[8];
+  for (int b = 0; b < DIM / 32; ++b) to.x[b] = *reinterpret_cast<const Run<E, 8> *>(q + 32 * b);
+}
+
+// Its parts, scaled by a power of two that brings the row's largest channel to
+// 2^14 .. 2^15 so that f16 holds them: one part is exact for bf16 and f16 rows,
+// two are to 2^-23 for f32 (channels below 2^-38 of the largest lose bits that
+// no f32 sum would keep).  Returns what undoes the scaling.  A row that is not
+// `in` is zeros.
+template <RowType T, int DIM>
+__device__ __forceinline__ float cut_query(const QueryRow<T, DIM> &from, bool in,
+                                           v4u (&qf)[DIM / 32][AttnElem<T>::kQParts]) {
+  constexpr int NB = DIM / 32;
+  float x[NB][8], top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = in ? (float)v.x[i] : 0.f;
-      split8<AttnElem<T>::kQParts>(x, qf[b]);
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[b][i] = in ? (float)from.x[b].x[i] : 0.f;
+      top = fmaxf(top, fabsf(x[b][i]));
     }
-  }
+  top = across_groups_max(top);
+  const int up = top > 0.f && top < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y0 = ldexpf(x[b][2 * i], up), y1 = ldexpf(x[b][2 * i + 1], up);
+#pragma unroll
+      for (int n = 0; n < AttnElem<T>::kQParts; ++n) {
+        const v2h h = {(_Float16)y0, (_Float16)y1};
+        qf[b][n][i] = __builtin_bit_cast(uint32_t, h);
+        y0 -= (float)h.x;
+        y1 -= (float)h.y;
+      }
+    }
+  return ldexpf(1.f, -up);
 }
 
 // ---------------------------------------------------------------- the work list
@@ -196,10 +216,12 @@ __device__ __forceinline__ int item_keys(const AttnArgs &p, const Seq &q, int r)
   if (p.tree != nullptr) return q.length;
   return q.length - q.n + min(q.n, (r + 1) * p.tile_tokens);
 }
+// Units of an item: those of its keys, after p.item_cost that stand for what an
+// item costs whatever its length.
 __device__ __forceinline__ int item_units(const AttnArgs &p, const Seq &q, int r) {
-  if (q.bad) return 1;
-  const int u = (item_keys(p, q, r) + kAttnUnit - 1) / kAttnUnit;
-  return u < 1 ? 1 : u;
+  if (q.bad) return 1 + p.item_cost;
+  const int u = (item_keys(p, q, r) + (1 << p.unit_shift) - 1) >> p.unit_shift;
+  return (u < 1 ? 1 : u) + p.item_cost;
 }
 __device__ __forceinline__ int row_items(const AttnArgs &p, const Seq &q) {
   return (q.n + p.tile_tokens - 1) / p.tile_tokens;
@@ -213,63 +235,83 @@ __device__ __forceinline__ int64_t head_units(const AttnArgs &p, const Seq &q) {
   return u;
 }
 
+// a / b for a >= 0, b > 0: the usual small numbers without a 64-bit division
+// (over a hundred instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct Run0 {  // where a workgroup's run begins
   int b;
+  Seq seq;        // sequence b
   int64_t rest;   // units into sequence b
   int64_t begin, end, total;
   int wgs;        // workgroups with a run
 };
 
-// Every workgroup sums the sequences' units and finds its share of them.
-__device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int tid) {
-  __shared__ int64_t sums[kThreads];
-  __shared__ int64_t found_rest;
-  __shared__ int found_b;
+// Every wave sums the sequences' units, a stretch of them per lane, and finds
+// its workgroup's share.
+__device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int lane) {
   const int64_t heads = (int64_t)p.c.heads * p.subs;
-  const int per = (p.s.seqs + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.s.seqs), b1 = min(b0 + per, p.s.seqs);
+  const int per = (p.s.seqs + 63) / 64;
+  const int b0 = min(lane * per, p.s.seqs), b1 = min(b0 + per, p.s.seqs);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += heads * head_units(p, seq_at(p.s, b));
-  sums[tid] = mine;
-  __syncthreads();
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < kThreads; d <<= 1) {
-    const int64_t other = tid >= d ? sums[tid - d] : 0;
-    __syncthreads();
-    incl += other;
-    sums[tid] = incl;
-    __syncthreads();
+  Seq seq{0, 0, 0, false};
+  for (int b = b0; b < b1; ++b) {
+    seq = seq_at(p.s, b);
+    mine += heads * head_units(p, seq);
+  }
+  int64_t upto;
+  if (p.few_units) {  // the total fits 31 bits: a scan by DPP
+    int x = (int)mine;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+    upto = x;
+  } else {
+    upto = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t other = __shfl_up(upto, d);
+      if (lane >= d) upto += other;
+    }
   }
   Run0 r;
-  r.total = uniform(sums[kThreads - 1]);
+  r.total = (int64_t)((uint64_t)__builtin_amdgcn_readlane((uint32_t)((uint64_t)upto >> 32), 63) << 32 |
+                      (uint32_t)__builtin_amdgcn_readlane((uint32_t)upto, 63));
   r.wgs = (int)(r.total < wgs ? r.total : wgs);
-  r.begin = r.end = r.rest = 0;
-  r.b = 0;
-  if (wg < r.wgs) {
-    r.begin = r.total * wg / r.wgs;
-    r.end = r.total * (wg + 1) / r.wgs;
-    int64_t at = incl - mine;
-    if (r.begin >= at && r.begin < incl) {
-      int b = b0;
-      for (; b < b1 - 1; ++b) {
-        const int64_t u = heads * head_units(p, seq_at(p.s, b));
-        if (r.begin < at + u) break;
-        at += u;
-      }
-      found_b = b;
-      found_rest = r.begin - at;
+  if (wg >= r.wgs) return r;
+  r.begin = quotient(r.total * wg, r.wgs);
+  r.end = quotient(r.total * (wg + 1), r.wgs);
+  int64_t at = upto - mine;
+  const bool owner = r.begin >= at && r.begin < upto;
+  int b = b0;
+  if (owner && per > 1) {
+    for (;; ++b) {
+      seq = seq_at(p.s, b);
+      const int64_t u = heads * head_units(p, seq);
+      if (r.begin < at + u) break;  // before b1: the stretch holds the unit
+      at += u;
     }
-    __syncthreads();
-    r.b = __builtin_amdgcn_readfirstlane(found_b);
-    r.rest = uniform(found_rest);
   }
+  const int from = __builtin_ctzll(__ballot(owner));
+  const int64_t rest = r.begin - at;
+  r.b = __builtin_amdgcn_readlane(b, from);
+  r.rest = (int64_t)((uint64_t)__builtin_amdgcn_readlane((uint32_t)((uint64_t)rest >> 32), from) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((uint32_t)rest, from));
+  r.seq.start = __builtin_amdgcn_readlane(seq.start, from);
+  r.seq.n = __builtin_amdgcn_readlane(seq.n, from);
+  r.seq.length = __builtin_amdgcn_readlane(seq.length, from);
+  r.seq.bad = __builtin_amdgcn_readlane((int)seq.bad, from) != 0;
   return r;
 }
 
 // The workgroup whose run holds unit u.
 __device__ __forceinline__ int wg_of(int64_t u, const Run0 &r) {
-  return (int)(((u + 1) * r.wgs - 1) / r.total);
+  return (int)quotient((u + 1) * r.wgs - 1, r.total);
 }
 
 // Whether row `t` sees any key; only asked for rows without weight.
@@ -319,19 +361,22 @@ __device__ __forceinline__ float load_scale(__amdgpu_buffer_rsrc_t rs, int offse
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, 0));
 }
 
-// The token row, of head kvh, where the 16 keys at `pos` begin.  poison: NaN,
-// to be added to the scales, where the table holds no page of the cache.
-__device__ __forceinline__ int64_t half_base(const AttnArgs &p, const int *pages, int pos, int last, int kvh,
-                                             float &poison) {
+// 16 keys of a sequence, on the way to their address: the page is read ahead.
+struct Keys16 {
+  int page, in;  // the table's entry, and the first token within the page
+};
+// The 16 keys at `pos`, or those of the last key where they lie past it.
+__device__ __forceinline__ Keys16 keys_at(const AttnArgs &p, const int *pages, int pos, int last) {
   const int at = min(pos, last);
-  int page = uniform_load(pages + (at >> p.c.page_shift));
-  const bool ok = (uint32_t)page < p.c.pages;
-  page = ok ? page : 0;
+  // 16 keys lie within a page (pages hold 16 tokens or more).
+  return Keys16{uniform_load(pages + (at >> p.c.page_shift)), at & ((1 << p.c.page_shift) - 1) & ~15};
+}
+// The token row, of head kvh, where they begin.  poison: NaN, to be added to
+// the scales, where the table holds no page of the cache.
+__device__ __forceinline__ int64_t token_row(const AttnArgs &p, const Keys16 &k, int kvh, float &poison) {
+  const bool ok = (uint32_t)k.page < p.c.pages;
   poison = ok ? 0.f : NAN;
-  // 16 keys lie within a page (pages hold 16 tokens or more); a half past the
-  // last key reads the last key's instead.
-  const int in = at & ((1 << p.c.page_shift) - 1) & ~15;
-  return (((int64_t)page * p.c.heads + kvh) << p.c.page_shift) + in;
+  return (((int64_t)(ok ? k.page : 0) * p.c.heads + kvh) << p.c.page_shift) + k.in;
 }
 
 // How much larger (as a power of two) a score may be than the maximum its row
@@ -339,9 +384,24 @@ __device__ __forceinline__ int64_t half_base(const AttnArgs &p, const int *pages
 // most tiles leave the sums as they are.
 constexpr float kMaxSlack = 8.f;
 
-// Scores (already times alpha log2 e) to weights, against the rows' kept maxima.
-template <int NRT, int NK, int NB>
-__device__ __forceinline__ void weigh(float (&s)[NRT][NK], float *m, float *l, v4f (*acc)[NB][2]) {
+// The largest of a row's values over the lanes that hold its keys: four groups
+// of 16 lanes, and PACK places within each.
+template <int PACK>
+__device__ __forceinline__ float row_max(float x) {
+  if constexpr (PACK == 4) x = fmaxf(x, dpp<0x124>(x));  // row_ror:4
+  if constexpr (PACK >= 2) x = fmaxf(x, dpp<0x128>(x));  // row_ror:8
+  return across_groups_max(x);
+}
+template <int PACK>
+__device__ __forceinline__ float row_sum(float x) {
+  if constexpr (PACK == 4) x += dpp<0x124>(x);
+  if constexpr (PACK >= 2) x += dpp<0x128>(x);
+  return across_groups_sum(x);
+}
+
+// Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
+template <int NRT, int NK, int NB, int PACK>
+__device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   float top[NRT];
   bool above = false;
 #pragma unroll
@@ -349,7 +409,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], float *m, float *l, v
     top[rt] = s[rt][0];
 #pragma unroll
     for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
-    top[rt] = across_groups_max(top[rt]);
+    top[rt] = row_max<PACK>(top[rt]) * undo[rt];
     above |= top[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
   }
   if (__ballot(above) != 0) {
@@ -371,7 +431,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], float *m, float *l, v
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k] - from);
+      s[rt][k] = __builtin_amdgcn_exp2f(fmaf(s[rt][k], undo[rt], -from));
       sum += s[rt][k];
     }
     l[rt] += sum;
@@ -385,13 +445,14 @@ __device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
-template <RowType T, int DIM, int RT>
+template <RowType T, int DIM, int RT_>
 struct Attn {
   typedef typename AttnElem<T>::type E;
+  static constexpr int RT = RT_;
   static constexpr int NB = DIM / 32;             // blocks
   static constexpr int QP = AttnElem<T>::kQParts;
   static constexpr int PP = AttnElem<T>::kPParts;
-  static constexpr bool QHALF = AttnElem<T>::kQHalf;
+  static constexpr int PACK = 1, NK = 8;          // keys of a tile per lane
   static constexpr int KW = DIM / 16;             // words of a lane's quarter row of K
   static constexpr int VW = DIM / 64;             // words of a lane's pairs of V
   static constexpr int SW = (4 * NB + 15) / 16;   // scale words per lane for 4 keys
@@ -400,42 +461,65 @@ struct Attn {
 
   // Codes and scales of one 32-key tile: 16-key half h in kw[h] / ks[h]; keys
   // 16 h + 4 c + i in vw[4 h + i], vs[h] (c the lane's group).
-  uint32_t kw[2][KW];
-  float ks[2][SW];
-  uint32_t vw[8][VW];
-  float vs[2][SW];
+  struct Tile {
+    uint32_t kw[2][KW];
+    float ks[2][SW];
+    uint32_t vw[8][VW];
+    float vs[2][SW];
+    float poison[2];  // as token_row gives it
+  };
   v4u qf[RT][NB][QP];
   v4f acc[RT][NB][2];
-  float m[RT], l[RT];
+  float m[RT], l[RT], undo[RT];
 
   const AttnArgs *p;
   float scale;       // alpha log2 e, multiplied into the key scales
-  int lane, row, c;  // row = lane % 16, c = lane / 16
+  int row, c;        // lane % 16 and lane / 16
+
+  __device__ __forceinline__ int row_of(int rt) const { return 16 * rt + row; }  // of the item
+  __device__ __forceinline__ bool holds_row() const { return true; }             // in its sums
+  __device__ __forceinline__ void start() {}
 
   // live: 0 for a tile that does not exist (nothing is read), 1 otherwise.
-  __device__ __forceinline__ void load_k(const int64_t (&base)[2], const float (&poison)[2], int live) {
+  // Scales are left as they come: arithmetic here would wait for them.
+  __device__ __forceinline__ void load_k(Tile &t, const int64_t (&base)[2], const float (&poison)[2], int live) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load_words<KW>(buffer_of(p->c.K + base[h] * DIM, 16 * DIM * live), row * DIM + c * (DIM / 4), kw[h]);
+      t.poison[h] = poison[h];
+      load_words<KW>(buffer_of(p->c.K + base[h] * DIM, 16 * DIM * live), row * DIM + c * (DIM / 4), t.kw[h]);
       const __amdgpu_buffer_rsrc_t rs = buffer_of(p->c.KS + base[h] * NB, 64 * NB * live);
 #pragma unroll
-      for (int w = 0; w < SW; ++w) ks[h][w] = fmaf(load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB))), scale, poison[h]);
+      for (int w = 0; w < SW; ++w)
+        t.ks[h][w] = load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB)));
     }
   }
-  __device__ __forceinline__ void load_v(const int64_t (&base)[2], const float (&poison)[2], int live) {
+  __device__ __forceinline__ void load_v(Tile &t, const int64_t (&base)[2], int live) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const __amdgpu_buffer_rsrc_t codes = buffer_of(p->c.V + base[h] * DIM, 16 * DIM * live);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), vw[4 * h + i]);
+      for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), t.vw[4 * h + i]);
       const __amdgpu_buffer_rsrc_t rs = buffer_of(p->c.VS + base[h] * NB, 64 * NB * live);
 #pragma unroll
-      for (int w = 0; w < SW; ++w) vs[h][w] = load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB))) + poison[h];
+      for (int w = 0; w < SW; ++w)
+        t.vs[h][w] = load_scale(rs, 4 * (4 * c * NB + (16 * w + row) % (4 * NB)));
     }
   }
 
+  // Once the key scales are used: marks the value scales of a missing page.
+  __device__ __forceinline__ void add_poison(Tile &t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < SW; ++w) t.vs[h][w] += t.poison[h];
+  }
+
   // Scores of the tile: s[rt][4 h + i] for key 16 h + 4 c + i and row `row` of row tile rt.
-  __device__ __forceinline__ void scores(float (&s)[RT][8]) {
+  __device__ __forceinline__ void scores(Tile &t, float (&s)[RT][8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < SW; ++w) t.ks[h][w] = fmaf(t.ks[h][w], scale, t.poison[h]);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -448,21 +532,22 @@ struct Attn {
 #pragma unroll
         for (int jl = 0; jl < 4; ++jl) {
           constexpr int byte = 2 * b;  // within the pair's NB * 2 bytes
-          a[jl] = pair_q<QHALF>(kw[h][jl * VW + byte / 4], (byte / 2) % 2);
+          a[jl] = pair_f16(t.kw[h][jl * VW + byte / 4], (byte / 2) % 2);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a, qf[rt][b][q], x);  // small parts first
+          for (int q = QP - 1; q >= 0; --q) x = mfma_f16(a, qf[rt][b][q], x);  // small parts first
           static_for<0, 4>([&](auto i_) {
             constexpr int i = decltype(i_)::value;
             constexpr int e = i * NB + b;
-            s[rt][4 * h + i] += bcast<e % 16>(ks[h][e / 16]) * x[i];
+            s[rt][4 * h + i] += bcast<e % 16>(t.ks[h][e / 16]) * x[i];
+            pin(s[rt][4 * h + i]);
           });
         }
+        __builtin_amdgcn_sched_barrier(0);
       });
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -470,7 +555,7 @@ struct Attn {
   // score of no weight.  Their value scales may be anything: a scale that is
   // not finite is taken out, and the rows that do see it are remembered in
   // lost[rt], bit b for block b.  Returns whether there is any such scale.
-  __device__ __forceinline__ bool mask(float (&s)[RT][8], const uint32_t (&sees)[RT], uint32_t (&lost)[RT]) {
+  __device__ __forceinline__ bool mask(Tile &t, float (&s)[RT][8], const uint32_t (&sees)[RT], uint32_t (&lost)[RT]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -480,14 +565,14 @@ struct Attn {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int w = 0; w < SW; ++w) bad |= !finite(vs[h][w]);
+      for (int w = 0; w < SW; ++w) bad |= !finite(t.vs[h][w]);
     if (__ballot(bad) == 0) return false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) lost[rt] = 0;
     static_for<0, 8>([&](auto k_) {
       static_for<0, NB>([&](auto b_) {
         constexpr int k = decltype(k_)::value, b = decltype(b_)::value, e = (k % 4) * NB + b;
-        const bool gone = !finite(bcast<e % 16>(vs[k / 4][e / 16]));
+        const bool gone = !finite(bcast<e % 16>(t.vs[k / 4][e / 16]));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           if (gone && ((sees[rt] >> (16 * (k / 4) + 4 * c + k % 4)) & 1)) lost[rt] |= 1u << b;
@@ -501,18 +586,18 @@ struct Attn {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int w = 0; w < SW; ++w) vs[h][w] = finite(vs[h][w]) ? vs[h][w] : 0.f;
+      for (int w = 0; w < SW; ++w) t.vs[h][w] = finite(t.vs[h][w]) ? t.vs[h][w] : 0.f;
     return true;
   }
 
-  __device__ __forceinline__ void values(const float (&s)[RT][8]) {
+  __device__ __forceinline__ void values(const Tile &t, const float (&s)[RT][8]) {
     static_for<0, NB>([&](auto b_) {
       constexpr int b = decltype(b_)::value;
       // Lane: codes of keys (k index 4 h + i) at channels 32 b + 2 row + 0, 1.
       v4u a[2];
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t w0 = vw[2 * kk][b / 2], w1 = vw[2 * kk + 1][b / 2];
+        const uint32_t w0 = t.vw[2 * kk][b / 2], w1 = t.vw[2 * kk + 1][b / 2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float x0 = (float)(int8_t)(w0 >> (16 * (b % 2) + 8 * i));
@@ -526,7 +611,7 @@ struct Attn {
         static_for<0, 8>([&](auto k_) {
           constexpr int k = decltype(k_)::value;
           constexpr int e = (k % 4) * NB + b;
-          w[k] = bcast<e % 16>(vs[k / 4][e / 16]) * s[rt][k];
+          w[k] = bcast<e % 16>(t.vs[k / 4][e / 16]) * s[rt][k];
         });
         v4u parts[PP];
         split8<PP>(w, parts);
@@ -534,9 +619,216 @@ struct Attn {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) pin(acc[rt][b][i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     });
+  }
+};
+
+// The same for items of at most 16 / PACK rows (one new token of a small group):
+// the query's columns repeat PACK times across the matrix operand, so that the
+// lanes of a row's repeats hold the same scores, and each keeps a PACK-th of the
+// keys (KPL).  Exponentials, weights and their parts, most of the other
+// kernel's instructions, are then made once instead of PACK times; the parts
+// return to the lanes of the first columns by DPP as matrix operands.  Scores
+// take biased codes (one instruction a pair); what the bias adds, 128 times the
+// sum of the query's block, is taken off the packed products.
+template <RowType T, int DIM, int PACK_>
+struct AttnFew {
+  typedef typename AttnElem<T>::type E;
+  static constexpr int RT = 1, PACK = PACK_, NK = 8 / PACK;
+  static constexpr int NB = DIM / 32;
+  static constexpr int QP = AttnElem<T>::kQParts;
+  static constexpr int PP = AttnElem<T>::kPParts;
+  static constexpr int KW = DIM / 16, VW = DIM / 64;
+  static constexpr int ROWS = 16 / PACK;
+  static constexpr int PITCH = DIM + 4;
+
+  // As in the other kernel, but for the scales: those of the lane's NK keys,
+  // key by key.
+  struct Tile {
+    uint32_t kw[2][KW];
+    uint32_t vw[8][VW];
+    Run<float, NK * NB> ks, vs;
+    float poison;
+  };
+  v4u qf[1][NB][QP];
+  v4f acc[1][NB][2];
+  float m[1], l[1], undo[1];
+  float bias[NB];
+
+  const AttnArgs *p;
+  float scale;
+  int row, c;
+
+  __device__ __forceinline__ int row_of(int) const { return row % ROWS; }
+  __device__ __forceinline__ bool holds_row() const { return row < ROWS; }
+  __device__ __forceinline__ int part() const { return row / ROWS; }
+  // The lane's first key within the tile: the others follow it.
+  __device__ __forceinline__ int first_key() const {
+    return PACK == 4 ? 16 * (part() / 2) + 4 * c + 2 * (part() % 2) : 16 * part() + 4 * c;
+  }
+  __device__ __forceinline__ bool upper_half() const { return part() >= PACK / 2; }
+
+  // After the query: its blocks' sums.
+  __device__ __forceinline__ void start() {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float x = 0.f;
+#pragma unroll
+      for (int q = QP - 1; q >= 0; --q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const v2h h = __builtin_bit_cast(v2h, (uint32_t)qf[0][b][q][i]);
+          x += (float)h.x + (float)h.y;
+        }
+      bias[b] = across_groups_sum(x) * (128.f * kBiasedUnit);
+    }
+  }
+
+  __device__ __forceinline__ void load_scales(const float *from, const int64_t (&base)[2], Run<float, NK * NB> &to) {
+    to = *reinterpret_cast<const Run<float, NK * NB> *>(from + ((upper_half() ? base[1] : base[0]) + first_key() % 16) * NB);
+  }
+  __device__ __forceinline__ void load_k(Tile &t, const int64_t (&base)[2], const float (&poison)[2], int live) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_words<KW>(buffer_of(p->c.K + base[h] * DIM, 16 * DIM * live), row * DIM + c * (DIM / 4), t.kw[h]);
+    load_scales(p->c.KS, base, t.ks);
+    t.poison = upper_half() ? poison[1] : poison[0];
+  }
+  __device__ __forceinline__ void load_v(Tile &t, const int64_t (&base)[2], int live) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __amdgpu_buffer_rsrc_t codes = buffer_of(p->c.V + base[h] * DIM, 16 * DIM * live);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), t.vw[4 * h + i]);
+    }
+    load_scales(p->c.VS, base, t.vs);
+  }
+
+  __device__ __forceinline__ void add_poison(Tile &t) {
+#pragma unroll
+    for (int e = 0; e < NK * NB; ++e) t.vs.x[e] += t.poison;
+  }
+
+  // s[k]: the lane's k-th key.
+  __device__ __forceinline__ void scores(Tile &t, float (&s)[1][NK]) {
+    const float unit = scale * (1.f / kBiasedUnit);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) t.kw[h][w] ^= 0x80808080u;
+    static_for<0, NB>([&](auto b_) {
+      constexpr int b = decltype(b_)::value;
+      v4f x[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4u a;
+#pragma unroll
+        for (int jl = 0; jl < 4; ++jl) a[jl] = pair_biased(t.kw[h][jl * VW + b / 2], b % 2);
+        x[h] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = QP - 1; q >= 0; --q) x[h] = mfma_f16(a, qf[0][b][q], x[h]);
+      }
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        float y;
+        if constexpr (PACK == 4) {
+          y = in_bank<1>(x[0][k], x[0][2 + k]);
+          y = in_bank<2>(y, x[1][k]);
+          y = in_bank<3>(y, x[1][2 + k]);
+        } else {
+          y = in_bank<2>(x[0][k], x[1][k]);
+          y = in_bank<3>(y, x[1][k]);
+        }
+        const float ks = fmaf(t.ks.x[k * NB + b], unit, t.poison);
+        s[0][k] = b == 0 ? ks * (y - bias[b]) : fmaf(ks, y - bias[b], s[0][k]);
+        pin(s[0][k]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  // other, in lanes 4 BANK .. 4 BANK + 3 of each 16.
+  template <int BANK>
+  static __device__ __forceinline__ float in_bank(float x, float other) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(other), 0xe4, 0xf, 1 << BANK, false));
+  }
+
+  __device__ __forceinline__ bool mask(Tile &t, float (&s)[1][NK], const uint32_t (&sees)[1], uint32_t (&lost)[1]) {
+    const uint32_t mine = sees[0] >> first_key();
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+      if (!((mine >> k) & 1)) s[0][k] = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < NK * NB; ++e) bad |= !finite(t.vs.x[e]);
+    if (__ballot(bad) == 0) return false;
+    uint32_t gone = 0;
+#pragma unroll
+    for (int e = 0; e < NK * NB; ++e)
+      if (!finite(t.vs.x[e])) {
+        gone |= ((mine >> (e / NB)) & 1) << (e % NB);
+        t.vs.x[e] = 0.f;
+      }
+    if constexpr (PACK == 4) gone |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)gone, 0x124, 0xf, 0xf, true);
+    gone |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)gone, 0x128, 0xf, 0xf, true);
+    gone |= __shfl_xor(gone, 16);
+    gone |= __shfl_xor(gone, 32);
+    lost[0] = gone;
+    return true;
+  }
+
+  __device__ __forceinline__ void values(const Tile &t, const float (&s)[1][NK]) {
+    static_for<0, NB>([&](auto b_) {
+      constexpr int b = decltype(b_)::value;
+      v4u a[2];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t w0 = t.vw[2 * kk][b / 2], w1 = t.vw[2 * kk + 1][b / 2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x0 = (float)(int8_t)(w0 >> (16 * (b % 2) + 8 * i));
+          const float x1 = (float)(int8_t)(w1 >> (16 * (b % 2) + 8 * i));
+          a[i][kk] = pack_hi(x0, x1);
+        }
+      }
+      float w[NK];
+#pragma unroll
+      for (int k = 0; k < NK; ++k) w[k] = t.vs.x[k * NB + b] * s[0][k];
+      v4u parts[PP];
+#pragma unroll
+      for (int q = 0; q < PP; ++q)
+#pragma unroll
+        for (int d = 0; d < NK / 2; ++d) {
+          const uint32_t pair = pack_hi(w[2 * d], w[2 * d + 1]);
+          if (q + 1 < PP) {
+            w[2 * d] = less<0>(pair, w[2 * d]);
+            w[2 * d + 1] = less<1>(pair, w[2 * d + 1]);
+          }
+          parts[q][d] = pair;
+          if constexpr (PACK == 4) {  // keys 2 m, 2 m + 1 of the operand are those of part m's lanes
+            parts[q][1] = shifted<4>(pair);
+            parts[q][2] = shifted<8>(pair);
+            parts[q][3] = shifted<12>(pair);
+          } else {
+            parts[q][2 + d] = shifted<8>(pair);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int q = PP - 1; q >= 0; --q) acc[0][b][i] = mfma(a[i], parts[q], acc[0][b][i]);
+        pin(acc[0][b][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  template <int BY>
+  static __device__ __forceinline__ uint32_t shifted(uint32_t x) {  // from BY lanes above (row_shl)
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x100 + BY, 0xf, 0xf, true);
   }
 };
 
@@ -584,22 +876,22 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
   // Neighbouring runs, which may share keys or an item, on one XCD.
   const int per_xcd = gridDim.x / kXcds;
   const int wg = gridDim.x % kXcds == 0 ? (int)(blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds : (int)blockIdx.x;
-  const Run0 run = find_run(p, wg, gridDim.x, tid);
-  if (tid == 0) p.items[wg].valid = 0;
+  const Run0 run = find_run(p, wg, gridDim.x, tid & 63);
+  if (tid == 0 && p.items != nullptr) p.items[wg].valid = 0;
   if (wg >= run.wgs) return;
 
   // Where the run begins: sequence b, head vh (with its sub-group), row item r, unit k0.
   Share h;
   int b = run.b;
-  h.seq = uniform_seq_at(p.s, b);
+  h.seq = run.seq;
   int vh, r;
   {
     const int64_t per_head = head_units(p, h.seq);
-    vh = (int)(run.rest / per_head);
+    vh = (int)quotient(run.rest, per_head);
     int64_t rest = run.rest - vh * per_head;
     if (p.tree != nullptr || h.seq.bad) {
       const int u = item_units(p, h.seq, 0);
-      r = (int)(rest / u);
+      r = (int)quotient(rest, u);
       h.k0 = (int)(rest - (int64_t)r * u);
     } else {
       r = 0;
@@ -608,11 +900,14 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
     }
   }
 
+  int v0 = h.k0;  // units into the item, its cost included
   for (int64_t unit = run.begin;;) {
     const int units = item_units(p, h.seq, r);
     const int64_t left = run.end - unit;
-    h.k1 = left < units - h.k0 ? h.k0 + (int)left : units;
-    h.whole = h.k0 == 0 && h.k1 == units;
+    const int v1 = left < units - v0 ? v0 + (int)left : units;
+    h.k0 = max(v0 - p.item_cost, 0);
+    h.k1 = max(v1 - p.item_cost, 0);
+    h.whole = h.k0 == 0 && v1 == units;
     h.kvh = vh / p.subs;
     const int sub = vh - h.kvh * p.subs;
     h.sub_heads = min(p.sub_heads, p.group - sub * p.sub_heads);
@@ -627,11 +922,11 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
     // Slot 1 holds the run's last item, cut short at its end; slot 0 an item
     // that an earlier run began.
     h.slot = p.partial + (2 * (int64_t)wg + (h.k0 == 0 ? 1 : 0)) * attn_slot_floats(slot_rows, DIM);
-    work(h);
-    if (tid == 0 && h.k0 == 0 && !h.whole) {
+    if (h.k1 > 0) work(h);
+    if (tid == 0 && h.k0 == 0 && h.k1 > 0 && !h.whole) {
       AttnItem it;
       it.valid = 1;
-      it.last = wg_of(unit + units - 1, run);
+      it.last = wg_of(unit - v0 + units - 1, run);
       it.row0 = h.seq.start + h.i0;
       it.tokens = h.tokens;
       it.head0 = h.head0;
@@ -640,10 +935,10 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
       it.context = h.context;
       p.items[wg] = it;
     }
-    unit += h.k1 - h.k0;
+    unit += v1 - v0;
     if (unit >= run.end) return;
     // The next item.
-    h.k0 = 0;
+    v0 = 0;
     if (++r == row_items(p, h.seq)) {
       r = 0;
       if (++vh == p.c.heads * p.subs) {
@@ -667,106 +962,139 @@ __device__ __forceinline__ void finish_row(const AttnArgs &p, const Share &h, in
   for (int i = 0; i < N; ++i) x[i] = nothing ? 0.f : x[i] * scale;
 }
 
-template <RowType T, int DIM, int RT>
-__global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_kernel(AttnArgs p) {
-  typedef Attn<T, DIM, RT> A;
+template <RowType T, int DIM, int ROWS_>
+struct AttnOf {
+  typedef Attn<T, DIM, ROWS_ / 16> type;
+};
+template <RowType T, int DIM>
+struct AttnOf<T, DIM, 4> {
+  typedef AttnFew<T, DIM, 4> type;
+};
+template <RowType T, int DIM>
+struct AttnOf<T, DIM, 8> {
+  typedef AttnFew<T, DIM, 2> type;
+};
+
+// WAVES: 4, or 8 where a workgroup takes all keys of its items.
+template <RowType T, int DIM, int ROWS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? attn_wgs_per_cu(T, DIM, ROWS) : 1) void attention_kernel(AttnArgs p) {
+  typedef typename AttnOf<T, DIM, ROWS>::type A;
   typedef typename A::E E;
-  constexpr int NB = A::NB, ROWS = A::ROWS, PITCH = A::PITCH;
-  __shared__ __attribute__((aligned(16))) float sums[kWaves][ROWS][PITCH];
-  __shared__ float tops[kWaves][ROWS], weights[kWaves][ROWS];
+  constexpr int NB = A::NB, RT = A::RT, PITCH = A::PITCH, STEP = kAttnTile * WAVES;
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][ROWS][PITCH];
+  __shared__ float tops[WAVES][ROWS], weights[WAVES][ROWS];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   A a;
   a.p = &p;
   a.scale = p.alpha * 1.4426950408889634f;
-  a.lane = tid & 63;
-  a.row = a.lane & 15;
-  a.c = a.lane >> 4;
+  a.row = tid & 15;
+  a.c = (tid & 63) >> 4;
 
   walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
+    // The query's rows, the first tile and the second one's pages are asked
+    // for before the first of them is needed.
     int index[RT];
+    bool in[RT];
+    QueryRow<T, DIM> q[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int rho = 16 * rt + a.row;
+      const int rho = a.row_of(rt);
       const int tok = rho / h.sub_heads;
-      const bool in = rho < h.rows;
+      in[rt] = rho < h.rows;
       index[rt] = h.i0 + min(tok, h.tokens - 1);
-      load_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, a.c, in, a.qf[rt]);
+      fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, a.c, q[rt]);
+    }
+    const int last = h.keys - 1;
+    const int begin = (h.k0 << p.unit_shift) + wave * kAttnTile;
+    const int end = h.seq.bad ? 0 : min(h.k1 << p.unit_shift, h.keys);
+    Keys16 keys[2];  // a page's number is read one tile before the page
+    int64_t base[2];
+    float poison[2];
+    auto ahead = [&](int at) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) keys[k] = keys_at(p, h.pages, at + 16 * k, last);
+    };
+    auto place = [&]() {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) base[k] = token_row(p, keys[k], h.kvh, poison[k]);
+    };
+    typename A::Tile t;
+    if (begin < end) {
+      ahead(begin);
+      place();
+      ahead(begin + STEP);
+      a.load_k(t, base, poison, 1);
+      a.load_v(t, base, 1);
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      a.undo[rt] = cut_query<T, DIM>(q[rt], in[rt], a.qf[rt]);
       a.m[rt] = -INFINITY;
       a.l[rt] = 0.f;
 #pragma unroll
       for (int bb = 0; bb < NB; ++bb) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{0.f, 0.f, 0.f, 0.f};
     }
+    a.start();
 
-    if (!h.seq.bad) {
-      const int last = h.keys - 1;
-      const int begin = h.k0 * kAttnUnit + wave * kAttnTile;
-      const int end = min(h.k1 * kAttnUnit, h.keys);
-      if (begin < end) {
-        int64_t base[2];
-        float poison[2];
+    for (int at = begin; at < end; at += STEP) {
+      // The next tile's parts are loaded as this one's are used up.
+      const int more = at + STEP < end;
+      place();
+      ahead(at + 2 * STEP);
+      float s[RT][A::NK];
+      a.scores(t, s);
+      a.add_poison(t);
+      a.load_k(t, base, poison, more);
+      bool some_lost = false;
+      uint32_t lost[RT];
+      if (at + kAttnTile > h.all) {
+        uint32_t sees[RT];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) base[k] = half_base(p, h.pages, begin + 16 * k, last, h.kvh, poison[k]);
-        a.load_k(base, poison, 1);
-        a.load_v(base, poison, 1);
-        for (int at = begin; at < end; at += kAttnUnit) {
-          const int next = at + kAttnUnit;
-          const int more = next < end;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) base[k] = half_base(p, h.pages, next + 16 * k, last, h.kvh, poison[k]);
-          float s[RT][8];
-          a.scores(s);
-          a.load_k(base, poison, more);
-          bool some_lost = false;
-          uint32_t lost[RT];
-          if (at + kAttnTile > h.all) {
-            uint32_t sees[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-              sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], h.seq.start + index[rt]);
-            some_lost = a.mask(s, sees, lost);
-          }
-          weigh<RT, 8, NB>(s, a.m, a.l, a.acc);
-          a.values(s);
-          if (some_lost) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int bb = 0; bb < NB; ++bb)
-                if (lost[rt] >> bb & 1) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{NAN, NAN, NAN, NAN};
-          }
-          a.load_v(base, poison, more);
-        }
+        for (int rt = 0; rt < RT; ++rt)
+          sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], h.seq.start + index[rt]);
+        some_lost = a.mask(t, s, sees, lost);
       }
+      weigh<RT, A::NK, NB, A::PACK>(s, a.undo, a.m, a.l, a.acc);
+      a.values(t, s);
+      if (some_lost) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int bb = 0; bb < NB; ++bb)
+            if (lost[rt] >> bb & 1) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{NAN, NAN, NAN, NAN};
+      }
+      a.load_v(t, base, more);
     }
 
-    // The four waves' sums, through LDS.
+    // The waves' sums, through LDS.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float l = across_groups_sum(a.l[rt]);
+      const float l = row_sum<A::PACK>(a.l[rt]);
+      if (!a.holds_row()) continue;
       if (a.c == 0) {
-        tops[wave][16 * rt + a.row] = a.m[rt];
-        weights[wave][16 * rt + a.row] = l;
+        tops[wave][a.row_of(rt)] = a.m[rt];
+        weights[wave][a.row_of(rt)] = l;
       }
 #pragma unroll
       for (int bb = 0; bb < NB; ++bb) {
-        float *to = &sums[wave][16 * rt + a.row][32 * bb + 8 * a.c];
+        float *to = &sums[wave][a.row_of(rt)][32 * bb + 8 * a.c];
         const v4f x = a.acc[rt][bb][0], y = a.acc[rt][bb][1];  // channels 2 i and 2 i + 1 of the lane's eight
         *reinterpret_cast<v4f *>(to) = v4f{x[0], y[0], x[1], y[1]};
         *reinterpret_cast<v4f *>(to + 4) = v4f{x[2], y[2], x[3], y[3]};
       }
     }
     __syncthreads();
-    for (int e = tid; e < h.rows * (DIM / 8); e += kThreads) {
+    for (int e = tid; e < h.rows * (DIM / 8); e += 64 * WAVES) {
       const int rho = e / (DIM / 8), d = 8 * (e % (DIM / 8));
       float top = tops[0][rho];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, tops[w][rho]);
+      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w][rho]);
       const float from = top == -INFINITY ? 0.f : top;
       float weight = 0.f, x[8] = {};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         const float f = __builtin_amdgcn_exp2f(tops[w][rho] - from);
         weight += f * weights[w][rho];
 #pragma unroll
@@ -815,10 +1143,9 @@ struct WideLds {
 };
 
 template <RowType T, int DIM, int RT>
-__global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel(AttnArgs p) {
+__global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void attention_wide_kernel(AttnArgs p) {
   typedef typename AttnElem<T>::type E;
   constexpr int NB = DIM / 32, QP = AttnElem<T>::kQParts, PP = AttnElem<T>::kPParts;
-  constexpr bool QHALF = AttnElem<T>::kQHalf;
   constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;
   constexpr int ROWS = 64 * RT, BUFS = WideLds<DIM>::BUFS;
   constexpr int SPL = (16 * NB + 63) / 64;  // scale words a lane stages
@@ -833,7 +1160,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
   // This wave's 16 keys of a step, on their way to LDS.
   uint32_t kw[KW], vw[4][VW];
   float ksw[SPL], vsw[SPL];
-  auto load = [&](int64_t base, float poison) {
+  float poison = 0.f;
+  auto load = [&](int64_t base) {
     load_words<KW>(buffer_of(p.c.K + base * DIM, 16 * DIM), row * DIM + c * (DIM / 4), kw);
     const __amdgpu_buffer_rsrc_t codes = buffer_of(p.c.V + base * DIM, 16 * DIM);
 #pragma unroll
@@ -841,8 +1169,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 #pragma unroll
     for (int w = 0; w < SPL; ++w) {
       const int e = (64 * w + lane) % (16 * NB);
-      ksw[w] = fmaf(p.c.KS[base * NB + e], scale, poison);
-      vsw[w] = p.c.VS[base * NB + e] + poison;
+      ksw[w] = p.c.KS[base * NB + e];
+      vsw[w] = p.c.VS[base * NB + e];
     }
   };
   auto lay = [&](int buf) {
@@ -850,7 +1178,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       constexpr int b = decltype(b_)::value;
       v4u x;
 #pragma unroll
-      for (int jl = 0; jl < 4; ++jl) x[jl] = pair_q<QHALF>(kw[jl * VW + b / 2], b % 2);
+      for (int jl = 0; jl < 4; ++jl) x[jl] = pair_f16(kw[jl * VW + b / 2], b % 2);
       lds.k[buf][wave][b][lane] = x;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -862,6 +1190,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
     });
 #pragma unroll
     for (int w = 0; w < SPL; ++w) {
+      ksw[w] = fmaf(ksw[w], scale, poison);
+      vsw[w] += poison;
       const uint64_t gone = __ballot(64 * w + lane < 16 * NB && !finite(vsw[w]));
       if (lane == 0) lds.gone[buf][wave][w] = gone;
       if (64 * w + lane < 16 * NB) {
@@ -876,7 +1206,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
     // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
     v4u qf[RT][NB][QP];
     v4f acc[RT][NB][2];
-    float m[RT], l[RT];
+    float m[RT], l[RT], undo[RT];
     int index[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -884,7 +1214,9 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       const int tok = rho / h.sub_heads;
       const bool in = rho < h.rows;
       index[rt] = h.i0 + min(tok, h.tokens - 1);
-      load_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, c, in, qf[rt]);
+      QueryRow<T, DIM> q;
+      fetch_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q);
+      undo[rt] = cut_query<T, DIM>(q, in, qf[rt]);
       m[rt] = -INFINITY;
       l[rt] = 0.f;
 #pragma unroll
@@ -914,7 +1246,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
           for (int rt = 0; rt < NRT; ++rt) {
             v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = QP - 1; q >= 0; --q) x = mfma_q<QHALF>(a[n % 2], qf[rt][b][q], x);
+            for (int q = QP - 1; q >= 0; --q) x = mfma_f16(a[n % 2], qf[rt][b][q], x);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               s[rt][4 * kt + i] = b == 0 ? ks[n % 2][i] * x[i] : fmaf(ks[n % 2][i], x[i], s[rt][4 * kt + i]);
@@ -942,7 +1274,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      weigh<NRT, 16, NB>(s, m, l, acc);
+      weigh<NRT, 16, NB, 1>(s, undo, m, l, acc);
       {
         v4u a[2][2];
         v4f vs[2][2];
@@ -1007,16 +1339,14 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 
     if (!h.seq.bad) {
       const int last = h.keys - 1;
-      const int begin = h.k0 * kAttnUnit;
-      const int end = min(h.k1 * kAttnUnit, h.keys);
-      float poison;
-      int64_t base = half_base(p, h.pages, begin + 16 * wave, last, h.kvh, poison);
-      load(base, poison);
+      const int begin = h.k0 << p.unit_shift;
+      const int end = min(h.k1 << p.unit_shift, h.keys);
+      auto load_at = [&](int at) {
+        load(token_row(p, keys_at(p, h.pages, at + 16 * wave, last), h.kvh, poison));
+      };
+      load_at(begin);
       lay(0);
-      if (begin + kWideKeys < end) {
-        base = half_base(p, h.pages, begin + kWideKeys + 16 * wave, last, h.kvh, poison);
-        load(base, poison);
-      }
+      if (begin + kWideKeys < end) load_at(begin + kWideKeys);
       __syncthreads();
       auto steps = [&](auto nrt_) {
         for (int at = begin; at < end; at += kWideKeys) {
@@ -1025,10 +1355,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
           if constexpr (BUFS == 1) __syncthreads();
           if (at + kWideKeys < end) {
             lay(BUFS == 2 ? buf ^ 1 : 0);
-            if (at + 2 * kWideKeys < end) {
-              base = half_base(p, h.pages, at + 2 * kWideKeys + 16 * wave, last, h.kvh, poison);
-              load(base, poison);
-            }
+            if (at + 2 * kWideKeys < end) load_at(at + 2 * kWideKeys);
           }
           __syncthreads();
         }
@@ -1072,82 +1399,94 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 
 // ---------------------------------------------------------------- joining the parts
 
-// Workgroup (w, y): the split item that workgroup w began, rows 4 y .. 4 y + 3
-// (one per wave); parts are taken in key order, several in flight.
+// Workgroup (w, y): the split item that workgroup w began, a row per wave and
+// turn; parts are taken in key order.
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;
   const AttnItem it = p.items[blockIdx.x];
   if (!it.valid) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int rho = blockIdx.y * kWaves + wave;
-  if (rho >= it.tokens * it.heads) return;
   constexpr int PER = DIM / 64;  // channels per lane
   const int64_t size = attn_slot_floats(slot_rows, DIM);
   const int first = blockIdx.x, parts = it.last - first + 1;
   // Contributor k: the first one's slot 1, then slot 0 of the following ones.
   const float *base = p.partial + (2 * (int64_t)first + 1) * size;
   auto part = [&](int k) { return k == 0 ? base : p.partial + 2 * (int64_t)(first + k) * size; };
-  // The largest maximum, then every part's factor, a lane per part.
-  float top = -INFINITY;
-  for (int k = lane; k < parts; k += 64) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
+  for (int rho = blockIdx.y * kWaves + wave; rho < it.tokens * it.heads; rho += gridDim.y * kWaves) {
+    // The largest maximum, then every part's factor, a lane per part.
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 64) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float from = top == -INFINITY ? 0.f : top;
-  float weight = 0.f, x[PER] = {};
-  for (int k0 = 0; k0 < parts; k0 += 64) {
-    float f = 0.f, wt = 0.f;
-    if (k0 + lane < parts) {
-      const float *s = part(k0 + lane) + (int64_t)slot_rows * DIM + rho;
-      f = __builtin_amdgcn_exp2f(s[0] - from);
-      wt = f * s[slot_rows];
-    }
-    const int n = min(64, parts - k0);
-    for (int k = 0; k < n; ++k) {
-      const float g = __shfl(f, k);
-      weight += __shfl(wt, k);
-      const float *s = part(k0 + k) + (int64_t)rho * DIM + lane * PER;
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float from = top == -INFINITY ? 0.f : top;
+    float weight = 0.f, x[PER] = {};
+    for (int k0 = 0; k0 < parts; k0 += 64) {
+      float f = 0.f, wt = 0.f;
+      if (k0 + lane < parts) {
+        const float *s = part(k0 + lane) + (int64_t)slot_rows * DIM + rho;
+        f = __builtin_amdgcn_exp2f(s[0] - from);
+        wt = f * s[slot_rows];
+      }
+      const int n = min(64, parts - k0);
+      // Four parts' rows in flight; past the last one the last one again, with no weight.
+      for (int k = 0; k < n; k += 4) {
+        Run<float, PER> y[4];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] += g * s[i];
+        for (int u = 0; u < 4; ++u)
+          y[u] = *reinterpret_cast<const Run<float, PER> *>(part(k0 + min(k + u, n - 1)) + (int64_t)rho * DIM + lane * PER);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (k + u >= n) break;
+          const float g = __shfl(f, k + u);
+          weight += __shfl(wt, k + u);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) x[i] += g * y[u].x[i];
+        }
+      }
     }
+    const int tok = rho / it.heads;
+    const int64_t t = it.row0 + tok;
+    bool nothing = false;
+    if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, it.context, it.seq_new, t);
+    const float scale = 1.f / weight;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = nothing ? 0.f : x[i] * scale;
+    store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
   }
-  const int tok = rho / it.heads;
-  const int64_t t = it.row0 + tok;
-  bool nothing = false;
-  if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, it.context, it.seq_new, t);
-  const float scale = 1.f / weight;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) x[i] = nothing ? 0.f : x[i] * scale;
-  store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
 }
 
-template <RowType T, int DIM, int RT, bool WIDE>
+template <RowType T, int DIM, int ROWS>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
-  if constexpr (WIDE)
-    hipLaunchKernelGGL((attention_wide_kernel<T, DIM, RT>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  if constexpr (ROWS >= 64)
+    hipLaunchKernelGGL((attention_wide_kernel<T, DIM, ROWS / 64>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  else if (ROWS <= 16 && a.items == nullptr)
+    hipLaunchKernelGGL((attention_kernel<T, DIM, ROWS, ROWS <= 16 ? 8 : 4>), dim3((unsigned)wgs), dim3(512), 0, stream, a);
   else
-    hipLaunchKernelGGL((attention_kernel<T, DIM, RT>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attention_kernel<T, DIM, ROWS, 4>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  constexpr int rows = (WIDE ? 64 : 16) * RT;
-  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, rows / kWaves), dim3(kThreads), 0, stream, a,
-                     rows);
+  if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
+  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, ROWS >= 32 ? 8 : ROWS >= 16 ? 4 : ROWS / kWaves),
+                     dim3(kThreads), 0, stream, a, ROWS);
   return hipGetLastError();
 }
 
 template <RowType T, int DIM>
 hipError_t launch_rows(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
-  constexpr int most = attn_max_rows(T, DIM);
-  if (rows == 16) return launch_instance<T, DIM, 1, false>(a, wgs, stream);
+  if constexpr (DIM <= 128) {
+    if (rows == 4) return launch_instance<T, DIM, 4>(a, wgs, stream);
+    if (rows == 8) return launch_instance<T, DIM, 8>(a, wgs, stream);
+  }
+  if (rows == 16) return launch_instance<T, DIM, 16>(a, wgs, stream);
   if constexpr (attn_direct_rows(DIM) == 32)
-    if (rows == 32) return launch_instance<T, DIM, 2, false>(a, wgs, stream);
-  if (rows == 64) return launch_instance<T, DIM, 1, true>(a, wgs, stream);
-  if constexpr (most == 128)
-    if (rows == 128) return launch_instance<T, DIM, 2, true>(a, wgs, stream);
+    if (rows == 32) return launch_instance<T, DIM, 32>(a, wgs, stream);
+  if (rows == 64) return launch_instance<T, DIM, 64>(a, wgs, stream);
+  if constexpr (attn_max_rows(T, DIM) == 128)
+    if (rows == 128) return launch_instance<T, DIM, 128>(a, wgs, stream);
   return hipErrorInvalidValue;
 }
 
-// rows: of an item, 16, 32, 64 or 128.
+// rows: of an item, a power of two from 4 to 128.
 template <RowType T>
 hipError_t launch_attention(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
   switch (a.c.dim) {
