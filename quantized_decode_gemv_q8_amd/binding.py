@@ -377,28 +377,35 @@ class Q8Cache:
             raise TypeError("k must be a torch.Tensor")
         if k.dim() != 4:
             raise ValueError(f"k must be rank 4, got {k.dim()} dimensions")
-        pages, heads, page_size, dim = k.shape
+        codes = k.shape
+        pages, heads, page_size, dim = codes
         if dim not in (64, 128, 256):
             raise ValueError(f"dim must be 64, 128 or 256, got {dim}")
         if page_size not in (16, 32, 64, 128, 256, 512, 1024):
             raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
-        device, scales = k.device, (pages, heads, page_size, dim // BLOCK)
-        for name, t, dtype, shape in (("k", k, torch.int8, k.shape), ("k_scale", k_scale, torch.float32, scales),
-                                      ("v", v, torch.int8, k.shape), ("v_scale", v_scale, torch.float32, scales)):
+        scales, device = (pages, heads, page_size, dim // BLOCK), k.device
+        for name, t, dtype, shape in (("k", k, torch.int8, codes), ("k_scale", k_scale, torch.float32, scales),
+                                      ("v", v, torch.int8, codes), ("v_scale", v_scale, torch.float32, scales)):
             _check_tensor(name, t, dtype, shape)
-            if t.device != device:
+            if t.get_device() != device.index:
                 raise ValueError("all tensors must be on one device")
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
         self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, dim, device
-        at = k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr()
-        codes = pages * heads * page_size * dim
-        self._spans = tuple((a, a + n) for a, n in zip(at, (codes, codes // 8) * 2))
+        n = pages * heads * page_size * dim
+        a, b, c, d = at = k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr()
+        self._spans = (a, a + n), (b, b + n // 8), (c, c + n), (d, d + n // 8)
         edge = 0
         for a, b in sorted(self._spans):
-            if a < edge and codes:
+            if a < edge and n:
                 raise ValueError("the cache's tensors overlap")
             edge = b
         self._struct = _CacheStruct(*at, pages, heads, page_size, dim)
+
+    def _apart(self, name, a, b):
+        """Refuses a tensor of a call (bytes a .. b - 1) that shares any with the cache."""
+        for c, d in self._spans:
+            if a < d and c < b:
+                raise ValueError(f"{name} overlaps the cache")
 
     @classmethod
     def empty(cls, pages, heads, page_size, dim, device="cuda"):
@@ -413,16 +420,17 @@ def _cache_seqs(cache, table, lengths, offsets):
     """The checked descriptor of a call's sequences."""
     if not isinstance(cache, Q8Cache):
         raise TypeError("cache must be a Q8Cache")
+    index, i32 = cache.device.index, torch.int32
     for name, t, rank in (("table", table, 2), ("lengths", lengths, 1), ("offsets", offsets, 1)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != torch.int32:
+        if t.dtype is not i32:
             raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
-        if t.device != cache.device:
+        if t.get_device() != index and t.device != cache.device:
             raise ValueError("all tensors must be on one device")
         if t.dim() != rank:
             raise ValueError(f"{name} must be rank {rank}, got {t.dim()} dimensions")
-        if t.stride(-1) != 1 and t.numel():
+        if not t.is_contiguous() and t.numel() and t.stride(-1) != 1:
             raise ValueError(f"{name} must be contiguous in its last dimension")
     n, pages = table.shape
     if lengths.shape[0] != n or offsets.shape[0] != n + 1:
@@ -434,14 +442,22 @@ def _cache_seqs(cache, table, lengths, offsets):
     return _SeqsStruct(table.data_ptr(), lengths.data_ptr(), offsets.data_ptr(), n, pages, stride)
 
 
+def _seqs_spans(seqs):
+    """Names and bytes of a descriptor's tensors."""
+    n, t, l, o = seqs.seqs, seqs.table or 0, seqs.lengths or 0, seqs.offsets or 0
+    return (("table", t, t + 4 * ((n - 1) * seqs.table_stride + seqs.max_pages) if n else t),
+            ("lengths", l, l + 4 * n), ("offsets", o, o + 4 * n + 4))
+
+
 def _cache_rows(name, t, rows, heads, cache, dtype=None):
-    """Checks a row tensor [rows, heads, dim]: rows may be apart, a row is dense.  Returns its row stride."""
+    """Checks a row tensor [rows, heads, dim]: rows may be apart, a row is dense.
+    Returns its row stride and the address of its first byte."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
         want = dtype if dtype is not None else "float32, bfloat16 or float16"
         raise ValueError(f"{name} must be {want}, got {t.dtype}")
-    if t.device != cache.device:
+    if t.get_device() != cache.device.index and t.device != cache.device:
         raise ValueError("all tensors must be on one device")
     shape = t.shape
     if len(shape) != 3 or shape[2] != cache.dim or (rows is not None and shape[0] != rows) or \
@@ -449,14 +465,14 @@ def _cache_rows(name, t, rows, heads, cache, dtype=None):
         raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, "
                          f"{'heads' if heads is None else heads}, {cache.dim}), got {tuple(shape)}")
     n, h, dim = shape
-    if n == 0 or h == 0:
-        return h * dim
+    if n == 0 or h == 0 or t.is_contiguous():
+        return h * dim, t.data_ptr()
     s0, s1, s2 = t.stride()
     if s2 != 1 or (h > 1 and s1 != dim):
         raise ValueError(f"{name} must be dense in its last two dimensions")
     if n > 1 and s0 < h * dim:
         raise ValueError(f"rows of {name} must not overlap")
-    return s0
+    return s0, t.data_ptr()
 
 
 def _span(t):
@@ -478,15 +494,6 @@ def _check_apart(out_name, out, others):
         b0, b1 = _span(t)
         if a0 < b1 and b0 < a1 and not _interleaved(out, t):
             raise ValueError(f"{out_name} overlaps {name}")
-
-
-def _check_outside(cache, *tensors):
-    """No tensor (pairs of a name and a tensor) of a call shares a byte with the cache."""
-    (a0, a1), (b0, b1), (c0, c1), (d0, d1) = cache._spans
-    for name, t in tensors:
-        p, q = _span(t)
-        if (p < a1 and a0 < q) or (p < b1 and b0 < q) or (p < c1 and c0 < q) or (p < d1 and d0 < q):
-            raise ValueError(f"{name} overlaps the cache")
 
 
 def _interleaved(a, b):
@@ -526,11 +533,17 @@ def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
     newest offsets[b+1] - offsets[b] tokens of lengths[b] are rows offsets[b]
     .. of k and v, and live in the pages table[b]."""
     seqs = _cache_seqs(cache, table, lengths, offsets)
-    ks = _cache_rows("k", k, None, cache.heads, cache)
-    vs = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
-    _check_outside(cache, ("k", k), ("v", v), ("table", table), ("lengths", lengths), ("offsets", offsets))
-    _call(cache, stream, "q8_cache_write", load().q8_cache_write, cache._struct, k.data_ptr(), v.data_ptr(),
-          _ROW_TYPES[k.dtype], k.shape[0], ks, vs, seqs)
+    ks, k0 = _cache_rows("k", k, None, cache.heads, cache)
+    vs, v0 = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
+    rows, size = k.shape[0], k.element_size()
+    width = cache.heads * cache.dim
+    if rows:
+        cache._apart("k", k0, k0 + ((rows - 1) * ks + width) * size)
+        cache._apart("v", v0, v0 + ((rows - 1) * vs + width) * size)
+    for name, a, b in _seqs_spans(seqs):
+        cache._apart(name, a, b)
+    _call(cache, stream, "q8_cache_write", load().q8_cache_write, cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks,
+          vs, seqs)
 
 
 def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
@@ -538,25 +551,26 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
     [rows, heads, dim] of dtype; returns (k, v).  Rows of no sequence keep what
     the given k and v hold (new tensors: undefined)."""
     seqs = _cache_seqs(cache, table, lengths, offsets)
-    shape = (int(rows), cache.heads, cache.dim)
-    given = k is not None or v is not None
-    if not given or k is None or v is None:
+    rows = int(rows)
+    shape = (rows, cache.heads, cache.dim)
+    if k is None and v is None:
         if dtype not in _ROW_TYPES:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-        if k is None:
-            k = _empty_on(stream, shape, dtype, cache.device)
-        if v is None:
-            v = _empty_on(stream, shape, dtype, cache.device)
-    ks = vs = cache.heads * cache.dim
-    if given:
-        ks = _cache_rows("k", k, shape[0], cache.heads, cache)
-        vs = _cache_rows("v", v, shape[0], cache.heads, cache, k.dtype)
-        _check_outside(cache, ("k", k), ("v", v))
+        k, v = _empty_on(stream, (2,) + shape, dtype, cache.device).unbind()
+        ks = vs = cache.heads * cache.dim
+        k0, v0 = k.data_ptr(), v.data_ptr()
+    elif k is None or v is None:
+        raise ValueError("pass both k and v, or neither")
+    else:
+        ks, k0 = _cache_rows("k", k, rows, cache.heads, cache)
+        vs, v0 = _cache_rows("v", v, rows, cache.heads, cache, k.dtype)
         inputs = (("table", table), ("lengths", lengths), ("offsets", offsets))
+        cache._apart("k", *_span(k))
+        cache._apart("v", *_span(v))
         _check_apart("k", k, inputs)
         _check_apart("v", v, inputs + (("k", k),))
-    _call(cache, stream, "q8_cache_read", load().q8_cache_read, cache._struct, k.data_ptr(), v.data_ptr(),
-          _ROW_TYPES[k.dtype], shape[0], ks, vs, seqs)
+    _call(cache, stream, "q8_cache_read", load().q8_cache_read, cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks, vs,
+          seqs)
     return k, v
 
 
@@ -572,7 +586,9 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
     _check_tensor("keep", keep, torch.int32, (table.shape[0], keep.shape[1]))
     if keep.device != cache.device:
         raise ValueError("all tensors must be on one device")
-    _check_outside(cache, ("keep", keep), ("table", table), ("lengths", lengths), ("offsets", offsets))
+    cache._apart("keep", *_span(keep))
+    for name, a, b in _seqs_spans(seqs):
+        cache._apart(name, a, b)
     _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(),
           keep.shape[1])
 
@@ -592,7 +608,7 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
     (a new out: undefined); rows that see nothing are zeros.
     """
     seqs = _cache_seqs(cache, table, lengths, offsets)
-    qs = _cache_rows("q", q, None, None, cache)
+    qs, q0 = _cache_rows("q", q, None, None, cache)
     rows, q_heads = q.shape[0], q.shape[1]
     if q_heads == 0 or q_heads % cache.heads:
         raise ValueError(f"the heads of q must be a multiple of the cache's {cache.heads}, got {q_heads}")
@@ -610,10 +626,10 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
         alpha = cache.dim ** -0.5
     if out is None:
         out = _empty_on(stream, (rows, q_heads, cache.dim), q.dtype, cache.device)
-        os_ = q_heads * cache.dim
+        os_, out0 = q_heads * cache.dim, out.data_ptr()
     else:
-        os_ = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
-        _check_outside(cache, ("out", out))
+        os_, out0 = _cache_rows("out", out, rows, q_heads, cache, q.dtype)
+        cache._apart("out", *_span(out))
         _check_apart("out", out, (("q", q), ("table", table), ("lengths", lengths), ("offsets", offsets),
                                   ("tree", tree)))
     need = _attention_workspace(cache, _ROW_TYPES[q.dtype], rows, q_heads, seqs)
@@ -621,7 +637,7 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
     mask = None
     if tree is not None:  # an empty tree still is one: no new token is seen
         mask = tree.data_ptr() if words and rows else offsets.data_ptr() & -8
-    _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q.data_ptr(), out.data_ptr(),
+    _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q0, out0,
           _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha), work, need)
     return out
 

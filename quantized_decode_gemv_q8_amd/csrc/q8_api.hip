@@ -805,8 +805,10 @@ struct AttnPlan {
 // workgroup takes all keys of an item, and the second launch that joins parts
 // is saved.
 constexpr int64_t kAttnWholeTokens = 1024;
-// What an item costs besides its keys (its query, its first loads' latency and
-// its sums' way out), in units of kAttnStep keys, when work is dealt out.
+// What an item of few rows costs besides its keys (its query, its first loads'
+// latency and its sums' way out), in units of kAttnStep keys, when work is
+// dealt out.  A batch of 32 sequences of 1 .. 8192 keys takes 92 us at 0, 82 at
+// 1, 73 at 2 and 75 at 3 and 4; with many rows a unit takes so long that 0 is best.
 constexpr int kAttnItemCost = 2;
 
 AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens,
@@ -829,7 +831,7 @@ AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows
   p.split = max_tokens > kAttnWholeTokens || tile > 16;
   p.unit_shift = __builtin_ctz((unsigned)(p.split ? q8::kAttnStep : kAttnWholeTokens));
   const int64_t units = p.split ? ceil_div(max_tokens, q8::kAttnStep) : 1;
-  p.item_cost = p.split ? kAttnItemCost : 0;
+  p.item_cost = p.split && tile < 64 ? kAttnItemCost : 0;
   p.few_units = items <= (kIndexLimit - 1) / (units + p.item_cost);
   p.wgs = (int64_t)cus * q8::attn_wgs_per_cu(type, dim, tile);
   if (items < p.wgs && items * units < p.wgs) p.wgs = items * units;
@@ -1016,6 +1018,7 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
   a.items = pl.split ? reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256) : nullptr;
   a.unit_shift = pl.unit_shift;
+  a.half_rows = pl.tile == 128 ? 64 : 0;
   a.item_cost = pl.item_cost;
   a.few_units = pl.few_units;
   if (log_debug())

@@ -36,6 +36,7 @@ struct AttnArgs {
   int tile_tokens;  // tokens (rows of q) per item
   float alpha;
   int unit_shift;    // log2 of the keys of a unit of work, a multiple of kAttnStep
+  int half_rows;     // items of at most this many rows have units of twice the keys (0: none)
   int item_cost;     // units that an item is charged besides its keys
   int few_units;     // the units of all items are sure to stay below 2^31
   float *partial;    // 2 * gridDim.x slots of attn_slot_floats(rows, dim)

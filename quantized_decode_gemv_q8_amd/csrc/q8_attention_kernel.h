@@ -216,30 +216,47 @@ __device__ __forceinline__ int item_keys(const AttnArgs &p, const Seq &q, int r)
   if (p.tree != nullptr) return q.length;
   return q.length - q.n + min(q.n, (r + 1) * p.tile_tokens);
 }
+__device__ __forceinline__ int row_items(const AttnArgs &p, const Seq &q) {
+  return (q.n + p.tile_tokens - 1) / p.tile_tokens;
+}
+// log2 of the keys of a unit: those of an item that leaves half of a wide
+// kernel's row tiles empty are twice as long, so that units cost about the same.
+__device__ __forceinline__ int item_shift(const AttnArgs &p, const Seq &q, int r) {
+  return p.unit_shift + (p.half_rows > 0 && min(p.tile_tokens, q.n - r * p.tile_tokens) * p.sub_heads <= p.half_rows);
+}
 // Units of an item: those of its keys, after p.item_cost that stand for what an
 // item costs whatever its length.
 __device__ __forceinline__ int item_units(const AttnArgs &p, const Seq &q, int r) {
   if (q.bad) return 1 + p.item_cost;
-  const int u = (item_keys(p, q, r) + (1 << p.unit_shift) - 1) >> p.unit_shift;
+  const int shift = item_shift(p, q, r);
+  const int u = (item_keys(p, q, r) + (1 << shift) - 1) >> shift;
   return (u < 1 ? 1 : u) + p.item_cost;
-}
-__device__ __forceinline__ int row_items(const AttnArgs &p, const Seq &q) {
-  return (q.n + p.tile_tokens - 1) / p.tile_tokens;
 }
 // Units of a sequence's items for one head (and sub-group of heads).
 __device__ __forceinline__ int64_t head_units(const AttnArgs &p, const Seq &q) {
   const int items = row_items(p, q);
-  if (items <= 1 || p.tree != nullptr || q.bad) return items == 0 ? 0 : (int64_t)items * item_units(p, q, items - 1);
+  if (items == 0) return 0;
+  if (items == 1 || p.tree != nullptr || q.bad)  // all items but the last are alike
+    return (int64_t)(items - 1) * item_units(p, q, 0) + item_units(p, q, items - 1);
   int64_t u = 0;
   for (int r = 0; r < items; ++r) u += item_units(p, q, r);
   return u;
 }
 
-// a / b for a >= 0, b > 0: the usual small numbers without a 64-bit division
-// (over a hundred instructions).
+// a / b for a >= 0, b > 0 and quotients below 2^50: the double's quotient is off
+// by at most one (a 64-bit integer division is over a hundred instructions).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
+  const double d = (double)b;
+  double x = __builtin_amdgcn_rcp(d);  // some 24 bits, doubled by each step
+  x = fma(fma(-d, x, 1.0), x, x);
+  x = fma(fma(-d, x, 1.0), x, x);
+  int64_t q = (int64_t)((double)a * x);
+  int64_t rest = a - q * b;
+  if (rest < 0) {
+    --q;
+    rest += b;
+  }
+  return rest >= b ? q + 1 : q;
 }
 
 struct Run0 {  // where a workgroup's run begins
@@ -866,6 +883,7 @@ struct Share {
   int keys;              // keys the item's rows may see
   int all;               // keys that all of its rows see
   int k0, k1;
+  int shift;             // log2 of the keys of a unit
   bool whole;            // all of the item's units
   float *slot;           // where the sums go otherwise
 };
@@ -891,7 +909,7 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
     int64_t rest = run.rest - vh * per_head;
     if (p.tree != nullptr || h.seq.bad) {
       const int u = item_units(p, h.seq, 0);
-      r = (int)quotient(rest, u);
+      r = min((int)quotient(rest, u), row_items(p, h.seq) - 1);
       h.k0 = (int)(rest - (int64_t)r * u);
     } else {
       r = 0;
@@ -908,6 +926,7 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
     h.k0 = max(v0 - p.item_cost, 0);
     h.k1 = max(v1 - p.item_cost, 0);
     h.whole = h.k0 == 0 && v1 == units;
+    h.shift = item_shift(p, h.seq, r);
     h.kvh = vh / p.subs;
     const int sub = vh - h.kvh * p.subs;
     h.sub_heads = min(p.sub_heads, p.group - sub * p.sub_heads);
@@ -1007,8 +1026,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? attn_wgs_per_cu(T, DIM, RO
       fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, a.c, q[rt]);
     }
     const int last = h.keys - 1;
-    const int begin = (h.k0 << p.unit_shift) + wave * kAttnTile;
-    const int end = h.seq.bad ? 0 : min(h.k1 << p.unit_shift, h.keys);
+    const int begin = (h.k0 << h.shift) + wave * kAttnTile;
+    const int end = h.seq.bad ? 0 : min(h.k1 << h.shift, h.keys);
     Keys16 keys[2];  // a page's number is read one tile before the page
     int64_t base[2];
     float poison[2];
@@ -1339,8 +1358,8 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
 
     if (!h.seq.bad) {
       const int last = h.keys - 1;
-      const int begin = h.k0 << p.unit_shift;
-      const int end = min(h.k1 << p.unit_shift, h.keys);
+      const int begin = h.k0 << h.shift;
+      const int end = min(h.k1 << h.shift, h.keys);
       auto load_at = [&](int at) {
         load(token_row(p, keys_at(p, h.pages, at + 16 * wave, last), h.kvh, poison));
       };

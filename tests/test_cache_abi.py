@@ -157,10 +157,10 @@ def test_row_tensors_are_checked():
     class Fake:
         device, dim, heads = torch.device("cpu"), 64, 2
     good = torch.zeros((5, 2, 64))
-    assert binding._cache_rows("k", good, 5, 2, Fake) == 128
+    assert binding._cache_rows("k", good, 5, 2, Fake) [0] == 128
     wide = torch.zeros((5, 300))[:, 3:131].unflatten(1, (2, 64))
-    assert binding._cache_rows("k", wide, 5, 2, Fake) == 300
-    assert binding._cache_rows("k", good[:0], 0, 2, Fake) == 128
+    assert binding._cache_rows("k", wide, 5, 2, Fake)[0] == 300
+    assert binding._cache_rows("k", good[:0], 0, 2, Fake)[0] == 128
     with pytest.raises(TypeError):
         binding._cache_rows("k", [1], None, 2, Fake)
     with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
