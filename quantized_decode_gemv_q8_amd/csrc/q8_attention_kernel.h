@@ -1222,20 +1222,32 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
   };
 
   walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
+    // The first step's codes are asked for before the query's rows are needed.
+    const int last = h.keys - 1;
+    const int begin = h.k0 << h.shift;
+    const int end = h.seq.bad ? begin : min(h.k1 << h.shift, h.keys);
+    auto load_at = [&](int at) {
+      load(token_row(p, keys_at(p, h.pages, at + 16 * wave, last), h.kvh, poison));
+    };
     // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
     v4u qf[RT][NB][QP];
     v4f acc[RT][NB][2];
     float m[RT], l[RT], undo[RT];
     int index[RT];
+    bool in[RT];
+    QueryRow<T, DIM> q[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int rho = 16 * (4 * rt + wave) + row;
       const int tok = rho / h.sub_heads;
-      const bool in = rho < h.rows;
+      in[rt] = rho < h.rows;
       index[rt] = h.i0 + min(tok, h.tokens - 1);
-      QueryRow<T, DIM> q;
-      fetch_query<T, DIM>(p, h.seq.start + index[rt], in ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q);
-      undo[rt] = cut_query<T, DIM>(q, in, qf[rt]);
+      fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q[rt]);
+    }
+    if (begin < end) load_at(begin);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      undo[rt] = cut_query<T, DIM>(q[rt], in[rt], qf[rt]);
       m[rt] = -INFINITY;
       l[rt] = 0.f;
 #pragma unroll
@@ -1356,14 +1368,7 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
       }
     };
 
-    if (!h.seq.bad) {
-      const int last = h.keys - 1;
-      const int begin = h.k0 << h.shift;
-      const int end = min(h.k1 << h.shift, h.keys);
-      auto load_at = [&](int at) {
-        load(token_row(p, keys_at(p, h.pages, at + 16 * wave, last), h.kvh, poison));
-      };
-      load_at(begin);
+    if (begin < end) {
       lay(0);
       if (begin + kWideKeys < end) load_at(begin + kWideKeys);
       __syncthreads();
@@ -1418,8 +1423,8 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
 
 // ---------------------------------------------------------------- joining the parts
 
-// Workgroup (w, y): the split item that workgroup w began, a row per wave and
-// turn; parts are taken in key order.
+// Workgroup (w, y): the split item that workgroup w began, rows 4 y .. 4 y + 3,
+// one per wave; parts are taken in key order.
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;
@@ -1432,47 +1437,47 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, in
   // Contributor k: the first one's slot 1, then slot 0 of the following ones.
   const float *base = p.partial + (2 * (int64_t)first + 1) * size;
   auto part = [&](int k) { return k == 0 ? base : p.partial + 2 * (int64_t)(first + k) * size; };
-  for (int rho = blockIdx.y * kWaves + wave; rho < it.tokens * it.heads; rho += gridDim.y * kWaves) {
-    // The largest maximum, then every part's factor, a lane per part.
-    float top = -INFINITY;
-    for (int k = lane; k < parts; k += 64) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
+  const int rho = blockIdx.y * kWaves + wave;
+  if (rho >= it.tokens * it.heads) return;
+  // The largest maximum, then every part's factor, a lane per part.
+  float top = -INFINITY;
+  for (int k = lane; k < parts; k += 64) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float from = top == -INFINITY ? 0.f : top;
-    float weight = 0.f, x[PER] = {};
-    for (int k0 = 0; k0 < parts; k0 += 64) {
-      float f = 0.f, wt = 0.f;
-      if (k0 + lane < parts) {
-        const float *s = part(k0 + lane) + (int64_t)slot_rows * DIM + rho;
-        f = __builtin_amdgcn_exp2f(s[0] - from);
-        wt = f * s[slot_rows];
-      }
-      const int n = min(64, parts - k0);
-      // Four parts' rows in flight; past the last one the last one again, with no weight.
-      for (int k = 0; k < n; k += 4) {
-        Run<float, PER> y[4];
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float from = top == -INFINITY ? 0.f : top;
+  float weight = 0.f, x[PER] = {};
+  for (int k0 = 0; k0 < parts; k0 += 64) {
+    float f = 0.f, wt = 0.f;
+    if (k0 + lane < parts) {
+      const float *s = part(k0 + lane) + (int64_t)slot_rows * DIM + rho;
+      f = __builtin_amdgcn_exp2f(s[0] - from);
+      wt = f * s[slot_rows];
+    }
+    const int n = min(64, parts - k0);
+    // Four parts' rows in flight; past the last one the last one again, with no weight.
+    for (int k = 0; k < n; k += 4) {
+      Run<float, PER> y[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          y[u] = *reinterpret_cast<const Run<float, PER> *>(part(k0 + min(k + u, n - 1)) + (int64_t)rho * DIM + lane * PER);
+      for (int u = 0; u < 4; ++u)
+        y[u] = *reinterpret_cast<const Run<float, PER> *>(part(k0 + min(k + u, n - 1)) + (int64_t)rho * DIM + lane * PER);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (k + u >= n) break;
-          const float g = __shfl(f, k + u);
-          weight += __shfl(wt, k + u);
+      for (int u = 0; u < 4; ++u) {
+        if (k + u >= n) break;
+        const float g = __shfl(f, k + u);
+        weight += __shfl(wt, k + u);
 #pragma unroll
-          for (int i = 0; i < PER; ++i) x[i] += g * y[u].x[i];
-        }
+        for (int i = 0; i < PER; ++i) x[i] += g * y[u].x[i];
       }
     }
-    const int tok = rho / it.heads;
-    const int64_t t = it.row0 + tok;
-    bool nothing = false;
-    if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, it.context, it.seq_new, t);
-    const float scale = 1.f / weight;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = nothing ? 0.f : x[i] * scale;
-    store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
   }
+  const int tok = rho / it.heads;
+  const int64_t t = it.row0 + tok;
+  bool nothing = false;
+  if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, it.context, it.seq_new, t);
+  const float scale = 1.f / weight;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = nothing ? 0.f : x[i] * scale;
+  store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
 }
 
 template <RowType T, int DIM, int ROWS>
@@ -1485,7 +1490,7 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
     hipLaunchKernelGGL((attention_kernel<T, DIM, ROWS, 4>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
-  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, ROWS >= 32 ? 8 : ROWS >= 16 ? 4 : ROWS / kWaves),
+  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, ROWS / kWaves),
                      dim3(kThreads), 0, stream, a, ROWS);
   return hipGetLastError();
 }
