@@ -53,21 +53,25 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 template <RowType T>
 struct AttnElem;
-// kQParts f16 parts of a query, kPParts bf16 parts of a weight.
+// kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalf: with
+// many rows, one f16 part instead, which is 8 times finer than a bf16 output.
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
   static constexpr int kQParts = 2, kPParts = 3;
+  static constexpr bool kHalf = false;
 };
 template <>
 struct AttnElem<kRowBf16> {
   typedef __bf16 type;
   static constexpr int kQParts = 1, kPParts = 2;
+  static constexpr bool kHalf = true;
 };
 template <>
 struct AttnElem<kRowF16> {
   typedef _Float16 type;
   static constexpr int kQParts = 1, kPParts = 2;
+  static constexpr bool kHalf = false;
 };
 
 template <typename E, int N>
@@ -417,7 +421,10 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
-template <int NRT, int NK, int NB, int PACK>
+// HALF: for weights that go to f16 as they are.  They are kept 2^5 larger and
+// the maximum closer, so that with a scale below 2^7 they stay below 2^15.
+constexpr float kHalfSlack = 3.f, kHalfRaise = 5.f;
+template <int NRT, int NK, int NB, int PACK, bool HALF = false>
 __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   float top[NRT];
   bool above = false;
@@ -427,7 +434,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 #pragma unroll
     for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
     top[rt] = row_max<PACK>(top[rt]) * undo[rt];
-    above |= top[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
+    above |= top[rt] > m[rt] + (HALF ? kHalfSlack : kMaxSlack);  // the first key that is seen, too
   }
   if (__ballot(above) != 0) {
 #pragma unroll
@@ -444,7 +451,8 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
   }
 #pragma unroll
   for (int rt = 0; rt < NRT; ++rt) {
-    const float from = m[rt] == -INFINITY ? 0.f : m[rt];  // nothing seen yet: weights are exp2(-inf) = 0
+    // Nothing seen yet: weights are exp2(-inf) = 0.
+    const float from = (m[rt] == -INFINITY ? 0.f : m[rt]) - (HALF ? kHalfRaise : 0.f);
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
@@ -459,6 +467,24 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 // compiler spreads one step's operands over all steps and runs out of registers.
 __device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
+
+// Two floats as f16, cut: exact for codes.
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+}
+// Eight floats as f16, rounded to the nearest.
+__device__ __forceinline__ v4u round_half(const float (&x)[8]) {
+  v4u y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2h h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
+    y[i] = __builtin_bit_cast(uint32_t, h);
+  }
+  return y;
+}
+// Value scales that f16 weights allow: at 2^-8 and 2^7 a weight of 2^8 still
+// has all its bits and stays below 2^15, one of 2^-6 has all its bits.
+__device__ __forceinline__ bool in_window(float s) { return s == 0.f || (s >= 0x1p-8f && s <= 0x1p7f); }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
@@ -1149,7 +1175,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? attn_wgs_per_cu(T, DIM, RO
 // tiles are dealt to the waves in turn, so a short item still uses all four.
 constexpr int kWideKeys = 64;
 
-template <int DIM>
+template <int DIM, bool HALF>
 struct WideLds {
   static constexpr int NB = DIM / 32;
   static constexpr int BUFS = DIM == 256 ? 1 : 2;  // two workgroups must fit a CU
@@ -1159,6 +1185,10 @@ struct WideLds {
   // Value scales that are not finite are zeros in vs; bit e % 64 of word e / 64
   // marks the one of key e / NB and block e % NB of a 16-key tile.
   uint64_t gone[BUFS][4][(16 * NB + 63) / 64];
+  // For f16 weights: scales outside what they allow are zeros in vs too, and
+  // here; outside: of a 16-key tile, whether there are any.
+  float left[BUFS][HALF ? 4 : 1][NB][16];
+  int outside[BUFS][4];
 };
 
 template <RowType T, int DIM, int RT>
@@ -1166,9 +1196,10 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
   typedef typename AttnElem<T>::type E;
   constexpr int NB = DIM / 32, QP = AttnElem<T>::kQParts, PP = AttnElem<T>::kPParts;
   constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;
-  constexpr int ROWS = 64 * RT, BUFS = WideLds<DIM>::BUFS;
+  constexpr int ROWS = 64 * RT, BUFS = DIM == 256 ? 1 : 2;
   constexpr int SPL = (16 * NB + 63) / 64;  // scale words a lane stages
-  __shared__ WideLds<DIM> lds;
+  constexpr bool HALF = AttnElem<T>::kHalf;
+  __shared__ WideLds<DIM, AttnElem<T>::kHalf> lds;
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1180,43 +1211,72 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
   uint32_t kw[KW], vw[4][VW];
   float ksw[SPL], vsw[SPL];
   float poison = 0.f;
+  // HALF: a power of two per block, that of block lane % NB, which brings the
+  // value scales near 1.
+  float near_one = 1.f;
+  // Offsets are made anew from the lane at each step: kept, they would be
+  // spilled, and waiting for one to come back waits for all loads before it.
   auto load = [&](int64_t base) {
+    int own = lane;
+    asm volatile("" : "+v"(own));
+    const int row = own & 15, c = own >> 4;
     load_words<KW>(buffer_of(p.c.K + base * DIM, 16 * DIM), row * DIM + c * (DIM / 4), kw);
     const __amdgpu_buffer_rsrc_t codes = buffer_of(p.c.V + base * DIM, 16 * DIM);
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_words<VW>(codes, (4 * c + i) * DIM + row * (DIM / 16), vw[i]);
 #pragma unroll
     for (int w = 0; w < SPL; ++w) {
-      const int e = (64 * w + lane) % (16 * NB);
+      const int e = (64 * w + own) % (16 * NB);
       ksw[w] = p.c.KS[base * NB + e];
       vsw[w] = p.c.VS[base * NB + e];
     }
   };
   auto lay = [&](int buf) {
+    int own = lane;
+    asm volatile("" : "+v"(own));
     static_for<0, NB>([&](auto b_) {
       constexpr int b = decltype(b_)::value;
       v4u x;
 #pragma unroll
       for (int jl = 0; jl < 4; ++jl) x[jl] = pair_f16(kw[jl * VW + b / 2], b % 2);
-      lds.k[buf][wave][b][lane] = x;
+      lds.k[buf][wave][b][own] = x;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = (float)(int8_t)(vw[k][b / 2] >> (16 * (b % 2) + 8 * i));
-        lds.v[buf][wave / 2][b][i][lane][wave % 2] = v2u{pack_hi(y[0], y[1]), pack_hi(y[2], y[3])};
+        if constexpr (HALF)
+          lds.v[buf][wave / 2][b][i][own][wave % 2] = v2u{pack_half(y[0], y[1]), pack_half(y[2], y[3])};
+        else
+          lds.v[buf][wave / 2][b][i][own][wave % 2] = v2u{pack_hi(y[0], y[1]), pack_hi(y[2], y[3])};
       }
     });
+    if constexpr (HALF) {
+      bool outside = false;
+#pragma unroll
+      for (int w = 0; w < SPL; ++w) {
+        vsw[w] *= near_one;
+        outside |= !in_window(vsw[w]);
+      }
+      const int any = __ballot(outside) != 0;
+      if (own == 0) lds.outside[buf][wave] = any;
+    }
 #pragma unroll
     for (int w = 0; w < SPL; ++w) {
       ksw[w] = fmaf(ksw[w], scale, poison);
       vsw[w] += poison;
-      const uint64_t gone = __ballot(64 * w + lane < 16 * NB && !finite(vsw[w]));
-      if (lane == 0) lds.gone[buf][wave][w] = gone;
-      if (64 * w + lane < 16 * NB) {
-        const int e = 64 * w + lane;  // key e / NB, block e % NB
+      const uint64_t gone = __ballot(64 * w + own < 16 * NB && !finite(vsw[w]));
+      if (own == 0) lds.gone[buf][wave][w] = gone;
+      if (64 * w + own < 16 * NB) {
+        const int e = 64 * w + own;  // key e / NB, block e % NB
         lds.ks[buf][wave][e % NB][e / NB] = ksw[w];
-        lds.vs[buf][wave][e % NB][e / NB] = finite(vsw[w]) ? vsw[w] : 0.f;
+        if constexpr (HALF) {
+          const bool in = in_window(vsw[w]);
+          lds.vs[buf][wave][e % NB][e / NB] = in ? vsw[w] : 0.f;
+          lds.left[buf][wave][e % NB][e / NB] = in || !finite(vsw[w]) ? 0.f : vsw[w];
+        } else {
+          lds.vs[buf][wave][e % NB][e / NB] = finite(vsw[w]) ? vsw[w] : 0.f;
+        }
       }
     }
   };
@@ -1245,6 +1305,18 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
       fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q[rt]);
     }
     if (begin < end) load_at(begin);
+    float first[SPL];  // HALF: value scales of the share's first 16 keys, if all rows see them
+    if constexpr (HALF) {
+      if (begin < end && begin + 16 <= h.all) {
+        float unused;
+        const int64_t at = token_row(p, keys_at(p, h.pages, begin, last), h.kvh, unused);
+#pragma unroll
+        for (int w = 0; w < SPL; ++w) first[w] = p.c.VS[at * NB + (64 * w + lane) % (16 * NB)];
+      } else {
+#pragma unroll
+        for (int w = 0; w < SPL; ++w) first[w] = 0.f;
+      }
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       undo[rt] = cut_query<T, DIM>(q[rt], in[rt], qf[rt]);
@@ -1252,6 +1324,15 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
       l[rt] = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[rt][b][0] = acc[rt][b][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    if constexpr (HALF) {
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < SPL; ++w) top = fmaxf(top, finite(first[w]) ? first[w] : 0.f);
+#pragma unroll
+      for (int d = NB; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      const int up = top > 0.f ? 1 - __builtin_amdgcn_frexp_expf(top) : 0;
+      near_one = ldexpf(1.f, min(max(up, -60), 60));
     }
     const int tiles = (h.rows + 15) / 16;
     const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has
@@ -1305,7 +1386,7 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      weigh<NRT, 16, NB, 1>(s, undo, m, l, acc);
+      weigh<NRT, 16, NB, 1, HALF>(s, undo, m, l, acc);
       {
         v4u a[2][2];
         v4f vs[2][2];
@@ -1327,18 +1408,62 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
             float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = vs[n % 2][k / 4][k % 4] * s[rt][8 * g + k];
-            v4u parts[PP];
-            split8<PP>(w, parts);
+            if constexpr (HALF) {
+              const v4u half = round_half(w);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 2; ++i) acc[rt][b][i] = mfma_f16(a[n % 2][i], half, acc[rt][b][i]);
+            } else {
+              v4u parts[PP];
+              split8<PP>(w, parts);
 #pragma unroll
-              for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[n % 2][i], parts[q], acc[rt][b][i]);
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[n % 2][i], parts[q], acc[rt][b][i]);
+            }
           }
 #pragma unroll
           for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) pin(acc[rt][b][i]);
         });
+      }
+      // Keys whose value scale is outside the window: once more over the step with
+      // those alone, their weights in bf16 parts (whose range is f32's) against
+      // the same codes.
+      if constexpr (HALF) {
+        const int *o = lds.outside[buf];
+        if (__builtin_amdgcn_readfirstlane(o[0] | o[1] | o[2] | o[3]) != 0) {
+          static_for<0, 2 * NB>([&](auto n_) {
+            constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
+            v4u a[2];
+            v4f left[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const v4u half = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const v2h h = __builtin_bit_cast(v2h, (uint32_t)half[k]);
+                a[i][k] = pack_hi((float)h.x, (float)h.y);
+              }
+              left[i] = *reinterpret_cast<const v4f *>(&lds.left[buf][2 * g + i][b][4 * c]);
+            }
+#pragma unroll
+            for (int rt = 0; rt < NRT; ++rt) {
+              float w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = left[k / 4][k % 4] * s[rt][8 * g + k];
+              v4u parts[PP];
+              split8<PP>(w, parts);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
+                pin(acc[rt][b][i]);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        }
       }
       // Blocks of rows that see a value scale that is not finite are lost.
       uint64_t any = 0;
@@ -1392,6 +1517,11 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
         steps(std::integral_constant<int, 0>{});
     }
 
+    float back[NB];  // HALF: undoes near_one
+    if constexpr (HALF) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) back[b] = 1.f / __int_as_float(__builtin_amdgcn_readlane(__float_as_int(near_one), b));
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int rho = 16 * (4 * rt + wave) + row;
@@ -1403,6 +1533,10 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
       for (int b = 0; b < NB; ++b) {
         const v4f u = acc[rt][b][0], v = acc[rt][b][1];
         float x[8] = {u[0], v[0], u[1], v[1], u[2], v[2], u[3], v[3]};
+        if constexpr (HALF) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= back[b];
+        }
         const int d = 32 * b + 8 * c;
         if (h.whole) {
           finish_row(p, h, t, weight, x);

@@ -6,9 +6,10 @@
 // correctly rounded, so codes and scales do not depend on how the work is
 // split:
 //   * the scale is one correctly rounded division;
-//   * the code is the rounded f32 quotient, corrected by at most one step with
-//     the exact remainder x - code * s (a multiple of ulp(s) / 2 no larger
-//     than 2 s, so the fused multiply-add that forms it does not round).
+//   * the code is x times the scale's reciprocal, rounded, then corrected by at
+//     most one step with the exact remainder x - code * s (a multiple of
+//     ulp(s) / 2 no larger than 2 s, so the fused multiply-add that forms it
+//     does not round).
 // A block that holds an infinity or a NaN has no scale; it is stored as s =
 // NaN and reads back as NaN.
 //
@@ -52,16 +53,37 @@ struct __attribute__((packed, aligned(sizeof(E)))) Pair {
   E x, y;
 };
 
-// Largest |x| of a 16-lane group, NaN if any lane's is.
-__device__ __forceinline__ float group_max(float m) {
-#define Q8_STEP(ctrl)                                                                                    \
-  {                                                                                                      \
-    const float o = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), ctrl, 0xf, 0xf, false)); \
-    m = (o > m || o != o) ? o : m;                                                                       \
-  }
-  Q8_STEP(0x128) Q8_STEP(0x124) Q8_STEP(0x122) Q8_STEP(0x121)  // row_ror:8, 4, 2, 1
-#undef Q8_STEP
+// Largest of a 16-lane group.  For |x| as bits: infinities above all numbers,
+// NaN above them.
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xf, 0xf, true));  // row_ror:8, 4, 2, 1
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xf, 0xf, true));
   return m;
+}
+
+// f32(top / 127) for finite top >= 0.  1 / 127 is 2^-28 from its f32, so the
+// product is within an ulp of the quotient and one corrected step rounds it
+// correctly; not where the quotient loses bits to denormals.
+__device__ __forceinline__ float scale_of(float top) {
+  if (top < 0x1p-90f) return top / 127.f;
+  constexpr float r = 1.f / 127.f;
+  const float q = top * r;
+  return fmaf(fmaf(-q, 127.f, top), r, q);
+}
+
+// x / s to the nearest whole number, ties to even, for any finite x and s > 0
+// with |x| < 2^8 s or so: from the reciprocal's product, off by less than one,
+// and the exact remainder.
+__device__ __forceinline__ float exact_code(float x, float s) {
+  const float up = s < 0x1p-100f ? 0x1p100f : 1.f;  // exact, and the reciprocal does not overflow
+  const float step = s * up, y = x * up;
+  float c = rintf(y * __builtin_amdgcn_rcpf(step));
+  const float rest = fmaf(-c, step, y);
+  const float twice = 2.f * fabsf(rest);
+  if (twice > step || (twice == step && ((int)c & 1) != 0)) c += rest > 0.f ? 1.f : -1.f;
+  return fminf(fmaxf(c, -127.f), 127.f);
 }
 
 // Where row t of the row tensors lives: found by the whole wave (t is the same
@@ -117,7 +139,10 @@ struct CodeWord<128> { typedef uint2 type; };
 template <>
 struct CodeWord<256> { typedef uint4 type; };
 
-constexpr int kRowsPerGroup = 2;                              // (head, K or V) rows per 16-lane group
+// (head, K or V) rows per 16-lane group.  With one, two and four a step of 64
+// tokens is written and read back in 5.4, 6.3 and 10.4 us, 18432 tokens of
+// prompts in 64, 58 and 74 us, and 147000 tokens are read in 150, 132 and 138.
+constexpr int kRowsPerGroup = 2;
 constexpr int kRowsPerWave = kRowsPerGroup * 4;
 
 // A wave takes one token's rows r = kRowsPerWave * blockIdx.y ..: row r is
@@ -162,26 +187,24 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
     float mine = 0.f;  // lane b keeps block b's scale
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const float a0 = fabsf(x[q][b][0]), a1 = fabsf(x[q][b][1]);
-      const float top = group_max((a1 > a0 || a1 != a1) ? a1 : a0);
-      const bool fine = top < INFINITY;  // not for NaN either
-      const float s = fine ? top / 127.f : NAN;
+      const float x0 = x[q][b][0], x1 = x[q][b][1];
+      const uint32_t top = group_max(max(__float_as_uint(x0) & 0x7fffffffu, __float_as_uint(x1) & 0x7fffffffu));
+      const bool fine = top < 0x7f800000u;
+      const float s = fine ? scale_of(__uint_as_float(top)) : NAN;
       if (j == b) mine = s;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float c = 0.f;
-        if (fine && s > 0.f) {
-          c = rintf(x[q][b][i] / s);
-          const float rest = fmaf(-c, s, x[q][b][i]);
-          const float half = 0.5f * s;
-          // Past half a step the next code is nearer; at half a step the even one is.
-          const bool odd = ((int)c & 1) != 0;
-          if (rest > half || (rest == half && odd)) c += 1.f;
-          if (rest < -half || (rest == -half && odd)) c -= 1.f;
-          c = fminf(fmaxf(c, -127.f), 127.f);
-        }
-        out.c[2 * b + i] = (int8_t)(int)c;
+      // The rounded product with the reciprocal is the code unless the exact
+      // remainder comes to half a step: about once in a million values.
+      const float r = __builtin_amdgcn_rcpf(s);
+      float c0 = rintf(x0 * r), c1 = rintf(x1 * r);
+      const float rest = fmaxf(fabsf(fmaf(-c0, s, x0)), fabsf(fmaf(-c1, s, x1)));
+      const bool sure = s >= 0x1p-100f && 2.f * rest < s;  // not for NaN, zero or tiny scales
+      if (!sure) {
+        const bool some = fine && s > 0.f;
+        c0 = some ? exact_code(x0, s) : 0.f;
+        c1 = some ? exact_code(x1, s) : 0.f;
       }
+      out.c[2 * b] = (int8_t)(int)c0;
+      out.c[2 * b + 1] = (int8_t)(int)c1;
     }
     if (r < nrows) {
       const int64_t row = base + ((int64_t)(r >> 1) << p.c.page_shift);
@@ -193,7 +216,11 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
   }
 }
 
-template <RowType T, int DIM>
+// PAST: the rows are written past the caches.  They leave the Infinity Cache
+// anyway where they are larger than it (512 MB of rows: 142 us through the
+// caches, 135 past them); smaller ones are better kept for whoever reads them.
+constexpr int64_t kPastCachesBytes = (int64_t)256 << 20;
+template <RowType T, int DIM, bool PAST>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
   typedef typename Elem<T>::type E;
   typedef typename CodeWord<DIM>::type Word;
@@ -232,10 +259,14 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
              (int64_t)(r >> 1) * DIM;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      Pair<E> v;
-      v.x = Elem<T>::from_float((float)in.c[2 * b] * s[b]);
-      v.y = Elem<T>::from_float((float)in.c[2 * b + 1] * s[b]);
-      *reinterpret_cast<Pair<E> *>(row + 32 * b + 2 * j) = v;
+      typedef E Two __attribute__((ext_vector_type(2)));
+      typedef Two Unaligned __attribute__((aligned(sizeof(E))));
+      const Two v = {Elem<T>::from_float((float)in.c[2 * b] * s[b]), Elem<T>::from_float((float)in.c[2 * b + 1] * s[b])};
+      Unaligned *to = reinterpret_cast<Unaligned *>(row + 32 * b + 2 * j);
+      if constexpr (PAST)
+        __builtin_nontemporal_store(v, to);
+      else
+        *to = v;
     }
   }
 }
@@ -311,12 +342,15 @@ __global__ __launch_bounds__(kThreads) void cache_keep_kernel(CacheKeepArgs p) {
 template <RowType T>
 hipError_t launch_rows(const CacheRowsArgs &a, bool write, hipStream_t stream) {
   const dim3 grid((unsigned)((a.s.rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kRowsPerWave - 1) / kRowsPerWave));
+  const bool past = 2 * (int64_t)sizeof(typename Elem<T>::type) * a.s.rows * a.c.heads * a.c.dim > kPastCachesBytes;
 #define Q8_LAUNCH(DIM)                                                                                   \
   case DIM:                                                                                              \
     if (write)                                                                                           \
       hipLaunchKernelGGL((cache_write_kernel<T, DIM>), grid, dim3(kThreads), 0, stream, a);              \
+    else if (past)                                                                                       \
+      hipLaunchKernelGGL((cache_read_kernel<T, DIM, true>), grid, dim3(kThreads), 0, stream, a);         \
     else                                                                                                 \
-      hipLaunchKernelGGL((cache_read_kernel<T, DIM>), grid, dim3(kThreads), 0, stream, a);               \
+      hipLaunchKernelGGL((cache_read_kernel<T, DIM, false>), grid, dim3(kThreads), 0, stream, a);        \
     return hipGetLastError();
   switch (a.c.dim) {
     Q8_LAUNCH(64)

@@ -69,11 +69,12 @@ def attention_bound(out, spread, size, dtype):
     with the two roundings of the exponent's argument a score is off by at most
     16 * 2^-24 size, below 1e-6 size, and a weight by that factor.  It shifts the
     numerator and the sum of weights, so it counts twice.
-    Weights and sums: the weights' parts drop at most 2^-16 of a term for 16-bit
-    rows, nothing for f32; the sum over some thousand keys is a random walk of
+    Weights and sums: the weights' parts drop at most 2^-16 of a term for f16
+    rows, nothing for f32; for bf16 rows a weight may be one f16, off by at most
+    2^-11 of itself; the sum over some thousand keys is a random walk of
     f32 roundings, under 64 * 2^-24 of the terms; exp2 and the joins add a few.
     Last, half a step of the output's type.
     """
-    eps = 4e-6 + 2e-6 * size[..., None] + (0 if dtype == torch.float32 else 2.0 ** -16)
+    eps = 4e-6 + 2e-6 * size[..., None] + {torch.float32: 0, torch.float16: 2.0 ** -16, torch.bfloat16: 2.0 ** -11}[dtype]
     half = torch.finfo(dtype).eps / 2
     return spread * eps * (1 + half) + half * np.abs(out) + torch.finfo(dtype).smallest_normal * half

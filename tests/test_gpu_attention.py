@@ -57,7 +57,13 @@ class Case:
         ref, spread, size = self.want()
         own = slice(int(self.offsets[0]), int(self.offsets[-1]))
         got = out.float().cpu().numpy().astype(np.float64)
-        far = np.abs(got - ref)[own] / cc.attention_bound(ref, spread, size, self.dtype)[own]
+        bound = cc.attention_bound(ref, spread, size, self.dtype)
+        if self.dtype == torch.float16:  # from 65520 on a value rounds to an infinity
+            assert np.isinf(got[own][(np.abs(ref) - bound)[own] >= 65520]).all()
+            may = (np.abs(ref) + bound >= 65520) & np.isinf(got)
+            assert (np.sign(got) == np.sign(ref))[may].all()
+            got = np.where(may, ref, got)
+        far = np.abs(got - ref)[own] / bound[own]
         assert far.size == 0 or far.max() <= 1, f"{far.max():.3f} of the bound at {np.unravel_index(far.argmax(), far.shape)}"
 
 
@@ -126,6 +132,59 @@ def test_wide_tree():
     """Trees over several words, beside sequences with fewer tokens than the words hold."""
     c = Case(26, [400, 130, 65], [200, 130, 1], 1, 2, 64, 16, torch.float32, tree=True)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("spread", [6, 30])
+def test_value_scales_of_all_sizes(spread, dim, dtype):
+    """Value scales from 2^-spread to 2^spread, token by token and block by block,
+    zeros among them, with few rows and with many; a sequence whose first keys
+    are zeros and one whose first keys are the smallest."""
+    for news, lengths in (([1, 2, 1], [300, 40, 70]), ([40, 33, 70], [300, 200, 500])):
+        c = Case((43, spread, dim, len(news)), lengths, news, 1, 4, dim, 16, dtype, tree=news[0] == 40)
+        rng = np.random.default_rng((44, spread))
+        v = c.c["v_scale"]
+        v *= (2.0 ** rng.integers(-spread, spread + 1, v.shape)).astype(np.float32)
+        v[rng.random(v.shape) < 0.1] = 0
+        v[c.table[1, :2]] = 0
+        v[c.table[2, :2]] = 2.0 ** -spread / 73
+        print(f"[attention] value scales 2^{spread} dim {dim} {dtype} new {news}", flush=True)
+        c.check(c.run())
+
+
+def test_scales_of_tokens_that_are_not_seen_change_nothing_with_many_rows():
+    """Behind the last token, and of a draft that no row sees: any bits."""
+    c = Case(45, [300, 90], [40, 60], 1, 4, 128, 64, torch.bfloat16, tree=True)
+    for bits in (c.trees[1],):
+        for i in range(60):
+            bits[i] &= ~(1 << 7)
+    want = c.run()
+    page, at = oc.slot_of(c.table, 64, 1, 30 + 7)
+    for value in (1e30, 1e-30, float("inf"), float("nan")):
+        c.c["v_scale"][page, :, at] = value
+        c.c["k_scale"][page, :, at] = value
+        for b, n in enumerate(c.lengths):
+            p, a = oc.slot_of(c.table, 64, b, int(n))
+            c.c["v_scale"][p, :, a:] = value
+            c.c["k_scale"][p, :, a:] = value
+        assert torch.equal(c.run(), want), value
+
+
+def test_lost_values_with_many_rows():
+    """A value scale that is not finite loses its block of the rows that see it, and no other."""
+    for dtype in TYPES:
+        c = Case(46, [300, 90], [40, 60], 1, 4, 128, 64, dtype, tree=True)
+        for seq, pos, block in ((0, 5, 2), (1, 30 + 9, 0), (1, 30 + 20, 3)):
+            page, at = oc.slot_of(c.table, 64, seq, pos)
+            c.c["v_scale"][page, :, at, block] = np.nan
+        out = c.run().float().cpu().numpy()
+        ref = c.want()[0]
+        assert np.array_equal(np.isnan(out), np.isnan(ref))
+        fine = ~np.isnan(ref)
+        ref2, spread, size = c.want()
+        bound = cc.attention_bound(ref2, spread, size, dtype)
+        assert (np.abs(out - ref)[fine] <= bound[fine]).all()
 
 
 def test_rows_that_see_nothing():
