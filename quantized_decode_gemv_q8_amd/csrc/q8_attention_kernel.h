@@ -1557,61 +1557,74 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void at
 
 // ---------------------------------------------------------------- joining the parts
 
-// Workgroup (w, y): the split item that workgroup w began, rows 4 y .. 4 y + 3,
-// one per wave; parts are taken in key order.
+// Rows that a wave of the join takes: four channels of a row per lane.
+constexpr int join_rows(int dim) { return 256 / dim; }
+
+// Workgroup (w, y): the split item that workgroup w began, and its y-th run of
+// kWaves * join_rows rows; parts are taken in key order.
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;
   const AttnItem it = p.items[blockIdx.x];
   if (!it.valid) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  constexpr int PER = DIM / 64;  // channels per lane
+  constexpr int LANES = 64 / join_rows(DIM);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & (LANES - 1);
+  const int live = it.tokens * it.heads, rho0 = (blockIdx.y * kWaves + wave) * join_rows(DIM);
+  if (rho0 >= live) return;
+  const bool mine = rho0 + lane / LANES < live;
+  const int rho = mine ? rho0 + lane / LANES : rho0;
   const int64_t size = attn_slot_floats(slot_rows, DIM);
   const int first = blockIdx.x, parts = it.last - first + 1;
   // Contributor k: the first one's slot 1, then slot 0 of the following ones.
   const float *base = p.partial + (2 * (int64_t)first + 1) * size;
   auto part = [&](int k) { return k == 0 ? base : p.partial + 2 * (int64_t)(first + k) * size; };
-  const int rho = blockIdx.y * kWaves + wave;
-  if (rho >= it.tokens * it.heads) return;
-  // The largest maximum, then every part's factor, a lane per part.
+  // Four parts' rows in flight; past the last one the last one again, unused.
+  v4f y[4];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      y[u] = *reinterpret_cast<const v4f *>(part(min(k + u, parts - 1)) + (int64_t)rho * DIM + c * 4);
+  };
+  load(0);
+  // The largest maximum, then the parts' factors, a lane per part.
   float top = -INFINITY;
-  for (int k = lane; k < parts; k += 64) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
+  for (int k = c; k < parts; k += LANES) top = fmaxf(top, part(k)[(int64_t)slot_rows * DIM + rho]);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   const float from = top == -INFINITY ? 0.f : top;
-  float weight = 0.f, x[PER] = {};
-  for (int k0 = 0; k0 < parts; k0 += 64) {
-    float f = 0.f, wt = 0.f;
-    if (k0 + lane < parts) {
-      const float *s = part(k0 + lane) + (int64_t)slot_rows * DIM + rho;
-      f = __builtin_amdgcn_exp2f(s[0] - from);
-      wt = f * s[slot_rows];
-    }
-    const int n = min(64, parts - k0);
-    // Four parts' rows in flight; past the last one the last one again, with no weight.
-    for (int k = 0; k < n; k += 4) {
-      Run<float, PER> y[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        y[u] = *reinterpret_cast<const Run<float, PER> *>(part(k0 + min(k + u, n - 1)) + (int64_t)rho * DIM + lane * PER);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (k + u >= n) break;
-        const float g = __shfl(f, k + u);
-        weight += __shfl(wt, k + u);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] += g * y[u].x[i];
+  float weight = 0.f, f = 0.f, wt = 0.f;
+  float x[4] = {};
+  for (int k = 0;;) {
+    if ((k & (LANES - 1)) == 0) {
+      f = wt = 0.f;
+      if (k + c < parts) {
+        const float *s = part(k + c) + (int64_t)slot_rows * DIM + rho;
+        f = __builtin_amdgcn_exp2f(s[0] - from);
+        wt = f * s[slot_rows];
       }
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k + u >= parts) break;
+      const int from_lane = (k + u) & (LANES - 1);
+      const float g = __shfl(f, from_lane, LANES);
+      weight += __shfl(wt, from_lane, LANES);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] += g * y[u][i];
+    }
+    k += 4;
+    if (k >= parts) break;
+    load(k);
   }
+  if (!mine) return;
   const int tok = rho / it.heads;
   const int64_t t = it.row0 + tok;
   bool nothing = false;
   if (weight == 0.f) nothing = !sees_any(p.tree, p.tree_words, it.context, it.seq_new, t);
   const float scale = 1.f / weight;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) x[i] = nothing ? 0.f : x[i] * scale;
-  store_run<E, PER>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + lane * PER, x);
+  for (int i = 0; i < 4; ++i) x[i] = nothing ? 0.f : x[i] * scale;
+  store_run<E, 4>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(it.head0 + rho - tok * it.heads) * DIM + c * 4, x);
 }
 
 template <RowType T, int DIM, int ROWS>
@@ -1624,7 +1637,7 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
     hipLaunchKernelGGL((attention_kernel<T, DIM, ROWS, 4>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
-  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, ROWS / kWaves),
+  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, (ROWS + kWaves * join_rows(DIM) - 1) / (kWaves * join_rows(DIM))),
                      dim3(kThreads), 0, stream, a, ROWS);
   return hipGetLastError();
 }
