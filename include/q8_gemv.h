@@ -302,7 +302,8 @@ typedef struct q8_cache {
  * not ascend within the rows has no rows; one with lengths[b] < n, or with more
  * tokens than its table row holds, and a position whose page is not one of
  * the cache's (0 .. pages-1), is skipped by a write or keep, and gives NaN in
- * the rows of a read or an attention that would need it.  A row that the
+ * the rows of a read or an attention that would need it (a cache of no pages
+ * holds no tokens at all).  A row that the
  * offsets give to two sequences holds either one's result.
  */
 typedef struct q8_cache_seqs {
@@ -369,17 +370,26 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  *           apart; out must not overlap anything else
  *   workspace  device memory of at least the size that
  *           q8_cache_attention_workspace gives for the same cache, type, rows,
- *           q_heads, seqs and max_pages (which may be none), 16-byte aligned; its contents need no
- *           preparation and are free again when the call's work is done.  Calls that may
- *           overlap in time (and graphs whose replays may) need one each
- * f32 accuracy for f32 rows: codes are exact in the bf16 matrix operands, q and
- * the scaled weights are cut into enough bf16 parts to lose nothing (weights
- * for bf16 and f16 rows: 16 bits), sums, maxima and scales are f32.  Products
- * of q and the codes must stay finite before they are scaled: |q| below
- * 2^115.  Deterministic: the order of the sums depends on the extents, the lengths and
+ *           q_heads, seqs and max_pages, 16-byte aligned (NULL where that size is 0); its
+ *           contents need no preparation and are free again when the call's work is done.
+ *           Calls that may overlap in time (and graphs whose replays may) need one each
+ * Sums, maxima, scores, weights and scales are f32, and codes are exact.  What
+ * the matrix cores take of the rest is rounded as follows.
+ *   q        f32 rows: to 2^-23 of the row's largest channel; bf16 and f16 rows: not
+ *            at all (channels below 2^-32 of the row's largest lose bits)
+ *   weights  (each times its value scale) f32 rows: not at all; f16 rows: to
+ *            2^-16; bf16 rows: to 2^-16, or to 2^-11 where sequences bring more than 32
+ *            rows for each head on average (new tokens times g; more than 16 if dim
+ *            is 256)
+ * A query that is not finite, a key whose score is NaN or +infinity and a value
+ * scale that is not finite give NaN in the rows that see them (a value scale in
+ * its block of channels).
+ * Deterministic: the order of the sums depends on the extents, the lengths and
  * offsets, never on timing.
  * Errors: as q8_cache_write; Q8_ERR_INVALID also for q_heads that is no multiple
- * of heads and for a missing, misaligned or small workspace.
+ * of heads and for a missing, misaligned or small workspace; Q8_ERR_TOO_LARGE also
+ * for more than 2^24 query heads and where seqs * rows * heads * max_pages * page_size
+ * is so large (about 2^57 and more) that the work cannot be numbered.
  */
 q8_status q8_cache_attention_workspace(const q8_cache *cache, q8_type type, int64_t rows,
                                        int32_t q_heads, const q8_cache_seqs *seqs, int64_t *bytes);

@@ -5,6 +5,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -753,7 +754,9 @@ q8_status cache_args(const q8_cache *c, const q8_cache_seqs *s, int64_t rows, q8
   seqs->lengths = s->lengths;
   seqs->offsets = s->offsets;
   seqs->table_stride = s->table_stride;
-  seqs->max_tokens = s->max_pages * c->page_size;
+  // A cache without pages holds no tokens, whatever the table says: its arrays
+  // may be null, and sequences that claim some are described wrongly.
+  seqs->max_tokens = c->pages > 0 ? s->max_pages * c->page_size : 0;
   seqs->seqs = (int)s->seqs;
   seqs->rows = (int)rows;
   return Q8_OK;
@@ -796,10 +799,14 @@ struct AttnPlan {
   int tile, subs, sub_heads, tile_tokens;
   int unit_shift;      // log2 of the keys of a unit
   int item_cost;       // units that an item is charged besides its keys
-  bool few_units;      // the units of all items are sure to stay below 2^31
+  double most_units;   // at least as many as the units of all items, whatever the offsets
+  double few;          // the same for ascending offsets, without the items' cost, up to kIndexLimit
   bool split;          // an item may have several units
   int64_t wgs, bytes;  // workgroups; workspace
 };
+// The work list is numbered in 64 bits, and products with the workgroups must fit them.
+constexpr double kAttnMostUnits = 1125899906842624.0;  // 2^50
+constexpr int kAttnMostHeads = 1 << 24;
 
 // Sequences that the table bounds to this many tokens are not split: one
 // workgroup takes all keys of an item, and the second launch that joins parts
@@ -811,9 +818,8 @@ constexpr int64_t kAttnWholeTokens = 1024;
 // 1, 73 at 2 and 75 at 3 and 4; with many rows a unit takes so long that 0 is best.
 constexpr int kAttnItemCost = 2;
 
-AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens,
-                   int cus) {
-  AttnPlan p;
+AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
+  AttnPlan p = {};
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
   // The instances for 4 and 8 rows do not fit the registers at dim 256.
   p.tile = mean <= 4 && dim <= 128                 ? 4
@@ -827,18 +833,24 @@ AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows
   p.sub_heads = (int)ceil_div(group, p.subs);
   p.subs = (int)ceil_div(group, p.sub_heads);  // no empty sub-group
   p.tile_tokens = tile / p.sub_heads;
-  const int64_t items = (rows / p.tile_tokens + seqs) * heads * p.subs;
   p.split = max_tokens > kAttnWholeTokens || tile > 16;
   p.unit_shift = __builtin_ctz((unsigned)(p.split ? q8::kAttnStep : kAttnWholeTokens));
-  const int64_t units = p.split ? ceil_div(max_tokens, q8::kAttnStep) : 1;
+  const int64_t units = p.split && max_tokens > 0 ? ceil_div(max_tokens, q8::kAttnStep) : 1;
   p.item_cost = p.split && tile < 64 ? kAttnItemCost : 0;
-  p.few_units = items <= (kIndexLimit - 1) / (units + p.item_cost);
-  p.wgs = (int64_t)cus * q8::attn_wgs_per_cu(type, dim, tile);
-  if (items < p.wgs && items * units < p.wgs) p.wgs = items * units;
-  p.bytes = 0;
-  if (p.split)
-    p.bytes = ceil_div(2 * p.wgs * q8::attn_slot_floats(tile, dim) * 4, 256) * 256 + p.wgs * (int64_t)sizeof(q8::AttnItem);
+  // Offsets that are no ascending ones may give a row to every sequence.
+  p.most_units = (double)seqs * (double)(rows / p.tile_tokens + 1) * heads * p.subs * (double)(units + p.item_cost);
+  // Where they do ascend, at most:
+  p.few = std::min((double)(rows / p.tile_tokens + seqs) * heads * p.subs * (double)units, (double)kIndexLimit);
   return p;
+}
+
+// What depends on the device: workgroups, as many as there are units if those
+// are fewer, and their workspace.
+void deal(AttnPlan *p, int dim, int cus) {
+  p->wgs = std::min((int64_t)cus * q8::kAttnWgsPerCu, (int64_t)p->few);
+  if (p->split)
+    p->bytes =
+        ceil_div(2 * p->wgs * q8::attn_slot_floats(p->tile, dim) * 4, 256) * 256 + p->wgs * (int64_t)sizeof(q8::AttnItem);
 }
 
 }  // namespace
@@ -970,13 +982,17 @@ q8_status q8_cache_attention_workspace(const q8_cache *cache, q8_type type, int6
   q8_status st = cache_args(cache, seqs, rows, &c, &s);
   if (st != Q8_OK) return st;
   if (q_heads < 1 || q_heads % cache->heads != 0) return Q8_ERR_INVALID;
+  if (q_heads > kAttnMostHeads) return Q8_ERR_TOO_LARGE;
   *bytes = 0;
   if (rows == 0 || seqs->seqs == 0) return Q8_OK;
+  AttnPlan pl = attn_plan((q8::RowType)type, c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens);
+  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
   int dev = 0;
   DevInfo info;
   st = current_device(&dev, &info);
   if (st != Q8_OK) return st;
-  *bytes = attn_plan((q8::RowType)type, c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens, info.cus).bytes;
+  deal(&pl, c.dim, info.cus);
+  *bytes = pl.bytes;
   return Q8_OK;
 }
 
@@ -989,18 +1005,19 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
   if (st != Q8_OK) return st;
   if (!row_type(type, &bytes) || q_heads < 1 || q_heads % cache->heads != 0 || tree_words < 0) return Q8_ERR_INVALID;
-  if (q_heads > (1 << 24) || tree_words >= kIndexLimit / 64) return Q8_ERR_TOO_LARGE;
+  if (q_heads > kAttnMostHeads || tree_words >= kIndexLimit / 64) return Q8_ERR_TOO_LARGE;
   if (rows == 0 || seqs->seqs == 0) return Q8_OK;
   const int64_t width = (int64_t)q_heads * cache->dim;
   if (q == nullptr || out == nullptr || address_alignment(q) < bytes || address_alignment(out) < bytes) return Q8_ERR_INVALID;
   if (rows > 1 && (q_stride < width || out_stride < width)) return Q8_ERR_INVALID;
   if (address_alignment(tree) < 8) return Q8_ERR_INVALID;
+  AttnPlan pl = attn_plan((q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens);
+  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
   int dev = 0;
   DevInfo info;
   st = current_device(&dev, &info);
   if (st != Q8_OK) return st;
-  const AttnPlan pl =
-      attn_plan((q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens, info.cus);
+  deal(&pl, a.c.dim, info.cus);
   if (pl.split && (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes))
     return Q8_ERR_INVALID;
   a.q = q;
@@ -1020,7 +1037,7 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   a.unit_shift = pl.unit_shift;
   a.half_rows = pl.tile == 128 ? 64 : 0;
   a.item_cost = pl.item_cost;
-  a.few_units = pl.few_units;
+  a.few_units = pl.most_units < (double)kIndexLimit;
   if (log_debug())
     log_line("cache_attention rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", (long long)rows,
              q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", pl.tile,

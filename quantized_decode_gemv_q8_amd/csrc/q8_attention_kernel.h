@@ -1022,7 +1022,7 @@ struct AttnOf<T, DIM, 8> {
 
 // WAVES: 4, or 8 where a workgroup takes all keys of its items.
 template <RowType T, int DIM, int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? attn_wgs_per_cu(T, DIM, ROWS) : 1) void attention_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? kAttnWgsPerCu : 1) void attention_kernel(AttnArgs p) {
   typedef typename AttnOf<T, DIM, ROWS>::type A;
   typedef typename A::E E;
   constexpr int NB = A::NB, RT = A::RT, PITCH = A::PITCH, STEP = kAttnTile * WAVES;
@@ -1192,7 +1192,7 @@ struct WideLds {
 };
 
 template <RowType T, int DIM, int RT>
-__global__ __launch_bounds__(kThreads, attn_wgs_per_cu(T, DIM, 64 * RT)) void attention_wide_kernel(AttnArgs p) {
+__global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel(AttnArgs p) {
   typedef typename AttnElem<T>::type E;
   constexpr int NB = DIM / 32, QP = AttnElem<T>::kQParts, PP = AttnElem<T>::kPParts;
   constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;

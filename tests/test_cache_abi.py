@@ -96,6 +96,15 @@ def test_bad_attention():
     assert binding.load().q8_cache_attention_workspace(cache(), 0, 5, 4, seqs(), None) == binding.Q8_ERR_INVALID
 
 
+def test_attention_past_the_work_list():
+    """More units of work than the list can number; the same sizes alone are allowed."""
+    for kw in (dict(seqs=1 << 29, max_pages=1, table_stride=1), dict(seqs=1 << 12, max_pages=1 << 25, table_stride=1 << 25)):
+        st = calls(cache(heads=256), seqs(**kw), rows=(1 << 31) - 1, q_heads=256, q_stride=1 << 14)
+        assert st[3:] == LARGE[:2], kw
+    st = calls(cache(), seqs(), q_heads=1 << 25, q_stride=1 << 31)
+    assert st[3:] == LARGE[:2]
+
+
 def test_nothing_to_do_touches_nothing():
     ok = (binding.Q8_OK,) * 5
     assert calls(cache(), seqs(), rows=0, k=None) == ok

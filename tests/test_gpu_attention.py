@@ -303,6 +303,74 @@ def test_bad_descriptions():
             assert bool(torch.isnan(got[2:5]).all()) and torch.equal(got[5], want[5]), name
 
 
+@pytest.mark.parametrize("news", [[1, 2], [70, 3]])
+def test_caches_and_tables_without_pages(news):
+    """Sequences that claim tokens of a cache that has no pages, or of a table
+    that has no columns, give NaN, and those that have none nothing."""
+    c = Case((43, len(news)), [90, 200], news, 2, 2, 64, 16, torch.float32)
+    q, (table, lengths, offsets) = c.q.to(DEV), c.held()
+    none = binding.Q8Cache.empty(0, 2, 16, 64, DEV)
+    assert bool(torch.isnan(binding.q8_cache_attention(q, none, table, lengths, offsets)).all())
+    assert bool(torch.isnan(binding.q8_cache_attention(q, handle(c.c), table[:, :0], lengths, offsets)).all())
+    k = torch.ones((c.rows, 2, 64), device=DEV)
+    binding.q8_cache_write(none, k, k, table, lengths, offsets)
+    for x in binding.q8_cache_read(none, table, lengths, offsets, c.rows):
+        assert bool(torch.isnan(x).all())
+    binding.q8_cache_keep(none, table, lengths, offsets, torch.zeros((2, 1), dtype=torch.int32, device=DEV))
+    nobody = torch.zeros(3, dtype=torch.int32, device=DEV)
+    out = binding.q8_cache_attention(q, none, table, nobody[:2], nobody, out=torch.full_like(q, 5.0))
+    assert bool((out == 5).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bad_descriptions_with_many_rows(dtype):
+    """The same for items of many rows, beside sequences of other sizes."""
+    c = Case((44, 0), [90, 300, 64], [70, 130, 1], 2, 2, 64, 16, dtype)
+    cache, q = handle(c.c), c.q.to(DEV)
+    want = c.run(cache).cpu()
+    c.check(want)
+    for name, where, at, value in (("page", 0, 4, len(c.c["k"])), ("length", 1, 1, 129), ("offset", 2, 2, 2 ** 30)):
+        held = [c.table.copy(), c.lengths.copy(), c.offsets.copy()]
+        held[where][(1, at) if where == 0 else at] = value
+        print(f"[attention] {name} {dtype}", flush=True)
+        out = torch.full(q.shape, 5.0, device=DEV, dtype=dtype)
+        got = binding.q8_cache_attention(q, cache, *(dev(x) for x in held), alpha=c.alpha, out=out).cpu()
+        assert torch.equal(got[:70], want[:70])
+        if where == 2:
+            assert bool((got[70:] == 5).all())
+        else:
+            assert bool(torch.isnan(got[70:200]).all()) and torch.equal(got[200], want[200])
+
+
+def test_rows_given_to_many_sequences():
+    """Offsets that go back and forth give the same rows to several sequences:
+    alike, they give what one of them gives."""
+    c = Case(45, [200], [40], 2, 4, 64, 16, torch.float32)
+    table, lengths, _ = c.held()
+    n = 601
+    offsets = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    offsets[1::2] = 40
+    c.check(binding.q8_cache_attention(c.q.to(DEV), handle(c.c), table.repeat(n, 1), lengths.repeat(n), offsets, alpha=c.alpha))
+
+
+@pytest.mark.parametrize("page", [64, 256, 1024])
+@pytest.mark.parametrize("columns", [1024, 2048])
+def test_tables_at_the_border_of_one_launch(columns, page):
+    """Tables of up to 1024 tokens are taken whole, longer ones in parts; every page size."""
+    for length in (columns, columns - 1, 1023):
+        c = Case((46, columns, page, length), [length, 1], [1, 1], 1, 4, 128, page, torch.bfloat16)
+        c.table = np.pad(c.table, ((0, 0), (0, columns)), constant_values=-1)[:, :columns // page]
+        print(f"[attention] {length} of {columns} tokens, pages of {page}", flush=True)
+        c.check(c.run())
+
+
+def test_shared_pages():
+    """Sequences that share the pages of a common beginning read them as their own."""
+    c = Case(47, [150, 130, 140], [1, 2, 1], 2, 4, 64, 32, torch.float16)
+    c.table[1:, :4] = c.table[0, :4]
+    c.check(c.run())
+
+
 def test_table_entries_past_the_tokens_are_not_read():
     c = Case(35, [20, 65], [1, 2], 1, 2, 128, 16, torch.float32)
     want = c.run()
