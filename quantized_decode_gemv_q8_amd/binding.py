@@ -502,7 +502,7 @@ def _interleaved(a, b):
     if a.dim() != 3 or b.dim() != 3:
         return False
     pitch = a.stride(0) * a.element_size()
-    if pitch != b.stride(0) * b.element_size():
+    if pitch == 0 or pitch != b.stride(0) * b.element_size():
         return False
     between = (b.data_ptr() - a.data_ptr()) % pitch
     return between >= _span(a[0])[1] - _span(a[0])[0] and pitch - between >= _span(b[0])[1] - _span(b[0])[0]

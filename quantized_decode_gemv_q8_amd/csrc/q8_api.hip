@@ -809,8 +809,10 @@ constexpr double kAttnMostUnits = 1125899906842624.0;  // 2^50
 constexpr int kAttnMostHeads = 1 << 24;
 
 // Sequences that the table bounds to this many tokens are not split: one
-// workgroup takes all keys of an item, and the second launch that joins parts
-// is saved.
+// workgroup of 8 waves takes all keys of an item, and the second launch that
+// joins parts is saved.  One sequence of 512 keys: 12.6 us of device time, 13.0
+// split over workgroups; of 1024 keys: 15.9 and 13.5, but the second launch is
+// 3.3 us of the host's time.
 constexpr int64_t kAttnWholeTokens = 1024;
 // What an item of few rows costs besides its keys (its query, its first loads'
 // latency and its sums' way out), in units of kAttnStep keys, when work is
@@ -821,6 +823,17 @@ constexpr int kAttnItemCost = 2;
 AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
   AttnPlan p = {};
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
+  // The smallest items that hold an average sequence's rows of a head; past 32,
+  // the kernel whose waves share keys.  24 sequences of 4096 keys, us by the rows
+  // of an item:
+  //    4 rows, dim  64, f32     4: 41.9    8: 42.8   16: 44.9
+  //    4 rows, dim 128, f32     4: 45.7    8: 45.4   16: 44.7
+  //    8 rows, dim  64, f32     8: 43.5   16: 45.2   32: 66.4
+  //   16 rows, dim 128, f32     8: 76.0   16: 48.1   32: 64.3
+  //   32 rows, dim 128, f32    16: 80.3   32: 70.5   64: 102.7
+  //   40 rows, dim 128, bf16   16: 99.7   32: 90.5   64: 79.9   128: 82.1
+  //   72 rows, dim 128, bf16   32: 129.8  64: 139.2  128: 104.4
+  //  128 rows, dim 128, f16    32: 162.8  64: 159.9  128: 149.9
   // The instances for 4 and 8 rows do not fit the registers at dim 256.
   p.tile = mean <= 4 && dim <= 128                 ? 4
            : mean <= 8 && dim <= 128               ? 8
@@ -1035,7 +1048,7 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
   const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
   a.items = pl.split ? reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256) : nullptr;
   a.unit_shift = pl.unit_shift;
-  a.half_rows = pl.tile == 128 ? 64 : 0;
+  a.half_rows = pl.tile == 128 ? 64 : 0;  // rows of one of the two row tiles a wave has
   a.item_cost = pl.item_cost;
   a.few_units = pl.most_units < (double)kIndexLimit;
   if (log_debug())

@@ -3,18 +3,19 @@
 // over the tokens j that the row sees, in one pass with a running maximum m
 // and running sums.
 //
-// Arithmetic.  Codes are exact in bf16 (|code| <= 128 has at most 8 bits), and
-// the k-slice of v_mfma_f32_16x16x32_bf16 is exactly one 32-channel block, so
-//   * scores: q is cut into bf16 parts that add up to it exactly (1 part for
-//     bf16, 2 for f16, 3 for f32; cut by truncation, so no part overflows); a
-//     block's unscaled partial comes out of the matrix core and is multiplied
-//     by the key's scale once, in f32;
+// Arithmetic.  The k-slice of v_mfma_f32_16x16x32 is exactly one 32-channel
+// block, and codes (|code| <= 128) are exact in f16 and bf16, so
+//   * scores: q is cut into f16 parts (1 for bf16 and f16 rows, 2 for f32), each
+//     row scaled by a power of two so that f16 holds it; a block's unscaled
+//     partial comes out of the matrix core and is multiplied by the key's scale
+//     once, in f32;
 //   * output: the value scale depends on the key and the block, so it is
-//     multiplied into the weight, p_j s_jb, which is cut into bf16 parts (2:
-//     exact to 2^-16, for bf16 and f16 outputs; 3: exact, for f32) against the
-//     exact codes.
-// Maxima, sums and outputs are f32 throughout; the only rounding beyond f32 is
-// the last one to the output's type.
+//     multiplied into the weight, p_j s_jb, which is cut into bf16 parts against
+//     the exact codes (2 for bf16 and f16 rows: 2^-16; 3 for f32: exact).  bf16,
+//     not f16, since the product spans f32's range.  Items of many bf16 rows
+//     take one f16 part instead where the value scales allow it (2^-11, an
+//     eighth of the output's own step).
+// Maxima, sums, weights and outputs are f32 throughout.
 //
 // Layout.  The scores are computed transposed, S^T = K Q^T, and so is the
 // output, O^T = V^T P^T: lane l then holds, for its row (l % 16), the weights
@@ -22,18 +23,30 @@
 // product needs from it when its k index is read as those keys.  Weights never
 // leave their lane, a row's maximum is two cross-lane steps, and the cache's
 // pair order lets K, V and their scales go from memory to registers with no
-// shared memory between.  Scales arrive one per lane and are broadcast within
-// the 16-lane group by DPP.
+// shared memory between.
+//
+// Three kernels share this.  Attn (16 or 32 rows): every wave takes its own
+// keys.  AttnFew (4 or 8 rows): the same, with the lanes that the missing rows
+// leave idle put to the weights' work.  attention_wide_kernel (64 or 128 rows):
+// the waves take the same keys and different rows, operands go through LDS.
 //
 // Work.  An item is a sequence's tile of rows for one head of the cache; its
-// keys are cut into units (of 128, 32 for each wave, or one unit with all of a
-// short sequence).  The units of all items
-// form one list that is dealt to the workgroups in equal contiguous runs, so
-// sequences of all lengths load the device evenly.  A workgroup that has all
-// of an item's units writes the rows; otherwise it leaves sums, maxima and
-// weights, which a second kernel joins in key order (so results do not depend
-// on timing).  Lengths and offsets are read on the device: a captured graph
-// follows them.
+// keys are cut into units (of 128, or one unit with all of a short sequence).
+// The units of all items form one list that is dealt to the workgroups in equal
+// contiguous runs, so sequences of all lengths load the device evenly.  A
+// workgroup that has all of an item's units writes the rows; otherwise it
+// leaves sums, maxima and weights, which a second kernel joins in key order (so
+// results do not depend on timing).  Lengths and offsets are read on the
+// device: a captured graph follows them.
+//
+// What bounds it.  Few rows: memory.  With 4 rows of f32 per head, dim 128, time
+// grows by 1 us per 5.85 MB of cache (a large copy moves 4.7 TB/s, a large
+// read 6.15); a batch of 32 ragged sequences (316 MB) takes 64 us and its join
+// 5, two sequences of 131072 keys (604 MB) 112 and 8.  From 16 rows on:
+// vector instructions, for the codes' conversion, the exponentials and the
+// weights' parts, some 2 per score and matrix instruction of 16 cycles; 68 GFLOP of
+// bf16 trees take 150 us (0.45 PFLOP/s), 16 GFLOP of f32 pieces of prompts 80
+// (0.2 PFLOP/s, two parts of q and three of the weights).
 #pragma once
 
 #include <type_traits>
@@ -54,7 +67,8 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 template <RowType T>
 struct AttnElem;
 // kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalf: with
-// many rows, one f16 part instead, which is 8 times finer than a bf16 output.
+// many rows, one f16 part instead, which is 8 times finer than a bf16 output
+// (68 GFLOP of trees: 159 us, 185 with two bf16 parts).
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
@@ -178,9 +192,9 @@ __device__ __forceinline__ void fetch_query(const AttnArgs &p, int t, int head, 
 }
 
 // Its parts, scaled by a power of two that brings the row's largest channel to
-// 2^14 .. 2^15 so that f16 holds them: one part is exact for bf16 and f16 rows,
-// two are to 2^-23 for f32 (channels below 2^-38 of the largest lose bits that
-// no f32 sum would keep).  Returns what undoes the scaling.  A row that is not
+// 2^14 .. 2^15 so that f16 holds them: one part is exact for bf16 and f16 rows
+// (channels below 2^-32 of the largest lose bits that no f32 sum would keep), two
+// are to 2^-23 for f32.  Returns what undoes the scaling.  A row that is not
 // `in` is zeros.
 template <RowType T, int DIM>
 __device__ __forceinline__ float cut_query(const QueryRow<T, DIM> &from, bool in,
@@ -263,7 +277,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return rest >= b ? q + 1 : q;
 }
 
-struct Run0 {  // where a workgroup's run begins
+struct RunStart {  // where a workgroup's run begins
   int b;
   Seq seq;        // sequence b
   int64_t rest;   // units into sequence b
@@ -273,7 +287,7 @@ struct Run0 {  // where a workgroup's run begins
 
 // Every wave sums the sequences' units, a stretch of them per lane, and finds
 // its workgroup's share.
-__device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int lane) {
+__device__ __forceinline__ RunStart find_run(const AttnArgs &p, int wg, int wgs, int lane) {
   const int64_t heads = (int64_t)p.c.heads * p.subs;
   const int per = (p.s.seqs + 63) / 64;
   const int b0 = min(lane * per, p.s.seqs), b1 = min(b0 + per, p.s.seqs);
@@ -300,7 +314,7 @@ __device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int
       if (lane >= d) upto += other;
     }
   }
-  Run0 r;
+  RunStart r;
   r.total = (int64_t)((uint64_t)__builtin_amdgcn_readlane((uint32_t)((uint64_t)upto >> 32), 63) << 32 |
                       (uint32_t)__builtin_amdgcn_readlane((uint32_t)upto, 63));
   r.wgs = (int)(r.total < wgs ? r.total : wgs);
@@ -331,7 +345,7 @@ __device__ __forceinline__ Run0 find_run(const AttnArgs &p, int wg, int wgs, int
 }
 
 // The workgroup whose run holds unit u.
-__device__ __forceinline__ int wg_of(int64_t u, const Run0 &r) {
+__device__ __forceinline__ int wg_of(int64_t u, const RunStart &r) {
   return (int)quotient((u + 1) * r.wgs - 1, r.total);
 }
 
@@ -670,7 +684,9 @@ struct Attn {
   }
 };
 
-// The same for items of at most 16 / PACK rows (one new token of a small group):
+// The same for items of at most 16 / PACK rows (one new token of a small group;
+// 24 sequences of 4096 keys, dim 64, 4 rows of f32: 41.9 us, 44.9 with 16-row
+// items; one sequence of 1000 keys, dim 128: 16.2 and 16.9):
 // the query's columns repeat PACK times across the matrix operand, so that the
 // lanes of a row's repeats hold the same scores, and each keeps a PACK-th of the
 // keys (KPL).  Exponentials, weights and their parts, most of the other
@@ -920,7 +936,7 @@ __device__ __forceinline__ void walk_shares(const AttnArgs &p, int slot_rows, in
   // Neighbouring runs, which may share keys or an item, on one XCD.
   const int per_xcd = gridDim.x / kXcds;
   const int wg = gridDim.x % kXcds == 0 ? (int)(blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds : (int)blockIdx.x;
-  const Run0 run = find_run(p, wg, gridDim.x, tid & 63);
+  const RunStart run = find_run(p, wg, gridDim.x, tid & 63);
   if (tid == 0 && p.items != nullptr) p.items[wg].valid = 0;
   if (wg >= run.wgs) return;
 
@@ -1166,7 +1182,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? kAttnWgsPerCu : 1) void at
 
 // ---------------------------------------------------------------- many rows
 
-// The same for items of more rows (trees, prompts): up to 64 * RT rows, 16 * RT
+// The same for items of more rows (trees, prompts; 24 sequences of 4096 keys, 72
+// rows of bf16, dim 128: 104 us, 130 with 32-row items): up to 64 * RT rows, 16 * RT
 // for each wave, and all four waves take the same keys.  Converting the codes
 // costs as much as the rest of the work on 32 rows, so a workgroup does it
 // once: per step of 64 keys each wave loads 16 keys' codes, converts them and
@@ -1557,24 +1574,30 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 
 // ---------------------------------------------------------------- joining the parts
 
-// Rows that a wave of the join takes: four channels of a row per lane.
+// Rows that a wave of the join takes: four channels of a row per lane (one row
+// per wave took 28 us instead of 14 for 128-row items of dim 64).  The parts are at
+// most two slots per workgroup, 68 MB for 128 rows of dim 128, and a join of
+// those takes 20 us.
 constexpr int join_rows(int dim) { return 256 / dim; }
 
-// Workgroup (w, y): the split item that workgroup w began, and its y-th run of
-// kWaves * join_rows rows; parts are taken in key order.
+// Workgroup (y, w): the split item that workgroup w began, and its y-th run of
+// kWaves * join_rows rows; parts are taken in key order.  Runs come first in the
+// grid: split items often begin every 2nd, 4th ... workgroup, and with w first
+// they would all land on a few of the XCDs.
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;
-  const AttnItem it = p.items[blockIdx.x];
+  const int first = blockIdx.y;
+  const AttnItem it = p.items[first];
   if (!it.valid) return;
   constexpr int LANES = 64 / join_rows(DIM);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & (LANES - 1);
-  const int live = it.tokens * it.heads, rho0 = (blockIdx.y * kWaves + wave) * join_rows(DIM);
+  const int live = it.tokens * it.heads, rho0 = (blockIdx.x * kWaves + wave) * join_rows(DIM);
   if (rho0 >= live) return;
   const bool mine = rho0 + lane / LANES < live;
   const int rho = mine ? rho0 + lane / LANES : rho0;
   const int64_t size = attn_slot_floats(slot_rows, DIM);
-  const int first = blockIdx.x, parts = it.last - first + 1;
+  const int parts = it.last - first + 1;
   // Contributor k: the first one's slot 1, then slot 0 of the following ones.
   const float *base = p.partial + (2 * (int64_t)first + 1) * size;
   auto part = [&](int k) { return k == 0 ? base : p.partial + 2 * (int64_t)(first + k) * size; };
@@ -1637,7 +1660,7 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
     hipLaunchKernelGGL((attention_kernel<T, DIM, ROWS, 4>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
-  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((unsigned)wgs, (ROWS + kWaves * join_rows(DIM) - 1) / (kWaves * join_rows(DIM))),
+  hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((ROWS + kWaves * join_rows(DIM) - 1) / (kWaves * join_rows(DIM)), (unsigned)wgs),
                      dim3(kThreads), 0, stream, a, ROWS);
   return hipGetLastError();
 }
