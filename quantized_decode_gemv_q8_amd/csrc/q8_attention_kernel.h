@@ -42,7 +42,7 @@
 // What bounds it.  Few rows: memory.  With 4 rows of f32 per head, dim 128, time
 // grows by 1 us per 5.85 MB of cache (a large copy moves 4.7 TB/s, a large
 // read 6.15); a batch of 32 ragged sequences (316 MB) takes 64 us and its join
-// 5, two sequences of 131072 keys (604 MB) 112 and 8.  From 16 rows on:
+// 5, two sequences of 131072 keys (604 MB) 110 and 7.  From 16 rows on:
 // vector instructions, for the codes' conversion, the exponentials and the
 // weights' parts, some 2 per score and matrix instruction of 16 cycles; 68 GFLOP of
 // bf16 trees take 150 us (0.45 PFLOP/s), 16 GFLOP of f32 pieces of prompts 80
@@ -68,7 +68,7 @@ template <RowType T>
 struct AttnElem;
 // kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalf: with
 // many rows, one f16 part instead, which is 8 times finer than a bf16 output
-// (68 GFLOP of trees: 159 us, 185 with two bf16 parts).
+// (68 GFLOP of trees: 159 us, 185 with two bf16 parts, the join then 26 of each).
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
@@ -1575,15 +1575,14 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 // ---------------------------------------------------------------- joining the parts
 
 // Rows that a wave of the join takes: four channels of a row per lane (one row
-// per wave took 28 us instead of 14 for 128-row items of dim 64).  The parts are at
-// most two slots per workgroup, 68 MB for 128 rows of dim 128, and a join of
-// those takes 20 us.
+// per wave took 28 us instead of 14 for 128-row items of dim 64).
 constexpr int join_rows(int dim) { return 256 / dim; }
 
 // Workgroup (y, w): the split item that workgroup w began, and its y-th run of
 // kWaves * join_rows rows; parts are taken in key order.  Runs come first in the
 // grid: split items often begin every 2nd, 4th ... workgroup, and with w first
-// they would all land on a few of the XCDs.
+// they would all land on a few of the XCDs (512 slots of 128 rows of dim 128, 34
+// MB: 20 us instead of 10).
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;
@@ -1597,16 +1596,22 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, in
   const bool mine = rho0 + lane / LANES < live;
   const int rho = mine ? rho0 + lane / LANES : rho0;
   const int64_t size = attn_slot_floats(slot_rows, DIM);
-  const int parts = it.last - first + 1;
+  const int parts = __builtin_amdgcn_readfirstlane(it.last) - first + 1;
   // Contributor k: the first one's slot 1, then slot 0 of the following ones.
   const float *base = p.partial + (2 * (int64_t)first + 1) * size;
   auto part = [&](int k) { return k == 0 ? base : p.partial + 2 * (int64_t)(first + k) * size; };
-  // Four parts' rows in flight; past the last one the last one again, unused.
-  v4f y[4];
+  // Eight parts' rows in flight, where there are more than two (32 parts: 7 us,
+  // 8 with four); past the last one the last one again, unused.
+  constexpr int AHEAD = 8;
+  v4f y[AHEAD];
   auto load = [&](int k) {
+    auto some = [&](auto from, auto to) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      y[u] = *reinterpret_cast<const v4f *>(part(min(k + u, parts - 1)) + (int64_t)rho * DIM + c * 4);
+      for (int u = decltype(from)::value; u < decltype(to)::value; ++u)
+        y[u] = *reinterpret_cast<const v4f *>(part(min(k + u, parts - 1)) + (int64_t)rho * DIM + c * 4);
+    };
+    some(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+    if (k + 2 < parts) some(std::integral_constant<int, 2>{}, std::integral_constant<int, AHEAD>{});
   };
   load(0);
   // The largest maximum, then the parts' factors, a lane per part.
@@ -1627,7 +1632,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, in
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       if (k + u >= parts) break;
       const int from_lane = (k + u) & (LANES - 1);
       const float g = __shfl(f, from_lane, LANES);
@@ -1635,7 +1640,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, in
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] += g * y[u][i];
     }
-    k += 4;
+    k += AHEAD;
     if (k >= parts) break;
     load(k);
   }
