@@ -810,9 +810,9 @@ constexpr int kAttnMostHeads = 1 << 24;
 
 // Sequences that the table bounds to this many tokens are not split: one
 // workgroup of 8 waves takes all keys of an item, and the second launch that
-// joins parts is saved.  One sequence of 512 keys: 12.6 us of device time, 13.0
-// split over workgroups; of 1024 keys: 15.9 and 13.5, but the second launch is
-// 3.3 us of the host's time.
+// joins parts is saved.  One sequence of 1023 keys, in a run of calls: 15.7 us,
+// 17.5 split over workgroups; the same calls captured in a graph, where the gap
+// between the two kernels is smaller: 16.2 and 12.4.
 constexpr int64_t kAttnWholeTokens = 1024;
 // What an item of few rows costs besides its keys (its query, its first loads'
 // latency and its sums' way out), in units of kAttnStep keys, when work is
