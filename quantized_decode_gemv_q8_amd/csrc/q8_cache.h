@@ -47,6 +47,7 @@ struct CacheRowsArgs {
   Seqs s;
   void *k, *v;                 // rows of [heads, dim] elements (read: written)
   int64_t k_stride, v_stride;  // elements between rows
+  int row0;                    // first row of the launch (set by the launcher)
 };
 hipError_t launch_cache_write(const CacheRowsArgs &a, RowType type, hipStream_t stream);
 hipError_t launch_cache_read(const CacheRowsArgs &a, RowType type, hipStream_t stream);
@@ -56,6 +57,7 @@ struct CacheKeepArgs {
   Seqs s;
   const int *keep;  // [seqs, width]
   int width;
+  int seq0;  // first sequence of the launch (set by the launcher)
 };
 hipError_t launch_cache_keep(const CacheKeepArgs &a, hipStream_t stream);
 

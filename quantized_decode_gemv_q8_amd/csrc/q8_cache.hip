@@ -21,6 +21,8 @@
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
+#include <algorithm>
+
 #include "q8_cache.h"
 
 namespace q8 {
@@ -153,8 +155,9 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
   typedef typename CodeWord<DIM>::type Word;
   constexpr int NB = DIM / 32;
   const int lane = threadIdx.x & 63;
-  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
-  if (t >= p.s.rows) return;
+  const uint32_t row = __builtin_amdgcn_readfirstlane(p.row0 + blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (row >= (uint32_t)p.s.rows) return;  // unsigned: the last workgroup may pass 2^31
+  const int t = (int)row;
   const int group = lane >> 4, j = lane & 15;
   const int nrows = 2 * p.c.heads;
   const int r0 = blockIdx.y * kRowsPerWave + group;
@@ -164,11 +167,11 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
   for (int q = 0; q < kRowsPerGroup; ++q) {
     const int r = r0 + 4 * q;
     const int rr = r < nrows ? r : 0;
-    const E *row = static_cast<const E *>((rr & 1) ? p.v : p.k) + (int64_t)t * ((rr & 1) ? p.v_stride : p.k_stride) +
+    const E *from = static_cast<const E *>((rr & 1) ? p.v : p.k) + (int64_t)t * ((rr & 1) ? p.v_stride : p.k_stride) +
                    (int64_t)(rr >> 1) * DIM;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Pair<E> v = *reinterpret_cast<const Pair<E> *>(row + 32 * b + 2 * j);
+      const Pair<E> v = *reinterpret_cast<const Pair<E> *>(from + 32 * b + 2 * j);
       x[q][b][0] = Elem<T>::to_float(v.x);
       x[q][b][1] = Elem<T>::to_float(v.y);
     }
@@ -207,11 +210,11 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
       out.c[2 * b + 1] = (int8_t)(int)c1;
     }
     if (r < nrows) {
-      const int64_t row = base + ((int64_t)(r >> 1) << p.c.page_shift);
+      const int64_t at_head = base + ((int64_t)(r >> 1) << p.c.page_shift);
       int8_t *codes = (r & 1) ? p.c.V : p.c.K;
       float *scales = (r & 1) ? p.c.VS : p.c.KS;
-      *reinterpret_cast<Word *>(codes + row * DIM + j * (DIM / 16)) = out.w;
-      if (j < NB) scales[row * NB + j] = mine;
+      *reinterpret_cast<Word *>(codes + at_head * DIM + j * (DIM / 16)) = out.w;
+      if (j < NB) scales[at_head * NB + j] = mine;
     }
   }
 }
@@ -226,8 +229,9 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
   typedef typename CodeWord<DIM>::type Word;
   constexpr int NB = DIM / 32;
   const int lane = threadIdx.x & 63;
-  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
-  if (t >= p.s.rows) return;
+  const uint32_t row = __builtin_amdgcn_readfirstlane(p.row0 + blockIdx.x * kWaves + (threadIdx.x >> 6));
+  if (row >= (uint32_t)p.s.rows) return;  // unsigned: the last workgroup may pass 2^31
+  const int t = (int)row;
   const int group = lane >> 4, j = lane & 15;
   const int nrows = 2 * p.c.heads;
   const int r0 = blockIdx.y * kRowsPerWave + group;
@@ -245,9 +249,9 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
     } in;
     float s[NB];
     if (base >= 0) {
-      const int64_t row = base + ((int64_t)(r >> 1) << p.c.page_shift);
-      in.w = *reinterpret_cast<const Word *>(((r & 1) ? p.c.V : p.c.K) + row * DIM + j * (DIM / 16));
-      const float *scales = ((r & 1) ? p.c.VS : p.c.KS) + row * NB;
+      const int64_t at_head = base + ((int64_t)(r >> 1) << p.c.page_shift);
+      in.w = *reinterpret_cast<const Word *>(((r & 1) ? p.c.V : p.c.K) + at_head * DIM + j * (DIM / 16));
+      const float *scales = ((r & 1) ? p.c.VS : p.c.KS) + at_head * NB;
 #pragma unroll
       for (int b = 0; b < NB; ++b) s[b] = scales[b];
     } else {  // no such token: NaN, never a wrong value
@@ -255,14 +259,14 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) s[b] = NAN;
     }
-    E *row = static_cast<E *>((r & 1) ? p.v : p.k) + (int64_t)t * ((r & 1) ? p.v_stride : p.k_stride) +
+    E *out = static_cast<E *>((r & 1) ? p.v : p.k) + (int64_t)t * ((r & 1) ? p.v_stride : p.k_stride) +
              (int64_t)(r >> 1) * DIM;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       typedef E Two __attribute__((ext_vector_type(2)));
       typedef Two Unaligned __attribute__((aligned(sizeof(E))));
       const Two v = {Elem<T>::from_float((float)in.c[2 * b] * s[b]), Elem<T>::from_float((float)in.c[2 * b + 1] * s[b])};
-      Unaligned *to = reinterpret_cast<Unaligned *>(row + 32 * b + 2 * j);
+      Unaligned *to = reinterpret_cast<Unaligned *>(out + 32 * b + 2 * j);
       if constexpr (PAST)
         __builtin_nontemporal_store(v, to);
       else
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(kThreads) void cache_keep_kernel(CacheKeepArgs p) {
   typedef typename CodeWord<DIM>::type Word;
   constexpr int NB = DIM / 32;
   constexpr int kChunk = kThreads / 16;  // 16-lane groups: one kept token each
-  const int b = blockIdx.x;
+  const int b = p.seq0 + blockIdx.x;
   const int tid = threadIdx.x;
   const int group = tid >> 4, j = tid & 15;
   const Seq seq = seq_at(p.s, b);
@@ -339,9 +343,12 @@ __global__ __launch_bounds__(kThreads) void cache_keep_kernel(CacheKeepArgs p) {
   }
 }
 
+// Workgroups of one launch: a grid holds less than 2^32 threads in a direction.
+constexpr int kMostGroups = 1 << 22;
+
 template <RowType T>
-hipError_t launch_rows(const CacheRowsArgs &a, bool write, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.s.rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kRowsPerWave - 1) / kRowsPerWave));
+hipError_t launch_rows(const CacheRowsArgs &a, int rows, bool write, hipStream_t stream) {
+  const dim3 grid((unsigned)((rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kRowsPerWave - 1) / kRowsPerWave));
   const bool past = 2 * (int64_t)sizeof(typename Elem<T>::type) * a.s.rows * a.c.heads * a.c.dim > kPastCachesBytes;
 #define Q8_LAUNCH(DIM)                                                                                   \
   case DIM:                                                                                              \
@@ -361,13 +368,19 @@ hipError_t launch_rows(const CacheRowsArgs &a, bool write, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_typed(const CacheRowsArgs &a, RowType type, bool write, hipStream_t stream) {
-  switch (type) {
-    case kRowF32: return launch_rows<kRowF32>(a, write, stream);
-    case kRowBf16: return launch_rows<kRowBf16>(a, write, stream);
-    case kRowF16: return launch_rows<kRowF16>(a, write, stream);
+hipError_t launch_typed(CacheRowsArgs a, RowType type, bool write, hipStream_t stream) {
+  for (int64_t row0 = 0; row0 < a.s.rows; row0 += kMostGroups * kWaves) {
+    a.row0 = (int)row0;
+    const int rows = (int)std::min<int64_t>(a.s.rows - row0, kMostGroups * kWaves);
+    hipError_t e = hipErrorInvalidValue;
+    switch (type) {
+      case kRowF32: e = launch_rows<kRowF32>(a, rows, write, stream); break;
+      case kRowBf16: e = launch_rows<kRowBf16>(a, rows, write, stream); break;
+      case kRowF16: e = launch_rows<kRowF16>(a, rows, write, stream); break;
+    }
+    if (e != hipSuccess) return e;
   }
-  return hipErrorInvalidValue;
+  return hipSuccess;
 }
 
 }  // namespace
@@ -380,15 +393,21 @@ hipError_t launch_cache_read(const CacheRowsArgs &a, RowType type, hipStream_t s
   return launch_typed(a, type, false, stream);
 }
 
-hipError_t launch_cache_keep(const CacheKeepArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.s.seqs, (unsigned)(a.c.heads < 65535 ? a.c.heads : 65535));
-  switch (a.c.dim) {
-    case 64: hipLaunchKernelGGL((cache_keep_kernel<64>), grid, dim3(kThreads), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((cache_keep_kernel<128>), grid, dim3(kThreads), 0, stream, a); break;
-    case 256: hipLaunchKernelGGL((cache_keep_kernel<256>), grid, dim3(kThreads), 0, stream, a); break;
-    default: return hipErrorInvalidValue;
+hipError_t launch_cache_keep(const CacheKeepArgs &args, hipStream_t stream) {
+  CacheKeepArgs a = args;
+  hipError_t e = hipSuccess;
+  for (int64_t seq0 = 0; seq0 < a.s.seqs && e == hipSuccess; seq0 += kMostGroups) {
+    a.seq0 = (int)seq0;
+    const dim3 grid((unsigned)std::min<int64_t>(a.s.seqs - seq0, kMostGroups), (unsigned)std::min(a.c.heads, 65535));
+    switch (a.c.dim) {
+      case 64: hipLaunchKernelGGL((cache_keep_kernel<64>), grid, dim3(kThreads), 0, stream, a); break;
+      case 128: hipLaunchKernelGGL((cache_keep_kernel<128>), grid, dim3(kThreads), 0, stream, a); break;
+      case 256: hipLaunchKernelGGL((cache_keep_kernel<256>), grid, dim3(kThreads), 0, stream, a); break;
+      default: return hipErrorInvalidValue;
+    }
+    e = hipGetLastError();
   }
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace q8

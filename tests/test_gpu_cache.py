@@ -266,3 +266,40 @@ def test_offsets_past_32_bits():
     out = binding.q8_cache_attention(q.to(DEV), cache, *held)
     ref, spread, size = oc.attention(qf, want, np.array([[0, 1]]), lengths, offsets, dim ** -0.5)
     assert (np.abs(out.cpu().numpy() - ref) <= cc.attention_bound(ref, spread, size, torch.float32)).all()
+
+
+def test_more_rows_and_sequences_than_one_launch_takes():
+    """2^24 rows are a launch of writes and reads, 2^22 sequences one of keep."""
+    rows, page = (1 << 24) + 5, 1024
+    pages = -(-rows // page)
+    cache = binding.Q8Cache.empty(pages, 1, page, 64, DEV)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    k = torch.randn((rows, 1, 64), generator=gen, device=DEV, dtype=torch.float16)
+    held = (torch.arange(pages, dtype=torch.int32, device=DEV)[None],
+            torch.tensor([rows], dtype=torch.int32, device=DEV), torch.tensor([0, rows], dtype=torch.int32, device=DEV))
+    print("[cache] rows past one launch", flush=True)
+    binding.q8_cache_write(cache, k, k, *held)
+    rk, rv = binding.q8_cache_read(cache, *held, rows, dtype=torch.float16)
+    at = torch.cat([torch.arange(8), torch.arange((1 << 24) - 8, rows)])
+    kf = k[at.to(DEV)].float().cpu().numpy()
+    small = {"k": np.zeros((1, 1, 32, 64), np.int8), "k_scale": np.zeros((1, 1, 32, 2), np.float32)}
+    small["v"], small["v_scale"] = small["k"].copy(), small["k_scale"].copy()
+    one = (np.array([[0]], np.int32), np.array([len(at)], np.int32), np.array([0, len(at)], np.int32))
+    oc.write(small, kf, kf, *one)
+    want = torch.from_numpy(oc.read(small, *one)[0].astype(np.float32)).half()
+    assert torch.equal(rk[at.to(DEV)].cpu(), want) and torch.equal(rk, rv)
+    far = (rk - k).abs().amax().item()  # half a step of the largest block, and f16's rounding of both
+    assert far <= float(k.abs().amax()) * (1 / 254 + 2 ** -9)
+
+    seqs = (1 << 22) + 3
+    table = torch.zeros((seqs, 1), dtype=torch.int32, device=DEV)
+    table[-3:, 0] = torch.arange(1, 4, device=DEV)
+    lengths = torch.zeros(seqs, dtype=torch.int32, device=DEV)
+    lengths[-3:] = 2
+    offsets = torch.zeros(seqs + 1, dtype=torch.int32, device=DEV)
+    offsets[-3:] = torch.tensor([2, 4, 6], device=DEV)
+    before = cache.k[:4, 0, :2].clone()
+    print("[cache] sequences past one launch", flush=True)
+    binding.q8_cache_keep(cache, table, lengths, offsets, torch.ones((seqs, 1), dtype=torch.int32, device=DEV))
+    assert torch.equal(cache.k[1:4, 0, 0], before[1:, 1]) and torch.equal(cache.k[1:4, 0, 1], before[1:, 1])
+    assert torch.equal(cache.k[0, 0, :2], before[0])
