@@ -830,7 +830,7 @@ AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows
   //    4 rows, dim 128, f32     4: 45.7    8: 45.4   16: 44.7
   //    8 rows, dim  64, f32     8: 43.5   16: 45.2   32: 66.4
   //   16 rows, dim 128, f32     8: 76.0   16: 48.1   32: 64.3
-  //   32 rows, dim 128, f32    16: 80.3   32: 70.5   64: 102.7
+  //   32 rows, dim 128, bf16   16: 78.4   32: 56.7   64: 76.9
   //   40 rows, dim 128, bf16   16: 99.7   32: 90.5   64: 79.9   128: 82.1
   //   72 rows, dim 128, bf16   32: 129.8  64: 139.2  128: 104.4
   //  128 rows, dim 128, f16    32: 162.8  64: 159.9  128: 149.9

@@ -12,9 +12,9 @@
 //   * output: the value scale depends on the key and the block, so it is
 //     multiplied into the weight, p_j s_jb, which is cut into bf16 parts against
 //     the exact codes (2 for bf16 and f16 rows: 2^-16; 3 for f32: exact).  bf16,
-//     not f16, since the product spans f32's range.  Items of many bf16 rows
-//     take one f16 part instead where the value scales allow it (2^-11, an
-//     eighth of the output's own step).
+//     not f16, since the product spans f32's range.  Items of many rows take f16
+//     parts instead where the value scales allow it: one for bf16 rows (2^-11,
+//     an eighth of the output's own step), two for f32 rows (2^-21).
 // Maxima, sums, weights and outputs are f32 throughout.
 //
 // Layout.  The scores are computed transposed, S^T = K Q^T, and so is the
@@ -45,8 +45,8 @@
 // 5, two sequences of 131072 keys (604 MB) 110 and 7.  From 16 rows on:
 // vector instructions, for the codes' conversion, the exponentials and the
 // weights' parts, some 2 per score and matrix instruction of 16 cycles; 68 GFLOP of
-// bf16 trees take 150 us (0.45 PFLOP/s), 16 GFLOP of f32 pieces of prompts 80
-// (0.2 PFLOP/s, two parts of q and three of the weights).
+// bf16 trees take 150 us (0.45 PFLOP/s), 16 GFLOP of f32 pieces of prompts 77
+// (0.2 PFLOP/s, two parts of q and two of the weights).
 #pragma once
 
 #include <type_traits>
@@ -66,26 +66,26 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 template <RowType T>
 struct AttnElem;
-// kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalf: with
-// many rows, one f16 part instead, which is 8 times finer than a bf16 output
-// (68 GFLOP of trees: 159 us, 185 with two bf16 parts, the join then 26 of each).
+// kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalfParts: with
+// many rows, so many f16 parts instead (0: not).  One for bf16 rows is 8 times
+// finer than their output (trees of 64 drafts over 8 x 8192 keys: 185 us with
+// two bf16 parts, 159 so).  Two for f32 rows: cut to 11 bits, the rest rounded to
+// 11 bits, 2^-21 at most (24 sequences of 4096 keys, 128 rows of dim 128: 198 us
+// with three bf16 parts, 183 so).  f16 rows would need two of either.
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
-  static constexpr int kQParts = 2, kPParts = 3;
-  static constexpr bool kHalf = false;
+  static constexpr int kQParts = 2, kPParts = 3, kHalfParts = 2;
 };
 template <>
 struct AttnElem<kRowBf16> {
   typedef __bf16 type;
-  static constexpr int kQParts = 1, kPParts = 2;
-  static constexpr bool kHalf = true;
+  static constexpr int kQParts = 1, kPParts = 2, kHalfParts = 1;
 };
 template <>
 struct AttnElem<kRowF16> {
   typedef _Float16 type;
-  static constexpr int kQParts = 1, kPParts = 2;
-  static constexpr bool kHalf = false;
+  static constexpr int kQParts = 1, kPParts = 2, kHalfParts = 0;
 };
 
 template <typename E, int N>
@@ -486,15 +486,27 @@ __device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
 }
-// Eight floats as f16, rounded to the nearest.
-__device__ __forceinline__ v4u round_half(const float (&x)[8]) {
-  v4u y;
+// Parts of eight floats as f16 operands: all but the last cut, the last one
+// rounded to the nearest.
+template <int PARTS>
+__device__ __forceinline__ void split8_half(const float (&x)[8], v4u (&out)[PARTS]) {
+  float r[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const v2h h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
-    y[i] = __builtin_bit_cast(uint32_t, h);
-  }
-  return y;
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p + 1 < PARTS) {
+        out[p][i] = pack_half(r[2 * i], r[2 * i + 1]);
+        const v2h h = __builtin_bit_cast(v2h, (uint32_t)out[p][i]);
+        r[2 * i] = fmaf((float)h.x, -1.f, r[2 * i]);
+        r[2 * i + 1] = fmaf((float)h.y, -1.f, r[2 * i + 1]);
+      } else {
+        const v2h h = {(_Float16)r[2 * i], (_Float16)r[2 * i + 1]};
+        out[p][i] = __builtin_bit_cast(uint32_t, h);
+      }
+    }
 }
 // Value scales that f16 weights allow: at 2^-8 and 2^7 a weight of 2^8 still
 // has all its bits and stays below 2^15, one of 2^-6 has all its bits.
@@ -1215,8 +1227,9 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
   constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;
   constexpr int ROWS = 64 * RT, BUFS = DIM == 256 ? 1 : 2;
   constexpr int SPL = (16 * NB + 63) / 64;  // scale words a lane stages
-  constexpr bool HALF = AttnElem<T>::kHalf;
-  __shared__ WideLds<DIM, AttnElem<T>::kHalf> lds;
+  constexpr int HP = AttnElem<T>::kHalfParts;
+  constexpr bool HALF = HP > 0;
+  __shared__ WideLds<DIM, HALF> lds;
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1426,9 +1439,12 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = vs[n % 2][k / 4][k % 4] * s[rt][8 * g + k];
             if constexpr (HALF) {
-              const v4u half = round_half(w);
+              v4u parts[HP];
+              split8_half<HP>(w, parts);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) acc[rt][b][i] = mfma_f16(a[n % 2][i], half, acc[rt][b][i]);
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = HP - 1; q >= 0; --q) acc[rt][b][i] = mfma_f16(a[n % 2][i], parts[q], acc[rt][b][i]);
             } else {
               v4u parts[PP];
               split8<PP>(w, parts);

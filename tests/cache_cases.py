@@ -70,7 +70,9 @@ def attention_bound(out, spread, size, dtype):
     16 * 2^-24 size, below 1e-6 size, and a weight by that factor.  It shifts the
     numerator and the sum of weights, so it counts twice.
     Weights and sums: the weights' parts drop at most 2^-16 of a term for f16
-    rows, nothing for f32; for bf16 rows a weight may be one f16, off by at most
+    rows, nothing for f32; with many rows a weight of f32 rows may be two f16, off
+    by at most 2^-21 of itself (below 0.5e-6, which counts where few keys carry the
+    weight and the walk below is short), one of bf16 rows one f16, off by at most
     2^-11 of itself; the sum over some thousand keys is a random walk of
     f32 roundings, under 64 * 2^-24 of the terms; exp2 and the joins add a few.
     Last, half a step of the output's type.
