@@ -384,6 +384,7 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  * A query that is not finite, a key whose score is NaN or +infinity and a value
  * scale that is not finite give NaN in the rows that see them (a value scale in
  * its block of channels).
+ * With scales up to 2^60 (values up to 2^67) no sum overflows.
  * Deterministic: the order of the sums depends on the extents, the lengths and
  * offsets, never on timing.
  * Errors: as q8_cache_write; Q8_ERR_INVALID also for q_heads that is no multiple

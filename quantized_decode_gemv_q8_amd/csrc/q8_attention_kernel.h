@@ -1362,7 +1362,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 #pragma unroll
       for (int d = NB; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
       const int up = top > 0.f ? 1 - __builtin_amdgcn_frexp_expf(top) : 0;
-      near_one = ldexpf(1.f, min(max(up, -60), 60));
+      // Upwards by no more than leaves later scales of 2^60 room in the sums.
+      near_one = ldexpf(1.f, min(max(up, -60), 24));
     }
     const int tiles = (h.rows + 15) / 16;
     const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has

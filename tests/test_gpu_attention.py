@@ -153,6 +153,23 @@ def test_value_scales_of_all_sizes(spread, dim, dtype):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("news", [1, 70])
+def test_value_scales_far_apart(news, dtype):
+    """Tiny scales first and large ones later, the other way round, and a block of zeros."""
+    for first, later in ((-70, 60), (60, -70), (-30, 60)):
+        c = Case((48, news, first + 100), [300], [news], 2, 2, 64, 16, dtype)
+        where = np.zeros((len(c.c["v"]), 16), np.int64)
+        for at in range(300):
+            page, i = oc.slot_of(c.table, 16, 0, at)
+            where[page, i] = at
+        big = np.where(where < 100, first, later)[:, None, :, None]
+        c.c["v_scale"] = (c.c["v_scale"] * 2.0 ** big).astype(np.float32)
+        c.c["v_scale"][:, 1, :, 1] = 0
+        print(f"[attention] value scales 2^{first}, then 2^{later}, {news} new {dtype}", flush=True)
+        c.check(c.run())
+
+
 def test_scales_of_tokens_that_are_not_seen_change_nothing_with_many_rows():
     """Behind the last token, and of a draft that no row sees: any bits."""
     c = Case(45, [300, 90], [40, 60], 1, 4, 128, 64, torch.bfloat16, tree=True)
