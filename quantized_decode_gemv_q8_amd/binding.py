@@ -647,7 +647,9 @@ _WORKSPACE = {}
 
 
 def _attention_workspace(cache, type_, rows, q_heads, seqs):
-    key = (cache.device.index, cache.heads, cache.page_size, cache.dim, type_, rows, q_heads, seqs.seqs, seqs.max_pages)
+    # whether there are any pages counts: without, no token of the table is one
+    key = (cache.device.index, cache.pages > 0, cache.heads, cache.page_size, cache.dim, type_, rows, q_heads,
+           seqs.seqs, seqs.max_pages)
     need = _WORKSPACE.get(key)
     if need is None:
         size = ctypes.c_int64(0)

@@ -548,3 +548,16 @@ def test_a_drafting_step(dtype):
     ek, ev = oc.read(c, table, lengths, offsets)
     for got, want in ((k, ek), (v, ev)):
         assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(dtype))
+
+
+@pytest.mark.parametrize("news", [[1, 1], [70, 3]])
+def test_a_cache_without_pages_and_then_one_with_pages(news):
+    """A call on a cache that has no pages leaves nothing behind that a call of
+    the same extents on a real one would meet."""
+    c = Case((50, len(news), news[0]), [1500, 2011], news, 2, 2, 64, 32, torch.float32)
+    c.table = np.pad(c.table, ((0, 0), (0, 99 - c.table.shape[1])), constant_values=-1)
+    none = binding.Q8Cache.empty(0, 2, 32, 64, DEV)
+    print(f"[attention] no pages, then pages {news}", flush=True)
+    assert bool(torch.isnan(c.run(none)).all())
+    c.check(c.run())
+    assert bool(torch.isnan(c.run(none)).all())
