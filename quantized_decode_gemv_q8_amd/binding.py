@@ -633,12 +633,15 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
         _check_apart("out", out, (("q", q), ("table", table), ("lengths", lengths), ("offsets", offsets),
                                   ("tree", tree)))
     need = _attention_workspace(cache, _ROW_TYPES[q.dtype], rows, q_heads, seqs)
-    work = _empty_on(stream, (need,), torch.uint8, cache.device).data_ptr() if need else None
+    # Held until both of the call's kernels are enqueued: what the same stream's
+    # next owner of the memory enqueues then comes after them.
+    work = _empty_on(stream, (need,), torch.uint8, cache.device) if need else None
     mask = None
     if tree is not None:  # an empty tree still is one: no new token is seen
         mask = tree.data_ptr() if words and rows else offsets.data_ptr() & -8
     _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q0, out0,
-          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha), work, need)
+          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha),
+          None if work is None else work.data_ptr(), need)
     return out
 
 

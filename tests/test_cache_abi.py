@@ -225,3 +225,34 @@ def test_sequences_are_checked():
         binding._cache_seqs(c, table, torch.zeros(4, dtype=i32)[::2], offsets)
     with pytest.raises(ValueError, match="overlap"):
         binding._cache_seqs(c, torch.zeros(4, dtype=i32).as_strided((2, 3), (1, 1)), lengths, offsets)
+
+
+def test_attention_holds_its_workspace_until_the_call_returns(monkeypatch):
+    """The library enqueues two kernels that use it; freed before, another
+    thread's allocation on the same stream could get the same memory in between."""
+    import weakref
+    made, seen = [], []
+    empty = binding._empty_on
+
+    def tracked(*args):
+        t = empty(*args)
+        made.append((weakref.ref(t), t.dtype, t.data_ptr()))
+        return t
+
+    def call(cache, stream, what, fn, *args):
+        for ref, dtype, at in made:
+            if dtype is torch.uint8:
+                seen.append((ref() is not None, at in args))
+
+    monkeypatch.setattr(binding, "_empty_on", tracked)
+    monkeypatch.setattr(binding, "_call", call)
+    monkeypatch.setattr(binding, "_attention_workspace", lambda *args: 4096)
+    c = object.__new__(binding.Q8Cache)
+    c.device, c.heads, c.dim, c.page_size, c.pages = torch.device("cpu"), 2, 64, 16, 3
+    c._struct, c._spans = cache(), ()
+    i32 = torch.int32
+    q = torch.zeros((5, 4, 64))
+    out = binding.q8_cache_attention(q, c, torch.zeros((2, 3), dtype=i32), torch.zeros(2, dtype=i32),
+                                     torch.zeros(3, dtype=i32))
+    assert out.shape == q.shape
+    assert seen == [(True, True)]
