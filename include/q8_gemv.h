@@ -378,9 +378,7 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  *   q        f32 rows: to 2^-23 of the row's largest channel; bf16 and f16 rows: not
  *            at all (channels below 2^-32 of the row's largest lose bits)
  *   weights  (each times its value scale) f32 rows: not at all; bf16 and f16
- *            rows: to 2^-16.  Where sequences bring more than 32 rows for each head
- *            on average (new tokens times g; more than 16 if dim is 256) f32 rows: to
- *            2^-21, bf16 rows: to 2^-11
+ *            rows: to 2^-16 of itself (products below 2^-110 may lose more)
  * A query that is not finite, a key whose score is NaN or +infinity and a value
  * scale that is not finite give NaN in the rows that see them (a value scale in
  * its block of channels).

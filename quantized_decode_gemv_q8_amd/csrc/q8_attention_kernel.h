@@ -12,9 +12,9 @@
 //   * output: the value scale depends on the key and the block, so it is
 //     multiplied into the weight, p_j s_jb, which is cut into bf16 parts against
 //     the exact codes (2 for bf16 and f16 rows: 2^-16; 3 for f32: exact).  bf16,
-//     not f16, since the product spans f32's range.  Items of many rows take f16
-//     parts instead where the value scales allow it: one for bf16 rows (2^-11,
-//     an eighth of the output's own step), two for f32 rows (2^-21).
+//     not f16: the product spans f32's range, and its size says nothing about
+//     what it counts.  Where the keys with large weights hold values of zero, the
+//     smallest weights make the output, and f16 has no bits left for them.
 // Maxima, sums, weights and outputs are f32 throughout.
 //
 // Layout.  The scores are computed transposed, S^T = K Q^T, and so is the
@@ -45,8 +45,8 @@
 // 5, two sequences of 131072 keys (604 MB) 110 and 7.  From 16 rows on:
 // vector instructions, for the codes' conversion, the exponentials and the
 // weights' parts, some 2 per score and matrix instruction of 16 cycles; 68 GFLOP of
-// bf16 trees take 150 us (0.45 PFLOP/s), 16 GFLOP of f32 pieces of prompts 77
-// (0.2 PFLOP/s, two parts of q and two of the weights).
+// bf16 trees take 169 us (0.40 PFLOP/s), 16 GFLOP of f32 pieces of prompts 81
+// (0.2 PFLOP/s, two parts of q and three of the weights).
 #pragma once
 
 #include <type_traits>
@@ -66,26 +66,23 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 template <RowType T>
 struct AttnElem;
-// kQParts f16 parts of a query, kPParts bf16 parts of a weight.  kHalfParts: with
-// many rows, so many f16 parts instead (0: not).  One for bf16 rows is 8 times
-// finer than their output (trees of 64 drafts over 8 x 8192 keys: 185 us with
-// two bf16 parts, 159 so).  Two for f32 rows: cut to 11 bits, the rest rounded to
-// 11 bits, 2^-21 at most (24 sequences of 4096 keys, 128 rows of dim 128: 198 us
-// with three bf16 parts, 183 so).  f16 rows would need two of either.
+// kQParts f16 parts of a query, kPParts bf16 parts of a weight, each cut to what
+// the ones before leave: two are to 2^-16, 2^-8 of a 16-bit output's half step or
+// 2^-5, three are all of an f32.
 template <>
 struct AttnElem<kRowF32> {
   typedef float type;
-  static constexpr int kQParts = 2, kPParts = 3, kHalfParts = 2;
+  static constexpr int kQParts = 2, kPParts = 3;
 };
 template <>
 struct AttnElem<kRowBf16> {
   typedef __bf16 type;
-  static constexpr int kQParts = 1, kPParts = 2, kHalfParts = 1;
+  static constexpr int kQParts = 1, kPParts = 2;
 };
 template <>
 struct AttnElem<kRowF16> {
   typedef _Float16 type;
-  static constexpr int kQParts = 1, kPParts = 2, kHalfParts = 0;
+  static constexpr int kQParts = 1, kPParts = 2;
 };
 
 template <typename E, int N>
@@ -435,10 +432,7 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
-// HALF: for weights that go to f16 as they are.  They are kept 2^5 larger and
-// the maximum closer, so that with a scale below 2^7 they stay below 2^15.
-constexpr float kHalfSlack = 3.f, kHalfRaise = 5.f;
-template <int NRT, int NK, int NB, int PACK, bool HALF = false>
+template <int NRT, int NK, int NB, int PACK>
 __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   float top[NRT];
   bool above = false;
@@ -448,7 +442,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 #pragma unroll
     for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
     top[rt] = row_max<PACK>(top[rt]) * undo[rt];
-    above |= top[rt] > m[rt] + (HALF ? kHalfSlack : kMaxSlack);  // the first key that is seen, too
+    above |= top[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
   }
   if (__ballot(above) != 0) {
 #pragma unroll
@@ -466,7 +460,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 #pragma unroll
   for (int rt = 0; rt < NRT; ++rt) {
     // Nothing seen yet: weights are exp2(-inf) = 0.
-    const float from = (m[rt] == -INFINITY ? 0.f : m[rt]) - (HALF ? kHalfRaise : 0.f);
+    const float from = m[rt] == -INFINITY ? 0.f : m[rt];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
@@ -481,36 +475,6 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 // compiler spreads one step's operands over all steps and runs out of registers.
 __device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
-
-// Two floats as f16, cut: exact for codes.
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
-}
-// Parts of eight floats as f16 operands: all but the last cut, the last one
-// rounded to the nearest.
-template <int PARTS>
-__device__ __forceinline__ void split8_half(const float (&x)[8], v4u (&out)[PARTS]) {
-  float r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = x[i];
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (p + 1 < PARTS) {
-        out[p][i] = pack_half(r[2 * i], r[2 * i + 1]);
-        const v2h h = __builtin_bit_cast(v2h, (uint32_t)out[p][i]);
-        r[2 * i] = fmaf((float)h.x, -1.f, r[2 * i]);
-        r[2 * i + 1] = fmaf((float)h.y, -1.f, r[2 * i + 1]);
-      } else {
-        const v2h h = {(_Float16)r[2 * i], (_Float16)r[2 * i + 1]};
-        out[p][i] = __builtin_bit_cast(uint32_t, h);
-      }
-    }
-}
-// Value scales that f16 weights allow: at 2^-8 and 2^7 a weight of 2^8 still
-// has all its bits and stays below 2^15, one of 2^-6 has all its bits.
-__device__ __forceinline__ bool in_window(float s) { return s == 0.f || (s >= 0x1p-8f && s <= 0x1p7f); }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
@@ -1204,7 +1168,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? kAttnWgsPerCu : 1) void at
 // tiles are dealt to the waves in turn, so a short item still uses all four.
 constexpr int kWideKeys = 64;
 
-template <int DIM, bool HALF>
+template <int DIM>
 struct WideLds {
   static constexpr int NB = DIM / 32;
   static constexpr int BUFS = DIM == 256 ? 1 : 2;  // two workgroups must fit a CU
@@ -1214,10 +1178,6 @@ struct WideLds {
   // Value scales that are not finite are zeros in vs; bit e % 64 of word e / 64
   // marks the one of key e / NB and block e % NB of a 16-key tile.
   uint64_t gone[BUFS][4][(16 * NB + 63) / 64];
-  // For f16 weights: scales outside what they allow are zeros in vs too, and
-  // here; outside: of a 16-key tile, whether there are any.
-  float left[BUFS][HALF ? 4 : 1][NB][16];
-  int outside[BUFS][4];
 };
 
 template <RowType T, int DIM, int RT>
@@ -1227,9 +1187,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
   constexpr int KW = DIM / 16, VW = DIM / 64, SW = (4 * NB + 15) / 16;
   constexpr int ROWS = 64 * RT, BUFS = DIM == 256 ? 1 : 2;
   constexpr int SPL = (16 * NB + 63) / 64;  // scale words a lane stages
-  constexpr int HP = AttnElem<T>::kHalfParts;
-  constexpr bool HALF = HP > 0;
-  __shared__ WideLds<DIM, HALF> lds;
+  __shared__ WideLds<DIM> lds;
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1241,9 +1199,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
   uint32_t kw[KW], vw[4][VW];
   float ksw[SPL], vsw[SPL];
   float poison = 0.f;
-  // HALF: a power of two per block, that of block lane % NB, which brings the
-  // value scales near 1.
-  float near_one = 1.f;
   // Offsets are made anew from the lane at each step: kept, they would be
   // spilled, and waiting for one to come back waits for all loads before it.
   auto load = [&](int64_t base) {
@@ -1275,22 +1230,9 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
         float y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = (float)(int8_t)(vw[k][b / 2] >> (16 * (b % 2) + 8 * i));
-        if constexpr (HALF)
-          lds.v[buf][wave / 2][b][i][own][wave % 2] = v2u{pack_half(y[0], y[1]), pack_half(y[2], y[3])};
-        else
-          lds.v[buf][wave / 2][b][i][own][wave % 2] = v2u{pack_hi(y[0], y[1]), pack_hi(y[2], y[3])};
+        lds.v[buf][wave / 2][b][i][own][wave % 2] = v2u{pack_hi(y[0], y[1]), pack_hi(y[2], y[3])};
       }
     });
-    if constexpr (HALF) {
-      bool outside = false;
-#pragma unroll
-      for (int w = 0; w < SPL; ++w) {
-        vsw[w] *= near_one;
-        outside |= !in_window(vsw[w]);
-      }
-      const int any = __ballot(outside) != 0;
-      if (own == 0) lds.outside[buf][wave] = any;
-    }
 #pragma unroll
     for (int w = 0; w < SPL; ++w) {
       ksw[w] = fmaf(ksw[w], scale, poison);
@@ -1300,13 +1242,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       if (64 * w + own < 16 * NB) {
         const int e = 64 * w + own;  // key e / NB, block e % NB
         lds.ks[buf][wave][e % NB][e / NB] = ksw[w];
-        if constexpr (HALF) {
-          const bool in = in_window(vsw[w]);
-          lds.vs[buf][wave][e % NB][e / NB] = in ? vsw[w] : 0.f;
-          lds.left[buf][wave][e % NB][e / NB] = in || !finite(vsw[w]) ? 0.f : vsw[w];
-        } else {
-          lds.vs[buf][wave][e % NB][e / NB] = finite(vsw[w]) ? vsw[w] : 0.f;
-        }
+        lds.vs[buf][wave][e % NB][e / NB] = finite(vsw[w]) ? vsw[w] : 0.f;
       }
     }
   };
@@ -1335,18 +1271,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q[rt]);
     }
     if (begin < end) load_at(begin);
-    float first[SPL];  // HALF: value scales of the share's first 16 keys, if all rows see them
-    if constexpr (HALF) {
-      if (begin < end && begin + 16 <= h.all) {
-        float unused;
-        const int64_t at = token_row(p, keys_at(p, h.pages, begin, last), h.kvh, unused);
-#pragma unroll
-        for (int w = 0; w < SPL; ++w) first[w] = p.c.VS[at * NB + (64 * w + lane) % (16 * NB)];
-      } else {
-#pragma unroll
-        for (int w = 0; w < SPL; ++w) first[w] = 0.f;
-      }
-    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       undo[rt] = cut_query<T, DIM>(q[rt], in[rt], qf[rt]);
@@ -1354,16 +1278,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       l[rt] = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[rt][b][0] = acc[rt][b][1] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
-    if constexpr (HALF) {
-      float top = 0.f;
-#pragma unroll
-      for (int w = 0; w < SPL; ++w) top = fmaxf(top, finite(first[w]) ? first[w] : 0.f);
-#pragma unroll
-      for (int d = NB; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-      const int up = top > 0.f ? 1 - __builtin_amdgcn_frexp_expf(top) : 0;
-      // Upwards by no more than leaves later scales of 2^60 room in the sums.
-      near_one = ldexpf(1.f, min(max(up, -60), 24));
     }
     const int tiles = (h.rows + 15) / 16;
     const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has
@@ -1417,7 +1331,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      weigh<NRT, 16, NB, 1, HALF>(s, undo, m, l, acc);
+      weigh<NRT, 16, NB, 1>(s, undo, m, l, acc);
       {
         v4u a[2][2];
         v4f vs[2][2];
@@ -1439,65 +1353,18 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
             float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = vs[n % 2][k / 4][k % 4] * s[rt][8 * g + k];
-            if constexpr (HALF) {
-              v4u parts[HP];
-              split8_half<HP>(w, parts);
+            v4u parts[PP];
+            split8<PP>(w, parts);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int q = HP - 1; q >= 0; --q) acc[rt][b][i] = mfma_f16(a[n % 2][i], parts[q], acc[rt][b][i]);
-            } else {
-              v4u parts[PP];
-              split8<PP>(w, parts);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[n % 2][i], parts[q], acc[rt][b][i]);
-            }
+              for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[n % 2][i], parts[q], acc[rt][b][i]);
           }
 #pragma unroll
           for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) pin(acc[rt][b][i]);
         });
-      }
-      // Keys whose value scale is outside the window: once more over the step with
-      // those alone, their weights in bf16 parts (whose range is f32's) against
-      // the same codes.
-      if constexpr (HALF) {
-        const int *o = lds.outside[buf];
-        if (__builtin_amdgcn_readfirstlane(o[0] | o[1] | o[2] | o[3]) != 0) {
-          static_for<0, 2 * NB>([&](auto n_) {
-            constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
-            v4u a[2];
-            v4f left[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const v4u half = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const v2h h = __builtin_bit_cast(v2h, (uint32_t)half[k]);
-                a[i][k] = pack_hi((float)h.x, (float)h.y);
-              }
-              left[i] = *reinterpret_cast<const v4f *>(&lds.left[buf][2 * g + i][b][4 * c]);
-            }
-#pragma unroll
-            for (int rt = 0; rt < NRT; ++rt) {
-              float w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = left[k / 4][k % 4] * s[rt][8 * g + k];
-              v4u parts[PP];
-              split8<PP>(w, parts);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int q = PP - 1; q >= 0; --q) acc[rt][b][i] = mfma(a[i], parts[q], acc[rt][b][i]);
-                pin(acc[rt][b][i]);
-              }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          });
-        }
       }
       // Blocks of rows that see a value scale that is not finite are lost.
       uint64_t any = 0;
@@ -1551,11 +1418,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
         steps(std::integral_constant<int, 0>{});
     }
 
-    float back[NB];  // HALF: undoes near_one
-    if constexpr (HALF) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) back[b] = 1.f / __int_as_float(__builtin_amdgcn_readlane(__float_as_int(near_one), b));
-    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int rho = 16 * (4 * rt + wave) + row;
@@ -1567,10 +1429,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
       for (int b = 0; b < NB; ++b) {
         const v4f u = acc[rt][b][0], v = acc[rt][b][1];
         float x[8] = {u[0], v[0], u[1], v[1], u[2], v[2], u[3], v[3]};
-        if constexpr (HALF) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= back[b];
-        }
         const int d = 32 * b + 8 * c;
         if (h.whole) {
           finish_row(p, h, t, weight, x);

@@ -561,3 +561,26 @@ def test_a_cache_without_pages_and_then_one_with_pages(news):
     assert bool(torch.isnan(c.run(none)).all())
     c.check(c.run())
     assert bool(torch.isnan(c.run(none)).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news,dim", [([1], 128), ([8], 64), ([40], 64), ([40], 128), ([40], 256), ([12], 128)])
+@pytest.mark.parametrize("tiny", [0.0, 2.0 ** -40])
+def test_dominant_keys_without_values(tiny, news, dim, dtype):
+    """A key that takes nearly all the weight, with values of zero or next to
+    none: what is left of the weights, 2^-11 to 2^-35, makes the output."""
+    for gap in (8, 12, 16, 20, 24):
+        c = Case((51, dim, news[0]), [300], news, 1, 4, dim, 16, dtype)
+        q = c.q.float()
+        q[..., 0] = gap * dim ** 0.5
+        c.q = q.to(dtype)
+        c.qf = c.q.float().numpy()
+        first = oc.place_of_channel(dim)[0]
+        page, at = oc.slot_of(c.table, 16, 0, 3)
+        c.c["k"][..., first] = 0                     # alpha q . K is about gap for this key and of unit size for the others
+        c.c["k"][page, :, at] = 0
+        c.c["k"][page, :, at, first] = 127
+        c.c["k_scale"][page, :, at] = 1 / 127
+        c.c["v_scale"][page, :, at] = tiny
+        print(f"[attention] dominant key, gap {gap} new {news} dim {dim} {dtype}", flush=True)
+        c.check(c.run())
