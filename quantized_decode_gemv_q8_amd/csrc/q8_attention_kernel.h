@@ -66,7 +66,7 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 template <RowType T>
 struct AttnElem;
-// kQParts f16 parts of a query, kPParts bf16 parts of a weight, each cut to what
+// kQParts f16 parts of a query, kPParts bf16 parts of a weight, each of what
 // the ones before leave: two are to 2^-16, 2^-8 of a 16-bit output's half step or
 // 2^-5, three are all of an f32.
 template <>
@@ -97,6 +97,11 @@ __device__ __forceinline__ uint32_t pack_hi(float lo, float hi) {
   return __builtin_amdgcn_perm(bits(hi), bits(lo), 0x07060302u);
 }
 
+// The same rounded to bf16, to the nearest.
+__device__ __forceinline__ uint32_t pack_near(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
+}
+
 // Codes at byte pair `half` of a word as two f16: 1024 + (code + 128) by its
 // bits, less 1152.
 __device__ __forceinline__ uint32_t pair_f16(uint32_t w, int half) {
@@ -122,7 +127,8 @@ __device__ __forceinline__ float less(uint32_t pair, float x) {
 }
 
 // Parts of eight floats as matrix operands, each the first 8 bits of what the
-// ones before left.
+// ones before left; of two, the last is rounded (cut it would be off by twice
+// as much, always downwards), of three it is all that is left.
 template <int PARTS>
 __device__ __forceinline__ void split8(const float (&x)[8], v4u (&out)[PARTS]) {
   float r[8];
@@ -132,7 +138,8 @@ __device__ __forceinline__ void split8(const float (&x)[8], v4u (&out)[PARTS]) {
   for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      out[p][i] = pack_hi(r[2 * i], r[2 * i + 1]);
+      const bool rest = PARTS < 3 && p + 1 == PARTS;
+      out[p][i] = rest ? pack_near(r[2 * i], r[2 * i + 1]) : pack_hi(r[2 * i], r[2 * i + 1]);
       if (p + 1 < PARTS) {
         r[2 * i] = less<0>(out[p][i], r[2 * i]);
         r[2 * i + 1] = less<1>(out[p][i], r[2 * i + 1]);
@@ -838,7 +845,8 @@ struct AttnFew {
       for (int q = 0; q < PP; ++q)
 #pragma unroll
         for (int d = 0; d < NK / 2; ++d) {
-          const uint32_t pair = pack_hi(w[2 * d], w[2 * d + 1]);
+          const bool rest = PP < 3 && q + 1 == PP;
+          const uint32_t pair = rest ? pack_near(w[2 * d], w[2 * d + 1]) : pack_hi(w[2 * d], w[2 * d + 1]);
           if (q + 1 < PP) {
             w[2 * d] = less<0>(pair, w[2 * d]);
             w[2 * d + 1] = less<1>(pair, w[2 * d + 1]);

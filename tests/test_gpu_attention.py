@@ -584,3 +584,17 @@ def test_dominant_keys_without_values(tiny, news, dim, dtype):
         c.c["v_scale"][page, :, at] = tiny
         print(f"[attention] dominant key, gap {gap} new {news} dim {dim} {dtype}", flush=True)
         c.check(c.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 2, 4, 8, 40])
+def test_weights_are_rounded_not_cut(news, dim):
+    """One visible key: the output is its value.  Codes are powers of two and
+    the value scale lies above a tie of f16 by less than 2^-15, the bits of a
+    weight past the first 16: cut, they would leave a tie, which goes down."""
+    c = Case((54, dim, news), [news], [news], 1, 4, dim, 64, torch.float16, tree=True)
+    c.c["v"][:] = 1 << np.random.default_rng(55).integers(0, 7, c.c["v"].shape)
+    c.c["v_scale"][:] = np.float32(1 + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15 - 2.0 ** -23)
+    c.trees = [[1] * news]
+    print(f"[attention] one visible key, dim {dim} new {news}", flush=True)
+    assert torch.equal(c.run().cpu(), torch.from_numpy(c.want()[0]).to(torch.float16))
