@@ -213,7 +213,9 @@ __device__ __forceinline__ float cut_query(const QueryRow<T, DIM> &from, bool in
       top = fmaxf(top, fabsf(x[b][i]));
     }
   top = across_groups_max(top);
-  const int up = top > 0.f && top < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+  // No further than 2^126, so that what undoes it is no zero (which would make a
+  // NaN of a masked score); even the smallest f32 is 2^-23 then, and kept.
+  const int up = top > 0.f && top < INFINITY ? min(15 - __builtin_amdgcn_frexp_expf(top), 126) : 0;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll

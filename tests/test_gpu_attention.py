@@ -598,3 +598,14 @@ def test_weights_are_rounded_not_cut(news, dim):
     c.trees = [[1] * news]
     print(f"[attention] one visible key, dim {dim} new {news}", flush=True)
     assert torch.equal(c.run().cpu(), torch.from_numpy(c.want()[0]).to(torch.float16))
+
+
+@pytest.mark.parametrize("news", [[1], [3], [9], [40]])
+@pytest.mark.parametrize("scale", [1e-36, 1e-38, 1e-40, 1e-42, 2e-45])
+def test_tiny_queries(scale, news):
+    """Query rows down to the smallest numbers make scores next to zero: the mean of the values seen."""
+    c = Case((53, len(news)), [300], news, 1, 4, 64, 16, torch.float32, q_scale=scale)
+    print(f"[attention] queries of {scale} new {news}", flush=True)
+    c.check(c.run())
+    c = Case((53, len(news)), [300], news, 1, 4, 64, 16, torch.bfloat16, tree=True, q_scale=max(scale, 1e-40))
+    c.check(c.run())
