@@ -303,3 +303,39 @@ def test_more_rows_and_sequences_than_one_launch_takes():
     binding.q8_cache_keep(cache, table, lengths, offsets, torch.ones((seqs, 1), dtype=torch.int32, device=DEV))
     assert torch.equal(cache.k[1:4, 0, 0], before[1:, 1]) and torch.equal(cache.k[1:4, 0, 1], before[1:, 1])
     assert torch.equal(cache.k[0, 0, :2], before[0])
+
+
+@pytest.mark.parametrize("seqs,where,value", [(4, 2, 1 << 30), (4, 2, -1), (4, 4, 2), (130, 72, 1 << 30), (130, 72, -1),
+                                              (130, 71, 1 << 30), (130, 0, -5), (700, 330, -1), (700, 341, 1 << 30)])
+def test_a_wrong_offset_loses_only_its_own_sequences(seqs, where, value):
+    """Sequences that end past the rows, begin before them or descend have no
+    rows; all others keep theirs, in batches of any size."""
+    heads, dim, page_size, pad = 1, 64, 16, 3
+    rng = np.random.default_rng((17, seqs, where))
+    offsets = np.arange(seqs + 1, dtype=np.int32) * 2
+    offsets[where] = value
+    rows = 2 * seqs + pad
+    lengths = np.full(seqs, 20, np.int32)
+    table = rng.permutation(2 * seqs).reshape(seqs, 2).astype(np.int32)
+    c = cc.random_cache(rng, 2 * seqs, heads, page_size, dim)
+    k, kf = cc.rows_of(rng, (rows, heads, dim), torch.float32)
+    fine = [b for b in range(seqs) if 0 <= offsets[b] <= offsets[b + 1] <= rows and offsets[b + 1] - offsets[b] == 2]
+    assert seqs - 2 <= len(fine) < seqs
+    cache = handle(c)
+    held = (dev(table), dev(lengths), dev(offsets))
+    print(f"[cache] offset {where} of {seqs} is {value}", flush=True)
+    binding.q8_cache_write(cache, k.to(DEV), k.to(DEV), *held)
+    own = np.zeros(rows, bool)
+    for b in fine:
+        t = slice(offsets[b], offsets[b + 1])
+        oc.write(c, kf[t], kf[t], table[b:b + 1], lengths[:1], [0, 2])
+        own[t] = True
+    check_cache(cache, c)
+    ko = torch.full((rows, heads, dim), 5.0, device=DEV)
+    vo = ko.clone()
+    binding.q8_cache_read(cache, *held, rows, k=ko, v=vo)
+    ko = ko.cpu().numpy()
+    for b in fine:
+        t = slice(offsets[b], offsets[b + 1])
+        assert np.array_equal(ko[t], oc.read(c, table[b:b + 1], lengths[:1], [0, 2])[0].astype(np.float32)), b
+    assert bool((ko[~own] == 5).all())
