@@ -574,10 +574,12 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
     return k, v
 
 
-def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
+def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
     """Moves new token keep[b, a] of sequence b to the place of its new token a,
     a = 0, 1, ...; keep is i32 [sequences, width], strictly ascending until its
-    first negative entry."""
+    first negative entry.  rows: of the row tensors that the offsets refer to; a
+    sequence whose offsets pass them has no new tokens, as in q8_cache_write
+    (None: offsets may be of any size)."""
     seqs = _cache_seqs(cache, table, lengths, offsets)
     if not isinstance(keep, torch.Tensor):
         raise TypeError("keep must be a torch.Tensor")
@@ -589,8 +591,8 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None):
     cache._apart("keep", *_span(keep))
     for name, a, b in _seqs_spans(seqs):
         cache._apart(name, a, b)
-    _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct, MAX_CACHE_ROWS, seqs, keep.data_ptr(),
-          keep.shape[1])
+    _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct,
+          MAX_CACHE_ROWS if rows is None else int(rows), seqs, keep.data_ptr(), keep.shape[1])
 
 
 #: Most rows a call's offsets may refer to.

@@ -339,3 +339,25 @@ def test_a_wrong_offset_loses_only_its_own_sequences(seqs, where, value):
         t = slice(offsets[b], offsets[b + 1])
         assert np.array_equal(ko[t], oc.read(c, table[b:b + 1], lengths[:1], [0, 2])[0].astype(np.float32)), b
     assert bool((ko[~own] == 5).all())
+
+
+def test_keep_with_offsets_past_the_rows():
+    """With the number of rows given, a sequence whose offsets pass it has none, as in a write."""
+    rng, table, c, offsets, _ = case(18, [40, 40, 40], [8, 8, 8], 2, 64, 16)
+    cache = handle(c)
+    held = (dev(table), dev(np.array([40, 40, 40], np.int32)), dev(offsets))
+    keep = dev(np.tile(np.array([[2, 5, 7]], np.int32), (3, 1)))
+    print("[cache] keep with offsets past the rows", flush=True)
+    binding.q8_cache_keep(cache, *held, keep, rows=23)
+    oc.keep(c, table, [40, 40, 40], offsets, [[2, 5, 7], [2, 5, 7], []])
+    check_cache(cache, c)
+    binding.q8_cache_keep(cache, *held, keep, rows=24)
+    oc.keep(c, table, [40, 40, 40], offsets, [[2, 5, 7]] * 3)
+    check_cache(cache, c)
+    binding.q8_cache_keep(cache, *held, keep)
+    oc.keep(c, table, [40, 40, 40], offsets, [[2, 5, 7]] * 3)
+    check_cache(cache, c)
+    binding.q8_cache_keep(cache, *held, keep, rows=0)
+    check_cache(cache, c)
+    with pytest.raises(binding.Q8Error):
+        binding.q8_cache_keep(cache, *held, keep, rows=-1)
