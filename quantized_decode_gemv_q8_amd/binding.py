@@ -612,7 +612,7 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
     seqs = _cache_seqs(cache, table, lengths, offsets)
     qs, q0 = _cache_rows("q", q, None, None, cache)
     rows, q_heads = q.shape[0], q.shape[1]
-    if q_heads == 0 or q_heads % cache.heads:
+    if q_heads == 0 or cache.heads == 0 or q_heads % cache.heads:
         raise ValueError(f"the heads of q must be a multiple of the cache's {cache.heads}, got {q_heads}")
     words = 0
     if tree is not None:

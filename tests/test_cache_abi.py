@@ -256,3 +256,14 @@ def test_attention_holds_its_workspace_until_the_call_returns(monkeypatch):
                                      torch.zeros(3, dtype=i32))
     assert out.shape == q.shape
     assert seen == [(True, True)]
+
+
+def test_attention_refuses_heads_that_do_not_fit():
+    """A cache of no heads among them."""
+    c = object.__new__(binding.Q8Cache)
+    c.device, c.dim, c.page_size, c.pages = torch.device("cpu"), 64, 16, 3
+    i32 = torch.int32
+    held = torch.zeros((2, 3), dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(3, dtype=i32)
+    for c.heads, q_heads in ((2, 3), (2, 0), (4, 2), (0, 4), (0, 0)):
+        with pytest.raises(ValueError, match="multiple"):
+            binding.q8_cache_attention(torch.zeros((5, q_heads, 64)), c, *held)
