@@ -295,8 +295,9 @@ typedef struct q8_cache {
  * table[b, 0], table[b, 1], ... and holds lengths[b] tokens, the new ones
  * among them: its newest n = offsets[b+1] - offsets[b] tokens are rows
  * offsets[b] .. offsets[b+1]-1 of the call's row tensors.  Rows before
- * offsets[0] and from offsets[seqs] on belong to no sequence and are neither
- * read nor written.  Sequences must not share pages that a call writes.
+ * offsets[0] and from offsets[seqs] on belong to no sequence: what they hold
+ * counts for nothing (a write may load it), and none of them is written.  Sequences must
+ * not share pages that a call writes.
  *
  * The contents are checked where they are used: a sequence whose offsets do
  * not ascend within the rows has no rows; one with lengths[b] < n, or with more
@@ -324,10 +325,11 @@ typedef enum q8_type { Q8_F32 = 0, Q8_BF16 = 1, Q8_F16 = 2 } q8_type;
  *         (at least heads * dim), aligned to their elements
  * Per 32 channels x: scale = f32(max|x| / 127), code = x / scale rounded to
  * the nearest, ties to even, both correctly rounded (a scale of zero gives
- * zeros).  A block that holds an infinity or a NaN is stored so that it reads
+ * zeros; where the scale is denormal and so coarse that a quotient passes 127,
+ * the code is 127).  A block that holds an infinity or a NaN is stored so that it reads
  * back as NaN.  Everything else in the cache is left as it was.
- * q8_cache_read -- the reverse: k, v = code * scale, rounded once to `type`, for
- * the newest tokens of each sequence (offsets that count all of its tokens
+ * q8_cache_read -- the reverse: k, v = code * scale, an f32 product that is then
+ * rounded to `type`, for the newest tokens of each sequence (offsets that count all of its tokens
  * read the whole sequence).
  * Errors of both: Q8_ERR_INVALID, Q8_ERR_TOO_LARGE, Q8_ERR_UNSUPPORTED_DEVICE,
  * Q8_ERR_HIP.
@@ -378,7 +380,8 @@ q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs
  *   q        f32 rows: to 2^-23 of the row's largest channel; bf16 and f16 rows: not
  *            at all (channels below 2^-32 of the row's largest lose bits)
  *   weights  (each times its value scale) f32 rows: not at all; bf16 and f16
- *            rows: to 2^-16 of itself (products below 2^-110 may lose more)
+ *            rows: to 2^-16 of itself (products below 2^-110 may lose more).  This
+ *            holds for any number of rows and whatever else a call brings
  * A query that is not finite, a key whose score is NaN or +infinity and a value
  * scale that is not finite give NaN in the rows that see them (a value scale in
  * its block of channels).

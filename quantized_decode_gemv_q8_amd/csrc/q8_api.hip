@@ -810,14 +810,17 @@ constexpr int kAttnMostHeads = 1 << 24;
 
 // Sequences that the table bounds to this many tokens are not split: one
 // workgroup of 8 waves takes all keys of an item, and the second launch that
-// joins parts is saved.  One sequence of 1023 keys, in a run of calls: 15.7 us,
-// 17.5 split over workgroups; the same calls captured in a graph, where the gap
-// between the two kernels is smaller: 16.2 and 12.4.
+// joins parts is saved.  One sequence, whole and split, us:
+//    keys             100           300           1023
+//    in a run of calls 14.2, 18.4   14.1, 18.8    15.8, 18.9
+//    captured           9.5, 10.4   11.2, 11.8    15.8, 12.0
+// The border is that of calls; captured it would lie between 300 and 1023.
 constexpr int64_t kAttnWholeTokens = 1024;
 // What an item of few rows costs besides its keys (its query, its first loads'
 // latency and its sums' way out), in units of kAttnStep keys, when work is
-// dealt out.  A batch of 32 sequences of 1 .. 8192 keys takes 92 us at 0, 82 at
-// 1, 73 at 2 and 75 at 3 and 4; with many rows a unit takes so long that 0 is best.
+// dealt out.  A batch of 32 sequences of 1 .. 8192 keys takes 82 us at 0, 70 at
+// 1, 62 at 2 and 3 and 63 at 4 (bf16 rows: 75, 65, 60, 61, 61); with many rows a
+// unit takes so long that 0 is best.
 constexpr int kAttnItemCost = 2;
 
 AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
@@ -826,14 +829,19 @@ AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows
   // The smallest items that hold an average sequence's rows of a head; past 32,
   // the kernel whose waves share keys.  24 sequences of 4096 keys, us by the rows
   // of an item:
-  //    4 rows, dim  64, f32     4: 41.9    8: 42.8   16: 44.9
-  //    4 rows, dim 128, f32     4: 45.7    8: 45.4   16: 44.7
-  //    8 rows, dim  64, f32     8: 43.5   16: 45.2   32: 66.4
-  //   16 rows, dim 128, f32     8: 76.0   16: 48.1   32: 64.3
-  //   32 rows, dim 128, bf16   16: 78.4   32: 56.7   64: 76.9
-  //   40 rows, dim 128, bf16   16: 99.7   32: 90.5   64: 79.9   128: 82.1
-  //   72 rows, dim 128, bf16   32: 129.8  64: 139.2  128: 104.4
-  //  128 rows, dim 128, f16    32: 162.8  64: 159.9  128: 149.9
+  //    4 rows, dim  64, f32     4: 41.6    8: 42.9   16: 45.1
+  //    4 rows, dim 128, f32     4: 47.0    8: 46.0   16: 45.8
+  //    4 rows, dim 128, bf16    4: 43.9    8: 43.5   16: 43.4
+  //    8 rows, dim  64, f32     8: 43.6   16: 45.4   32: 66.5
+  //   16 rows, dim 128, f32     8: 75.3   16: 48.0   32: 65.4
+  //   32 rows, dim 128, bf16   16: 76.9   32: 56.9   64: 84.2
+  //   40 rows, dim 128, bf16   16: 99.2   32: 90.8   64: 85.9   128: 90.7
+  //   72 rows, dim 128, bf16   32: 130.2  64: 154.1  128: 117.8
+  //  128 rows, dim 128, f16    32: 162.7  64: 161.4  128: 143.7
+  // At 4 rows of dim 128 the three are within 3% over such batches; 4 is the
+  // fastest for one short sequence (15.9 us, 16.6 with 16).  Two borders could be
+  // drawn better: 17 to 32 rows of dim 256 take 81 us of bf16 and 96 of f32 in
+  // 16-row items, 87 and 107 in the 64-row ones that the rule gives them.
   // The instances for 4 and 8 rows do not fit the registers at dim 256.
   p.tile = mean <= 4 && dim <= 128                 ? 4
            : mean <= 8 && dim <= 128               ? 8

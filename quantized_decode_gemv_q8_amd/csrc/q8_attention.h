@@ -53,8 +53,9 @@ constexpr int attn_direct_rows(int dim) { return dim <= 128 ? 32 : 16; }
 constexpr int attn_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
 
 // Workgroups per CU: a wave then has half of a SIMD's registers.  With 3 or 4
-// the kernels for few rows spill (106 and 162 registers at dim 128), and a batch
-// of 32 sequences of 1 .. 8192 keys took 97 us instead of 92.
+// the kernel for 4 rows of f32 spills (26 and 93 registers at dim 128), and a
+// batch of 32 sequences of 1 .. 8192 keys takes 81 and 134 us instead of 64
+// (bf16 rows: 60, 60 and 93).
 constexpr int kAttnWgsPerCu = 2;
 
 hipError_t launch_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);

@@ -40,13 +40,16 @@
 // device: a captured graph follows them.
 //
 // What bounds it.  Few rows: memory.  With 4 rows of f32 per head, dim 128, time
-// grows by 1 us per 5.85 MB of cache (a large copy moves 4.7 TB/s, a large
-// read 6.15); a batch of 32 ragged sequences (316 MB) takes 64 us and its join
-// 5, two sequences of 131072 keys (604 MB) 110 and 7.  From 16 rows on:
+// grows by 1 us per 5.85 MB of cache.  A large copy moves 4.9 TB/s; a large read
+// of contiguous runs 6.1, 7.1 with loads that leave no trace in the caches, which
+// are not used here.  A batch of 32 ragged sequences (316 MB) takes 64 us and its
+// join 5, two sequences of 131072 keys (604 MB) 112 and 7.  From 16 rows on:
 // vector instructions, for the codes' conversion, the exponentials and the
-// weights' parts, some 2 per score and matrix instruction of 16 cycles; 68 GFLOP of
-// bf16 trees take 169 us (0.40 PFLOP/s), 16 GFLOP of f32 pieces of prompts 81
-// (0.2 PFLOP/s, two parts of q and three of the weights).
+// weights' parts.  68 GFLOP of bf16 trees take 169 us (0.40 PFLOP/s); of the 160
+// of the main kernel vector instructions issue for 107 on every SIMD and the
+// matrix cores are busy for 43, 9 of them at the same time.  16 GFLOP of f32
+// pieces of prompts take 81 us (0.2 PFLOP/s, two parts of q and three of the
+// weights): 42, 17 and 4 of 68.
 #pragma once
 
 #include <type_traits>
@@ -670,8 +673,8 @@ struct Attn {
 };
 
 // The same for items of at most 16 / PACK rows (one new token of a small group;
-// 24 sequences of 4096 keys, dim 64, 4 rows of f32: 41.9 us, 44.9 with 16-row
-// items; one sequence of 1000 keys, dim 128: 16.2 and 16.9):
+// 24 sequences of 4096 keys, dim 64, 4 rows of f32: 41.6 us, 45.1 with 16-row
+// items; one sequence of 1000 keys, dim 128: 15.9 and 16.6):
 // the query's columns repeat PACK times across the matrix operand, so that the
 // lanes of a row's repeats hold the same scores, and each keeps a PACK-th of the
 // keys (KPL).  Exponentials, weights and their parts, most of the other
@@ -1169,7 +1172,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? kAttnWgsPerCu : 1) void at
 // ---------------------------------------------------------------- many rows
 
 // The same for items of more rows (trees, prompts; 24 sequences of 4096 keys, 72
-// rows of bf16, dim 128: 104 us, 130 with 32-row items): up to 64 * RT rows, 16 * RT
+// rows of bf16, dim 128: 118 us, 130 with 32-row items): up to 64 * RT rows, 16 * RT
 // for each wave, and all four waves take the same keys.  Converting the codes
 // costs as much as the rest of the work on 32 rows, so a workgroup does it
 // once: per step of 64 keys each wave loads 16 keys' codes, converts them and
@@ -1459,15 +1462,16 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void attention_wide_kernel
 
 // ---------------------------------------------------------------- joining the parts
 
-// Rows that a wave of the join takes: four channels of a row per lane (one row
-// per wave took 28 us instead of 14 for 128-row items of dim 64).
+// Rows that a wave of the join takes: four channels of a row per lane.  One row
+// per wave took twice as long for 128-row items of dim 64 (whose join takes 8.6 us
+// for the pieces of prompts above).
 constexpr int join_rows(int dim) { return 256 / dim; }
 
 // Workgroup (y, w): the split item that workgroup w began, and its y-th run of
 // kWaves * join_rows rows; parts are taken in key order.  Runs come first in the
 // grid: split items often begin every 2nd, 4th ... workgroup, and with w first
-// they would all land on a few of the XCDs (512 slots of 128 rows of dim 128, 34
-// MB: 20 us instead of 10).
+// they would all land on a few of the XCDs and take twice as long (512 slots of
+// 128 rows of dim 128, 34 MB: 10 us as it is).
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs p, int slot_rows) {
   typedef typename AttnElem<T>::type E;

@@ -169,8 +169,8 @@ template <>
 struct CodeWord<256> { typedef uint4 type; };
 
 // (head, K or V) rows per 16-lane group.  With one, two and four a step of 64
-// tokens is written and read back in 5.4, 6.3 and 10.4 us, 18432 tokens of
-// prompts in 64, 58 and 74 us, and 147000 tokens are read in 150, 132 and 138.
+// tokens is written and read back in 6.3, 7.2 and 8.8 us, 18432 tokens of
+// prompts in 65, 58 and 60 us, and 147000 tokens are read in 149, 130 and 135.
 constexpr int kRowsPerGroup = 2;
 constexpr int kRowsPerWave = kRowsPerGroup * 4;
 
@@ -247,8 +247,9 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsArgs p) 
 }
 
 // PAST: the rows are written past the caches.  They leave the Infinity Cache
-// anyway where they are larger than it (512 MB of rows: 142 us through the
-// caches, 135 past them); smaller ones are better kept for whoever reads them.
+// anyway where they are larger than it (376 MB of f16 rows: 138 us through the
+// caches, 130 past them; 512 MB of f32 rows: 188 and 179); smaller ones are
+// better kept for whoever reads them.
 constexpr int64_t kPastCachesBytes = (int64_t)256 << 20;
 template <RowType T, int DIM, bool PAST>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsArgs p) {
