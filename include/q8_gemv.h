@@ -12,11 +12,14 @@
  *   q8_dot_t   "dot and tensor cores" (docs/language/dot-and-tensor-cores),
  *              table of built-ins and section "Hardware paths":
  *              C[m,n] = sum_k A[m,k] * W[n,k], i8 operands, i32 result.
+ *   q8_cache_* a paged cache of keys and values in Q8_0 and the attention over
+ *              it (declared and described below).
  *
  * Conventions shared by every entry point:
  *   - All tensor pointers are DEVICE pointers (memory of the current HIP
  *     device) to dense row-major arrays; there are no leading-dimension
- *     arguments.  The caller owns them; the library only reads the inputs
+ *     arguments (but for the rows and the page table that q8_cache_* take, which
+ *     may be apart).  The caller owns them; the library only reads the inputs
  *     and overwrites the output.  It reads C only through an epilogue with
  *     row factors (corr != NULL, below).  C must not alias an input.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).
@@ -29,8 +32,9 @@
  *     below 2^31 (otherwise Q8_ERR_TOO_LARGE).
  *   - Thread safety: concurrent calls are safe on distinct streams.  Host
  *     threads that share one stream must serialise their calls.
- *   - Workspace: the split-K workspace (partial sums and arrival counters)
- *     is owned by the library, one per (device, stream).  It is allocated by
+ *   - Workspace (q8_cache_attention takes its own from the caller, the other
+ *     q8_cache_* need none): the split-K workspace (partial sums and arrival
+ *     counters) is owned by the library, one per (device, stream).  It is allocated by
  *     the first call that needs it on that stream and grown by a later call
  *     that needs more; buffers it grows out of stay allocated (a graph
  *     captured earlier may still use them) until q8_release() frees them
