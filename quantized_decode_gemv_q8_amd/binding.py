@@ -416,10 +416,12 @@ class Q8Cache:
                    new(dim, torch.int8), new(dim // BLOCK, torch.float32))
 
 
-def _cache_seqs(cache, table, lengths, offsets):
-    """The checked descriptor of a call's sequences."""
+def _cache_seqs(cache, table, lengths, offsets, stream=None):
+    """The checked descriptor of a call's sequences; the call's stream is checked too."""
     if not isinstance(cache, Q8Cache):
         raise TypeError("cache must be a Q8Cache")
+    if stream is not None and stream.device != cache.device:
+        raise ValueError(f"the stream is of {stream.device}, the cache of {cache.device}")
     index, i32 = cache.device.index, torch.int32
     for name, t, rank in (("table", table, 2), ("lengths", lengths, 1), ("offsets", offsets, 1)):
         if not isinstance(t, torch.Tensor):
@@ -532,7 +534,7 @@ def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
     """Quantises rows k and v ([rows, heads, dim]) into the cache: sequence b's
     newest offsets[b+1] - offsets[b] tokens of lengths[b] are rows offsets[b]
     .. of k and v, and live in the pages table[b]."""
-    seqs = _cache_seqs(cache, table, lengths, offsets)
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
     ks, k0 = _cache_rows("k", k, None, cache.heads, cache)
     vs, v0 = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
     rows, size = k.shape[0], k.element_size()
@@ -550,7 +552,7 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
     """The newest offsets[b+1] - offsets[b] tokens of each sequence as rows
     [rows, heads, dim] of dtype; returns (k, v).  Rows of no sequence keep what
     the given k and v hold (new tensors: undefined)."""
-    seqs = _cache_seqs(cache, table, lengths, offsets)
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
     rows = int(rows)
     shape = (rows, cache.heads, cache.dim)
     if k is None and v is None:
@@ -580,7 +582,7 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
     first negative entry.  rows: of the row tensors that the offsets refer to; a
     sequence whose offsets pass them has no new tokens, as in q8_cache_write
     (None: offsets may be of any size)."""
-    seqs = _cache_seqs(cache, table, lengths, offsets)
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
     if not isinstance(keep, torch.Tensor):
         raise TypeError("keep must be a torch.Tensor")
     if keep.dim() != 2:
@@ -609,7 +611,7 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
     the scores, 1 / sqrt(dim) if None.  Rows of no sequence keep what out holds
     (a new out: undefined); rows that see nothing are zeros.
     """
-    seqs = _cache_seqs(cache, table, lengths, offsets)
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
     qs, q0 = _cache_rows("q", q, None, None, cache)
     rows, q_heads = q.shape[0], q.shape[1]
     if q_heads == 0 or cache.heads == 0 or q_heads % cache.heads:

@@ -267,3 +267,18 @@ def test_attention_refuses_heads_that_do_not_fit():
     for c.heads, q_heads in ((2, 3), (2, 0), (4, 2), (0, 4), (0, 0)):
         with pytest.raises(ValueError, match="multiple"):
             binding.q8_cache_attention(torch.zeros((5, q_heads, 64)), c, *held)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is allocated or enqueued on it."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    c = object.__new__(binding.Q8Cache)
+    c.device, c.heads, c.dim, c.page_size, c.pages = torch.device("cuda", 0), 2, 64, 16, 3
+    rows, held = torch.zeros((5, 2, 64)), (torch.zeros((2, 3), dtype=torch.int32),) * 3
+    for call in (lambda: binding.q8_cache_write(c, rows, rows, *held, stream=Stream()),
+                 lambda: binding.q8_cache_read(c, *held, 5, stream=Stream()),
+                 lambda: binding.q8_cache_keep(c, *held, held[0], stream=Stream()),
+                 lambda: binding.q8_cache_attention(rows, c, *held, stream=Stream())):
+        with pytest.raises(ValueError, match="stream"):
+            call()
