@@ -404,6 +404,225 @@ q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8
                              const q8_cache_seqs *seqs, const uint64_t *tree, int64_t tree_words,
                              float alpha, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * The cache in 4-bit floats: the same pages, sequences and operations as the
+ * Q8_0 cache in a little under half of its bytes (a token's key and value of 128
+ * channels: 136 instead of 288).
+ *
+ * A code is 4 bits: sign, then the index of 0, 0.5, 1, 1.5, 2, 3, 4 or 6.  32
+ * channels of a row share a scale byte e, which stands for 2^(e - 127); value = code
+ * * scale, exactly.  255 stands for NaN; bytes of 253 and 254 are not used, and
+ * what they give is not defined.
+ * Channel d = 32 b + 2 j + i of a token's row (j < 16, i < 2) is nibble i (low first) of
+ *   K  byte j * (dim / 32) + b of the row's dim / 2;
+ *   V  byte (4 j + token % 4) * (dim / 32) + b of the 2 * dim that tokens 4 n .. 4 n + 3 of
+ *      a page share (token: the place within the page).
+ * Block b's scale is byte b of the token's scales.
+ */
+typedef struct q8_mx4_cache {
+  uint8_t *K;        /* u8 [pages, heads, page_size, dim / 2], device; all four 16-byte aligned */
+  uint8_t *KS;       /* u8 [pages, heads, page_size, dim / 32] */
+  uint8_t *V;        /* as K */
+  uint8_t *VS;       /* as KS */
+  int64_t pages;     /* these as in q8_cache */
+  int32_t heads;
+  int32_t page_size;
+  int32_t dim;
+} q8_mx4_cache;
+
+/*
+ * q8_mx4_write, q8_mx4_read, q8_mx4_keep, q8_mx4_attention -- what q8_cache_write,
+ * q8_cache_read, q8_cache_keep and q8_cache_attention do, for this cache; the
+ * arguments, what is checked where, and what happens to sequences that are
+ * described wrongly are the same, but for
+ *   write      per 32 channels x: s = the smallest power of two with max|x| <= 7 s, from 2^-125
+ *              to 2^125; code = x / s to the nearest, ties to the even code, with its
+ *              sign, at most 6.  A block that holds an infinity or a NaN reads back as NaN
+ *   read       code * s, rounded once to `type`
+ *   attention  alpha must be finite.  Keys, values and queries reach the matrix cores
+ *              exactly (parts of a query below 2^-126, or of a value below 2^-126,
+ *              may be lost).  Weights are rounded to 2^-16 of themselves for bf16 and f16
+ *              rows, not at all for f32; those below 2^-126 of the row's largest count
+ *              for nothing.  Everything else is f32
+ * Errors: as theirs; Q8_ERR_INVALID also for arrays that are not 16-byte aligned and an alpha
+ * that is not finite.
+ */
+q8_status q8_mx4_write(const q8_mx4_cache *cache, const void *k, const void *v, q8_type type,
+                       int64_t rows, int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs,
+                       void *stream);
+q8_status q8_mx4_read(const q8_mx4_cache *cache, void *k, void *v, q8_type type, int64_t rows,
+                      int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs, void *stream);
+q8_status q8_mx4_keep(const q8_mx4_cache *cache, int64_t rows, const q8_cache_seqs *seqs,
+                      const int32_t *keep, int64_t width, void *stream);
+q8_status q8_mx4_attention_workspace(const q8_mx4_cache *cache, q8_type type, int64_t rows,
+                                     int32_t q_heads, const q8_cache_seqs *seqs, int64_t *bytes);
+q8_status q8_mx4_attention(const q8_mx4_cache *cache, const void *q, void *out, q8_type type,
+                           int64_t rows, int32_t q_heads, int64_t q_stride, int64_t out_stride,
+                           const q8_cache_seqs *seqs, const uint64_t *tree, int64_t tree_words,
+                           float alpha, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * The pages of a cache: who owns them, and how they are shared.
+ *
+ * A pool counts owners: refs[p] is the number of table rows that own page p; a
+ * page with refs[p] <= 0 is free.  The caches of all layers share one pool and one
+ * table.  Everything is on the device and read when the work runs, so a captured
+ * decode step can grow its sequences.  Table rows hold -1 where they own no page.
+ * Results depend on the order of pages and sequences, never on timing.
+ */
+typedef struct q8_pool {
+  int32_t *refs;     /* i32 [pages], device */
+  int64_t pages;     /* 0 .. 2^31 - 1 */
+  int32_t page_size; /* tokens: a power of two, 16 .. 1024 */
+} q8_pool;
+
+typedef struct q8_page_table {
+  int32_t *table;       /* i32 [seqs, max_pages], device, rows table_stride apart */
+  int64_t seqs;
+  int64_t max_pages;    /* max_pages * page_size below 2^30 */
+  int64_t table_stride; /* at least max_pages */
+} q8_page_table;
+
+/*
+ * q8_pages_fork -- children share their parents' pages: row i of `to` becomes
+ * the pages of the lengths[parent[i]] tokens of row parent[i] of `from`, each of
+ * which counts one owner more, and -1 behind them; lengths_out[i] = lengths[parent[i]].
+ * A child whose parent is no row of `from`, or whose length is negative or past either
+ * table's columns, gets no pages and length 0; an entry that is no page is copied as
+ * -1.  What the rows of `to` owned before is not released (resize them to 0 first).
+ *   lengths      i32 [from->seqs], device
+ *   parent       i32 [to->seqs], device; any row any number of times
+ *   lengths_out  i32 [to->seqs], device
+ * `to` and lengths_out must not overlap anything else.
+ */
+q8_status q8_pages_fork(const q8_pool *pool, const q8_page_table *from, const int32_t *lengths,
+                        const int32_t *parent, const q8_page_table *to, int32_t *lengths_out,
+                        void *stream);
+
+/*
+ * q8_pages_resize -- sequences grow, shrink or leave: sequence b holds the pages of
+ * before[b] tokens (entries 0 .. ceil(before / page_size) - 1 of its row) and is to
+ * hold those of after[b].
+ *   1. Pages past what after[b] needs lose an owner, and their entries become -1
+ *      (after[b] = 0 frees the sequence).
+ *   2. A sequence that grows and whose last page is partly filled and shared
+ *      (refs > 1 after step 1) gets a page of its own in its place, and then its new ones.
+ *      Pages are given in the order of the sequences, the lowest free ones first;
+ *      what step 1 released counts as free, what step 2 replaces does not yet.
+ *      A sequence that cannot have all that it lacks gets none, as does every later
+ *      one that lacks any.
+ *   moves    i32 [seqs, 2]: (replaced page, its replacement), or (-1, -1); copy them in
+ *            every layer's cache (q8_cache_copy, q8_mx4_copy) before the new tokens are
+ *            written
+ *   missing  i32 [seqs]: 0, or the pages that the sequence lacks (nothing of it has
+ *            changed: call again with the same lengths once pages are free, and do not
+ *            write its new tokens), or -1 where before[b] or after[b] is negative or
+ *            past the table (it is left alone)
+ *   workspace  q8_pages_workspace bytes of device memory, 16-byte aligned; needs no preparation, and
+ *            one call at a time may use it
+ * Entries that are no page are released as nothing and never replaced.
+ */
+q8_status q8_pages_resize(const q8_pool *pool, const q8_page_table *table, const int32_t *before,
+                          const int32_t *after, int32_t *moves, int32_t *missing, void *workspace,
+                          int64_t workspace_bytes, void *stream);
+
+/*
+ * q8_pages_compact -- the order in which the used pages of a pool lie at its
+ * front: with U used pages, those from page U on move to the free ones below U, both
+ * in ascending order; the others stay.
+ *   lengths    i32 [from->seqs], device: tokens of each row, whose pages are renamed
+ *   refs_out   i32 [pages]: the counts in the new order
+ *   to         the table with the new names, as many rows and columns as `from`; -1 behind a
+ *              row's pages, in rows whose length is negative or past the table, and for
+ *              entries that are no used page
+ *   moves      i32 [pages / 2, 2]: (from, to), and (-1, -1) behind the last move; copy them in
+ *              every layer's cache before the new table is used
+ *   used       i32 [1]: U
+ *   workspace  as of q8_pages_resize
+ * Nothing that is read is written: refs and `from` stay as they were.
+ */
+q8_status q8_pages_compact(const q8_pool *pool, const q8_page_table *from, const int32_t *lengths,
+                           int32_t *refs_out, const q8_page_table *to, int32_t *moves, int32_t *used,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes that q8_pages_resize and q8_pages_compact need for this many pages and sequences; host only. */
+q8_status q8_pages_workspace(int64_t pages, int64_t seqs, int64_t *bytes);
+
+/*
+ * q8_cache_copy, q8_mx4_copy -- page moves[i, 0] of the cache, all heads, codes and
+ * scales of keys and values, is copied to page moves[i, 1], for i < n.  A pair that
+ * is not two different pages of the cache is passed over.  No page may be written twice, or
+ * written and read (moves of one resize or compact never are).
+ *   moves  i32 [n, 2], device
+ * Errors of all page operations: Q8_ERR_INVALID, Q8_ERR_TOO_LARGE, Q8_ERR_UNSUPPORTED_DEVICE,
+ * Q8_ERR_HIP.
+ */
+q8_status q8_cache_copy(const q8_cache *cache, const int32_t *moves, int64_t n, void *stream);
+q8_status q8_mx4_copy(const q8_mx4_cache *cache, const int32_t *moves, int64_t n, void *stream);
+
+/*
+ * Rotary positions: the first `rot` channels of every head are rot / 2 pairs, and pair
+ * i of a row at position p turns by the angle p * f_i:
+ *   (x, y) -> amplitude * (x cos - y sin, x sin + y cos)
+ * Pair i is channels (2 i, 2 i + 1) if interleaved, (i, i + rot / 2) if not.  The other
+ * channels stay as they are.  Frequencies are held as fractions of a turn in 64 bits,
+ * so that the angle is exact at any position; sine, cosine and products are f32,
+ * rounded once to the rows' type.
+ */
+typedef struct q8_rope_angles {
+  const uint64_t *turns; /* [rot / 2], device, 8-byte aligned: as q8_rope_turns makes them */
+  int32_t rot;           /* even, 2 .. dim */
+  int32_t interleaved;
+  float amplitude;       /* 1 unless the scaling wants another */
+} q8_rope_angles;
+
+#define Q8_MAX_ROPE_TENSORS 4
+typedef struct q8_rope_rows {
+  const void *x;      /* [rows, heads, dim], rows x_stride elements apart (at least heads * dim) */
+  void *out;          /* the same, out_stride apart; x itself (with its stride), or no part of any x */
+  int32_t heads;
+  int64_t x_stride, out_stride;
+} q8_rope_rows;
+
+/*
+ * q8_rope -- turns the rows of up to Q8_MAX_ROPE_TENSORS tensors (queries and keys, say) that
+ * share their positions, in one launch.
+ *   positions  i32 [rows], device, of any sign; or NULL:
+ *   seqs       the rows' sequences (its lengths and offsets; the table is not used): new token i of
+ *              sequence b, row offsets[b] + i, is at lengths[b] - n + i.  Rows of no sequence are
+ *              not written.  NULL where positions are given
+ *   inverse    nonzero: turns back (the sine's sign changes, the amplitude stays): the gradient
+ *              of the forward turn, and with an amplitude of 1 its inverse
+ *   dim        2 .. 4096
+ * Errors: Q8_ERR_INVALID, Q8_ERR_TOO_LARGE, Q8_ERR_UNSUPPORTED_DEVICE, Q8_ERR_HIP.
+ */
+q8_status q8_rope(const q8_rope_angles *angles, const q8_rope_rows *tensors, int32_t n_tensors,
+                  q8_type type, int64_t rows, int32_t dim, const int32_t *positions,
+                  const q8_cache_seqs *seqs, int32_t inverse, void *stream);
+
+/* Host only: turns[i] = frequencies[i] / (2 pi) modulo 1, in units of 2^-64 (finite radians per position). */
+q8_status q8_rope_turns(const double *frequencies, int64_t n, uint64_t *turns);
+
+/*
+ * q8_rope_frequencies -- host only: frequencies[i] = base^(-2 i / rot), i < rot / 2, for a
+ * context stretched by `factor`:
+ *   Q8_ROPE_PLAIN   as they are (factor is not used)
+ *   Q8_ROPE_LINEAR  all divided by factor
+ *   Q8_ROPE_BASE    from base * factor^(rot / (rot - 2)) (rot of 4 or more), so that the slowest is
+ *                   divided by factor and the fastest stays
+ *   Q8_ROPE_TURNS   by the turns r that the pair makes in the `length` tokens of the
+ *                   unstretched context: divided for r <= low, kept for r >= high, and between
+ *                   w f + (1 - w) f / factor with w = (r - low) / (high - low)
+ *   Q8_ROPE_INDEX   the same, with w linear in the pair's index: 1 at
+ *                   max(floor(index(high)), 0), 0 at min(ceil(index(low)), rot - 1), where
+ *                   index(r) = rot ln(length / (2 pi r)) / (2 ln base)
+ */
+typedef enum q8_rope_scaling {
+  Q8_ROPE_PLAIN = 0, Q8_ROPE_LINEAR = 1, Q8_ROPE_BASE = 2, Q8_ROPE_TURNS = 3, Q8_ROPE_INDEX = 4
+} q8_rope_scaling;
+q8_status q8_rope_frequencies(int32_t rot, double base, q8_rope_scaling scaling, double factor,
+                              double length, double low, double high, double *frequencies);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *q8_status_string(q8_status s);
 

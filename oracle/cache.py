@@ -114,12 +114,12 @@ def sees(length, n, tree_bits=None):
     return m
 
 
-def attention(q, cache, table, lengths, offsets, alpha, trees=None):
+def attention(q, cache, table, lengths, offsets, alpha, trees=None, sequence=sequence):
     """(out, spread, size): out f64 [rows, q_heads, dim]; spread f64 of out's shape,
     sum_j w_j |V_j| with the softmax weights w (the size of the terms out is
     made of); size f64 [rows, q_heads], the largest alpha * sum_d |q_d K_jd|
     over the tokens seen (the size of the terms of a score).  trees: per
-    sequence the tree_bits of sees()."""
+    sequence the tree_bits of sees().  sequence: how the cache's values are read."""
     q = np.asarray(q, dtype=np.float64)
     heads = cache["k"].shape[1]
     group = q.shape[1] // heads

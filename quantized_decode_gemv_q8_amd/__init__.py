@@ -7,9 +7,12 @@ Importing this package loads nothing; the library is loaded on first use.
 
 from .binding import (  # noqa: F401
     EXPORTED,
+    Mx4Cache,
     Q8Cache,
     Q8Error,
+    Rope,
     q8_cache_attention,
+    q8_cache_copy,
     q8_cache_keep,
     q8_cache_read,
     q8_cache_write,
@@ -22,6 +25,15 @@ from .binding import (  # noqa: F401
     q8_matvec_fused,
     q8_matvec_noalloc,
     q8_matvec_with_plan,
+    q8_mx4_attention,
+    q8_mx4_copy,
+    q8_mx4_keep,
+    q8_mx4_read,
+    q8_mx4_write,
+    q8_pages_compact,
+    q8_pages_fork,
+    q8_pages_resize,
     q8_release,
+    q8_rope,
     q8_status_string,
 )

@@ -6,6 +6,7 @@ built this module raises; there is no fallback implementation.
 """
 
 import ctypes
+import math
 import os
 
 import torch
@@ -38,6 +39,20 @@ EXPORTED = (
     "q8_cache_keep",
     "q8_cache_attention_workspace",
     "q8_cache_attention",
+    "q8_cache_copy",
+    "q8_mx4_write",
+    "q8_mx4_read",
+    "q8_mx4_keep",
+    "q8_mx4_attention_workspace",
+    "q8_mx4_attention",
+    "q8_mx4_copy",
+    "q8_pages_fork",
+    "q8_pages_resize",
+    "q8_pages_compact",
+    "q8_pages_workspace",
+    "q8_rope",
+    "q8_rope_turns",
+    "q8_rope_frequencies",
     "q8_status_string",
     "q8_last_hip_error",
     "q8_release",
@@ -70,6 +85,25 @@ class _CacheStruct(ctypes.Structure):
 class _SeqsStruct(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
+
+
+class _PoolStruct(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
+
+
+class _TableStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64)]
+
+
+class _AnglesStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
+
+
+class _RopeRowsStruct(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
 class Q8Error(RuntimeError):
@@ -111,17 +145,28 @@ def load():
         fn.argtypes = [p, p, p, i64, i64, i64, ctypes.POINTER(Q8Epilogue), p]
         fn.restype = ctypes.c_int
     cache, seqs = ctypes.POINTER(_CacheStruct), ctypes.POINTER(_SeqsStruct)
-    for name in ("q8_cache_write", "q8_cache_read"):
-        fn = getattr(L, name)
-        fn.argtypes = [cache, p, p, ctypes.c_int, i64, i64, i64, seqs, p]
-        fn.restype = ctypes.c_int
-    L.q8_cache_keep.argtypes = [cache, i64, seqs, p, i64, p]
-    L.q8_cache_keep.restype = ctypes.c_int
-    L.q8_cache_attention_workspace.argtypes = [cache, ctypes.c_int, i64, i32, seqs, ctypes.POINTER(i64)]
-    L.q8_cache_attention_workspace.restype = ctypes.c_int
-    L.q8_cache_attention.argtypes = [cache, p, p, ctypes.c_int, i64, i32, i64, i64, seqs, p, i64, ctypes.c_float,
-                                     p, i64, p]
-    L.q8_cache_attention.restype = ctypes.c_int
+    pool, table, i = ctypes.POINTER(_PoolStruct), ctypes.POINTER(_TableStruct), ctypes.c_int
+    signatures = {
+        "write": [cache, p, p, i, i64, i64, i64, seqs, p],
+        "read": [cache, p, p, i, i64, i64, i64, seqs, p],
+        "keep": [cache, i64, seqs, p, i64, p],
+        "attention_workspace": [cache, i, i64, i32, seqs, ctypes.POINTER(i64)],
+        "attention": [cache, p, p, i, i64, i32, i64, i64, seqs, p, i64, ctypes.c_float, p, i64, p],
+        "copy": [cache, p, i64, p],
+    }
+    signatures = {f"q8_{kind}_{name}": args for name, args in signatures.items() for kind in ("cache", "mx4")}
+    f64 = ctypes.c_double
+    signatures.update(
+        q8_pages_fork=[pool, table, p, p, table, p, p],
+        q8_pages_resize=[pool, table, p, p, p, p, p, i64, p],
+        q8_pages_compact=[pool, table, p, p, table, p, p, p, i64, p],
+        q8_pages_workspace=[i64, i64, ctypes.POINTER(i64)],
+        q8_rope=[ctypes.POINTER(_AnglesStruct), ctypes.POINTER(_RopeRowsStruct), i32, i, i64, i32, p, seqs, i32, p],
+        q8_rope_turns=[p, i64, p],
+        q8_rope_frequencies=[i32, f64, i, f64, f64, f64, f64, p],
+    )
+    for name, args in signatures.items():
+        getattr(L, name).argtypes, getattr(L, name).restype = args, i
     L.q8_status_string.argtypes = [ctypes.c_int]
     L.q8_status_string.restype = ctypes.c_char_p
     L.q8_last_hip_error.argtypes = []
@@ -353,22 +398,16 @@ def q8_dot_t_f32(A, B, out=None, alpha=1.0, corr=None, stream=None):
     return _dense("q8_dot_t_f32", A, B, True, out, alpha, corr, stream)
 
 
-# ------------------------------------------------------------------ the Q8_0 cache
+# ------------------------------------------------------------------ the caches
 
 #: Element types of the rows outside the cache.
 _ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
+_PAGE_SIZES = (16, 32, 64, 128, 256, 512, 1024)
 
-class Q8Cache:
-    """Keys and values of an attention layer in pages, in Q8_0.
 
-    k, v              i8  [pages, heads, page_size, dim], codes
-    k_scale, v_scale  f32 [pages, heads, page_size, dim // 32]
-
-    A token's value is code * scale.  Codes of a row lie in pair order: the
-    natural order [dim // 32, 16, 2] is stored as [16, dim // 32, 2].  The tensors
-    stay the caller's; the handle only checks them once.
-    """
+class _Cache:
+    """What the handles of both caches share: their tensors are checked once."""
 
     __slots__ = ("k", "k_scale", "v", "v_scale", "pages", "heads", "page_size", "dim", "device", "_struct", "_spans")
 
@@ -379,21 +418,23 @@ class Q8Cache:
             raise ValueError(f"k must be rank 4, got {k.dim()} dimensions")
         codes = k.shape
         pages, heads, page_size, dim = codes
+        dim *= self._PER_CODE
         if dim not in (64, 128, 256):
             raise ValueError(f"dim must be 64, 128 or 256, got {dim}")
-        if page_size not in (16, 32, 64, 128, 256, 512, 1024):
+        if page_size not in _PAGE_SIZES:
             raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
         scales, device = (pages, heads, page_size, dim // BLOCK), k.device
-        for name, t, dtype, shape in (("k", k, torch.int8, codes), ("k_scale", k_scale, torch.float32, scales),
-                                      ("v", v, torch.int8, codes), ("v_scale", v_scale, torch.float32, scales)):
+        code, scale = self._CODE, self._SCALE
+        for name, t, dtype, shape in (("k", k, code, codes), ("k_scale", k_scale, scale, scales),
+                                      ("v", v, code, codes), ("v_scale", v_scale, scale, scales)):
             _check_tensor(name, t, dtype, shape)
             if t.get_device() != device.index:
                 raise ValueError("all tensors must be on one device")
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
         self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, dim, device
-        n = pages * heads * page_size * dim
+        n, m = k.numel(), k_scale.numel() * k_scale.element_size()
         a, b, c, d = at = k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr()
-        self._spans = (a, a + n), (b, b + n // 8), (c, c + n), (d, d + n // 8)
+        self._spans = (a, a + n), (b, b + m), (c, c + n), (d, d + m)
         edge = 0
         for a, b in sorted(self._spans):
             if a < edge and n:
@@ -412,14 +453,51 @@ class Q8Cache:
         """A cache with new tensors; what it holds is undefined until it is written."""
         def new(last, dtype):
             return torch.empty((pages, heads, page_size, last), dtype=dtype, device=device)
-        return cls(new(dim, torch.int8), new(dim // BLOCK, torch.float32),
-                   new(dim, torch.int8), new(dim // BLOCK, torch.float32))
+        return cls(new(dim // cls._PER_CODE, cls._CODE), new(dim // BLOCK, cls._SCALE),
+                   new(dim // cls._PER_CODE, cls._CODE), new(dim // BLOCK, cls._SCALE))
 
 
-def _cache_seqs(cache, table, lengths, offsets, stream=None):
+class Q8Cache(_Cache):
+    """Keys and values of an attention layer in pages, in Q8_0.
+
+    k, v              i8  [pages, heads, page_size, dim], codes
+    k_scale, v_scale  f32 [pages, heads, page_size, dim // 32]
+
+    A token's value is code * scale.  Codes of a row lie in pair order: the
+    natural order [dim // 32, 16, 2] is stored as [16, dim // 32, 2].  The tensors
+    stay the caller's; the handle only checks them once.
+    """
+
+    __slots__ = ()
+    _PER_CODE, _CODE, _SCALE, _PREFIX = 1, torch.int8, torch.float32, "q8_cache_"
+
+
+class Mx4Cache(_Cache):
+    """Keys and values of an attention layer in pages, in 4-bit floats.
+
+    k, v              u8 [pages, heads, page_size, dim // 2], two codes to a byte
+    k_scale, v_scale  u8 [pages, heads, page_size, dim // 32], 2^(byte - 127), 255: NaN
+
+    A code's sign and index 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Channels 32 b + 2 j
+    and 32 b + 2 j + 1 of a key are the low and the high half of byte j * (dim // 32) + b
+    of its row; of a value, of byte (4 j + token % 4) * (dim // 32) + b of the 2 * dim
+    bytes that four neighbouring tokens of a page share.  The tensors stay the
+    caller's; the handle only checks them once.
+    """
+
+    __slots__ = ()
+    _PER_CODE, _CODE, _SCALE, _PREFIX = 2, torch.uint8, torch.uint8, "q8_mx4_"
+
+    def __init__(self, k, k_scale, v, v_scale):
+        super().__init__(k, k_scale, v, v_scale)
+        if any(a % 16 for a, _ in self._spans):
+            raise ValueError("the cache's tensors must be 16-byte aligned")
+
+
+def _cache_seqs(cache, table, lengths, offsets, stream=None, kind=Q8Cache):
     """The checked descriptor of a call's sequences; the call's stream is checked too."""
-    if not isinstance(cache, Q8Cache):
-        raise TypeError("cache must be a Q8Cache")
+    if not isinstance(cache, kind):
+        raise TypeError(f"cache must be a {kind.__name__}")
     if stream is not None and stream.device != cache.device:
         raise ValueError(f"the stream is of {stream.device}, the cache of {cache.device}")
     index, i32 = cache.device.index, torch.int32
@@ -530,11 +608,8 @@ def _call(cache, stream, what, fn, *args):
         raise Q8Error(st, what)
 
 
-def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
-    """Quantises rows k and v ([rows, heads, dim]) into the cache: sequence b's
-    newest offsets[b+1] - offsets[b] tokens of lengths[b] are rows offsets[b]
-    .. of k and v, and live in the pages table[b]."""
-    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
+def _write(kind, cache, k, v, table, lengths, offsets, stream):
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream, kind)
     ks, k0 = _cache_rows("k", k, None, cache.heads, cache)
     vs, v0 = _cache_rows("v", v, k.shape[0], cache.heads, cache, k.dtype)
     rows, size = k.shape[0], k.element_size()
@@ -544,15 +619,12 @@ def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
         cache._apart("v", v0, v0 + ((rows - 1) * vs + width) * size)
     for name, a, b in _seqs_spans(seqs):
         cache._apart(name, a, b)
-    _call(cache, stream, "q8_cache_write", load().q8_cache_write, cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks,
-          vs, seqs)
+    what = kind._PREFIX + "write"
+    _call(cache, stream, what, getattr(load(), what), cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks, vs, seqs)
 
 
-def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
-    """The newest offsets[b+1] - offsets[b] tokens of each sequence as rows
-    [rows, heads, dim] of dtype; returns (k, v).  Rows of no sequence keep what
-    the given k and v hold (new tensors: undefined)."""
-    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
+def _read(kind, cache, table, lengths, offsets, rows, dtype, k, v, stream):
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream, kind)
     rows = int(rows)
     shape = (rows, cache.heads, cache.dim)
     if k is None and v is None:
@@ -571,18 +643,13 @@ def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=N
         cache._apart("v", *_span(v))
         _check_apart("k", k, inputs)
         _check_apart("v", v, inputs + (("k", k),))
-    _call(cache, stream, "q8_cache_read", load().q8_cache_read, cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks, vs,
-          seqs)
+    what = kind._PREFIX + "read"
+    _call(cache, stream, what, getattr(load(), what), cache._struct, k0, v0, _ROW_TYPES[k.dtype], rows, ks, vs, seqs)
     return k, v
 
 
-def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
-    """Moves new token keep[b, a] of sequence b to the place of its new token a,
-    a = 0, 1, ...; keep is i32 [sequences, width], strictly ascending until its
-    first negative entry.  rows: of the row tensors that the offsets refer to; a
-    sequence whose offsets pass them has no new tokens, as in q8_cache_write
-    (None: offsets may be of any size)."""
-    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
+def _keep(kind, cache, table, lengths, offsets, keep, stream, rows):
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream, kind)
     if not isinstance(keep, torch.Tensor):
         raise TypeError("keep must be a torch.Tensor")
     if keep.dim() != 2:
@@ -593,25 +660,17 @@ def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
     cache._apart("keep", *_span(keep))
     for name, a, b in _seqs_spans(seqs):
         cache._apart(name, a, b)
-    _call(cache, stream, "q8_cache_keep", load().q8_cache_keep, cache._struct,
-          MAX_CACHE_ROWS if rows is None else int(rows), seqs, keep.data_ptr(), keep.shape[1])
+    what = kind._PREFIX + "keep"
+    _call(cache, stream, what, getattr(load(), what), cache._struct, MAX_CACHE_ROWS if rows is None else int(rows), seqs,
+          keep.data_ptr(), keep.shape[1])
 
 
 #: Most rows a call's offsets may refer to.
 MAX_CACHE_ROWS = (1 << 31) - 1
 
 
-def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None, out=None, stream=None):
-    """Attention of the new tokens' queries q ([rows, q_heads, dim]) over the
-    cache, their own keys and values included; returns out, shaped like q.
-
-    Row offsets[b] + i (new token i of sequence b) sees every token before the
-    new ones and, of the new ones, those up to i; or with tree (i64 [rows, words])
-    those j whose bit j % 64 of word j // 64 of the row is set.  alpha: scale of
-    the scores, 1 / sqrt(dim) if None.  Rows of no sequence keep what out holds
-    (a new out: undefined); rows that see nothing are zeros.
-    """
-    seqs = _cache_seqs(cache, table, lengths, offsets, stream)
+def _attention(kind, q, cache, table, lengths, offsets, tree, alpha, out, stream):
+    seqs = _cache_seqs(cache, table, lengths, offsets, stream, kind)
     qs, q0 = _cache_rows("q", q, None, None, cache)
     rows, q_heads = q.shape[0], q.shape[1]
     if q_heads == 0 or cache.heads == 0 or q_heads % cache.heads:
@@ -643,9 +702,9 @@ def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None,
     mask = None
     if tree is not None:  # an empty tree still is one: no new token is seen
         mask = tree.data_ptr() if words and rows else offsets.data_ptr() & -8
-    _call(cache, stream, "q8_cache_attention", load().q8_cache_attention, cache._struct, q0, out0,
-          _ROW_TYPES[q.dtype], rows, q_heads, qs, os_, seqs, mask, words, float(alpha),
-          None if work is None else work.data_ptr(), need)
+    what = kind._PREFIX + "attention"
+    _call(cache, stream, what, getattr(load(), what), cache._struct, q0, out0, _ROW_TYPES[q.dtype], rows, q_heads, qs, os_,
+          seqs, mask, words, float(alpha), None if work is None else work.data_ptr(), need)
     return out
 
 
@@ -655,16 +714,376 @@ _WORKSPACE = {}
 
 def _attention_workspace(cache, type_, rows, q_heads, seqs):
     # whether there are any pages counts: without, no token of the table is one
+    prefix = cache._PREFIX
     key = (cache.device.index, cache.pages > 0, cache.heads, cache.page_size, cache.dim, type_, rows, q_heads,
-           seqs.seqs, seqs.max_pages)
+           seqs.seqs, seqs.max_pages, prefix)
     need = _WORKSPACE.get(key)
     if need is None:
         size = ctypes.c_int64(0)
         with torch.cuda.device(cache.device):
-            st = load().q8_cache_attention_workspace(cache._struct, type_, rows, q_heads, seqs, size)
+            st = getattr(load(), prefix + "attention_workspace")(cache._struct, type_, rows, q_heads, seqs, size)
         if st != Q8_OK:
-            raise Q8Error(st, "q8_cache_attention")
+            raise Q8Error(st, prefix + "attention")
         if len(_WORKSPACE) >= 4096:
             _WORKSPACE.clear()
         need = _WORKSPACE[key] = size.value
     return need
+
+
+def q8_cache_write(cache, k, v, table, lengths, offsets, stream=None):
+    """Quantises rows k and v ([rows, heads, dim]) into the cache: sequence b's
+    newest offsets[b+1] - offsets[b] tokens of lengths[b] are rows offsets[b]
+    .. of k and v, and live in the pages table[b]."""
+    _write(Q8Cache, cache, k, v, table, lengths, offsets, stream)
+
+
+def q8_cache_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
+    """The newest offsets[b+1] - offsets[b] tokens of each sequence as rows
+    [rows, heads, dim] of dtype; returns (k, v).  Rows of no sequence keep what
+    the given k and v hold (new tensors: undefined)."""
+    return _read(Q8Cache, cache, table, lengths, offsets, rows, dtype, k, v, stream)
+
+
+def q8_cache_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
+    """Moves new token keep[b, a] of sequence b to the place of its new token a,
+    a = 0, 1, ...; keep is i32 [sequences, width], strictly ascending until its
+    first negative entry.  rows: of the row tensors that the offsets refer to; a
+    sequence whose offsets pass them has no new tokens, as in q8_cache_write
+    (None: offsets may be of any size)."""
+    _keep(Q8Cache, cache, table, lengths, offsets, keep, stream, rows)
+
+
+def q8_cache_attention(q, cache, table, lengths, offsets, tree=None, alpha=None, out=None, stream=None):
+    """Attention of the new tokens' queries q ([rows, q_heads, dim]) over the
+    cache, their own keys and values included; returns out, shaped like q.
+
+    Row offsets[b] + i (new token i of sequence b) sees every token before the
+    new ones and, of the new ones, those up to i; or with tree (i64 [rows, words])
+    those j whose bit j % 64 of word j // 64 of the row is set.  alpha: scale of
+    the scores, 1 / sqrt(dim) if None.  Rows of no sequence keep what out holds
+    (a new out: undefined); rows that see nothing are zeros.
+    """
+    return _attention(Q8Cache, q, cache, table, lengths, offsets, tree, alpha, out, stream)
+
+
+def q8_mx4_write(cache, k, v, table, lengths, offsets, stream=None):
+    """q8_cache_write for an Mx4Cache: per 32 channels one power-of-two scale and
+    4-bit floats, rounded to the nearest."""
+    _write(Mx4Cache, cache, k, v, table, lengths, offsets, stream)
+
+
+def q8_mx4_read(cache, table, lengths, offsets, rows, dtype=torch.float32, k=None, v=None, stream=None):
+    """q8_cache_read for an Mx4Cache."""
+    return _read(Mx4Cache, cache, table, lengths, offsets, rows, dtype, k, v, stream)
+
+
+def q8_mx4_keep(cache, table, lengths, offsets, keep, stream=None, rows=None):
+    """q8_cache_keep for an Mx4Cache."""
+    _keep(Mx4Cache, cache, table, lengths, offsets, keep, stream, rows)
+
+
+def q8_mx4_attention(q, cache, table, lengths, offsets, tree=None, alpha=None, out=None, stream=None):
+    """q8_cache_attention over an Mx4Cache; alpha must be finite."""
+    return _attention(Mx4Cache, q, cache, table, lengths, offsets, tree, alpha, out, stream)
+
+
+# ------------------------------------------------------------------ pages
+
+def _ints(device, **named):
+    """Checks named i32 device tensors, given with their shapes: (tensor, shape)."""
+    for name, (t, shape) in named.items():
+        _check_tensor(name, t, torch.int32, shape)
+        if t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _pool(refs, page_size, stream):
+    if not isinstance(refs, torch.Tensor):
+        raise TypeError("refs must be a torch.Tensor")
+    if refs.dim() != 1:
+        raise ValueError(f"refs must be rank 1, got {refs.dim()} dimensions")
+    _check_tensor("refs", refs, torch.int32, refs.shape)
+    if page_size not in _PAGE_SIZES:
+        raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
+    if stream is not None and stream.device != refs.device:
+        raise ValueError(f"the stream is of {stream.device}, the pool of {refs.device}")
+    return _PoolStruct(refs.data_ptr(), refs.shape[0], int(page_size))
+
+
+def _table(name, t, device):
+    """The descriptor of a page table, whose rows may be apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError("all tensors must be on one device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be rank 2, got {t.dim()} dimensions")
+    n, pages = t.shape
+    if t.numel() and not t.is_contiguous() and pages > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    stride = t.stride(0) if n > 1 else pages
+    if stride < pages:
+        raise ValueError(f"rows of {name} must not overlap")
+    return _TableStruct(t.data_ptr(), n, pages, stride)
+
+
+def _all_apart(written, read):
+    """Refuses calls whose written tensors overlap each other or a read one."""
+    for i, (name, t) in enumerate(written):
+        a, b = _span(t)
+        for other, u in written[i + 1:] + read:
+            c, d = _span(u)
+            if a < d and c < b:
+                raise ValueError(f"{name} overlaps {other}")
+
+
+def _pages_workspace(pool, seqs, stream, device):
+    size = ctypes.c_int64(0)
+    st = load().q8_pages_workspace(pool.pages, seqs, size)
+    if st != Q8_OK:
+        raise Q8Error(st, "q8_pages_workspace")
+    # held by the caller until the call has returned, as the attention's is
+    return _empty_on(stream, (max(size.value, 16),), torch.uint8, device), size.value
+
+
+def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengths_out=None, stream=None):
+    """Children share their parents' pages: row i of table_out ([children, columns])
+    becomes the pages of row parent[i] of table, -1 behind them, and each page's count
+    of owners in refs grows by one; lengths_out[i] = lengths[parent[i]].  Returns
+    (table_out, lengths_out); new ones have as many columns as table.  What given ones
+    owned before is not released: resize it to 0 first.  A parent that is no row gives
+    no pages and length 0."""
+    pool = _pool(refs, page_size, stream)
+    device = refs.device
+    source = _table("table", table, device)
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 1:
+        raise TypeError("parent must be a torch.Tensor of rank 1")
+    n = parent.shape[0]
+    if table_out is None:
+        table_out = _empty_on(stream, (n, table.shape[1]), torch.int32, device)
+    if lengths_out is None:
+        lengths_out = _empty_on(stream, (n,), torch.int32, device)
+    to = _table("table_out", table_out, device)
+    if table_out.shape[0] != n:
+        raise ValueError(f"{n} parents need {n} rows of table_out, got {table_out.shape[0]}")
+    _ints(device, lengths=(lengths, (table.shape[0],)), parent=(parent, (n,)), lengths_out=(lengths_out, (n,)))
+    _all_apart([("table_out", table_out), ("lengths_out", lengths_out), ("refs", refs)],
+               [("table", table), ("lengths", lengths), ("parent", parent)])
+    _call(refs, stream, "q8_pages_fork", load().q8_pages_fork, pool, source, lengths.data_ptr(), parent.data_ptr(), to,
+          lengths_out.data_ptr())
+    return table_out, lengths_out
+
+
+def q8_pages_resize(refs, table, before, after, page_size, moves=None, missing=None, stream=None):
+    """Sequence b, which holds the pages of before[b] tokens in its row of table, comes
+    to hold those of after[b] (0: it leaves): released pages lose an owner in refs, new ones are the
+    lowest free ones in the order of the sequences.  A last page that is partly filled,
+    shared, and about to grow is replaced.  refs and table change in place.  Returns
+    (moves, missing): i32 [seqs, 2] pages to copy in every cache (q8_cache_copy,
+    q8_mx4_copy; -1 where there are none), and i32 [seqs] pages that a sequence could
+    not be given (nothing of it has changed then), or -1 for lengths that the table
+    cannot hold."""
+    pool = _pool(refs, page_size, stream)
+    device = refs.device
+    rows = _table("table", table, device)
+    n = table.shape[0]
+    if moves is None:
+        moves = _empty_on(stream, (n, 2), torch.int32, device)
+    if missing is None:
+        missing = _empty_on(stream, (n,), torch.int32, device)
+    _ints(device, before=(before, (n,)), after=(after, (n,)), moves=(moves, (n, 2)), missing=(missing, (n,)))
+    _all_apart([("refs", refs), ("table", table), ("moves", moves), ("missing", missing)],
+               [("before", before), ("after", after)])
+    work, need = _pages_workspace(pool, n, stream, device)
+    _call(refs, stream, "q8_pages_resize", load().q8_pages_resize, pool, rows, before.data_ptr(), after.data_ptr(),
+          moves.data_ptr(), missing.data_ptr(), work.data_ptr(), need)
+    return moves, missing
+
+
+def q8_pages_compact(refs, table, lengths, page_size, refs_out=None, table_out=None, moves=None, used=None, stream=None):
+    """The pool with its U used pages at the front: those from page U on move to the
+    free ones below, both in ascending order.  Returns (refs_out, table_out, moves,
+    used): the counts and the table (the pages of lengths[b] tokens of each row)
+    under the new names, i32 [pages // 2, 2] pages to copy in every cache, -1 behind the
+    last, and i32 [1] U.  refs and table stay as they were."""
+    pool = _pool(refs, page_size, stream)
+    device = refs.device
+    source = _table("table", table, device)
+    pages, n = refs.shape[0], table.shape[0]
+    new = lambda t, *shape: _empty_on(stream, shape, torch.int32, device) if t is None else t  # noqa: E731
+    refs_out, table_out = new(refs_out, pages), new(table_out, *table.shape)
+    moves, used = new(moves, pages // 2, 2), new(used, 1)
+    to = _table("table_out", table_out, device)
+    if table_out.shape != table.shape:
+        raise ValueError(f"table_out must have shape {tuple(table.shape)}, got {tuple(table_out.shape)}")
+    _ints(device, lengths=(lengths, (n,)), refs_out=(refs_out, (pages,)), moves=(moves, (pages // 2, 2)), used=(used, (1,)))
+    _all_apart([("refs_out", refs_out), ("table_out", table_out), ("moves", moves), ("used", used)],
+               [("refs", refs), ("table", table), ("lengths", lengths)])
+    work, need = _pages_workspace(pool, n, stream, device)
+    _call(refs, stream, "q8_pages_compact", load().q8_pages_compact, pool, source, lengths.data_ptr(), refs_out.data_ptr(),
+          to, moves.data_ptr(), used.data_ptr(), work.data_ptr(), need)
+    return refs_out, table_out, moves, used
+
+
+def _copy(kind, cache, moves, stream):
+    if not isinstance(cache, kind):
+        raise TypeError(f"cache must be a {kind.__name__}")
+    if stream is not None and stream.device != cache.device:
+        raise ValueError(f"the stream is of {stream.device}, the cache of {cache.device}")
+    if not isinstance(moves, torch.Tensor):
+        raise TypeError("moves must be a torch.Tensor")
+    if moves.dim() != 2:
+        raise ValueError(f"moves must be rank 2, got {moves.dim()} dimensions")
+    _ints(cache.device, moves=(moves, (moves.shape[0], 2)))
+    cache._apart("moves", *_span(moves))
+    what = kind._PREFIX + "copy"
+    _call(cache, stream, what, getattr(load(), what), cache._struct, moves.data_ptr(), moves.shape[0])
+
+
+def q8_cache_copy(cache, moves, stream=None):
+    """Copies page moves[i, 0] of a Q8Cache to its page moves[i, 1]; pairs that are not
+    two different pages of it are passed over.  No page may be written twice, or written
+    and read, as the moves of one q8_pages_resize or q8_pages_compact never are."""
+    _copy(Q8Cache, cache, moves, stream)
+
+
+def q8_mx4_copy(cache, moves, stream=None):
+    """q8_cache_copy for an Mx4Cache."""
+    _copy(Mx4Cache, cache, moves, stream)
+
+
+# ------------------------------------------------------------------ rotary positions
+
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
+
+
+class Rope:
+    """The frequencies of rotary positions, on the device.
+
+    frequencies: radians per position of each channel pair, rot // 2 of them (numbers,
+    or a tensor on the host).  interleaved: pair i is channels (2 i, 2 i + 1) of a head,
+    else (i, i + rot // 2).  amplitude: a factor of what is turned.
+    """
+
+    __slots__ = ("turns", "rot", "interleaved", "amplitude", "device", "_struct")
+
+    def __init__(self, frequencies, interleaved=False, amplitude=1.0, device="cuda"):
+        f = torch.as_tensor(frequencies, dtype=torch.float64, device="cpu").contiguous()
+        if f.dim() != 1 or f.shape[0] == 0:
+            raise ValueError("frequencies must be rank 1 and not empty")
+        turns = torch.empty(f.shape, dtype=torch.int64)
+        st = load().q8_rope_turns(f.data_ptr(), f.shape[0], turns.data_ptr())
+        if st != Q8_OK:
+            raise Q8Error(st, "q8_rope_turns")
+        self.turns = turns.to(device)
+        self.device = self.turns.device
+        self.rot, self.interleaved, self.amplitude = 2 * f.shape[0], bool(interleaved), float(amplitude)
+        self._struct = _AnglesStruct(self.turns.data_ptr(), self.rot, int(self.interleaved), self.amplitude)
+
+    @staticmethod
+    def frequencies(rot, base=10000.0, scaling="none", factor=1.0, length=0.0, low=None, high=None):
+        """base^(-2 i / rot) for a context of `length` tokens that is stretched by factor: all
+        divided by it ("linear"), from a larger base ("base"), or the slow ones only, by
+        the turns that a pair makes in the length ("turns": divided up to low = 1, kept from high = 4
+        on) or by its index ("index": low = 1, high = 32).  A list of floats."""
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}, got {scaling}")
+        low = 1.0 if low is None else low
+        high = (32.0 if scaling == "index" else 4.0) if high is None else high
+        out = (ctypes.c_double * max(int(rot) // 2, 1))()
+        st = load().q8_rope_frequencies(int(rot), base, _SCALINGS[scaling], factor, length, low, high, out)
+        if st != Q8_OK:
+            raise Q8Error(st, "q8_rope_frequencies")
+        return list(out)
+
+    @classmethod
+    def scaled(cls, rot, base=10000.0, scaling="none", factor=1.0, length=0.0, low=None, high=None, interleaved=False,
+               amplitude=None, device="cuda"):
+        """A Rope of those frequencies.  amplitude None: 0.1 ln(factor) + 1 for "index", 1 otherwise."""
+        f = cls.frequencies(rot, base, scaling, factor, length, low, high)
+        if amplitude is None:
+            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "index" else 1.0
+        return cls(f, interleaved, amplitude, device)
+
+
+def _rope_rows(name, t, rows, dim, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError("all tensors must be on one device")
+    if t.dim() != 3 or t.shape[2] != dim or t.shape[0] != rows:
+        raise ValueError(f"{name} must have shape ({rows}, heads, {dim}), got {tuple(t.shape)}")
+    n, h, _ = t.shape
+    if n == 0 or h == 0 or t.is_contiguous():
+        return h * dim
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != dim):
+        raise ValueError(f"{name} must be dense in its last two dimensions")
+    if n > 1 and s0 < h * dim:
+        raise ValueError(f"rows of {name} must not overlap")
+    return s0 if n > 1 else h * dim
+
+
+def q8_rope(x, rope, positions=None, lengths=None, offsets=None, inverse=False, out=None, stream=None):
+    """Turns the first rope.rot channels of every head of x by its row's position.
+
+    x: a tensor [rows, heads, dim] of float32, bfloat16 or float16, or up to four that
+    share rows, dim and type (queries and keys: one launch).  positions: i32 [rows]; or
+    lengths and offsets as a cache takes them: new token i of sequence b is at
+    lengths[b] - n + i, and rows of no sequence are not written.  inverse: turns back (the
+    gradient of the forward turn).  out: like x, and may be x itself.  Returns out, or
+    a tuple of them."""
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    device = rope.device
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the rope of {device}")
+    one = isinstance(x, torch.Tensor)
+    xs = (x,) if one else tuple(x)
+    if not 1 <= len(xs) <= 4:
+        raise ValueError(f"between one and four tensors, got {len(xs)}")
+    if not isinstance(xs[0], torch.Tensor) or xs[0].dim() != 3:
+        raise ValueError("x must be tensors of rank 3")
+    rows, _, dim = xs[0].shape
+    dtype = xs[0].dtype
+    if rope.rot > dim:
+        raise ValueError(f"the rope turns {rope.rot} channels, x has {dim}")
+    strides = [_rope_rows("x", t, rows, dim, dtype, device) for t in xs]
+    if out is None:
+        outs = tuple(_empty_on(stream, t.shape, dtype, device) for t in xs)
+        out_strides = [t.shape[1] * dim for t in xs]
+    else:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(xs):
+            raise ValueError(f"{len(xs)} tensors need as many outputs, got {len(outs)}")
+        out_strides = [_rope_rows("out", o, rows, dim, dtype, device) for o in outs]
+        for i, (t, o) in enumerate(zip(xs, outs)):
+            if o.shape != t.shape:
+                raise ValueError(f"out must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
+            same = o.data_ptr() == t.data_ptr() and out_strides[i] == strides[i]
+            others = [("x", u) for j, u in enumerate(xs) if j != i or not same]
+            others += [("another out", u) for u in outs[:i]]
+            _check_apart("out", o, others + [("positions", positions), ("lengths", lengths), ("offsets", offsets),
+                                             ("the rope", rope.turns)])
+    if positions is not None:
+        if lengths is not None or offsets is not None:
+            raise ValueError("pass positions, or lengths and offsets")
+        _ints(device, positions=(positions, (rows,)))
+        seqs = None
+    else:
+        if not isinstance(lengths, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+            raise TypeError("pass positions, or lengths and offsets")
+        if lengths.dim() != 1:
+            raise ValueError(f"lengths must be rank 1, got {lengths.dim()} dimensions")
+        n = lengths.shape[0]
+        _ints(device, lengths=(lengths, (n,)), offsets=(offsets, (n + 1,)))
+        seqs = _SeqsStruct(None, lengths.data_ptr(), offsets.data_ptr(), n, 0, 0)
+    tensors = (_RopeRowsStruct * len(xs))(*((t.data_ptr(), o.data_ptr(), t.shape[1], a, b)
+                                            for t, o, a, b in zip(xs, outs, strides, out_strides)))
+    _call(rope, stream, "q8_rope", load().q8_rope, rope._struct, tensors, len(xs), _ROW_TYPES[dtype], rows, dim,
+          None if positions is None else positions.data_ptr(), seqs, int(inverse))
+    return outs[0] if one else outs

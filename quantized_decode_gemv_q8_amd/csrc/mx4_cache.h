@@ -1,0 +1,43 @@
+// Internal declarations of the cache in 4-bit floats, and its attention.
+#pragma once
+
+#include "q8_attention.h"
+
+namespace q8 {
+
+// A cache of 4-bit floats: pages as those of the Q8_0 cache, u8 arrays
+//   K, V    [pages, heads, page_size, dim / 2]   codes, two to a byte
+//   KS, VS  [pages, heads, page_size, dim / 32]  scales, 2^(byte - 127)
+// Channel d = 32 b + 2 j + i of a row is nibble i (low first) of byte
+// j * (dim / 32) + b of the row in K.  In V four neighbouring tokens of a page
+// share 2 * dim bytes, and the byte is (4 j + token % 4) * (dim / 32) + b of them.
+// A lane of the attention then finds what it needs of a tile in one run of dim / 8
+// bytes: of K the pairs 4 c .. 4 c + 3 of all blocks of one key, of V the pair j of
+// all blocks of four keys.  A byte is what one conversion takes.
+// The kernels' arguments are those of the Q8_0 cache with these arrays in them.
+inline Cache mx4_cache(uint8_t *K, uint8_t *KS, uint8_t *V, uint8_t *VS) {
+  Cache c;
+  c.K = reinterpret_cast<int8_t *>(K);
+  c.KS = reinterpret_cast<float *>(KS);
+  c.V = reinterpret_cast<int8_t *>(V);
+  c.VS = reinterpret_cast<float *>(VS);
+  return c;
+}
+
+// Scale bytes: kMx4Least .. kMx4Most, and 255 for a block that holds an infinity
+// or a NaN.  Half of the least scale, the smallest value, is a normal bf16;
+// six times the largest is a finite one.
+constexpr int kMx4Least = 2, kMx4Most = 252;
+
+hipError_t launch_mx4_write(const CacheRowsArgs &a, RowType type, hipStream_t stream);
+hipError_t launch_mx4_read(const CacheRowsArgs &a, RowType type, hipStream_t stream);
+hipError_t launch_mx4_keep(const CacheKeepArgs &a, hipStream_t stream);
+
+// Rows of an item of the kernel whose waves share keys.
+constexpr int mx4_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
+
+hipError_t launch_mx4_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
+hipError_t launch_mx4_attention_bf16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
+hipError_t launch_mx4_attention_f16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
+
+}  // namespace q8

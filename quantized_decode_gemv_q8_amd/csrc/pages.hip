@@ -1,0 +1,490 @@
+// A pool of pages: forking, growing, freeing and compacting the page tables of
+// sequences, and copying pages.
+//
+// refs[p] counts the table rows that own page p; a page is free where it is not
+// above zero.  Everything is decided by order, never by timing: pages are given
+// to the sequences in their order, the lowest free ones first, and compacting
+// keeps the order of what it moves.
+//
+// resize and compact go through phases that each need all of the one before:
+// counts of tiles of pages, their prefixes, what follows from them.  A small pool
+// runs them in one workgroup, a large one as one launch each over the device.
+#include <algorithm>
+
+#include "pages.h"
+
+namespace q8 {
+namespace {
+
+constexpr int kBig = 1024;  // threads of a workgroup of resize and compact
+constexpr int kBigWaves = kBig / 64;
+
+__device__ __forceinline__ bool is_page(int p, int pages) { return (uint32_t)p < (uint32_t)pages; }
+
+// Pages of `tokens` tokens, for 0 <= tokens < 2^30.
+__device__ __forceinline__ int pages_of(int tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
+
+__device__ __forceinline__ bool fits(int tokens, const PageTable &t) { return tokens >= 0 && tokens <= t.max_tokens; }
+
+template <typename X>
+__device__ __forceinline__ X wave_sum_before(X x, int lane) {  // exclusive
+  X upto = x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const X other = __shfl_up(upto, d);
+    if (lane >= d) upto += other;
+  }
+  return upto - x;
+}
+
+// Exclusive sum over the workgroup's threads, and the sum of all.
+template <typename X>
+__device__ __forceinline__ X block_sum_before(X x, X *all) {
+  __shared__ X sums[kBigWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const X before = wave_sum_before(x, lane);
+  if (lane == 63) sums[wave] = before + x;
+  __syncthreads();
+  X base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kBigWaves; ++w) {
+    const X s = sums[w];
+    if (w < wave) base += s;
+    total += s;
+  }
+  __syncthreads();  // before `sums` is written again
+  *all = total;
+  return base + before;
+}
+
+// Sum of x[0 .. n - 1], by the whole workgroup.
+template <typename X>
+__device__ __forceinline__ int64_t block_total(const X *x, int64_t n) {
+  int64_t mine = 0, all;
+  for (int64_t i = threadIdx.x; i < n; i += kBig) mine += x[i];
+  block_sum_before(mine, &all);
+  return all;
+}
+
+// The four neighbouring pages of this thread in tile t: bit k of the result is set
+// where refs[first + k] > 0; pages past the pool are left out of `in`.
+__device__ __forceinline__ int used_bits(const int *refs, int pages, int64_t t, int64_t *first, int *in) {
+  const int64_t p = t * kPagesTile + 4 * (int64_t)threadIdx.x;
+  *first = p;
+  int used = 0;
+  *in = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (p + k < pages) {
+      *in |= 1 << k;
+      if (refs[p + k] > 0) used |= 1 << k;
+    }
+  return used;
+}
+
+// A workgroup's share of `tiles` tiles.
+struct Tiles {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Tiles share(int64_t tiles) {
+  const int64_t per = (tiles + gridDim.x - 1) / gridDim.x;
+  const int64_t begin = min(per * blockIdx.x, tiles);
+  return Tiles{begin, min(begin + per, tiles)};
+}
+
+// ---------------------------------------------------------------- fork
+
+// One wave per child.
+__global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t waves = (int64_t)gridDim.x * kWaves;
+  for (int64_t i = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); i < a.to.seqs; i += waves) {
+    const int parent = a.parent[i];
+    int length = 0;
+    if ((uint32_t)parent < (uint32_t)a.from.seqs) length = a.lengths[parent];
+    if (!fits(length, a.from) || !fits(length, a.to)) length = 0;
+    const int held = pages_of(length, a.page_shift);
+    int *to = a.to.table + i * a.to.stride;
+    const int *from = a.from.table + (int64_t)(held > 0 ? parent : 0) * a.from.stride;
+    for (int c = lane; c < a.to.max_pages; c += 64) {
+      int page = -1;
+      if (c < held) {
+        page = from[c];
+        if (is_page(page, a.pages))
+          atomicAdd(a.refs + page, 1);
+        else
+          page = -1;
+      }
+      to[c] = page;
+    }
+    if (lane == 0) a.lengths_out[i] = length;
+  }
+}
+
+// ---------------------------------------------------------------- resize
+
+struct Change {
+  int held, want;  // pages before and after
+  bool ok;         // neither is outside of the table
+  bool writes;     // into the last page that it holds
+};
+__device__ __forceinline__ Change change_of(const ResizeArgs &a, int64_t b) {
+  const int before = a.before[b], after = a.after[b];
+  Change c;
+  c.ok = fits(before, a.t) && fits(after, a.t);
+  c.held = c.ok ? pages_of(before, a.page_shift) : 0;
+  c.want = c.ok ? pages_of(after, a.page_shift) : 0;
+  c.writes = c.ok && after > before && (before & ((1 << a.page_shift) - 1)) != 0;
+  return c;
+}
+
+// Phase 0: pages past what is wanted are released, one wave per sequence.
+__device__ void resize_release(const ResizeArgs &a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t waves = (int64_t)gridDim.x * kBigWaves;
+  // A wave looks at up to 64 sequences at a time and takes those that shrink one by one.
+  const int64_t each = min((a.t.seqs + waves - 1) / waves, (int64_t)64);
+  for (int64_t b0 = ((int64_t)blockIdx.x * kBigWaves + (threadIdx.x >> 6)) * each; b0 < a.t.seqs; b0 += waves * each) {
+    Change c{};
+    if (lane < each && b0 + lane < a.t.seqs) c = change_of(a, b0 + lane);
+    uint64_t shrink = __ballot(c.want < c.held);
+    while (shrink != 0) {
+      const int s = __builtin_ctzll(shrink);
+      shrink &= shrink - 1;
+      const int held = __shfl(c.held, s), want = __shfl(c.want, s);
+      int *row = a.t.table + (b0 + s) * a.t.stride;
+      for (int i = want + lane; i < held; i += 64) {
+        const int page = row[i];
+        if (is_page(page, a.pages)) atomicAdd(a.refs + page, -1);
+        row[i] = -1;
+      }
+    }
+  }
+}
+
+constexpr int64_t kReplaced = (int64_t)1 << 62;
+
+// Phase 1: free pages of each tile; what each sequence wants, and that of the
+// sequences before it in its tile.
+__device__ void resize_count(const ResizeArgs &a) {
+  const Tiles tiles = share(pages_tiles(a.pages));
+  for (int64_t t = tiles.begin; t < tiles.end; ++t) {
+    int64_t first;
+    int in, all;
+    const int used = used_bits(a.refs, a.pages, t, &first, &in);
+    block_sum_before((int)__popc(in & ~used), &all);
+    if (threadIdx.x == 0) a.w.counts[t] = all;
+  }
+  const Tiles seqs = share(seqs_tiles(a.t.seqs));
+  for (int64_t t = seqs.begin; t < seqs.end; ++t) {
+    const int64_t b = t * kSeqsTile + threadIdx.x;
+    int64_t need = 0, all;
+    bool replaced = false;
+    if (b < a.t.seqs) {
+      const Change c = change_of(a, b);
+      if (c.writes) {
+        const int last = a.t.table[b * a.t.stride + c.held - 1];
+        replaced = is_page(last, a.pages) && a.refs[last] > 1;
+      }
+      need = max(c.want - c.held, 0) + (replaced ? 1 : 0);
+    }
+    const int64_t before = block_sum_before(need, &all);
+    if (b < a.t.seqs) a.w.start[b] = before | (replaced ? kReplaced : 0);
+    if (threadIdx.x == 0) a.w.totals[t] = all;
+  }
+}
+
+// Phase 2: the lowest free pages in order, as many as are wanted.
+__device__ void resize_list(const ResizeArgs &a) {
+  const Tiles tiles = share(pages_tiles(a.pages));
+  if (tiles.begin >= tiles.end) return;
+  const int64_t wanted = block_total(a.w.totals, seqs_tiles(a.t.seqs));
+  int64_t rank = block_total(a.w.counts, tiles.begin);
+  for (int64_t t = tiles.begin; t < tiles.end && rank < wanted; ++t) {
+    int64_t first;
+    int in, all;
+    const int used = used_bits(a.refs, a.pages, t, &first, &in);
+    int free = in & ~used;
+    int64_t r = rank + block_sum_before((int)__popc(free), &all);
+    for (; free != 0; free &= free - 1, ++r)
+      if (r < wanted) a.w.list[r] = (int)(first + __builtin_ctz(free));
+    rank += all;
+  }
+}
+
+// Phase 3: a thread gives a sequence its first pages, its wave the rest.
+__device__ void resize_give(const ResizeArgs &a) {
+  constexpr int kOwn = 4;
+  const Tiles seqs = share(seqs_tiles(a.t.seqs));
+  if (seqs.begin >= seqs.end) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t free = block_total(a.w.counts, pages_tiles(a.pages));
+  int64_t base = block_total(a.w.totals, seqs.begin);
+  for (int64_t t = seqs.begin; t < seqs.end; ++t) {
+    const int64_t b = t * kSeqsTile + threadIdx.x;
+    const bool in = b < a.t.seqs;
+    Change c{};
+    int64_t start = 0;
+    bool replaced = false;
+    if (in) {
+      c = change_of(a, b);
+      start = a.w.start[b];
+      replaced = (start & kReplaced) != 0;
+      start = base + (start & ~kReplaced);
+    }
+    int first = c.held - (replaced ? 1 : 0);  // column of the first page given
+    const int need = max(c.want - c.held, 0) + (replaced ? 1 : 0);
+    const bool served = start + need <= free;
+    int given = served ? need : 0;
+    int *row = a.t.table + (in ? b : 0) * a.t.stride;
+    if (in) {
+      int old = -1, fresh = -1;
+      if (replaced && served) {
+        old = row[first];
+        fresh = a.w.list[start];
+        atomicAdd(a.refs + old, -1);
+      }
+      a.moves[2 * b] = old;
+      a.moves[2 * b + 1] = fresh;
+      a.missing[b] = !c.ok ? -1 : served ? 0 : need;
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (i < given) {
+        const int page = a.w.list[start + i];
+        row[first + i] = page;
+        a.refs[page] = 1;
+      }
+    uint64_t more = __ballot(given > kOwn);
+    while (more != 0) {
+      const int s = __builtin_ctzll(more);
+      more &= more - 1;
+      const int n = __shfl(given, s), column = __shfl(first, s);
+      const int64_t from = __shfl(start, s);
+      int *to = a.t.table + (b - lane + s) * a.t.stride;
+      for (int i = kOwn + lane; i < n; i += 64) {
+        const int page = a.w.list[from + i];
+        to[column + i] = page;
+        a.refs[page] = 1;
+      }
+    }
+    base += a.w.totals[t];
+  }
+}
+
+// Between phases of one workgroup: what it has written is there, and nothing
+// older is read from its cache.
+__device__ __forceinline__ void phase_end() {
+  __threadfence();
+  __syncthreads();
+  __threadfence();
+}
+
+template <int PHASE>  // -1: all of them
+__global__ __launch_bounds__(kBig) void resize_kernel(ResizeArgs a) {
+  if constexpr (PHASE < 0 || PHASE == 0) resize_release(a);
+  if constexpr (PHASE < 0) phase_end();
+  if constexpr (PHASE < 0 || PHASE == 1) resize_count(a);
+  if constexpr (PHASE < 0) phase_end();
+  if constexpr (PHASE < 0 || PHASE == 2) resize_list(a);
+  if constexpr (PHASE < 0) phase_end();
+  if constexpr (PHASE < 0 || PHASE == 3) resize_give(a);
+}
+
+// ---------------------------------------------------------------- compact
+
+// Phase 0: used pages of each tile.
+__device__ void compact_count(const CompactArgs &a) {
+  const Tiles tiles = share(pages_tiles(a.pages));
+  for (int64_t t = tiles.begin; t < tiles.end; ++t) {
+    int64_t first;
+    int in, all;
+    const int used = used_bits(a.refs, a.pages, t, &first, &in);
+    block_sum_before((int)__popc(used), &all);
+    if (threadIdx.x == 0) a.w.counts[t] = all;
+  }
+}
+
+// Phase 1: with U used pages, the r-th used page from U on goes to the r-th free
+// page below U.  Both sides of the moves, and every page's rank r among its kind.
+__device__ void compact_rank(const CompactArgs &a) {
+  const Tiles tiles = share(pages_tiles(a.pages));
+  const int64_t U = block_total(a.w.counts, pages_tiles(a.pages));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.used = (int)U;
+  int64_t before = block_total(a.w.counts, tiles.begin);  // used pages before the tile
+  // Used pages below U: those that the ranks from U on do not count.
+  __shared__ int in_tile;
+  int64_t below = 0;
+  {
+    const int64_t tu = U / kPagesTile;  // the tile that U lies in, or the one past the last
+    below = block_total(a.w.counts, tu);
+    if (tu < pages_tiles(a.pages)) {
+      int64_t first;
+      int in, all;
+      int used = used_bits(a.refs, a.pages, tu, &first, &in);
+      for (int k = 0; k < 4; ++k)
+        if (first + k >= U) used &= ~(1 << k);
+      block_sum_before((int)__popc(used), &all);
+      if (threadIdx.x == 0) in_tile = all;
+      __syncthreads();
+      below += in_tile;
+    }
+  }
+  for (int64_t t = tiles.begin; t < tiles.end; ++t) {
+    int64_t first;
+    int in, all;
+    const int used = used_bits(a.refs, a.pages, t, &first, &in);
+    int64_t u = before + block_sum_before((int)__popc(used), &all);  // used pages before this thread's
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!(in >> k & 1)) continue;
+      const int64_t p = first + k;
+      const bool is = used >> k & 1;
+      if (is && p >= U) {
+        const int64_t r = u - below;
+        a.moves[2 * r] = (int)p;
+        a.w.list[p] = (int)r;
+      } else if (!is && p < U) {
+        const int64_t r = p - u;
+        a.moves[2 * r + 1] = (int)p;
+        a.w.list[p] = (int)r;
+      }
+      u += is;
+    }
+    before += all;
+  }
+  // Places that no move takes.
+  const int64_t moved = U - below;
+  for (int64_t i = (int64_t)blockIdx.x * kBig + threadIdx.x; i < a.pages / 2; i += (int64_t)gridDim.x * kBig)
+    if (i >= moved) a.moves[2 * i] = a.moves[2 * i + 1] = -1;
+}
+
+// Phase 2: counts and tables in the new order.
+__device__ void compact_apply(const CompactArgs &a) {
+  const int64_t U = *a.used;
+  const int64_t threads = (int64_t)gridDim.x * kBig, me = (int64_t)blockIdx.x * kBig + threadIdx.x;
+  for (int64_t p = me; p < a.pages; p += threads) {
+    int r = 0;
+    if (p < U) {
+      r = a.refs[p];
+      if (r <= 0) r = a.refs[a.moves[2 * (int64_t)a.w.list[p]]];
+    }
+    a.refs_out[p] = r;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = me >> 6; b < a.to.seqs; b += threads >> 6) {
+    const int length = a.lengths[b];
+    const int held = fits(length, a.from) ? pages_of(length, a.page_shift) : 0;
+    for (int c = lane; c < a.to.max_pages; c += 64) {
+      int page = -1;
+      if (c < held) {
+        page = a.from.table[b * a.from.stride + c];
+        if (!is_page(page, a.pages) || a.refs[page] <= 0)
+          page = -1;
+        else if (page >= U)
+          page = a.moves[2 * (int64_t)a.w.list[page] + 1];
+      }
+      a.to.table[b * a.to.stride + c] = page;
+    }
+  }
+}
+
+template <int PHASE>  // -1: all of them
+__global__ __launch_bounds__(kBig) void compact_kernel(CompactArgs a) {
+  if constexpr (PHASE < 0 || PHASE == 0) compact_count(a);
+  if constexpr (PHASE < 0) phase_end();
+  if constexpr (PHASE < 0 || PHASE == 1) compact_rank(a);
+  if constexpr (PHASE < 0) phase_end();
+  if constexpr (PHASE < 0 || PHASE == 2) compact_apply(a);
+}
+
+// ---------------------------------------------------------------- copying
+
+struct __attribute__((packed, aligned(4))) Sixteen {
+  uint32_t x[4];
+};
+constexpr int kCopyPiece = 4096;  // bytes a wave takes at a time: four loads of 16 bytes in flight per lane
+
+// A wave per piece of a page's four arrays, taken as one after another.
+__global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a, int pieces) {
+  const int lane = threadIdx.x & 63;
+  const int64_t units = a.n * pieces, waves = (int64_t)gridDim.x * kWaves;
+  const int64_t whole = a.bytes[0] + a.bytes[1] + a.bytes[2] + a.bytes[3];
+  for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < units; u += waves) {
+    const int64_t i = u / pieces;
+    const int from = a.moves[2 * i], to = a.moves[2 * i + 1];
+    if ((uint32_t)from >= (uint64_t)a.pages || (uint32_t)to >= (uint64_t)a.pages || from == to) continue;
+    const int64_t begin = (u - i * pieces) * kCopyPiece;
+    Sixteen x[4];
+    char *at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int64_t o = begin + 16 * (64 * k + lane);
+      at[k] = nullptr;
+      if (o >= whole) continue;
+      int64_t bytes = a.bytes[0];
+      char *base = a.base[0];
+#pragma unroll
+      for (int s = 1; s < 4; ++s)
+        if (o >= bytes) {
+          o -= bytes;
+          bytes = a.bytes[s];
+          base = a.base[s];
+        } else {
+          break;
+        }
+      x[k] = *reinterpret_cast<const Sixteen *>(base + from * bytes + o);
+      at[k] = base + to * bytes + o;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k] != nullptr) *reinterpret_cast<Sixteen *>(at[k]) = x[k];
+  }
+}
+
+// Pools and tables up to these sizes take one workgroup and one launch.
+constexpr int64_t kOnePages = 32768, kOneEntries = 32768;
+
+}  // namespace
+
+hipError_t launch_pages_fork(const ForkArgs &a, hipStream_t stream) {
+  const int64_t wgs = std::min<int64_t>(((int64_t)a.to.seqs + kWaves - 1) / kWaves, 1 << 20);
+  hipLaunchKernelGGL(fork_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_resize(const ResizeArgs &a, int cus, hipStream_t stream) {
+  if (a.pages <= kOnePages && (int64_t)a.t.seqs * a.t.max_pages <= kOneEntries) {
+    hipLaunchKernelGGL((resize_kernel<-1>), dim3(1), dim3(kBig), 0, stream, a);
+    return hipGetLastError();
+  }
+  const unsigned by_waves = (unsigned)std::min<int64_t>(((int64_t)a.t.seqs + kBigWaves - 1) / kBigWaves, 2 * cus);
+  const unsigned tiles = (unsigned)std::min<int64_t>(std::max(pages_tiles(a.pages), seqs_tiles(a.t.seqs)), 2 * cus);
+  hipLaunchKernelGGL((resize_kernel<0>), dim3(by_waves), dim3(kBig), 0, stream, a);
+  hipLaunchKernelGGL((resize_kernel<1>), dim3(tiles), dim3(kBig), 0, stream, a);
+  hipLaunchKernelGGL((resize_kernel<2>), dim3(tiles), dim3(kBig), 0, stream, a);
+  hipLaunchKernelGGL((resize_kernel<3>), dim3((unsigned)std::min<int64_t>(seqs_tiles(a.t.seqs), 2 * cus)), dim3(kBig), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const CompactArgs &a, int cus, hipStream_t stream) {
+  if (a.pages <= kOnePages && (int64_t)a.to.seqs * a.to.max_pages <= kOneEntries) {
+    hipLaunchKernelGGL((compact_kernel<-1>), dim3(1), dim3(kBig), 0, stream, a);
+    return hipGetLastError();
+  }
+  const unsigned tiles = (unsigned)std::max<int64_t>(std::min<int64_t>(pages_tiles(a.pages), 2 * cus), 1);
+  hipLaunchKernelGGL((compact_kernel<0>), dim3(tiles), dim3(kBig), 0, stream, a);
+  hipLaunchKernelGGL((compact_kernel<1>), dim3(tiles), dim3(kBig), 0, stream, a);
+  hipLaunchKernelGGL((compact_kernel<2>), dim3((unsigned)(2 * cus)), dim3(kBig), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_copy(const CopyArgs &a, int cus, hipStream_t stream) {
+  const int64_t whole = a.bytes[0] + a.bytes[1] + a.bytes[2] + a.bytes[3];
+  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece);
+  const int64_t wgs = std::min<int64_t>((a.n * pieces + kWaves - 1) / kWaves, (int64_t)cus * 16);
+  hipLaunchKernelGGL(copy_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream, a, pieces);
+  return hipGetLastError();
+}
+
+}  // namespace q8

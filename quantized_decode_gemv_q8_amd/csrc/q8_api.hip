@@ -1,5 +1,6 @@
 // C ABI of the Q8_0 matvec / i8 dot_t library: validation, launch planning,
 // the split-K workspace, and dispatch.  Declared in include/q8_gemv.h.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -11,9 +12,12 @@
 #include <utility>
 #include <vector>
 
+#include "mx4_cache.h"
+#include "pages.h"
 #include "q8_attention.h"
 #include "q8_common.h"
 #include "q8_gemv.h"
+#include "rope.h"
 
 namespace {
 
@@ -762,14 +766,27 @@ q8_status cache_args(const q8_cache *c, const q8_cache_seqs *s, int64_t rows, q8
   return Q8_OK;
 }
 
+// The same for the cache in 4-bit floats, whose arrays have alignments of their own.
+q8_status cache_args(const q8_mx4_cache *c, const q8_cache_seqs *s, int64_t rows, q8::Cache *cache, q8::Seqs *seqs) {
+  if (c == nullptr) return Q8_ERR_INVALID;
+  const q8::Cache arrays = q8::mx4_cache(c->K, c->KS, c->V, c->VS);
+  const q8_cache as{arrays.K, arrays.KS, arrays.V, arrays.VS, c->pages, c->heads, c->page_size, c->dim};
+  const q8_status st = cache_args(&as, s, rows, cache, seqs);
+  if (st != Q8_OK) return st;
+  if (rows > 0 && s->seqs > 0 && (address_alignment(c->KS) < 16 || address_alignment(c->VS) < 16)) return Q8_ERR_INVALID;
+  return Q8_OK;
+}
+
 bool row_type(q8_type type, int64_t *bytes) {
   if (type != Q8_F32 && type != Q8_BF16 && type != Q8_F16) return false;
   *bytes = type == Q8_F32 ? 4 : 2;
   return true;
 }
 
-q8_status cache_rows_impl(const q8_cache *c, const void *k, const void *v, q8_type type, int64_t rows,
-                          int64_t k_stride, int64_t v_stride, const q8_cache_seqs *s, bool write, void *stream_v) {
+typedef hipError_t (*RowsLaunch)(const q8::CacheRowsArgs &, q8::RowType, hipStream_t);
+template <typename C>
+q8_status cache_rows_impl(const C *c, const void *k, const void *v, q8_type type, int64_t rows, int64_t k_stride,
+                          int64_t v_stride, const q8_cache_seqs *s, RowsLaunch launch, const char *name, void *stream_v) {
   q8::CacheRowsArgs a;
   int64_t bytes = 0;
   q8_status st = cache_args(c, s, rows, &a.c, &a.s);
@@ -788,10 +805,22 @@ q8_status cache_rows_impl(const q8_cache *c, const void *k, const void *v, q8_ty
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   if (log_debug())
-    log_line("cache_%s rows=%lld heads=%d dim=%d seqs=%lld", write ? "write" : "read", (long long)rows, c->heads, c->dim,
-             (long long)s->seqs);
-  return hip_status((write ? q8::launch_cache_write : q8::launch_cache_read)(a, (q8::RowType)type, (hipStream_t)stream_v));
+    log_line("%s rows=%lld heads=%d dim=%d seqs=%lld", name, (long long)rows, c->heads, c->dim, (long long)s->seqs);
+  return hip_status(launch(a, (q8::RowType)type, (hipStream_t)stream_v));
 }
+
+// What the attentions over the two caches differ in.
+struct AttnFormat {
+  const char *name;
+  bool few;        // has kernels for items of 4 and 8 rows
+  bool any_alpha;  // takes a scale of the scores that is not finite
+  int (*max_rows)(q8::RowType type, int dim);
+  hipError_t (*launch[3])(const q8::AttnArgs &, int, int, hipStream_t);  // by the rows' type
+};
+const AttnFormat kQ8Attention = {"cache_attention", true, true, q8::attn_max_rows,
+                                 {q8::launch_attention_f32, q8::launch_attention_bf16, q8::launch_attention_f16}};
+const AttnFormat kMx4Attention = {"mx4_attention", false, false, q8::mx4_max_rows,
+                                  {q8::launch_mx4_attention_f32, q8::launch_mx4_attention_bf16, q8::launch_mx4_attention_f16}};
 
 // How the rows of an attention call are cut: items of up to `tile` rows
 // (tokens x heads of a group), and the workgroups the units are dealt to.
@@ -823,7 +852,7 @@ constexpr int64_t kAttnWholeTokens = 1024;
 // unit takes so long that 0 is best.
 constexpr int kAttnItemCost = 2;
 
-AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
+AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
   AttnPlan p = {};
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
   // The smallest items that hold an average sequence's rows of a head; past 32,
@@ -843,12 +872,12 @@ AttnPlan attn_plan(q8::RowType type, int heads, int group, int dim, int64_t rows
   // drawn better: 17 to 32 rows of dim 256 take 81 us of bf16 and 96 of f32 in
   // 16-row items, 87 and 107 in the 64-row ones that the rule gives them.
   // The instances for 4 and 8 rows do not fit the registers at dim 256.
-  p.tile = mean <= 4 && dim <= 128                 ? 4
-           : mean <= 8 && dim <= 128               ? 8
+  p.tile = mean <= 4 && dim <= 128 && format.few   ? 4
+           : mean <= 8 && dim <= 128 && format.few ? 8
            : mean <= 16                            ? 16
            : mean <= q8::attn_direct_rows(dim)     ? 32
            : mean <= 64                            ? 64
-                                                   : q8::attn_max_rows(type, dim);
+                                                   : format.max_rows(type, dim);
   const int tile = p.tile;
   p.subs = (int)ceil_div(group, tile);
   p.sub_heads = (int)ceil_div(group, p.subs);
@@ -872,6 +901,173 @@ void deal(AttnPlan *p, int dim, int cus) {
   if (p->split)
     p->bytes =
         ceil_div(2 * p->wgs * q8::attn_slot_floats(p->tile, dim) * 4, 256) * 256 + p->wgs * (int64_t)sizeof(q8::AttnItem);
+}
+
+template <typename C>
+q8_status cache_keep_impl(const C *cache, int64_t rows, const q8_cache_seqs *seqs, const int32_t *keep, int64_t width,
+                          hipError_t (*launch)(const q8::CacheKeepArgs &, hipStream_t), const char *name, void *stream) {
+  q8::CacheKeepArgs a;
+  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
+  if (st != Q8_OK) return st;
+  if (width < 0) return Q8_ERR_INVALID;
+  if (width >= kIndexLimit / 2) return Q8_ERR_TOO_LARGE;
+  if (rows == 0 || seqs->seqs == 0 || width == 0) return Q8_OK;
+  if (keep == nullptr || address_alignment(keep) < 4) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.keep = keep;
+  a.width = (int)width;
+  if (log_debug()) log_line("%s seqs=%lld width=%lld", name, (long long)seqs->seqs, (long long)width);
+  return hip_status(launch(a, (hipStream_t)stream));
+}
+
+template <typename C>
+q8_status attention_workspace_impl(const AttnFormat &format, const C *cache, q8_type type, int64_t rows, int32_t q_heads,
+                                   const q8_cache_seqs *seqs, int64_t *bytes) {
+  q8::Cache c;
+  q8::Seqs s;
+  int64_t elem = 0;
+  if (bytes == nullptr || !row_type(type, &elem)) return Q8_ERR_INVALID;
+  q8_status st = cache_args(cache, seqs, rows, &c, &s);
+  if (st != Q8_OK) return st;
+  if (q_heads < 1 || q_heads % cache->heads != 0) return Q8_ERR_INVALID;
+  if (q_heads > kAttnMostHeads) return Q8_ERR_TOO_LARGE;
+  *bytes = 0;
+  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
+  AttnPlan pl = attn_plan(format, (q8::RowType)type, c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens);
+  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  deal(&pl, c.dim, info.cus);
+  *bytes = pl.bytes;
+  return Q8_OK;
+}
+
+template <typename C>
+q8_status attention_impl(const AttnFormat &format, const C *cache, const void *q, void *out, q8_type type, int64_t rows,
+                         int32_t q_heads, int64_t q_stride, int64_t out_stride, const q8_cache_seqs *seqs,
+                         const uint64_t *tree, int64_t tree_words, float alpha, void *workspace,
+                         int64_t workspace_bytes, void *stream_v) {
+  q8::AttnArgs a;
+  int64_t bytes = 0;
+  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
+  if (st != Q8_OK) return st;
+  if (!format.any_alpha && !isfinite(alpha)) return Q8_ERR_INVALID;
+  if (!row_type(type, &bytes) || q_heads < 1 || q_heads % cache->heads != 0 || tree_words < 0) return Q8_ERR_INVALID;
+  if (q_heads > kAttnMostHeads || tree_words >= kIndexLimit / 64) return Q8_ERR_TOO_LARGE;
+  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
+  const int64_t width = (int64_t)q_heads * cache->dim;
+  if (q == nullptr || out == nullptr || address_alignment(q) < bytes || address_alignment(out) < bytes) return Q8_ERR_INVALID;
+  if (rows > 1 && (q_stride < width || out_stride < width)) return Q8_ERR_INVALID;
+  if (address_alignment(tree) < 8) return Q8_ERR_INVALID;
+  AttnPlan pl = attn_plan(format, (q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens);
+  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  deal(&pl, a.c.dim, info.cus);
+  if (pl.split && (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes))
+    return Q8_ERR_INVALID;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.tree = tree;
+  a.tree_words = (int)tree_words;
+  a.group = q_heads / a.c.heads;
+  a.subs = pl.subs;
+  a.sub_heads = pl.sub_heads;
+  a.tile_tokens = pl.tile_tokens;
+  a.alpha = alpha;
+  a.partial = static_cast<float *>(workspace);
+  const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
+  a.items = pl.split ? reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256) : nullptr;
+  a.unit_shift = pl.unit_shift;
+  a.half_rows = pl.tile == 128 ? 64 : 0;  // rows of one of the two row tiles a wave has
+  a.item_cost = pl.item_cost;
+  a.few_units = pl.most_units < (double)kIndexLimit;
+  if (log_debug())
+    log_line("%s rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", format.name, (long long)rows,
+             q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", pl.tile,
+             (long long)pl.wgs);
+  hipStream_t stream = (hipStream_t)stream_v;
+  return hip_status(format.launch[type](a, pl.tile, (int)pl.wgs, stream));
+}
+
+// ---------------------------------------------------------------- pages
+
+constexpr int kRopeMostHeads = 1 << 20;
+
+bool bad_words(const int32_t *p) { return p == nullptr || address_alignment(p) < 4; }
+
+q8_status pool_args(const q8_pool *p, int *pages, int *shift) {
+  if (p == nullptr || p->pages < 0) return Q8_ERR_INVALID;
+  if (p->page_size < 16 || p->page_size > 1024 || (p->page_size & (p->page_size - 1)) != 0) return Q8_ERR_INVALID;
+  if (p->pages >= kIndexLimit) return Q8_ERR_TOO_LARGE;
+  if (p->pages > 0 && bad_words(p->refs)) return Q8_ERR_INVALID;
+  *pages = (int)p->pages;
+  *shift = __builtin_ctz((unsigned)p->page_size);
+  return Q8_OK;
+}
+
+q8_status table_args(const q8_page_table *t, const q8_pool *p, q8::PageTable *out) {
+  if (t == nullptr || t->seqs < 0 || t->max_pages < 0) return Q8_ERR_INVALID;
+  if (t->seqs > 1 && t->table_stride < t->max_pages) return Q8_ERR_INVALID;
+  if (t->seqs >= kIndexLimit / 2 || t->max_pages >= kIndexLimit / 2 / p->page_size) return Q8_ERR_TOO_LARGE;
+  if (t->seqs > 0 && t->max_pages > 0 && bad_words(t->table)) return Q8_ERR_INVALID;
+  out->table = t->table;
+  out->stride = t->table_stride;
+  out->seqs = (int)t->seqs;
+  out->max_pages = (int)t->max_pages;
+  out->max_tokens = t->max_pages * p->page_size;
+  return Q8_OK;
+}
+
+bool pages_work(void *workspace, int64_t bytes, int64_t pages, int64_t seqs, q8::PagesWork *w) {
+  const int64_t need = q8::pages_work_bytes(pages, seqs);
+  if (bytes < need || (need > 0 && (workspace == nullptr || address_alignment(workspace) < 16))) return false;
+  w->totals = static_cast<int64_t *>(workspace);
+  w->start = w->totals + q8::seqs_tiles(seqs);
+  w->counts = reinterpret_cast<int *>(w->start + seqs);
+  w->list = w->counts + q8::pages_tiles(pages);
+  return true;
+}
+
+// code_bytes, scale_bytes: of a token's row of one head.
+template <typename C>
+q8_status copy_impl(const C *cache, int64_t code_bytes, int64_t scale_bytes, const int32_t *moves, int64_t n, void *stream) {
+  const q8_cache_seqs none{};
+  q8::Cache c;
+  q8::Seqs s;
+  q8_status st = cache_args(cache, &none, 0, &c, &s);
+  if (st != Q8_OK) return st;
+  if (n < 0) return Q8_ERR_INVALID;
+  if (n >= kIndexLimit) return Q8_ERR_TOO_LARGE;
+  if (n == 0 || cache->pages == 0) return Q8_OK;
+  if (bad_words(moves)) return Q8_ERR_INVALID;
+  const int64_t rows = (int64_t)cache->heads * cache->page_size;
+  q8::CopyArgs a;
+  const void *base[4] = {cache->K, cache->KS, cache->V, cache->VS};
+  for (int i = 0; i < 4; ++i) {
+    const bool codes = i % 2 == 0 || code_bytes != cache->dim;  // the Q8_0 cache's scales need 4 bytes only
+    if (base[i] == nullptr || address_alignment(base[i]) < (codes ? 16 : 4)) return Q8_ERR_INVALID;
+    a.base[i] = static_cast<char *>(const_cast<void *>(base[i]));
+    a.bytes[i] = rows * (i % 2 == 0 ? code_bytes : scale_bytes);
+  }
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.moves = moves;
+  a.n = n;
+  a.pages = cache->pages;
+  if (log_debug()) log_line("copy of up to %lld pages of %lld bytes", (long long)n, (long long)(2 * (a.bytes[0] + a.bytes[1])));
+  return hip_status(q8::launch_pages_copy(a, info.cus, (hipStream_t)stream));
 }
 
 }  // namespace
@@ -967,109 +1163,247 @@ q8_status q8_dot_t_f32(const float *A, const float *B, float *C, int64_t M, int6
 
 q8_status q8_cache_write(const q8_cache *cache, const void *k, const void *v, q8_type type, int64_t rows,
                          int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
-  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, true, stream);
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, q8::launch_cache_write, "cache_write", stream);
 }
 
 q8_status q8_cache_read(const q8_cache *cache, void *k, void *v, q8_type type, int64_t rows, int64_t k_stride,
                         int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
-  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, false, stream);
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, q8::launch_cache_read, "cache_read", stream);
 }
 
 q8_status q8_cache_keep(const q8_cache *cache, int64_t rows, const q8_cache_seqs *seqs, const int32_t *keep,
                         int64_t width, void *stream) {
-  q8::CacheKeepArgs a;
-  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
-  if (st != Q8_OK) return st;
-  if (width < 0) return Q8_ERR_INVALID;
-  if (width >= kIndexLimit / 2) return Q8_ERR_TOO_LARGE;
-  if (rows == 0 || seqs->seqs == 0 || width == 0) return Q8_OK;
-  if (keep == nullptr || address_alignment(keep) < 4) return Q8_ERR_INVALID;
-  int dev = 0;
-  DevInfo info;
-  st = current_device(&dev, &info);
-  if (st != Q8_OK) return st;
-  a.keep = keep;
-  a.width = (int)width;
-  if (log_debug()) log_line("cache_keep seqs=%lld width=%lld", (long long)seqs->seqs, (long long)width);
-  return hip_status(q8::launch_cache_keep(a, (hipStream_t)stream));
+  return cache_keep_impl(cache, rows, seqs, keep, width, q8::launch_cache_keep, "cache_keep", stream);
 }
 
 q8_status q8_cache_attention_workspace(const q8_cache *cache, q8_type type, int64_t rows, int32_t q_heads,
                                        const q8_cache_seqs *seqs, int64_t *bytes) {
-  q8::Cache c;
-  q8::Seqs s;
-  int64_t elem = 0;
-  if (bytes == nullptr || !row_type(type, &elem)) return Q8_ERR_INVALID;
-  q8_status st = cache_args(cache, seqs, rows, &c, &s);
-  if (st != Q8_OK) return st;
-  if (q_heads < 1 || q_heads % cache->heads != 0) return Q8_ERR_INVALID;
-  if (q_heads > kAttnMostHeads) return Q8_ERR_TOO_LARGE;
-  *bytes = 0;
-  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
-  AttnPlan pl = attn_plan((q8::RowType)type, c.heads, q_heads / c.heads, c.dim, rows, s.seqs, s.max_tokens);
-  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
-  int dev = 0;
-  DevInfo info;
-  st = current_device(&dev, &info);
-  if (st != Q8_OK) return st;
-  deal(&pl, c.dim, info.cus);
-  *bytes = pl.bytes;
-  return Q8_OK;
+  return attention_workspace_impl(kQ8Attention, cache, type, rows, q_heads, seqs, bytes);
 }
 
 q8_status q8_cache_attention(const q8_cache *cache, const void *q, void *out, q8_type type, int64_t rows,
                              int32_t q_heads, int64_t q_stride, int64_t out_stride, const q8_cache_seqs *seqs,
                              const uint64_t *tree, int64_t tree_words, float alpha, void *workspace,
-                             int64_t workspace_bytes, void *stream_v) {
-  q8::AttnArgs a;
-  int64_t bytes = 0;
-  q8_status st = cache_args(cache, seqs, rows, &a.c, &a.s);
+                             int64_t workspace_bytes, void *stream) {
+  return attention_impl(kQ8Attention, cache, q, out, type, rows, q_heads, q_stride, out_stride, seqs, tree, tree_words,
+                        alpha, workspace, workspace_bytes, stream);
+}
+
+q8_status q8_mx4_write(const q8_mx4_cache *cache, const void *k, const void *v, q8_type type, int64_t rows,
+                       int64_t k_stride, int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, q8::launch_mx4_write, "mx4_write", stream);
+}
+
+q8_status q8_mx4_read(const q8_mx4_cache *cache, void *k, void *v, q8_type type, int64_t rows, int64_t k_stride,
+                      int64_t v_stride, const q8_cache_seqs *seqs, void *stream) {
+  return cache_rows_impl(cache, k, v, type, rows, k_stride, v_stride, seqs, q8::launch_mx4_read, "mx4_read", stream);
+}
+
+q8_status q8_mx4_keep(const q8_mx4_cache *cache, int64_t rows, const q8_cache_seqs *seqs, const int32_t *keep,
+                      int64_t width, void *stream) {
+  return cache_keep_impl(cache, rows, seqs, keep, width, q8::launch_mx4_keep, "mx4_keep", stream);
+}
+
+q8_status q8_mx4_attention_workspace(const q8_mx4_cache *cache, q8_type type, int64_t rows, int32_t q_heads,
+                                     const q8_cache_seqs *seqs, int64_t *bytes) {
+  return attention_workspace_impl(kMx4Attention, cache, type, rows, q_heads, seqs, bytes);
+}
+
+q8_status q8_mx4_attention(const q8_mx4_cache *cache, const void *q, void *out, q8_type type, int64_t rows,
+                           int32_t q_heads, int64_t q_stride, int64_t out_stride, const q8_cache_seqs *seqs,
+                           const uint64_t *tree, int64_t tree_words, float alpha, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+  return attention_impl(kMx4Attention, cache, q, out, type, rows, q_heads, q_stride, out_stride, seqs, tree, tree_words,
+                        alpha, workspace, workspace_bytes, stream);
+}
+
+q8_status q8_pages_workspace(int64_t pages, int64_t seqs, int64_t *bytes) {
+  if (bytes == nullptr || pages < 0 || seqs < 0) return Q8_ERR_INVALID;
+  if (pages >= kIndexLimit || seqs >= kIndexLimit / 2) return Q8_ERR_TOO_LARGE;
+  *bytes = q8::pages_work_bytes(pages, seqs);
+  return Q8_OK;
+}
+
+q8_status q8_pages_fork(const q8_pool *pool, const q8_page_table *from, const int32_t *lengths, const int32_t *parent,
+                        const q8_page_table *to, int32_t *lengths_out, void *stream) {
+  q8::ForkArgs a;
+  q8_status st = pool_args(pool, &a.pages, &a.page_shift);
+  if (st == Q8_OK) st = table_args(from, pool, &a.from);
+  if (st == Q8_OK) st = table_args(to, pool, &a.to);
   if (st != Q8_OK) return st;
-  if (!row_type(type, &bytes) || q_heads < 1 || q_heads % cache->heads != 0 || tree_words < 0) return Q8_ERR_INVALID;
-  if (q_heads > kAttnMostHeads || tree_words >= kIndexLimit / 64) return Q8_ERR_TOO_LARGE;
-  if (rows == 0 || seqs->seqs == 0) return Q8_OK;
-  const int64_t width = (int64_t)q_heads * cache->dim;
-  if (q == nullptr || out == nullptr || address_alignment(q) < bytes || address_alignment(out) < bytes) return Q8_ERR_INVALID;
-  if (rows > 1 && (q_stride < width || out_stride < width)) return Q8_ERR_INVALID;
-  if (address_alignment(tree) < 8) return Q8_ERR_INVALID;
-  AttnPlan pl = attn_plan((q8::RowType)type, a.c.heads, q_heads / a.c.heads, a.c.dim, rows, a.s.seqs, a.s.max_tokens);
-  if (pl.most_units >= kAttnMostUnits) return Q8_ERR_TOO_LARGE;
+  if (to->seqs == 0) return Q8_OK;
+  if ((from->seqs > 0 && bad_words(lengths)) || bad_words(parent) || bad_words(lengths_out)) return Q8_ERR_INVALID;
   int dev = 0;
   DevInfo info;
   st = current_device(&dev, &info);
   if (st != Q8_OK) return st;
-  deal(&pl, a.c.dim, info.cus);
-  if (pl.split && (workspace == nullptr || address_alignment(workspace) < 16 || workspace_bytes < pl.bytes))
+  a.lengths = lengths;
+  a.parent = parent;
+  a.lengths_out = lengths_out;
+  a.refs = pool->refs;
+  if (log_debug()) log_line("pages_fork pages=%lld seqs=%lld to %lld", (long long)pool->pages, (long long)from->seqs, (long long)to->seqs);
+  return hip_status(q8::launch_pages_fork(a, (hipStream_t)stream));
+}
+
+q8_status q8_pages_resize(const q8_pool *pool, const q8_page_table *table, const int32_t *before, const int32_t *after,
+                          int32_t *moves, int32_t *missing, void *workspace, int64_t workspace_bytes, void *stream) {
+  q8::ResizeArgs a;
+  q8_status st = pool_args(pool, &a.pages, &a.page_shift);
+  if (st == Q8_OK) st = table_args(table, pool, &a.t);
+  if (st != Q8_OK) return st;
+  if (table->seqs == 0) return Q8_OK;
+  if (bad_words(before) || bad_words(after) || bad_words(moves) || bad_words(missing)) return Q8_ERR_INVALID;
+  if (!pages_work(workspace, workspace_bytes, pool->pages, table->seqs, &a.w)) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.before = before;
+  a.after = after;
+  a.refs = pool->refs;
+  a.moves = moves;
+  a.missing = missing;
+  if (log_debug()) log_line("pages_resize pages=%lld seqs=%lld", (long long)pool->pages, (long long)table->seqs);
+  return hip_status(q8::launch_pages_resize(a, info.cus, (hipStream_t)stream));
+}
+
+q8_status q8_pages_compact(const q8_pool *pool, const q8_page_table *from, const int32_t *lengths, int32_t *refs_out,
+                           const q8_page_table *to, int32_t *moves, int32_t *used, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+  q8::CompactArgs a;
+  q8_status st = pool_args(pool, &a.pages, &a.page_shift);
+  if (st == Q8_OK) st = table_args(from, pool, &a.from);
+  if (st == Q8_OK) st = table_args(to, pool, &a.to);
+  if (st != Q8_OK) return st;
+  if (to->seqs != from->seqs || to->max_pages != from->max_pages) return Q8_ERR_INVALID;
+  if ((from->seqs > 0 && bad_words(lengths)) || (pool->pages > 0 && bad_words(refs_out)) ||
+      (pool->pages > 1 && bad_words(moves)) || bad_words(used))
     return Q8_ERR_INVALID;
-  a.q = q;
-  a.out = out;
-  a.q_stride = q_stride;
-  a.out_stride = out_stride;
-  a.tree = tree;
-  a.tree_words = (int)tree_words;
-  a.group = q_heads / a.c.heads;
-  a.subs = pl.subs;
-  a.sub_heads = pl.sub_heads;
-  a.tile_tokens = pl.tile_tokens;
-  a.alpha = alpha;
-  a.partial = static_cast<float *>(workspace);
-  const int64_t partial = 2 * pl.wgs * q8::attn_slot_floats(pl.tile, a.c.dim) * 4;
-  a.items = pl.split ? reinterpret_cast<q8::AttnItem *>(static_cast<char *>(workspace) + ceil_div(partial, 256) * 256) : nullptr;
-  a.unit_shift = pl.unit_shift;
-  a.half_rows = pl.tile == 128 ? 64 : 0;  // rows of one of the two row tiles a wave has
-  a.item_cost = pl.item_cost;
-  a.few_units = pl.most_units < (double)kIndexLimit;
-  if (log_debug())
-    log_line("cache_attention rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", (long long)rows,
-             q_heads, a.c.heads, a.c.dim, (long long)seqs->seqs, tree ? " tree" : "", pl.tile,
-             (long long)pl.wgs);
-  hipStream_t stream = (hipStream_t)stream_v;
-  switch (type) {
-    case Q8_F32: return hip_status(q8::launch_attention_f32(a, pl.tile, (int)pl.wgs, stream));
-    case Q8_BF16: return hip_status(q8::launch_attention_bf16(a, pl.tile, (int)pl.wgs, stream));
-    case Q8_F16: return hip_status(q8::launch_attention_f16(a, pl.tile, (int)pl.wgs, stream));
+  if (!pages_work(workspace, workspace_bytes, pool->pages, from->seqs, &a.w)) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.lengths = lengths;
+  a.refs = pool->refs;
+  a.refs_out = refs_out;
+  a.moves = moves;
+  a.used = used;
+  if (log_debug()) log_line("pages_compact pages=%lld seqs=%lld", (long long)pool->pages, (long long)from->seqs);
+  return hip_status(q8::launch_pages_compact(a, info.cus, (hipStream_t)stream));
+}
+
+q8_status q8_cache_copy(const q8_cache *cache, const int32_t *moves, int64_t n, void *stream) {
+  return copy_impl(cache, (int64_t)(cache ? cache->dim : 0), (int64_t)(cache ? cache->dim / 32 * 4 : 0), moves, n, stream);
+}
+
+q8_status q8_mx4_copy(const q8_mx4_cache *cache, const int32_t *moves, int64_t n, void *stream) {
+  return copy_impl(cache, (int64_t)(cache ? cache->dim / 2 : 0), (int64_t)(cache ? cache->dim / 32 : 0), moves, n, stream);
+}
+
+q8_status q8_rope(const q8_rope_angles *angles, const q8_rope_rows *tensors, int32_t n_tensors, q8_type type,
+                  int64_t rows, int32_t dim, const int32_t *positions, const q8_cache_seqs *seqs, int32_t inverse,
+                  void *stream) {
+  int64_t bytes = 0;
+  if (angles == nullptr || tensors == nullptr || n_tensors < 1 || n_tensors > Q8_MAX_ROPE_TENSORS) return Q8_ERR_INVALID;
+  if (!row_type(type, &bytes) || rows < 0 || dim < 2 || angles->rot < 2 || angles->rot > dim || angles->rot % 2 != 0)
+    return Q8_ERR_INVALID;
+  if ((positions == nullptr) == (seqs == nullptr) && rows > 0) return Q8_ERR_INVALID;
+  if (seqs != nullptr && seqs->seqs < 0) return Q8_ERR_INVALID;
+  if (dim > 4096 || rows >= kIndexLimit || (seqs != nullptr && seqs->seqs >= kIndexLimit / 2)) return Q8_ERR_TOO_LARGE;
+  q8::RopeArgs a = {};
+  a.copy = 0;
+  int64_t heads = 0;
+  for (int i = 0; i < q8::kRopeTensors; ++i) {
+    const q8_rope_rows none{};
+    const q8_rope_rows &t = i < n_tensors ? tensors[i] : none;
+    if (i < n_tensors) {
+      if (t.heads < 0) return Q8_ERR_INVALID;
+      if (t.heads > kRopeMostHeads) return Q8_ERR_TOO_LARGE;
+      const int64_t width = (int64_t)t.heads * dim;
+      if (rows > 0 && t.heads > 0) {
+        if (t.x == nullptr || t.out == nullptr || address_alignment(t.x) < bytes || address_alignment(t.out) < bytes)
+          return Q8_ERR_INVALID;
+        if (rows > 1 && (t.x_stride < width || t.out_stride < width)) return Q8_ERR_INVALID;
+        if (t.x == t.out && rows > 1 && t.x_stride != t.out_stride) return Q8_ERR_INVALID;
+        if (t.x != t.out && angles->rot < dim) a.copy = 1;
+      }
+    }
+    heads += t.heads;
+    a.x[i] = t.x;
+    a.out[i] = t.out;
+    a.x_stride[i] = t.x_stride;
+    a.out_stride[i] = t.out_stride;
+    a.upto[i] = (int)heads;
   }
-  return Q8_ERR_INVALID;
+  if (rows == 0 || heads == 0 || (seqs != nullptr && seqs->seqs == 0)) return Q8_OK;
+  if (angles->turns == nullptr || address_alignment(angles->turns) < 8) return Q8_ERR_INVALID;
+  if (positions != nullptr ? bad_words(positions) : bad_words(seqs->lengths) || bad_words(seqs->offsets)) return Q8_ERR_INVALID;
+  int dev = 0;
+  DevInfo info;
+  const q8_status st = current_device(&dev, &info);
+  if (st != Q8_OK) return st;
+  a.heads = (int)heads;
+  a.turns = angles->turns;
+  a.positions = positions;
+  if (seqs != nullptr) {
+    a.s.lengths = seqs->lengths;
+    a.s.offsets = seqs->offsets;
+    a.s.seqs = (int)seqs->seqs;
+  }
+  a.s.rows = (int)rows;
+  a.dim = dim;
+  a.rot = angles->rot;
+  a.amplitude = angles->amplitude;
+  a.inverse = inverse != 0;
+  if (log_debug())
+    log_line("rope rows=%lld heads=%lld dim=%d rot=%d%s%s", (long long)rows, (long long)heads, dim, a.rot,
+             angles->interleaved ? " interleaved" : "", a.inverse ? " inverse" : "");
+  return hip_status(q8::launch_rope(a, (q8::RowType)type, angles->interleaved != 0, (hipStream_t)stream));
+}
+
+q8_status q8_rope_turns(const double *frequencies, int64_t n, uint64_t *turns) {
+  if (n < 0 || (n > 0 && (frequencies == nullptr || turns == nullptr))) return Q8_ERR_INVALID;
+  for (int64_t i = 0; i < n; ++i)
+    if (!isfinite(frequencies[i])) return Q8_ERR_INVALID;
+  for (int64_t i = 0; i < n; ++i) {
+    // 64 bits of the quotient; what rounds up to a whole turn is none
+    long double t = (long double)frequencies[i] / 6.283185307179586476925286766559L;
+    t -= floorl(t);
+    t = roundl(ldexpl(t, 64));
+    turns[i] = t >= ldexpl(1.0L, 64) ? 0 : (uint64_t)t;
+  }
+  return Q8_OK;
+}
+
+q8_status q8_rope_frequencies(int32_t rot, double base, q8_rope_scaling scaling, double factor, double length,
+                              double low, double high, double *frequencies) {
+  if (rot < 2 || rot % 2 != 0 || frequencies == nullptr || !(base > 1.0) || !isfinite(base)) return Q8_ERR_INVALID;
+  if (scaling < Q8_ROPE_PLAIN || scaling > Q8_ROPE_INDEX) return Q8_ERR_INVALID;
+  if (scaling != Q8_ROPE_PLAIN && !(factor > 0.0 && isfinite(factor))) return Q8_ERR_INVALID;
+  if (scaling == Q8_ROPE_BASE && rot < 4) return Q8_ERR_INVALID;
+  const bool blend = scaling == Q8_ROPE_TURNS || scaling == Q8_ROPE_INDEX;
+  if (blend && !(length > 0.0 && isfinite(length) && low > 0.0 && high > low && isfinite(high))) return Q8_ERR_INVALID;
+  constexpr double two_pi = 6.283185307179586476925286766559;
+  if (scaling == Q8_ROPE_BASE) base *= pow(factor, (double)rot / (rot - 2));
+  auto index = [&](double turns) { return rot * log(length / (two_pi * turns)) / (2.0 * log(base)); };
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot);
+    double w = 1.0;
+    if (scaling == Q8_ROPE_LINEAR) {
+      frequencies[i] = f / factor;
+      continue;
+    }
+    if (scaling == Q8_ROPE_TURNS) {
+      w = (length * f / two_pi - low) / (high - low);
+    } else if (scaling == Q8_ROPE_INDEX) {
+      const double first = std::max(floor(index(high)), 0.0), last = std::min(ceil(index(low)), rot - 1.0);
+      w = 1.0 - (i - first) / std::max(last - first, 1e-3);
+    }
+    w = std::min(std::max(w, 0.0), 1.0);
+    frequencies[i] = blend ? f * w + f / factor * (1.0 - w) : f;
+  }
+  return Q8_OK;
 }
 
 const char *q8_status_string(q8_status s) {
