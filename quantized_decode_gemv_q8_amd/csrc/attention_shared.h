@@ -114,13 +114,19 @@ __device__ __forceinline__ void static_for(F f) {
   }
 }
 
+// The same of the lanes 16 and 32 apart, by swaps of rows and halves of the wave:
+// no trip through LDS, whose latency the running softmax would wait for.
 __device__ __forceinline__ float across_groups_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float across_groups_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Channels 32 b + 8 c + 0..7 of every block of one row of q, as they come.
@@ -341,9 +347,10 @@ __device__ __forceinline__ float row_sum(float x) {
   return across_groups_sum(x);
 }
 
-// Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
+// Raises the rows' kept maxima where a score, up to the row's factor undo[rt], passes
+// one by kMaxSlack, and scales the rows' sums down to the new ones.
 template <int NRT, int NK, int NB, int PACK>
-__device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
+__device__ __forceinline__ void settle(const float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   float top[NRT];
   bool above = false;
 #pragma unroll
@@ -367,10 +374,19 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
         for (int i = 0; i < 2; ++i) acc[rt][b][i] *= f;
     }
   }
+}
+
+// What a row's scores are taken against: its kept maximum.  Nothing seen yet: weights
+// are exp2(-inf) = 0.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
+template <int NRT, int NK, int NB, int PACK>
+__device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
+  settle<NRT, NK, NB, PACK>(s, undo, m, l, acc);
 #pragma unroll
   for (int rt = 0; rt < NRT; ++rt) {
-    // Nothing seen yet: weights are exp2(-inf) = 0.
-    const float from = m[rt] == -INFINITY ? 0.f : m[rt];
+    const float from = base_of(m[rt]);
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {

@@ -237,6 +237,19 @@ struct Mx4Attn {
 // per lane, conflict-free); the next step's codes are in flight meanwhile.  Row
 // tiles are dealt to the waves in turn, so a short item still uses all four.
 constexpr int kMx4WideKeys = 64;
+// Operands that are on their way from LDS ahead of the product that takes them.
+constexpr int kAhead = 2;
+
+// The order of what lies before it back to the last one: products with VALU vector
+// instructions behind each.
+template <int PRODUCTS, int VALU>
+__device__ __forceinline__ void mix() {
+  static_for<0, PRODUCTS>([](auto) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 template <int DIM>
 struct Mx4WideLds {
@@ -274,7 +287,9 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     load_words<NB>(buffer_of(Vc + base * (DIM / 2), 8 * DIM), c * (2 * DIM) + row * (4 * NB), vw);
     load_words<NB>(buffer_of(Vs + base * NB, 16 * NB), c * (4 * NB), vsw);
   };
-  auto lay = [&](int buf) {
+  // Into LDS: scales that are no numbers first, then, for each block, its keys and
+  // its values.
+  auto lay_scales = [&](int buf) {
     const uint32_t lost = poison == 0.f ? 0u : ~0u;
     uint32_t bad = 0;
 #pragma unroll
@@ -293,25 +308,35 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
       }
     }
     if (lane == 0) lds.gone[buf][wave] = any;
-    static_for<0, NB>([&](auto b_) {
-      constexpr int b = decltype(b_)::value;
-      v4u x;
-      static_for<0, 4>([&](auto j_) {
-        constexpr int j = decltype(j_)::value, e = j * NB + b;
-        x[j] = pair_bf16<e % 4, b % 4>(kw[e / 4], ksw[b / 4]);
-      });
-      lds.k[buf][wave][b][lane] = x;
-      uint32_t u[4];
-      static_for<0, 4>([&](auto k_) {
-        constexpr int e = decltype(k_)::value * NB + b;
-        u[decltype(k_)::value] = pair_bf16<e % 4, e % 4>(vw[e / 4], vsw[e / 4]);
-      });
+  };
+  auto lay_keys = [&](auto b_, int buf) {
+    constexpr int b = decltype(b_)::value;
+    v4u x;
+    static_for<0, 4>([&](auto j_) {
+      constexpr int j = decltype(j_)::value, e = j * NB + b;
+      x[j] = pair_bf16<e % 4, b % 4>(kw[e / 4], ksw[b / 4]);
+    });
+    lds.k[buf][wave][b][lane] = x;
+  };
+  auto lay_values = [&](auto b_, int buf) {
+    constexpr int b = decltype(b_)::value;
+    uint32_t u[4];
+    static_for<0, 4>([&](auto k_) {
+      constexpr int e = decltype(k_)::value * NB + b;
+      u[decltype(k_)::value] = pair_bf16<e % 4, e % 4>(vw[e / 4], vsw[e / 4]);
+    });
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t sel = i ? 0x07060302u : 0x05040100u;
-        lds.v[buf][wave / 2][b][i][lane][wave % 2] =
-            v2u{__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel)};
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t sel = i ? 0x07060302u : 0x05040100u;
+      lds.v[buf][wave / 2][b][i][lane][wave % 2] =
+          v2u{__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel)};
+    }
+  };
+  auto lay = [&](int buf) {
+    lay_scales(buf);
+    static_for<0, NB>([&](auto b_) {
+      lay_keys(b_, buf);
+      lay_values(b_, buf);
     });
   };
 
@@ -351,28 +376,46 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     const int tiles = (h.rows + 15) / 16;
     const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has
 
-    // One step over the 64 keys from `at` on, for the wave's first NRT row tiles.
-    auto compute = [&](auto nrt_, int at, int buf) {
+    // One step over the 64 keys from `at` on, for the wave's first NRT row tiles.  With two
+    // buffers the next step's codes (more: there is one) are converted meanwhile, in the
+    // shadow of the products.
+    auto compute = [&](auto nrt_, int at, int buf, bool more) {
       constexpr int NRT = decltype(nrt_)::value;
       float s[NRT][16];
+      if (BUFS == 2 && more) lay_scales(buf ^ 1);
       {
         v4f x[NRT][4];
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt) x[rt][kt] = v4f{0.f, 0.f, 0.f, 0.f};
-        // Operands of product n + 1 are on their way while product n runs.
-        v4u a[2];
-        a[0] = lds.k[buf][0][0][lane];
-        static_for<0, 4 * NB>([&](auto n_) {
-          constexpr int n = decltype(n_)::value, kt = n % 4, b = n / 4;
-          if constexpr (n + 1 < 4 * NB) a[(n + 1) % 2] = lds.k[buf][(n + 1) % 4][(n + 1) / 4][lane];
-          __builtin_amdgcn_sched_barrier(0);
+        v4u a[kAhead + 1];
+        auto fetch = [&](auto n_) {
+          constexpr int n = decltype(n_)::value;
+          if constexpr (n < 4 * NB) a[n % (kAhead + 1)] = lds.k[buf][n % 4][n / 4][lane];
+        };
+        // Products first: what another wave of the SIMD does meanwhile fits between them
+        // (trees of bf16 124 us, 129 without).
+        __builtin_amdgcn_s_setprio(1);
+        static_for<0, kAhead>(fetch);
+        auto products = [&](auto lays_) {
+          static_for<0, 4 * NB>([&](auto n_) {
+            constexpr int n = decltype(n_)::value, kt = n % 4, b = n / 4;
+            fetch(std::integral_constant<int, n + kAhead>{});
+            if constexpr (decltype(lays_)::value && n % 4 == 1) lay_keys(std::integral_constant<int, b>{}, buf ^ 1);
+            if constexpr (decltype(lays_)::value && n % 4 == 3) lay_values(std::integral_constant<int, b>{}, buf ^ 1);
 #pragma unroll
-          for (int q = QP - 1; q >= 0; --q)
+            for (int q = QP - 1; q >= 0; --q)
 #pragma unroll
-            for (int rt = 0; rt < NRT; ++rt) x[rt][kt] = mfma(a[n % 2], qf[rt][b][q], x[rt][kt]);
-        });
+              for (int rt = 0; rt < NRT; ++rt) x[rt][kt] = mfma(a[n % (kAhead + 1)], qf[rt][b][q], x[rt][kt]);
+            mix<QP * NRT, 6>();
+          });
+        };
+        if (BUFS == 2 && more)
+          products(std::true_type{});
+        else
+          products(std::false_type{});
+        __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
@@ -395,36 +438,68 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      weigh<NRT, 16, NB, 1>(s, undo, m, l, acc);
-      v4u parts[NRT][2][PP];
-#pragma unroll
-      for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = s[rt][8 * g + k];
-          split8<PP>(w, parts[rt][g]);
-        }
+      settle<NRT, 16, NB, 1>(s, undo, m, l, acc);
       {
-        v4u a[2][2];
+        constexpr int RING = kAhead + 1;
+        v4u a[RING][2];
         auto fetch = [&](auto n_) {
           constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
+          if constexpr (n < 2 * NB)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) a[n % 2][i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
+            for (int i = 0; i < 2; ++i) a[n % RING][i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
         };
-        fetch(std::integral_constant<int, 0>{});
+        float from[NRT];
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt) from[rt] = base_of(m[rt]);
+        auto weight = [&](int rt, int k) {
+          s[rt][k] = __builtin_amdgcn_exp2f(fmaf(s[rt][k], undo[rt], -from[rt]));
+          l[rt] += s[rt][k];
+        };
+        // Sums are made here: later, the weights would have to be kept for them.
+        auto summed = [&]() {
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) pin(l[rt]);
+        };
+        v4u parts[NRT][PP];
+        auto cut = [&](int g) {
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) {
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = s[rt][8 * g + k];
+            split8<PP>(w, parts[rt]);
+          }
+        };
+        static_for<0, kAhead>(fetch);
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) weight(rt, k);
+        summed();
+        cut(0);
+        __builtin_amdgcn_s_setprio(1);
+        __builtin_amdgcn_sched_barrier(0);
         static_for<0, 2 * NB>([&](auto n_) {
           constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
-          if constexpr (n + 1 < 2 * NB) fetch(std::integral_constant<int, n + 1>{});
-          __builtin_amdgcn_sched_barrier(0);
+          fetch(std::integral_constant<int, n + kAhead>{});
+          // The second half's weights in the shadow of the first one's products.
+          if constexpr (g == 0)
+#pragma unroll
+            for (int e = b * NRT * 8 / NB; e < (b + 1) * NRT * 8 / NB; ++e) weight(e / 8, 8 + e % 8);
 #pragma unroll
           for (int q = PP - 1; q >= 0; --q)
 #pragma unroll
             for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) acc[rt][b][i] = mfma(a[n % 2][i], parts[rt][g][q], acc[rt][b][i]);
+              for (int i = 0; i < 2; ++i) acc[rt][b][i] = mfma(a[n % RING][i], parts[rt][q], acc[rt][b][i]);
+          mix<2 * PP * NRT, 2>();
+          if constexpr (n == NB - 1) {
+            summed();
+            cut(1);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         });
+        __builtin_amdgcn_s_setprio(0);
       }
       // Blocks of rows that see a value scale that is no number are lost.
       uint32_t any = 0;
@@ -459,10 +534,11 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
       auto steps = [&](auto nrt_) {
         for (int at = begin; at < end; at += kMx4WideKeys) {
           const int buf = BUFS == 2 ? (at - begin) / kMx4WideKeys % 2 : 0;
-          if constexpr (decltype(nrt_)::value > 0) compute(nrt_, at, buf);
+          const bool more = at + kMx4WideKeys < end;
+          if constexpr (decltype(nrt_)::value > 0) compute(nrt_, at, buf, more);
           if constexpr (BUFS == 1) __syncthreads();
-          if (at + kMx4WideKeys < end) {
-            lay(BUFS == 2 ? buf ^ 1 : 0);
+          if (more) {
+            if constexpr (BUFS == 1 || decltype(nrt_)::value == 0) lay(BUFS == 2 ? buf ^ 1 : 0);
             if (at + 2 * kMx4WideKeys < end) load_at(at + 2 * kMx4WideKeys);
           }
           __syncthreads();

@@ -7,8 +7,8 @@
 // keeps the order of what it moves.
 //
 // resize and compact go through phases that each need all of the one before:
-// counts of tiles of pages, their prefixes, what follows from them.  A small pool
-// runs them in one workgroup, a large one as one launch each over the device.
+// counts of tiles of pages, their prefixes, what follows from them.  A large pool
+// takes one launch each over the device, a small one is done by one workgroup.
 #include <algorithm>
 
 #include "pages.h"
@@ -272,23 +272,86 @@ __device__ void resize_give(const ResizeArgs &a) {
   }
 }
 
-// Between phases of one workgroup: what it has written is there, and nothing
-// older is read from its cache.
-__device__ __forceinline__ void phase_end() {
-  __threadfence();
-  __syncthreads();
-  __threadfence();
+template <int PHASE>
+__global__ __launch_bounds__(kBig) void resize_kernel(ResizeArgs a) {
+  if constexpr (PHASE == 0) resize_release(a);
+  if constexpr (PHASE == 1) resize_count(a);
+  if constexpr (PHASE == 2) resize_list(a);
+  if constexpr (PHASE == 3) resize_give(a);
 }
 
-template <int PHASE>  // -1: all of them
-__global__ __launch_bounds__(kBig) void resize_kernel(ResizeArgs a) {
-  if constexpr (PHASE < 0 || PHASE == 0) resize_release(a);
-  if constexpr (PHASE < 0) phase_end();
-  if constexpr (PHASE < 0 || PHASE == 1) resize_count(a);
-  if constexpr (PHASE < 0) phase_end();
-  if constexpr (PHASE < 0 || PHASE == 2) resize_list(a);
-  if constexpr (PHASE < 0) phase_end();
-  if constexpr (PHASE < 0 || PHASE == 3) resize_give(a);
+// The same by one workgroup, a thread for each of up to 1024 sequences: what the phases
+// keep in memory stays in registers, the free pages are looked at only as far as
+// they are wanted, and a call that wants none (most decode steps) looks at none.
+constexpr int kSmallSeqs = kBig;
+template <bool RELEASE>
+__global__ __launch_bounds__(kBig) void resize_small_kernel(ResizeArgs a) {
+  constexpr int kOwn = 4, kListed = 4096;
+  __shared__ int listed[kListed];  // the first ones; the others go through memory
+  const int b = threadIdx.x, lane = b & 63;
+  const bool in = b < a.t.seqs;
+  Change c{};
+  if (in) c = change_of(a, b);
+  int *row = a.t.table + (in ? b : 0) * a.t.stride;
+  int last = -1;
+  if (c.writes) last = row[c.held - 1];
+  if constexpr (RELEASE) {
+    if (__syncthreads_or(c.want < c.held)) {
+      resize_release(a);
+      __syncthreads();
+    }
+  }
+  const bool replaced = is_page(last, a.pages) && a.refs[last] > 1;
+  const int need = max(c.want - c.held, 0) + (replaced ? 1 : 0);
+  int64_t wanted;
+  const int64_t start = block_sum_before((int64_t)need, &wanted);
+  int64_t found = 0;
+  for (int64_t t = 0; t < pages_tiles(a.pages) && found < wanted; ++t) {
+    int64_t first;
+    int used_in, all;
+    const int used = used_bits(a.refs, a.pages, t, &first, &used_in);
+    int free = used_in & ~used;
+    int64_t r = found + block_sum_before((int)__popc(free), &all);
+    for (; free != 0; free &= free - 1, ++r) {
+      const int page = (int)(first + __builtin_ctz(free));
+      if (r < kListed)
+        listed[r] = page;
+      else if (r < wanted)
+        a.w.list[r] = page;
+    }
+    found += all;
+  }
+  __syncthreads();
+  const bool served = start + need <= found;
+  const int given = served ? need : 0, column = c.held - (replaced ? 1 : 0);
+  auto page_of = [&](int64_t r) { return r < kListed ? listed[r] : a.w.list[r]; };
+  if (in) {
+    const bool moves = replaced && served;
+    if (moves) atomicAdd(a.refs + last, -1);
+    a.moves[2 * b] = moves ? last : -1;
+    a.moves[2 * b + 1] = moves ? page_of(start) : -1;
+    a.missing[b] = !c.ok ? -1 : served ? 0 : need;
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i)
+    if (i < given) {
+      const int page = page_of(start + i);
+      row[column + i] = page;
+      a.refs[page] = 1;
+    }
+  uint64_t more = __ballot(given > kOwn);
+  while (more != 0) {
+    const int s = __builtin_ctzll(more);
+    more &= more - 1;
+    const int n = __shfl(given, s), at = __shfl(column, s);
+    const int64_t from = __shfl(start, s);
+    int *to = a.t.table + (b - lane + s) * a.t.stride;
+    for (int i = kOwn + lane; i < n; i += 64) {
+      const int page = page_of(from + i);
+      to[at + i] = page;
+      a.refs[page] = 1;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- compact
@@ -389,6 +452,10 @@ __device__ void compact_apply(const CompactArgs &a) {
   }
 }
 
+// Between phases of one workgroup.  A barrier is enough: its threads share a cache.  (A
+// fence for the device writes L2 back, and took most of a small call's 28 us.)
+__device__ __forceinline__ void phase_end() { __syncthreads(); }
+
 template <int PHASE>  // -1: all of them
 __global__ __launch_bounds__(kBig) void compact_kernel(CompactArgs a) {
   if constexpr (PHASE < 0 || PHASE == 0) compact_count(a);
@@ -400,49 +467,72 @@ __global__ __launch_bounds__(kBig) void compact_kernel(CompactArgs a) {
 
 // ---------------------------------------------------------------- copying
 
-struct __attribute__((packed, aligned(4))) Sixteen {
-  uint32_t x[4];
-};
-constexpr int kCopyPiece = 4096;  // bytes a wave takes at a time: four loads of 16 bytes in flight per lane
+// 16 bytes at any word: the Q8_0 cache's scales need no more.
+typedef uint32_t Sixteen __attribute__((ext_vector_type(4), aligned(4)));
+// Bytes of a page that a workgroup takes at a time, eight loads of 16 bytes in flight
+// per thread.
+constexpr int kCopyLoads = 8;
+constexpr int kCopyPiece = 16 * kThreads * kCopyLoads;
 
-// A wave per piece of a page's four arrays, taken as one after another.
-__global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a, int pieces) {
-  const int lane = threadIdx.x & 63;
-  const int64_t units = a.n * pieces, waves = (int64_t)gridDim.x * kWaves;
+// Workgroup (x, y): the x-th piece of pages moves[y], moves[y + gridDim.y], ...; a
+// page's four arrays are taken as one after another.  The next move is asked for
+// before this one's bytes are stored.
+__global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
   const int64_t whole = a.bytes[0] + a.bytes[1] + a.bytes[2] + a.bytes[3];
-  for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < units; u += waves) {
-    const int64_t i = u / pieces;
-    const int from = a.moves[2 * i], to = a.moves[2 * i + 1];
-    if ((uint32_t)from >= (uint64_t)a.pages || (uint32_t)to >= (uint64_t)a.pages || from == to) continue;
-    const int64_t begin = (u - i * pieces) * kCopyPiece;
-    Sixteen x[4];
-    char *at[4];
+  // Where this thread's bytes lie: array and offset, the same in every page.
+  const char *base[kCopyLoads];
+  int64_t step[kCopyLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      int64_t o = begin + 16 * (64 * k + lane);
-      at[k] = nullptr;
-      if (o >= whole) continue;
-      int64_t bytes = a.bytes[0];
-      char *base = a.base[0];
-#pragma unroll
-      for (int s = 1; s < 4; ++s)
-        if (o >= bytes) {
-          o -= bytes;
-          bytes = a.bytes[s];
-          base = a.base[s];
-        } else {
-          break;
+  for (int k = 0; k < kCopyLoads; ++k) {
+    int64_t o = (int64_t)blockIdx.x * kCopyPiece + 16 * (kThreads * k + (int)threadIdx.x);
+    base[k] = nullptr;
+    step[k] = 0;
+    if (o >= whole) continue;
+    base[k] = a.base[0];
+    step[k] = a.bytes[0];
+    if (o >= a.bytes[0]) {
+      o -= a.bytes[0];
+      base[k] = a.base[1];
+      step[k] = a.bytes[1];
+      if (o >= a.bytes[1]) {
+        o -= a.bytes[1];
+        base[k] = a.base[2];
+        step[k] = a.bytes[2];
+        if (o >= a.bytes[2]) {
+          o -= a.bytes[2];
+          base[k] = a.base[3];
+          step[k] = a.bytes[3];
         }
-      x[k] = *reinterpret_cast<const Sixteen *>(base + from * bytes + o);
-      at[k] = base + to * bytes + o;
+      }
     }
+    base[k] += o;
+  }
+  int64_t i = blockIdx.y;
+  int from = a.moves[2 * i], to = a.moves[2 * i + 1];
+  while (true) {
+    const int64_t next = i + gridDim.y;
+    int next_from = -1, next_to = -1;
+    if (next < a.n) {
+      next_from = a.moves[2 * next];
+      next_to = a.moves[2 * next + 1];
+    }
+    if ((uint32_t)from < (uint64_t)a.pages && (uint32_t)to < (uint64_t)a.pages && from != to) {
+      Sixteen x[kCopyLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at[k] != nullptr) *reinterpret_cast<Sixteen *>(at[k]) = x[k];
+      for (int k = 0; k < kCopyLoads; ++k)
+        if (base[k] != nullptr) x[k] = *reinterpret_cast<const Sixteen *>(base[k] + from * step[k]);
+#pragma unroll
+      for (int k = 0; k < kCopyLoads; ++k)
+        if (base[k] != nullptr) *reinterpret_cast<Sixteen *>(const_cast<char *>(base[k]) + to * step[k]) = x[k];
+    }
+    if (next >= a.n) return;
+    i = next;
+    from = next_from;
+    to = next_to;
   }
 }
 
-// Pools and tables up to these sizes take one workgroup and one launch.
+// Pools and tables up to these sizes are done by one workgroup.
 constexpr int64_t kOnePages = 32768, kOneEntries = 32768;
 
 }  // namespace
@@ -454,13 +544,19 @@ hipError_t launch_pages_fork(const ForkArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_pages_resize(const ResizeArgs &a, int cus, hipStream_t stream) {
-  if (a.pages <= kOnePages && (int64_t)a.t.seqs * a.t.max_pages <= kOneEntries) {
-    hipLaunchKernelGGL((resize_kernel<-1>), dim3(1), dim3(kBig), 0, stream, a);
+  const bool small = a.pages <= kOnePages && a.t.seqs <= kSmallSeqs;
+  // Releasing many entries takes the whole device.
+  if (small && (int64_t)a.t.seqs * a.t.max_pages <= kOneEntries) {
+    hipLaunchKernelGGL((resize_small_kernel<true>), dim3(1), dim3(kBig), 0, stream, a);
     return hipGetLastError();
   }
   const unsigned by_waves = (unsigned)std::min<int64_t>(((int64_t)a.t.seqs + kBigWaves - 1) / kBigWaves, 2 * cus);
-  const unsigned tiles = (unsigned)std::min<int64_t>(std::max(pages_tiles(a.pages), seqs_tiles(a.t.seqs)), 2 * cus);
   hipLaunchKernelGGL((resize_kernel<0>), dim3(by_waves), dim3(kBig), 0, stream, a);
+  if (small) {
+    hipLaunchKernelGGL((resize_small_kernel<false>), dim3(1), dim3(kBig), 0, stream, a);
+    return hipGetLastError();
+  }
+  const unsigned tiles = (unsigned)std::min<int64_t>(std::max(pages_tiles(a.pages), seqs_tiles(a.t.seqs)), 2 * cus);
   hipLaunchKernelGGL((resize_kernel<1>), dim3(tiles), dim3(kBig), 0, stream, a);
   hipLaunchKernelGGL((resize_kernel<2>), dim3(tiles), dim3(kBig), 0, stream, a);
   hipLaunchKernelGGL((resize_kernel<3>), dim3((unsigned)std::min<int64_t>(seqs_tiles(a.t.seqs), 2 * cus)), dim3(kBig), 0, stream, a);
@@ -479,11 +575,13 @@ hipError_t launch_pages_compact(const CompactArgs &a, int cus, hipStream_t strea
   return hipGetLastError();
 }
 
-hipError_t launch_pages_copy(const CopyArgs &a, int cus, hipStream_t stream) {
+hipError_t launch_pages_copy(const CopyArgs &args, int cus, hipStream_t stream) {
+  CopyArgs a = args;
   const int64_t whole = a.bytes[0] + a.bytes[1] + a.bytes[2] + a.bytes[3];
-  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece);
-  const int64_t wgs = std::min<int64_t>((a.n * pieces + kWaves - 1) / kWaves, (int64_t)cus * 16);
-  hipLaunchKernelGGL(copy_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream, a, pieces);
+  const int64_t pieces = (whole + kCopyPiece - 1) / kCopyPiece;  // below 2^22: a page is below 2^37 bytes
+  // Enough workgroups for the device; each takes moves that far apart.
+  const int64_t rows = std::max<int64_t>(std::min<int64_t>((int64_t)cus * 8 / pieces, 65535), 1);
+  hipLaunchKernelGGL(copy_kernel, dim3((unsigned)pieces, (unsigned)std::min(rows, a.n)), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -8,9 +8,8 @@
 // is brought to the nearest quarter turn, and sine and cosine come from their power
 // series on |a| <= pi / 4: up to a^9 and a^10, off by less than 2e-9 there.
 //
-// Bound by memory: every row once in and once out.  A workgroup takes a row; a
-// thread makes the angles of its pairs once and takes them through all heads of all
-// tensors.
+// Bound by memory: every row once in and once out.  The angles of a row are made once
+// for all heads of all tensors.
 #include <algorithm>
 
 #include "cache_rows.h"
@@ -39,11 +38,63 @@ __device__ __forceinline__ void angle_of(uint64_t turns, int position, float &co
   if (quarter & 2) sine = -sine;            // quarters 2 and 3
 }
 
-// P: pairs of a thread, neighbouring ones.
-template <RowType T, bool INTERLEAVED, int P>
+// Below this many rows a workgroup takes one, from there on each of its waves.
+constexpr int kFewRows = 2048;
+// Heads that a thread has in flight at a time.
+constexpr int kRopeHeads = 4;
+
+// A row is taken by TPR threads.  Each makes some of the row's angles, which meet in
+// LDS; then 2^lanes_shift of them share a head, and P neighbouring pairs are one
+// thread's.  The first heads are asked for before the row's position is looked for.
+template <RowType T, bool INTERLEAVED, int P, int TPR>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, int lanes_shift) {
   typedef typename Elem<T>::type E;
-  const uint32_t row = p.row0 + blockIdx.x;  // below rows, by the launcher's grid
+  extern __shared__ float2 angles[];  // [kThreads / TPR][rot / 2]
+  const int half = p.rot / 2;
+  const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t row = (int64_t)p.row0 + (int64_t)blockIdx.x * (kThreads / TPR) + sub;
+  if (row >= p.s.rows) return;  // whole waves
+  float2 *mine = angles + sub * half;
+  const int turning = half / P;  // threads of a head that turn pairs
+  const int chunks = turning + (p.copy ? (p.dim - p.rot + 2 * P - 1) / (2 * P) : 0);  // and that copy the rest
+  const int lanes = 1 << lanes_shift, step = TPR >> lanes_shift;
+  const int k0 = tid & (lanes - 1), first_head = tid >> lanes_shift;
+
+  // A chunk of a head: two runs of P elements, half a rotation apart or next to each other.
+  struct Chunk {
+    Run<E, P> u, v;
+  };
+  auto place = [&](int h, int &n) -> int64_t {  // of head h: its tensor, and the element within the row
+    n = 0;
+    int h0 = 0;
+#pragma unroll
+    for (int i = 1; i < kRopeTensors; ++i)
+      if (h >= p.upto[i - 1]) {
+        n = i;
+        h0 = p.upto[i - 1];
+      }
+    return (int64_t)(h - h0) * p.dim;
+  };
+  auto source = [&](int h) {
+    int n;
+    const int64_t at = place(h, n);
+    return static_cast<const E *>(p.x[n]) + row * p.x_stride[n] + at;
+  };
+  auto begin_of = [&](int k) { return k < turning ? (INTERLEAVED ? 2 : 1) * P * k : p.rot + 2 * P * (k - turning); };
+  auto second_of = [&](int k) { return k < turning && !INTERLEAVED ? P * k + half : begin_of(k) + P; };
+  auto is_whole = [&](int k) { return k < turning || begin_of(k) + 2 * P <= p.dim; };  // else a last piece, by elements
+  Chunk x[kRopeHeads];
+  auto load = [&](int k, int h0) {
+#pragma unroll
+    for (int j = 0; j < kRopeHeads; ++j)
+      if (h0 + j * step < p.heads) {
+        const E *from = source(h0 + j * step);
+        x[j].u = *reinterpret_cast<const Run<E, P> *>(from + begin_of(k));
+        x[j].v = *reinterpret_cast<const Run<E, P> *>(from + second_of(k));
+      }
+  };
+  if (k0 < chunks && is_whole(k0)) load(k0, first_head);
+
   int position;
   if (p.positions != nullptr) {
     position = p.positions[row];
@@ -52,80 +103,87 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, int lanes_sh
     if (!at.found) return;  // no sequence's row: left as it was
     position = (int)((uint32_t)at.seq.length - (uint32_t)at.seq.n + (uint32_t)at.index);
   }
-  const int half = p.rot / 2, turning = half / P;  // threads of a head that turn pairs
-  const int tail = p.copy ? (p.dim - p.rot + 2 * P - 1) / (2 * P) : 0;  // and that copy the rest
-  const int lanes = 1 << lanes_shift, step = kThreads >> lanes_shift;
-  for (int k = threadIdx.x & (lanes - 1); k < turning + tail; k += lanes) {
-    const bool turn = k < turning;
-    float c[P], s[P];
-    if (turn) {
+  for (int i = tid; i < half; i += TPR) {
+    float c, s;
+    angle_of(p.turns[i], position, c, s);
+    mine[i] = float2{c * p.amplitude, s * (p.inverse ? -p.amplitude : p.amplitude)};
+  }
+  if constexpr (TPR == 64) {  // a wave's own: no other waits for it
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+
+  for (int k = k0; k < chunks; k += lanes) {
+    const int begin = begin_of(k), second = second_of(k);
+    const bool turn = k < turning, whole = is_whole(k);
+    float2 cs[P];
+    if (turn)
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        angle_of(p.turns[k * P + i], position, c[i], s[i]);
-        c[i] *= p.amplitude;
-        s[i] *= p.inverse ? -p.amplitude : p.amplitude;
-      }
-    }
-    for (int h = threadIdx.x >> lanes_shift; h < p.heads; h += step) {
-      int n = 0, h0 = 0;
+      for (int i = 0; i < P; ++i) cs[i] = mine[k * P + i];
+    for (int h0 = first_head; h0 < p.heads; h0 += kRopeHeads * step) {
+      if (whole && (k != k0 || h0 != first_head)) load(k, h0);
 #pragma unroll
-      for (int i = 1; i < kRopeTensors; ++i)
-        if (h >= p.upto[i - 1]) {
-          n = i;
-          h0 = p.upto[i - 1];
+      for (int j = 0; j < kRopeHeads; ++j) {
+        const int h = h0 + j * step;
+        if (h >= p.heads) continue;
+        int n;
+        const int64_t at = place(h, n);
+        E *to = static_cast<E *>(p.out[n]) + row * p.out_stride[n] + at;
+        if (!whole) {
+          const E *from = source(h);
+          for (int d = begin; d < p.dim; ++d) to[d] = from[d];
+          continue;
         }
-      const E *x = static_cast<const E *>(p.x[n]) + (int64_t)row * p.x_stride[n] + (int64_t)(h - h0) * p.dim;
-      E *out = static_cast<E *>(p.out[n]) + (int64_t)row * p.out_stride[n] + (int64_t)(h - h0) * p.dim;
-      if (!turn) {
-        const int d0 = p.rot + (k - turning) * 2 * P;
+        if (turn) {
 #pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          if (d0 + i < p.dim) out[d0 + i] = x[d0 + i];
-      } else if constexpr (INTERLEAVED) {
-        const Run<E, 2 * P> in = *reinterpret_cast<const Run<E, 2 * P> *>(x + 2 * P * k);
-        Run<E, 2 * P> to;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float u = Elem<T>::to_float(in.x[2 * i]), v = Elem<T>::to_float(in.x[2 * i + 1]);
-          to.x[2 * i] = Elem<T>::from_float(u * c[i] - v * s[i]);
-          to.x[2 * i + 1] = Elem<T>::from_float(u * s[i] + v * c[i]);
+          for (int i = 0; i < P; ++i) {
+            // The i-th pair: interleaved, of the two runs taken as one.
+            E &eu = !INTERLEAVED ? x[j].u.x[i] : 2 * i < P ? x[j].u.x[2 * i % P] : x[j].v.x[2 * i % P];
+            E &ev = !INTERLEAVED ? x[j].v.x[i] : 2 * i + 1 < P ? x[j].u.x[(2 * i + 1) % P] : x[j].v.x[(2 * i + 1) % P];
+            const float u = Elem<T>::to_float(eu), v = Elem<T>::to_float(ev);
+            eu = Elem<T>::from_float(u * cs[i].x - v * cs[i].y);
+            ev = Elem<T>::from_float(u * cs[i].y + v * cs[i].x);
+          }
         }
-        *reinterpret_cast<Run<E, 2 * P> *>(out + 2 * P * k) = to;
-      } else {
-        const Run<E, P> iu = *reinterpret_cast<const Run<E, P> *>(x + P * k);
-        const Run<E, P> iv = *reinterpret_cast<const Run<E, P> *>(x + half + P * k);
-        Run<E, P> ou, ov;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float u = Elem<T>::to_float(iu.x[i]), v = Elem<T>::to_float(iv.x[i]);
-          ou.x[i] = Elem<T>::from_float(u * c[i] - v * s[i]);
-          ov.x[i] = Elem<T>::from_float(u * s[i] + v * c[i]);
-        }
-        *reinterpret_cast<Run<E, P> *>(out + P * k) = ou;
-        *reinterpret_cast<Run<E, P> *>(out + half + P * k) = ov;
+        *reinterpret_cast<Run<E, P> *>(to + begin) = x[j].u;
+        *reinterpret_cast<Run<E, P> *>(to + second) = x[j].v;
       }
     }
   }
 }
 
-template <RowType T, bool INTERLEAVED>
-hipError_t launch_typed(const RopeArgs &args, hipStream_t stream) {
-  RopeArgs a = args;
-  const int pairs = a.rot / 2 % 4 == 0 ? 4 : 1;
-  const int threads = a.rot / 2 / pairs + (a.copy ? (a.dim - a.rot + 2 * pairs - 1) / (2 * pairs) : 0);
+template <RowType T, bool INTERLEAVED, int P, int TPR>
+hipError_t launch_rows(RopeArgs a, hipStream_t stream) {
+  const int threads = a.rot / 2 / P + (a.copy ? (a.dim - a.rot + 2 * P - 1) / (2 * P) : 0);
   int shift = 0;
-  while (shift < 8 && (1 << shift) < threads) ++shift;
-  for (int64_t row0 = 0; row0 < a.s.rows; row0 += kMostGroups) {
+  while ((1 << shift) < TPR && (1 << shift) < threads) ++shift;
+  constexpr int kRows = kThreads / TPR;
+  const size_t lds = (size_t)kRows * (a.rot / 2) * sizeof(float2);  // at most 64 KiB
+  for (int64_t row0 = 0; row0 < a.s.rows; row0 += (int64_t)kMostGroups * kRows) {
     a.row0 = (int)row0;
-    const dim3 grid((unsigned)std::min<int64_t>(a.s.rows - row0, kMostGroups));
-    if (pairs == 4)
-      hipLaunchKernelGGL((rope_kernel<T, INTERLEAVED, 4>), grid, dim3(kThreads), 0, stream, a, shift);
-    else
-      hipLaunchKernelGGL((rope_kernel<T, INTERLEAVED, 1>), grid, dim3(kThreads), 0, stream, a, shift);
+    const dim3 grid((unsigned)std::min<int64_t>((a.s.rows - row0 + kRows - 1) / kRows, kMostGroups));
+    hipLaunchKernelGGL((rope_kernel<T, INTERLEAVED, P, TPR>), grid, dim3(kThreads), lds, stream, a, shift);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <RowType T, bool INTERLEAVED, int P>
+hipError_t launch_pairs(const RopeArgs &a, hipStream_t stream) {
+  if (a.s.rows < kFewRows) return launch_rows<T, INTERLEAVED, P, kThreads>(a, stream);
+  return launch_rows<T, INTERLEAVED, P, 64>(a, stream);
+}
+
+template <RowType T, bool INTERLEAVED>
+hipError_t launch_typed(const RopeArgs &a, hipStream_t stream) {
+  // Runs of 16 bytes where the pairs come in whole ones.
+  constexpr int kWide = T == kRowF32 ? 4 : 8;
+  if (a.rot / 2 % kWide == 0) return launch_pairs<T, INTERLEAVED, kWide>(a, stream);
+  if (a.rot / 2 % 4 == 0) return launch_pairs<T, INTERLEAVED, 4>(a, stream);
+  return launch_pairs<T, INTERLEAVED, 1>(a, stream);
 }
 
 }  // namespace
