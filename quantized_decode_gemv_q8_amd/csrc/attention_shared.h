@@ -348,7 +348,8 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // Raises the rows' kept maxima where a score, up to the row's factor undo[rt], passes
-// one by kMaxSlack, and scales the rows' sums down to the new ones.
+// one by kMaxSlack, and scales the rows' sums down to the new ones.  Every lane looks at
+// its own keys; the row's largest is only made where one of them passes.
 template <int NRT, int NK, int NB, int PACK>
 __device__ __forceinline__ void settle(const float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   float top[NRT];
@@ -358,13 +359,12 @@ __device__ __forceinline__ void settle(const float (&s)[NRT][NK], const float *u
     top[rt] = s[rt][0];
 #pragma unroll
     for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
-    top[rt] = row_max<PACK>(top[rt]) * undo[rt];
-    above |= top[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
+    above |= top[rt] * undo[rt] > m[rt] + kMaxSlack;  // the first key that is seen, too
   }
   if (__ballot(above) != 0) {
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
-      const float to = fmaxf(m[rt], top[rt]);
+      const float to = fmaxf(m[rt], row_max<PACK>(top[rt]) * undo[rt]);
       const float f = __builtin_amdgcn_exp2f(m[rt] - (to == -INFINITY ? 0.f : to));
       m[rt] = to;
       l[rt] *= f;
@@ -401,6 +401,7 @@ __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, fl
 // compiler spreads one step's operands over all steps and runs out of registers.
 __device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void pin(v4f &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void pin(v4u &x) { asm volatile("" : "+v"(x)); }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 

@@ -39,6 +39,24 @@ __device__ __forceinline__ uint32_t pair_bf16(uint32_t codes, uint32_t scales) {
 // Bit 7 of every byte of x that stands for no number (253 .. 255; 253 and 254 are no scales).
 __device__ __forceinline__ uint32_t no_numbers(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x03030303u) & x & 0x80808080u; }
 
+// split8 by vector instructions alone: v_dot2_f32_bf16, of which it takes one per
+// part and weight, runs on the matrix pipe, in the way of the products.
+template <int PARTS>
+__device__ __forceinline__ void cut8(const float (&x)[8], v4u (&out)[PARTS]) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    const bool rest = PARTS < 3 && p + 1 == PARTS;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[p][i] = rest ? pack_near(r[2 * i], r[2 * i + 1]) : pack_hi(r[2 * i], r[2 * i + 1]);
+    if (p + 1 < PARTS)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] -= __uint_as_float(bits(r[i]) & 0xffff0000u);
+  }
+}
+
 template <int BYTES>
 __device__ __forceinline__ void load_bytes(__amdgpu_buffer_rsrc_t rs, int offset, uint32_t (&w)[(BYTES + 3) / 4]) {
   if constexpr (BYTES == 2)
@@ -61,7 +79,7 @@ __device__ __forceinline__ void cut_bf16(const QueryRow<T, DIM> &from, bool in, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) qf[b][0][i] = pack_hi(x[2 * i], x[2 * i + 1]);
     } else {
-      split8<kMx4QParts<T>>(x, qf[b]);
+      cut8<kMx4QParts<T>>(x, qf[b]);
     }
   }
 }
@@ -204,7 +222,7 @@ struct Mx4Attn {
   __device__ __forceinline__ void values(const Tile &t, const float (&s)[RT][8]) {
     v4u parts[RT][PP];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) split8<PP>(s[rt], parts[rt]);
+    for (int rt = 0; rt < RT; ++rt) cut8<PP>(s[rt], parts[rt]);
     static_for<0, NB>([&](auto b_) {
       constexpr int b = decltype(b_)::value;
       // Lane: values of keys (k index 4 h + i) at channels 32 b + 2 row + 0, 1.
@@ -345,8 +363,11 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     const int last = h.keys - 1;
     const int begin = h.k0 << h.shift;
     const int end = h.seq.bad ? begin : min(h.k1 << h.shift, h.keys);
+    // A page's number is read one step before the page.
+    Keys16 ahead;
     auto load_at = [&](int at) {
-      load(token_row(p, keys_at(p, h.pages, at + 16 * wave, last), h.kvh, poison));
+      load(token_row(p, ahead, h.kvh, poison));
+      ahead = keys_at(p, h.pages, at + kMx4WideKeys + 16 * wave, last);
     };
     // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
     v4u qf[RT][NB][QP];
@@ -363,7 +384,10 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
       index[rt] = h.i0 + min(tok, h.tokens - 1);
       fetch_query<T, DIM>(p, h.seq.start + index[rt], in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q[rt]);
     }
-    if (begin < end) load_at(begin);
+    if (begin < end) {
+      ahead = keys_at(p, h.pages, begin + 16 * wave, last);
+      load_at(begin);
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       undo[rt] = scale == 0.f ? 1.f : fabsf(scale);
@@ -467,7 +491,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
             float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = s[rt][8 * g + k];
-            split8<PP>(w, parts[rt]);
+            cut8<PP>(w, parts[rt]);
           }
         };
         static_for<0, kAhead>(fetch);
@@ -581,9 +605,435 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
   });
 }
 
+// ---------------------------------------------------------------- very many rows
+
+// Scores to the exponents of their weights, against the row's kept maximum, which is
+// raised where one passes it by kMaxSlack (as in settle; looked for in the exponents,
+// which the scores become anyway).  What grows with the weights, v4f sums, is scaled down.
+template <int NRT, int NK, int NSUMS>
+__device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float *m, v4f (*sums)[NSUMS]) {
+  float from[NRT], top[NRT];
+  bool above = false;
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    from[rt] = base_of(m[rt]);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from[rt]);
+    top[rt] = s[rt][0];
+#pragma unroll
+    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
+    above |= top[rt] > (m[rt] == -INFINITY ? -INFINITY : kMaxSlack);  // the first key that is seen, too
+  }
+  if (__ballot(above) != 0) {
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
+      const float to = fmaxf(m[rt], from[rt] + row_max<1>(top[rt])), down = base_of(to) - from[rt];
+      const float f = __builtin_amdgcn_exp2f(m[rt] - base_of(to));
+      m[rt] = to;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) s[rt][k] -= down;
+#pragma unroll
+      for (int n = 0; n < NSUMS; ++n) sums[rt][n] *= f;
+    }
+  }
+}
+
+// The same for items of up to 256 rows, by eight waves of 32 that share the keys' codes.
+// Matrix and vector instructions of two waves overlap on a SIMD only where one wave is
+// at the first while the other is at the second; left to themselves, the two waves of a
+// SIMD do the same at the same time.  So the waves work in two groups of four, one on each
+// SIMD, half a step apart: between two barriers one group multiplies (the values of
+// its last 64 keys, the scores of the next) while the other makes its scores weights and
+// converts codes, keys in the first group, values in the second.
+//   slot 2 t:      first group PV(t - 1), S(t)       second group weights(t - 1), V(t) to LDS
+//   slot 2 t + 1:  first group weights(t), K(t + 1)  second group PV(t - 1), S(t)
+// Two buffers of each are enough: K(t + 1) replaces K(t - 1), last read in slot 2 t - 1, V(t)
+// replaces V(t - 2), last read there too.
+template <int DIM>
+struct Mx4DeepLds {
+  static constexpr int NB = DIM / 32;
+  v4u k[2][4][NB][64];        // 16-key tile, block, lane
+  v2u v[2][2][NB][2][64][2];  // 32-key group, block, channel of the pair, lane, half
+  uint32_t gone[2][4];        // as in the kernel above
+  uint32_t vs[2][4][4][NB];
+};
+
+template <RowType T, int DIM>
+__global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
+  typedef typename AttnElem<T>::type E;
+  constexpr int NB = DIM / 32, QP = kMx4QParts<T>, PP = AttnElem<T>::kPParts;
+  constexpr int KS = (NB + 3) / 4;
+  constexpr int ROWS = kMx4DeepRows, RT = ROWS / 128, RING = kAhead + 1;
+  __shared__ Mx4DeepLds<DIM> lds;
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = wave >> 2, quarter = wave & 3;  // of the keys of a step
+  const int lane = tid & 63, row = lane & 15, c = lane >> 4;
+  const float scale = p.alpha * 1.4426950408889634f;
+  const float undo = scale == 0.f ? 1.f : fabsf(scale);
+  const v4u ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+
+  // 16 keys of a step, on their way to LDS: keys in the first group, values in the second.
+  const uint8_t *codes = reinterpret_cast<const uint8_t *>(group == 0 ? p.c.K : p.c.V);
+  const uint8_t *scales = reinterpret_cast<const uint8_t *>(group == 0 ? p.c.KS : p.c.VS);
+  uint32_t cw[NB], sw[NB];
+  float poison = 0.f;
+  auto load = [&](int64_t base) {
+    const __amdgpu_buffer_rsrc_t cs = buffer_of(codes + base * (DIM / 2), 8 * DIM), ss = buffer_of(scales + base * NB, 16 * NB);
+    if (group == 0) {
+      load_words<NB>(cs, row * (DIM / 2) + c * (4 * NB), cw);
+      uint32_t s[KS];
+      load_bytes<NB>(ss, row * NB, s);
+#pragma unroll
+      for (int w = 0; w < KS; ++w) sw[w] = s[w];
+    } else {
+      load_words<NB>(cs, c * (2 * DIM) + row * (4 * NB), cw);
+      load_words<NB>(ss, c * (4 * NB), sw);
+    }
+  };
+  auto lay_keys = [&](int buf) {
+    const uint32_t lost = poison == 0.f ? 0u : ~0u;
+#pragma unroll
+    for (int w = 0; w < KS; ++w) sw[w] |= lost;
+    static_for<0, NB>([&](auto b_) {
+      constexpr int b = decltype(b_)::value;
+      v4u x;
+      static_for<0, 4>([&](auto j_) {
+        constexpr int j = decltype(j_)::value, e = j * NB + b;
+        x[j] = pair_bf16<e % 4, b % 4>(cw[e / 4], sw[b / 4]);
+      });
+      lds.k[buf][quarter][b][lane] = x;
+    });
+  };
+  auto lay_values = [&](int buf) {
+    const uint32_t lost = poison == 0.f ? 0u : ~0u;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int w = 0; w < NB; ++w) {
+      sw[w] |= lost;
+      bad |= no_numbers(sw[w]);
+    }
+    const bool any = __ballot(bad != 0) != 0;
+    if (any) {
+#pragma unroll
+      for (int w = 0; w < NB; ++w) {
+        if (row == 0) lds.vs[buf][quarter][c][w] = sw[w];
+        sw[w] &= ~((no_numbers(sw[w]) >> 7) * 0xffu);
+      }
+    }
+    if (lane == 0) lds.gone[buf][quarter] = any;
+    static_for<0, NB>([&](auto b_) {
+      constexpr int b = decltype(b_)::value;
+      uint32_t u[4];
+      static_for<0, 4>([&](auto k_) {
+        constexpr int e = decltype(k_)::value * NB + b;
+        u[decltype(k_)::value] = pair_bf16<e % 4, e % 4>(cw[e / 4], sw[e / 4]);
+      });
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t sel = i ? 0x07060302u : 0x05040100u;
+        lds.v[buf][quarter / 2][b][i][lane][quarter % 2] =
+            v2u{__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel)};
+      }
+    });
+  };
+
+  walk_shares<DIM>(p, ROWS, tid, [&](const Share &h) {
+    const int last = h.keys - 1;
+    const int begin = h.k0 << h.shift;
+    const int end = h.seq.bad ? begin : min(h.k1 << h.shift, h.keys);
+    const int steps = (end - begin + kMx4WideKeys - 1) / kMx4WideKeys;
+    // A page's number is read one step before the page.
+    auto find_step = [&](int t) { return keys_at(p, h.pages, begin + t * kMx4WideKeys + 16 * quarter, last); };
+    Keys16 ahead;
+    int64_t place;
+    float place_poison;
+    auto place_step = [&](int t) {
+      place = token_row(p, ahead, h.kvh, place_poison);
+      ahead = find_step(t + 1);
+    };
+    auto load_placed = [&]() {
+      load(place);
+      poison = place_poison;
+    };
+    if (steps > 0) {
+      ahead = find_step(0);
+      place_step(0);
+      load_placed();
+      place_step(1);
+    }
+    // Row tile rt of this wave: rows 16 (8 rt + wave) .. of the item.
+    v4u qf[RT][NB][QP];
+    // Sums over a row tile: of block b's channels at 2 b, 2 b + 1, of the weights at 2 NB.
+    v4f acc[RT][2 * NB + 1];
+    float m[RT];
+    {
+      QueryRow<T, DIM> q[RT];
+      bool in[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int rho = 16 * (8 * rt + wave) + row;
+        const int tok = rho / h.sub_heads;
+        in[rt] = rho < h.rows;
+        fetch_query<T, DIM>(p, h.seq.start + h.i0 + min(tok, h.tokens - 1), in[rt] ? h.head0 + rho - tok * h.sub_heads : h.head0, c, q[rt]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        cut_bf16<T, DIM>(q[rt], in[rt], scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f, qf[rt]);
+        m[rt] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n <= 2 * NB; ++n) acc[rt][n] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    const int tiles = (h.rows + 15) / 16;
+    const int mine = tiles <= wave ? 0 : (tiles - wave + 7) / 8;  // row tiles this wave has
+
+    // What the row of tile rt sees of the 64 keys at `at`, shifted: bit 16 kt + i is this lane's key i of tile kt.
+    auto seen = [&](int rt, int at) -> uint64_t {
+      if (at + kMx4WideKeys <= h.all) return ~0ull;
+      const int i = h.i0 + min((16 * (8 * rt + wave) + row) / h.sub_heads, h.tokens - 1);
+      const int64_t t = h.seq.start + i;
+      uint64_t x = seen_bits(p, at, h.context, h.seq.length, i, t);
+      if (at + 32 < h.seq.length) x |= (uint64_t)seen_bits(p, at + 32, h.context, h.seq.length, i, t) << 32;
+      return x >> 4 * c;
+    };
+
+    auto work = [&](auto nrt_) {
+      constexpr int NRT = decltype(nrt_)::value;
+      float s[NRT > 0 ? NRT : 1][16];
+      v4u parts[NRT > 0 ? NRT : 1][2][PP];
+      v4u va[RING][2];
+      auto fetch_v = [&](auto n_, int buf) {
+        constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
+        if constexpr (n < 2 * NB)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) va[n % RING][i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
+      };
+      v4u ka[RING];
+      auto fetch_k = [&](auto n_, int buf) {
+        constexpr int n = decltype(n_)::value;
+        if constexpr (n < 4 * NB) ka[n % RING] = lds.k[buf][n % 4][n / 4][lane];
+      };
+      // The values of step t, its first operands on their way; then those of the next
+      // step's scores are (more: there is one).
+      auto values = [&](int t, auto more_) {
+        if constexpr (NRT == 0) {
+          if constexpr (decltype(more_)::value) place_step(t + 3);
+        } else {
+          const int buf = t & 1;
+          __builtin_amdgcn_s_setprio(1);
+          static_for<0, 2 * NB>([&](auto n_) {
+            constexpr int n = decltype(n_)::value, g = n / NB, b = n % NB;
+            fetch_v(std::integral_constant<int, n + kAhead>{}, buf);
+            if constexpr (decltype(more_)::value && n + 1 == 2 * NB)
+              static_for<0, kAhead>([&](auto i_) { fetch_k(i_, buf ^ 1); });
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = PP - 1; q >= 0; --q)
+#pragma unroll
+              for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[rt][2 * b + i] = mfma(va[n % RING][i], parts[rt][g][q], acc[rt][2 * b + i]);
+            if constexpr (b == 0)  // the weights' sums: times ones
+#pragma unroll
+              for (int q = PP - 1; q >= 0; --q)
+#pragma unroll
+                for (int rt = 0; rt < NRT; ++rt) acc[rt][2 * NB] = mfma(ones, parts[rt][g][q], acc[rt][2 * NB]);
+            __builtin_amdgcn_sched_barrier(0);
+            // Where the codes after the next ones lie: scalar work, in the products' shadow.
+            if constexpr (decltype(more_)::value && n == 0) place_step(t + 3);
+          });
+          // Blocks of rows that see a value scale that is no number are lost.
+          uint32_t any = 0;
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) any |= lds.gone[buf][kt];
+          if (__builtin_amdgcn_readfirstlane(any) != 0) {
+#pragma unroll
+            for (int rt = 0; rt < NRT; ++rt) {
+              const uint64_t sees = seen(rt, begin + t * kMx4WideKeys);
+              uint32_t lost = 0;
+#pragma unroll 1
+              for (int kt = 0; kt < 4; ++kt) {
+                if (lds.gone[buf][kt] == 0) continue;
+#pragma unroll 1
+                for (int e = 0; e < 4 * NB; ++e)  // key 4 c + e / NB, block e % NB
+                  if (no_numbers(lds.vs[buf][kt][c][e / 4]) >> (8 * (e % 4) + 7) & 1)
+                    lost |= (uint32_t)(sees >> (16 * kt + e / NB) & 1) << (e % NB);
+              }
+              lost |= __shfl_xor(lost, 16);
+              lost |= __shfl_xor(lost, 32);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                if (lost >> b & 1) acc[rt][2 * b] = acc[rt][2 * b + 1] = v4f{NAN, NAN, NAN, NAN};
+            }
+          }
+          __builtin_amdgcn_s_setprio(0);
+        }
+      };
+      auto scores = [&](int t) {
+        if constexpr (NRT > 0) {
+          v4f x[NRT][4];
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) x[rt][kt] = v4f{0.f, 0.f, 0.f, 0.f};
+          __builtin_amdgcn_s_setprio(1);
+          static_for<0, 4 * NB>([&](auto n_) {
+            constexpr int n = decltype(n_)::value, kt = n % 4, b = n / 4;
+            fetch_k(std::integral_constant<int, n + kAhead>{}, t & 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = QP - 1; q >= 0; --q)
+#pragma unroll
+              for (int rt = 0; rt < NRT; ++rt) x[rt][kt] = mfma(ka[n % RING], qf[rt][b][q], x[rt][kt]);
+            __builtin_amdgcn_sched_barrier(0);
+          });
+          __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s[rt][k] = x[rt][k / 4][k % 4];
+        }
+      };
+      // The scores of step t to weights and their parts.
+      auto weights = [&](int t) {
+        if constexpr (NRT > 0) {
+          const int at = begin + t * kMx4WideKeys;
+          if (at + kMx4WideKeys > h.all) {
+#pragma unroll
+            for (int rt = 0; rt < NRT; ++rt) {
+              const uint64_t sees = seen(rt, at);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (!((sees >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
+            }
+          }
+          exponents<NRT, 16, 2 * NB + 1>(s, undo, m, acc);
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = s[rt][8 * g + k];
+              cut8<PP>(w, parts[rt][g]);
+#pragma unroll
+              for (int q = 0; q < PP; ++q) pin(parts[rt][g][q]);
+            }
+          }
+        }
+      };
+      auto ready = [&](int t) {  // for values(t)
+        if constexpr (NRT > 0) static_for<0, kAhead>([&](auto n_) { fetch_v(n_, t & 1); });
+      };
+      auto first_scores = [&]() {
+        if constexpr (NRT > 0) static_for<0, kAhead>([&](auto n_) { fetch_k(n_, 0); });
+        place_step(2);
+        scores(0);
+      };
+      auto keys_on = [&](int t) {  // those of step t, and the next ones asked for
+        if (t < steps) {
+          lay_keys(t & 1);
+          if (t + 1 < steps) load_placed();
+        }
+      };
+      auto values_on = [&](int t) {
+        if (t < steps) {
+          lay_values(t & 1);
+          if (t + 1 < steps) load_placed();
+        }
+      };
+
+      // Both groups pass the same barriers.
+      if (group == 0) {
+        keys_on(0);
+        __syncthreads();
+        first_scores();
+        __syncthreads();
+        weights(0);
+        keys_on(1);
+        ready(0);
+        __syncthreads();
+        for (int t = 1; t < steps; ++t) {
+          values(t - 1, std::true_type{});
+          scores(t);
+          __syncthreads();
+          weights(t);
+          keys_on(t + 1);
+          ready(t);
+          __syncthreads();
+        }
+        values(steps - 1, std::false_type{});
+        __syncthreads();
+        __syncthreads();
+      } else {
+        __syncthreads();
+        values_on(0);
+        __syncthreads();
+        first_scores();
+        __syncthreads();
+        for (int t = 1; t < steps; ++t) {
+          weights(t - 1);
+          values_on(t);
+          ready(t - 1);
+          __syncthreads();
+          values(t - 1, std::true_type{});
+          scores(t);
+          __syncthreads();
+        }
+        weights(steps - 1);
+        ready(steps - 1);
+        __syncthreads();
+        values(steps - 1, std::false_type{});
+        __syncthreads();
+      }
+    };
+    if (steps > 0) {
+      if (mine == 2)
+        work(std::integral_constant<int, 2>{});
+      else if (mine == 1)
+        work(std::integral_constant<int, 1>{});
+      else
+        work(std::integral_constant<int, 0>{});
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rho = 16 * (8 * rt + wave) + row;
+      const float weight = acc[rt][2 * NB][0];
+      if (rho >= h.rows) continue;
+      const int tok = rho / h.sub_heads;
+      const int64_t t = h.seq.start + h.i0 + tok;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const v4f u = acc[rt][2 * b], v = acc[rt][2 * b + 1];
+        float x[8] = {u[0], v[0], u[1], v[1], u[2], v[2], u[3], v[3]};
+        const int d = 32 * b + 8 * c;
+        if (h.whole) {
+          finish_row(p, h, t, weight, x);
+          store_run<E, 8>(static_cast<E *>(p.out) + t * p.out_stride + (int64_t)(h.head0 + rho - tok * h.sub_heads) * DIM + d, x);
+        } else {
+          v4f *to = reinterpret_cast<v4f *>(h.slot + (int64_t)rho * DIM + d);
+          to[0] = v4f{x[0], x[1], x[2], x[3]};
+          to[1] = v4f{x[4], x[5], x[6], x[7]};
+        }
+      }
+      if (!h.whole && c == 0) {
+        h.slot[(int64_t)ROWS * DIM + rho] = m[rt];
+        h.slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
+      }
+    }
+  });
+}
+
 template <RowType T, int DIM, int ROWS>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
-  if constexpr (ROWS >= 64) {
+  if constexpr (ROWS == kMx4DeepRows) {
+    hipLaunchKernelGGL((mx4_deep_kernel<T, DIM>), dim3((unsigned)wgs), dim3(2 * kThreads), 0, stream, a);
+  } else if constexpr (ROWS >= 64) {
     hipLaunchKernelGGL((mx4_wide_kernel<T, DIM, ROWS / 64>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   } else {
     typedef Mx4Attn<T, DIM, ROWS / 16> A;
@@ -607,10 +1057,12 @@ hipError_t launch_rows(const AttnArgs &a, int rows, int wgs, hipStream_t stream)
   if (rows == 64) return launch_instance<T, DIM, 64>(a, wgs, stream);
   if constexpr (mx4_max_rows(T, DIM) == 128)
     if (rows == 128) return launch_instance<T, DIM, 128>(a, wgs, stream);
+  if constexpr (mx4_has_deep(T, DIM))
+    if (rows == kMx4DeepRows) return launch_instance<T, DIM, kMx4DeepRows>(a, wgs, stream);
   return hipErrorInvalidValue;
 }
 
-// rows: of an item, a power of two from 16 to 128.
+// rows: of an item, a power of two from 16 to 256.
 template <RowType T>
 hipError_t launch_attention(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
   switch (a.c.dim) {

@@ -33,8 +33,15 @@ hipError_t launch_mx4_write(const CacheRowsArgs &a, RowType type, hipStream_t st
 hipError_t launch_mx4_read(const CacheRowsArgs &a, RowType type, hipStream_t stream);
 hipError_t launch_mx4_keep(const CacheKeepArgs &a, hipStream_t stream);
 
-// Rows of an item of the kernel whose waves share keys.
+// Rows of an item of the kernels whose waves share keys: 64 or 128, as far as half of a
+// SIMD's registers hold, or 256 where all of them do.
+constexpr int kMx4DeepRows = 256;
+constexpr bool mx4_has_deep(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32); }
 constexpr int mx4_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
+// For a mean of more than 64 rows.
+constexpr int mx4_many_rows(RowType type, int dim, int64_t mean) {
+  return mean > 128 && mx4_has_deep(type, dim) ? kMx4DeepRows : mx4_max_rows(type, dim);
+}
 
 hipError_t launch_mx4_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);
 hipError_t launch_mx4_attention_bf16(const AttnArgs &a, int rows, int wgs, hipStream_t stream);

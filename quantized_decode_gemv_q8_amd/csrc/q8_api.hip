@@ -814,12 +814,13 @@ struct AttnFormat {
   const char *name;
   bool few;        // has kernels for items of 4 and 8 rows
   bool any_alpha;  // takes a scale of the scores that is not finite
-  int (*max_rows)(q8::RowType type, int dim);
+  int (*many_rows)(q8::RowType type, int dim, int64_t mean);  // of an item, for a mean of more than 64
   hipError_t (*launch[3])(const q8::AttnArgs &, int, int, hipStream_t);  // by the rows' type
 };
-const AttnFormat kQ8Attention = {"cache_attention", true, true, q8::attn_max_rows,
+const AttnFormat kQ8Attention = {"cache_attention", true, true,
+                                 [](q8::RowType type, int dim, int64_t) { return q8::attn_max_rows(type, dim); },
                                  {q8::launch_attention_f32, q8::launch_attention_bf16, q8::launch_attention_f16}};
-const AttnFormat kMx4Attention = {"mx4_attention", false, false, q8::mx4_max_rows,
+const AttnFormat kMx4Attention = {"mx4_attention", false, false, q8::mx4_many_rows,
                                   {q8::launch_mx4_attention_f32, q8::launch_mx4_attention_bf16, q8::launch_mx4_attention_f16}};
 
 // How the rows of an attention call are cut: items of up to `tile` rows
@@ -877,7 +878,7 @@ AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int gr
            : mean <= 16                            ? 16
            : mean <= q8::attn_direct_rows(dim)     ? 32
            : mean <= 64                            ? 64
-                                                   : format.max_rows(type, dim);
+                                                   : format.many_rows(type, dim, mean);
   const int tile = p.tile;
   p.subs = (int)ceil_div(group, tile);
   p.sub_heads = (int)ceil_div(group, p.subs);
@@ -897,7 +898,7 @@ AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int gr
 // What depends on the device: workgroups, as many as there are units if those
 // are fewer, and their workspace.
 void deal(AttnPlan *p, int dim, int cus) {
-  p->wgs = std::min((int64_t)cus * q8::kAttnWgsPerCu, (int64_t)p->few);
+  p->wgs = std::min((int64_t)cus * (p->tile == q8::kMx4DeepRows ? 1 : q8::kAttnWgsPerCu), (int64_t)p->few);
   if (p->split)
     p->bytes =
         ceil_div(2 * p->wgs * q8::attn_slot_floats(p->tile, dim) * 4, 256) * 256 + p->wgs * (int64_t)sizeof(q8::AttnItem);
