@@ -831,21 +831,37 @@ def _table(name, t, device):
 
 def _all_apart(written, read):
     """Refuses calls whose written tensors overlap each other or a read one."""
-    for i, (name, t) in enumerate(written):
-        a, b = _span(t)
-        for other, u in written[i + 1:] + read:
-            c, d = _span(u)
+    spans = [(*_span(t), name) for name, t in written + read]
+    edge = 0
+    for a, b, _ in sorted(spans):
+        if a < edge and a < b:
+            break
+        edge = max(edge, b)
+    else:
+        return
+    # Some do: refused unless both are only read.
+    for i, (a, b, name) in enumerate(spans[:len(written)]):
+        for c, d, other in spans[i + 1:]:
             if a < d and c < b:
                 raise ValueError(f"{name} overlaps {other}")
 
 
+#: Workspace sizes by pages and sequences.
+_PAGES_WORKSPACE = {}
+
+
 def _pages_workspace(pool, seqs, stream, device):
-    size = ctypes.c_int64(0)
-    st = load().q8_pages_workspace(pool.pages, seqs, size)
-    if st != Q8_OK:
-        raise Q8Error(st, "q8_pages_workspace")
+    need = _PAGES_WORKSPACE.get((pool.pages, seqs))
+    if need is None:
+        size = ctypes.c_int64(0)
+        st = load().q8_pages_workspace(pool.pages, seqs, size)
+        if st != Q8_OK:
+            raise Q8Error(st, "q8_pages_workspace")
+        if len(_PAGES_WORKSPACE) >= 4096:
+            _PAGES_WORKSPACE.clear()
+        need = _PAGES_WORKSPACE[pool.pages, seqs] = size.value
     # held by the caller until the call has returned, as the attention's is
-    return _empty_on(stream, (max(size.value, 16),), torch.uint8, device), size.value
+    return _empty_on(stream, (max(need, 16),), torch.uint8, device), need
 
 
 def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengths_out=None, stream=None):
@@ -1015,9 +1031,10 @@ def _rope_rows(name, t, rows, dim, dtype, device):
         raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
     if t.device != device:
         raise ValueError("all tensors must be on one device")
-    if t.dim() != 3 or t.shape[2] != dim or t.shape[0] != rows:
-        raise ValueError(f"{name} must have shape ({rows}, heads, {dim}), got {tuple(t.shape)}")
-    n, h, _ = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or shape[0] != rows:
+        raise ValueError(f"{name} must have shape ({rows}, heads, {dim}), got {tuple(shape)}")
+    n, h, _ = shape
     if n == 0 or h == 0 or t.is_contiguous():
         return h * dim
     s0, s1, s2 = t.stride()

@@ -291,18 +291,18 @@ __device__ __forceinline__ void store_run(E *to, const float (&x)[N]) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
 }
-template <int WORDS>
+template <int WORDS, int AUX = 0>
 __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int offset, uint32_t (&w)[WORDS]) {
   if constexpr (WORDS == 1) {
-    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, 0);
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, AUX);
   } else if constexpr (WORDS == 2) {
-    const v2u v = __builtin_amdgcn_raw_buffer_load_b64(rs, offset, 0, 0);
+    const v2u v = __builtin_amdgcn_raw_buffer_load_b64(rs, offset, 0, AUX);
     w[0] = v[0];
     w[1] = v[1];
   } else {
 #pragma unroll
     for (int i = 0; i < WORDS / 4; ++i) {
-      const v4u v = __builtin_amdgcn_raw_buffer_load_b128(rs, offset + 16 * i, 0, 0);
+      const v4u v = __builtin_amdgcn_raw_buffer_load_b128(rs, offset + 16 * i, 0, AUX);
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
     }
@@ -541,7 +541,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs &p, const Share &h, in
 // (loads, scores, masks, values).  WAVES: 4, or 8 where a workgroup takes all
 // keys of its items.
 template <class A, RowType T, int DIM, int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? kAttnWgsPerCu : 1) void attention_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? A::WGS : 1) void attention_kernel(AttnArgs p) {
   typedef typename A::E E;
   constexpr int NB = A::NB, RT = A::RT, PITCH = A::PITCH, STEP = kAttnTile * WAVES;
   __shared__ __attribute__((aligned(16))) float sums[WAVES][ROWS][PITCH];

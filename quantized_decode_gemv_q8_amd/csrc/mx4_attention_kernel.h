@@ -84,7 +84,13 @@ __device__ __forceinline__ void cut_bf16(const QueryRow<T, DIM> &from, bool in, 
   }
 }
 
-template <RowType T, int DIM, int RT_>
+// Cache policy of loads that are not to stay in the caches (nt).
+constexpr int kPastCaches = 2;
+
+// PAST: codes are read past the caches: they leave the Infinity Cache anyway where
+// they are larger than it (596 MB of bf16 rows' keys: 117 us, 122 through the caches; 150 MB,
+// read again and again: 41 and 39).
+template <RowType T, int DIM, int RT_, bool PAST>
 struct Mx4Attn {
   typedef typename AttnElem<T>::type E;
   static constexpr int RT = RT_;
@@ -92,6 +98,7 @@ struct Mx4Attn {
   static constexpr int QP = kMx4QParts<T>;
   static constexpr int PP = AttnElem<T>::kPParts;
   static constexpr int PACK = 1, NK = 8;          // keys of a tile per lane
+  static constexpr int WGS = RT == 1 ? mx4_direct_wgs(T, DIM) : kAttnWgsPerCu;
   static constexpr int KS = (NB + 3) / 4;         // words of a key's scales
   static constexpr int ROWS = 16 * RT;
   static constexpr int PITCH = DIM + 4;           // LDS row of sums; 16 rows then start 4 banks apart
@@ -126,7 +133,7 @@ struct Mx4Attn {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       t.lost[h] = poison[h] == 0.f ? 0u : ~0u;
-      load_words<NB>(buffer_of(K + base[h] * (DIM / 2), 8 * DIM * live), row * (DIM / 2) + c * (4 * NB), t.kw[h]);
+      load_words<NB, PAST ? kPastCaches : 0>(buffer_of(K + base[h] * (DIM / 2), 8 * DIM * live), row * (DIM / 2) + c * (4 * NB), t.kw[h]);
       load_bytes<NB>(buffer_of(S + base[h] * NB, 16 * NB * live), row * NB, t.ks[h]);
     }
   }
@@ -134,7 +141,7 @@ struct Mx4Attn {
     const uint8_t *V = reinterpret_cast<const uint8_t *>(p->c.V), *S = reinterpret_cast<const uint8_t *>(p->c.VS);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load_words<NB>(buffer_of(V + base[h] * (DIM / 2), 8 * DIM * live), c * (2 * DIM) + row * (4 * NB), t.vw[h]);
+      load_words<NB, PAST ? kPastCaches : 0>(buffer_of(V + base[h] * (DIM / 2), 8 * DIM * live), c * (2 * DIM) + row * (4 * NB), t.vw[h]);
       load_words<NB>(buffer_of(S + base[h] * NB, 16 * NB * live), c * (4 * NB), t.vs[h]);
     }
   }
@@ -249,6 +256,38 @@ struct Mx4Attn {
 
 // ---------------------------------------------------------------- many rows
 
+// Scores to the exponents of their weights, against the row's kept maximum, which is
+// raised where one passes it by kMaxSlack (as in settle; looked for in the exponents,
+// which the scores become anyway).  What grows with the weights, sums and l, is scaled down.
+template <int NRT, int NK, int NSUMS>
+__device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float *m, v4f (*sums)[NSUMS], float *l = nullptr) {
+  float from[NRT], top[NRT];
+  bool above = false;
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    from[rt] = base_of(m[rt]);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from[rt]);
+    top[rt] = s[rt][0];
+#pragma unroll
+    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
+    above |= top[rt] > (m[rt] == -INFINITY ? -INFINITY : kMaxSlack);  // the first key that is seen, too
+  }
+  if (__ballot(above) != 0) {
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
+      const float to = fmaxf(m[rt], from[rt] + row_max<1>(top[rt])), down = base_of(to) - from[rt];
+      const float f = __builtin_amdgcn_exp2f(m[rt] - base_of(to));
+      m[rt] = to;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) s[rt][k] -= down;
+#pragma unroll
+      for (int n = 0; n < NSUMS; ++n) sums[rt][n] *= f;
+      if (l != nullptr) l[rt] *= f;
+    }
+  }
+}
+
 // The same for items of more rows (trees, prompts), up to 64 * RT: all four waves
 // take the same keys.  Per step of 64 keys each wave loads 16 keys' codes, converts
 // them and lays them into LDS as the matrix operands that all waves read (16 bytes
@@ -295,6 +334,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
   const uint8_t *Kc = reinterpret_cast<const uint8_t *>(p.c.K), *Ks = reinterpret_cast<const uint8_t *>(p.c.KS);
   const uint8_t *Vc = reinterpret_cast<const uint8_t *>(p.c.V), *Vs = reinterpret_cast<const uint8_t *>(p.c.VS);
   const float scale = p.alpha * 1.4426950408889634f;
+  const float undo = scale == 0.f ? 1.f : fabsf(scale);
 
   // This wave's 16 keys of a step, on their way to LDS.
   uint32_t kw[NB], ksw[KS], vw[NB], vsw[NB];
@@ -371,8 +411,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     };
     // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
     v4u qf[RT][NB][QP];
-    v4f acc[RT][NB][2];
-    float m[RT], l[RT], undo[RT];
+    v4f acc[RT][2 * NB];
+    float m[RT], l[RT];
     int index[RT];
     bool in[RT];
     QueryRow<T, DIM> q[RT];
@@ -390,12 +430,11 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      undo[rt] = scale == 0.f ? 1.f : fabsf(scale);
       cut_bf16<T, DIM>(q[rt], in[rt], scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f, qf[rt]);
       m[rt] = -INFINITY;
       l[rt] = 0.f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[rt][b][0] = acc[rt][b][1] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < 2 * NB; ++n) acc[rt][n] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     const int tiles = (h.rows + 15) / 16;
     const int mine = tiles <= wave ? 0 : (tiles - wave + 3) / 4;  // row tiles this wave has
@@ -462,7 +501,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      settle<NRT, 16, NB, 1>(s, undo, m, l, acc);
+      exponents<NRT, 16, 2 * NB>(s, undo, m, acc, l);
       {
         constexpr int RING = kAhead + 1;
         v4u a[RING][2];
@@ -472,11 +511,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
 #pragma unroll
             for (int i = 0; i < 2; ++i) a[n % RING][i] = *reinterpret_cast<const v4u *>(&lds.v[buf][g][b][i][lane][0]);
         };
-        float from[NRT];
-#pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) from[rt] = base_of(m[rt]);
         auto weight = [&](int rt, int k) {
-          s[rt][k] = __builtin_amdgcn_exp2f(fmaf(s[rt][k], undo[rt], -from[rt]));
+          s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k]);
           l[rt] += s[rt][k];
         };
         // Sums are made here: later, the weights would have to be kept for them.
@@ -515,7 +551,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
 #pragma unroll
             for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) acc[rt][b][i] = mfma(a[n % RING][i], parts[rt][q], acc[rt][b][i]);
+              for (int i = 0; i < 2; ++i) acc[rt][2 * b + i] = mfma(a[n % RING][i], parts[rt][q], acc[rt][2 * b + i]);
           mix<2 * PP * NRT, 2>();
           if constexpr (n == NB - 1) {
             summed();
@@ -546,7 +582,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
           lost[rt] |= __shfl_xor(lost[rt], 32);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            if (lost[rt] >> b & 1) acc[rt][b][0] = acc[rt][b][1] = v4f{NAN, NAN, NAN, NAN};
+            if (lost[rt] >> b & 1) acc[rt][2 * b] = acc[rt][2 * b + 1] = v4f{NAN, NAN, NAN, NAN};
         }
       }
     };
@@ -585,7 +621,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
       const int64_t t = h.seq.start + h.i0 + tok;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const v4f u = acc[rt][b][0], v = acc[rt][b][1];
+        const v4f u = acc[rt][2 * b], v = acc[rt][2 * b + 1];
         float x[8] = {u[0], v[0], u[1], v[1], u[2], v[2], u[3], v[3]};
         const int d = 32 * b + 8 * c;
         if (h.whole) {
@@ -606,37 +642,6 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
 }
 
 // ---------------------------------------------------------------- very many rows
-
-// Scores to the exponents of their weights, against the row's kept maximum, which is
-// raised where one passes it by kMaxSlack (as in settle; looked for in the exponents,
-// which the scores become anyway).  What grows with the weights, v4f sums, is scaled down.
-template <int NRT, int NK, int NSUMS>
-__device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float *m, v4f (*sums)[NSUMS]) {
-  float from[NRT], top[NRT];
-  bool above = false;
-#pragma unroll
-  for (int rt = 0; rt < NRT; ++rt) {
-    from[rt] = base_of(m[rt]);
-#pragma unroll
-    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from[rt]);
-    top[rt] = s[rt][0];
-#pragma unroll
-    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
-    above |= top[rt] > (m[rt] == -INFINITY ? -INFINITY : kMaxSlack);  // the first key that is seen, too
-  }
-  if (__ballot(above) != 0) {
-#pragma unroll
-    for (int rt = 0; rt < NRT; ++rt) {
-      const float to = fmaxf(m[rt], from[rt] + row_max<1>(top[rt])), down = base_of(to) - from[rt];
-      const float f = __builtin_amdgcn_exp2f(m[rt] - base_of(to));
-      m[rt] = to;
-#pragma unroll
-      for (int k = 0; k < NK; ++k) s[rt][k] -= down;
-#pragma unroll
-      for (int n = 0; n < NSUMS; ++n) sums[rt][n] *= f;
-    }
-  }
-}
 
 // The same for items of up to 256 rows, by eight waves of 32 that share the keys' codes.
 // Matrix and vector instructions of two waves overlap on a SIMD only where one wave is
@@ -1029,19 +1034,25 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
   });
 }
 
+template <class A, RowType T, int DIM, int ROWS, int WAVES>
+void launch_direct(const AttnArgs &a, int wgs, hipStream_t stream) {
+  hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, WAVES>), dim3((unsigned)wgs), dim3(64 * WAVES), 0, stream, a);
+}
+
 template <RowType T, int DIM, int ROWS>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
-  if constexpr (ROWS == kMx4DeepRows) {
+  if constexpr (ROWS == kMx4DeepRows)
     hipLaunchKernelGGL((mx4_deep_kernel<T, DIM>), dim3((unsigned)wgs), dim3(2 * kThreads), 0, stream, a);
-  } else if constexpr (ROWS >= 64) {
+  else if constexpr (ROWS >= 64)
     hipLaunchKernelGGL((mx4_wide_kernel<T, DIM, ROWS / 64>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
-  } else {
-    typedef Mx4Attn<T, DIM, ROWS / 16> A;
-    if (ROWS <= 16 && a.items == nullptr)
-      hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, ROWS <= 16 ? 8 : 4>), dim3((unsigned)wgs), dim3(512), 0, stream, a);
-    else
-      hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, 4>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
-  }
+  else if constexpr (ROWS > 16)
+    launch_direct<Mx4Attn<T, DIM, ROWS / 16, false>, T, DIM, ROWS, 4>(a, wgs, stream);
+  else if (a.items == nullptr)
+    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS, 8>(a, wgs, stream);
+  else if (a.past_caches)
+    launch_direct<Mx4Attn<T, DIM, 1, true>, T, DIM, ROWS, 4>(a, wgs, stream);
+  else
+    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS, 4>(a, wgs, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
   hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((ROWS + kWaves * join_rows(DIM) - 1) / (kWaves * join_rows(DIM)), (unsigned)wgs),

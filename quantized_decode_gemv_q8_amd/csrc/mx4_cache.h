@@ -33,14 +33,25 @@ hipError_t launch_mx4_write(const CacheRowsArgs &a, RowType type, hipStream_t st
 hipError_t launch_mx4_read(const CacheRowsArgs &a, RowType type, hipStream_t stream);
 hipError_t launch_mx4_keep(const CacheKeepArgs &a, hipStream_t stream);
 
+// Workgroups per CU of the kernel for 16 rows: as many as fit its registers, where more of
+// them have more bytes in flight (32 sequences of up to 32768 keys of dim 64: bf16 74 us
+// with 4, 84 with 2; f32 81 with 3, 91 with 2; at dim 128 3 are no faster for bf16 and spill
+// for f32).
+constexpr int mx4_direct_wgs(RowType type, int dim) { return dim > 64 ? kAttnWgsPerCu : type == kRowF32 ? 3 : 4; }
+
 // Rows of an item of the kernels whose waves share keys: 64 or 128, as far as half of a
 // SIMD's registers hold, or 256 where all of them do.
 constexpr int kMx4DeepRows = 256;
 constexpr bool mx4_has_deep(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32); }
 constexpr int mx4_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
-// For a mean of more than 64 rows.
+// For a mean of more than 64 rows.  At 128 rows of dim 128 the two are alike (f16 78 and 77
+// us over 8 x 8192 keys, bf16 70 and 74), below it items of 128 are faster (68 rows 70 and 75).
 constexpr int mx4_many_rows(RowType type, int dim, int64_t mean) {
   return mean > 128 && mx4_has_deep(type, dim) ? kMx4DeepRows : mx4_max_rows(type, dim);
+}
+
+constexpr int mx4_wgs(RowType type, int dim, int tile) {
+  return tile == kMx4DeepRows ? 1 : tile <= 16 ? mx4_direct_wgs(type, dim) : kAttnWgsPerCu;
 }
 
 hipError_t launch_mx4_attention_f32(const AttnArgs &a, int rows, int wgs, hipStream_t stream);

@@ -814,13 +814,17 @@ struct AttnFormat {
   const char *name;
   bool few;        // has kernels for items of 4 and 8 rows
   bool any_alpha;  // takes a scale of the scores that is not finite
+  double channel_bytes;  // of codes and scales, per channel of a key or value
   int (*many_rows)(q8::RowType type, int dim, int64_t mean);  // of an item, for a mean of more than 64
+  int (*per_cu)(q8::RowType type, int dim, int tile);         // workgroups
   hipError_t (*launch[3])(const q8::AttnArgs &, int, int, hipStream_t);  // by the rows' type
 };
-const AttnFormat kQ8Attention = {"cache_attention", true, true,
+constexpr double kCachesBytes = 256.0 * (1 << 20);  // the Infinity Cache
+const AttnFormat kQ8Attention = {"cache_attention", true, true, 1.125,
                                  [](q8::RowType type, int dim, int64_t) { return q8::attn_max_rows(type, dim); },
+                                 [](q8::RowType, int, int) { return q8::kAttnWgsPerCu; },
                                  {q8::launch_attention_f32, q8::launch_attention_bf16, q8::launch_attention_f16}};
-const AttnFormat kMx4Attention = {"mx4_attention", false, false, q8::mx4_many_rows,
+const AttnFormat kMx4Attention = {"mx4_attention", false, false, 17. / 32, q8::mx4_many_rows, q8::mx4_wgs,
                                   {q8::launch_mx4_attention_f32, q8::launch_mx4_attention_bf16, q8::launch_mx4_attention_f16}};
 
 // How the rows of an attention call are cut: items of up to `tile` rows
@@ -832,6 +836,7 @@ struct AttnPlan {
   double most_units;   // at least as many as the units of all items, whatever the offsets
   double few;          // the same for ascending offsets, without the items' cost, up to kIndexLimit
   bool split;          // an item may have several units
+  int per_cu;          // workgroups
   int64_t wgs, bytes;  // workgroups; workspace
 };
 // The work list is numbered in 64 bits, and products with the workgroups must fit them.
@@ -885,6 +890,7 @@ AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int gr
   p.subs = (int)ceil_div(group, p.sub_heads);  // no empty sub-group
   p.tile_tokens = tile / p.sub_heads;
   p.split = max_tokens > kAttnWholeTokens || tile > 16;
+  p.per_cu = format.per_cu(type, dim, tile);
   p.unit_shift = __builtin_ctz((unsigned)(p.split ? q8::kAttnStep : kAttnWholeTokens));
   const int64_t units = p.split && max_tokens > 0 ? ceil_div(max_tokens, q8::kAttnStep) : 1;
   p.item_cost = p.split && tile < 64 ? kAttnItemCost : 0;
@@ -898,7 +904,7 @@ AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int gr
 // What depends on the device: workgroups, as many as there are units if those
 // are fewer, and their workspace.
 void deal(AttnPlan *p, int dim, int cus) {
-  p->wgs = std::min((int64_t)cus * (p->tile == q8::kMx4DeepRows ? 1 : q8::kAttnWgsPerCu), (int64_t)p->few);
+  p->wgs = std::min((int64_t)cus * p->per_cu, (int64_t)p->few);
   if (p->split)
     p->bytes =
         ceil_div(2 * p->wgs * q8::attn_slot_floats(p->tile, dim) * 4, 256) * 256 + p->wgs * (int64_t)sizeof(q8::AttnItem);
@@ -991,6 +997,9 @@ q8_status attention_impl(const AttnFormat &format, const C *cache, const void *q
   a.unit_shift = pl.unit_shift;
   a.half_rows = pl.tile == 128 ? 64 : 0;  // rows of one of the two row tiles a wave has
   a.item_cost = pl.item_cost;
+  // An upper bound: the lengths are on the device.
+  const double tokens = std::min((double)a.s.seqs * (double)a.s.max_tokens, (double)cache->pages * cache->page_size);
+  a.past_caches = tokens * a.c.heads * a.c.dim * 2 * format.channel_bytes > kCachesBytes;
   a.few_units = pl.most_units < (double)kIndexLimit;
   if (log_debug())
     log_line("%s rows=%lld heads=%d/%d dim=%d seqs=%lld%s: %d-row items, %lld workgroups", format.name, (long long)rows,

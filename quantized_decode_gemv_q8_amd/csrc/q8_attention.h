@@ -39,6 +39,7 @@ struct AttnArgs {
   int half_rows;     // items of at most this many rows have units of twice the keys (0: none)
   int item_cost;     // units that an item is charged besides its keys
   int few_units;     // the units of all items are sure to stay below 2^31
+  int past_caches;   // the sequences may hold more than the caches do
   float *partial;    // 2 * gridDim.x slots of attn_slot_floats(rows, dim); null as items
   AttnItem *items;   // gridDim.x; null where every item is one unit
 };

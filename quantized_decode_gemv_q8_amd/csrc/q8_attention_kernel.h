@@ -121,6 +121,7 @@ struct Attn {
   static constexpr int QP = AttnElem<T>::kQParts;
   static constexpr int PP = AttnElem<T>::kPParts;
   static constexpr int PACK = 1, NK = 8;          // keys of a tile per lane
+  static constexpr int WGS = kAttnWgsPerCu;
   static constexpr int KW = DIM / 16;             // words of a lane's quarter row of K
   static constexpr int VW = DIM / 64;             // words of a lane's pairs of V
   static constexpr int SW = (4 * NB + 15) / 16;   // scale words per lane for 4 keys
@@ -312,6 +313,7 @@ template <RowType T, int DIM, int PACK_>
 struct AttnFew {
   typedef typename AttnElem<T>::type E;
   static constexpr int RT = 1, PACK = PACK_, NK = 8 / PACK;
+  static constexpr int WGS = kAttnWgsPerCu;
   static constexpr int NB = DIM / 32;
   static constexpr int QP = AttnElem<T>::kQParts;
   static constexpr int PP = AttnElem<T>::kPParts;
