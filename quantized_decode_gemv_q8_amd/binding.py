@@ -791,10 +791,13 @@ def q8_mx4_attention(q, cache, table, lengths, offsets, tree=None, alpha=None, o
 
 def _ints(device, **named):
     """Checks named i32 device tensors, given with their shapes: (tensor, shape)."""
+    index = device.index
     for name, (t, shape) in named.items():
+        if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and t.get_device() == index \
+                and t.is_cuda and t.is_contiguous():
+            continue
         _check_tensor(name, t, torch.int32, shape)
-        if t.device != device:
-            raise ValueError("all tensors must be on one device")
+        raise ValueError("all tensors must be on one device")
 
 
 def _pool(refs, page_size, stream):
@@ -814,14 +817,16 @@ def _table(name, t, device):
     """The descriptor of a page table, whose rows may be apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.device != device:
+    if t.get_device() != device.index and t.device != device:
         raise ValueError("all tensors must be on one device")
     if t.dim() != 2:
         raise ValueError(f"{name} must be rank 2, got {t.dim()} dimensions")
     n, pages = t.shape
-    if t.numel() and not t.is_contiguous() and pages > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return _TableStruct(t.data_ptr(), n, pages, pages)
+    if pages > 1 and n and t.stride(1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     stride = t.stride(0) if n > 1 else pages
     if stride < pages:
@@ -877,16 +882,20 @@ def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengt
     if not isinstance(parent, torch.Tensor) or parent.dim() != 1:
         raise TypeError("parent must be a torch.Tensor of rank 1")
     n = parent.shape[0]
+    written = [("refs", refs)]      # what is new overlaps nothing
     if table_out is None:
         table_out = _empty_on(stream, (n, table.shape[1]), torch.int32, device)
+    else:
+        written.append(("table_out", table_out))
     if lengths_out is None:
         lengths_out = _empty_on(stream, (n,), torch.int32, device)
+    else:
+        written.append(("lengths_out", lengths_out))
     to = _table("table_out", table_out, device)
     if table_out.shape[0] != n:
         raise ValueError(f"{n} parents need {n} rows of table_out, got {table_out.shape[0]}")
     _ints(device, lengths=(lengths, (table.shape[0],)), parent=(parent, (n,)), lengths_out=(lengths_out, (n,)))
-    _all_apart([("table_out", table_out), ("lengths_out", lengths_out), ("refs", refs)],
-               [("table", table), ("lengths", lengths), ("parent", parent)])
+    _all_apart(written, [("table", table), ("lengths", lengths), ("parent", parent)])
     _call(refs, stream, "q8_pages_fork", load().q8_pages_fork, pool, source, lengths.data_ptr(), parent.data_ptr(), to,
           lengths_out.data_ptr())
     return table_out, lengths_out
@@ -905,13 +914,17 @@ def q8_pages_resize(refs, table, before, after, page_size, moves=None, missing=N
     device = refs.device
     rows = _table("table", table, device)
     n = table.shape[0]
+    written = [("refs", refs), ("table", table)]
     if moves is None:
         moves = _empty_on(stream, (n, 2), torch.int32, device)
+    else:
+        written.append(("moves", moves))
     if missing is None:
         missing = _empty_on(stream, (n,), torch.int32, device)
+    else:
+        written.append(("missing", missing))
     _ints(device, before=(before, (n,)), after=(after, (n,)), moves=(moves, (n, 2)), missing=(missing, (n,)))
-    _all_apart([("refs", refs), ("table", table), ("moves", moves), ("missing", missing)],
-               [("before", before), ("after", after)])
+    _all_apart(written, [("before", before), ("after", after)])
     work, need = _pages_workspace(pool, n, stream, device)
     _call(refs, stream, "q8_pages_resize", load().q8_pages_resize, pool, rows, before.data_ptr(), after.data_ptr(),
           moves.data_ptr(), missing.data_ptr(), work.data_ptr(), need)
@@ -928,6 +941,8 @@ def q8_pages_compact(refs, table, lengths, page_size, refs_out=None, table_out=N
     device = refs.device
     source = _table("table", table, device)
     pages, n = refs.shape[0], table.shape[0]
+    written = [(name, t) for name, t in (("refs_out", refs_out), ("table_out", table_out), ("moves", moves), ("used", used))
+               if t is not None]
     new = lambda t, *shape: _empty_on(stream, shape, torch.int32, device) if t is None else t  # noqa: E731
     refs_out, table_out = new(refs_out, pages), new(table_out, *table.shape)
     moves, used = new(moves, pages // 2, 2), new(used, 1)
@@ -935,8 +950,8 @@ def q8_pages_compact(refs, table, lengths, page_size, refs_out=None, table_out=N
     if table_out.shape != table.shape:
         raise ValueError(f"table_out must have shape {tuple(table.shape)}, got {tuple(table_out.shape)}")
     _ints(device, lengths=(lengths, (n,)), refs_out=(refs_out, (pages,)), moves=(moves, (pages // 2, 2)), used=(used, (1,)))
-    _all_apart([("refs_out", refs_out), ("table_out", table_out), ("moves", moves), ("used", used)],
-               [("refs", refs), ("table", table), ("lengths", lengths)])
+    if written:
+        _all_apart(written, [("refs", refs), ("table", table), ("lengths", lengths)])
     work, need = _pages_workspace(pool, n, stream, device)
     _call(refs, stream, "q8_pages_compact", load().q8_pages_compact, pool, source, lengths.data_ptr(), refs_out.data_ptr(),
           to, moves.data_ptr(), used.data_ptr(), work.data_ptr(), need)
@@ -1029,7 +1044,7 @@ def _rope_rows(name, t, rows, dim, dtype, device):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
-    if t.device != device:
+    if t.get_device() != device.index and t.device != device:
         raise ValueError("all tensors must be on one device")
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or shape[0] != rows:

@@ -106,16 +106,20 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs a) {
     const int held = pages_of(length, a.page_shift);
     int *to = a.to.table + i * a.to.stride;
     const int *from = a.from.table + (int64_t)(held > 0 ? parent : 0) * a.from.stride;
-    for (int c = lane; c < a.to.max_pages; c += 64) {
-      int page = -1;
-      if (c < held) {
-        page = from[c];
-        if (is_page(page, a.pages))
-          atomicAdd(a.refs + page, 1);
+    constexpr int kAtOnce = 4;
+    for (int c0 = lane; c0 < a.to.max_pages; c0 += 64 * kAtOnce) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) page[k] = c0 + 64 * k < held ? from[c0 + 64 * k] : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int c = c0 + 64 * k;
+        if (is_page(page[k], a.pages))
+          atomicAdd(a.refs + page[k], 1);
         else
-          page = -1;
+          page[k] = -1;
+        if (c < a.to.max_pages) to[c] = page[k];
       }
-      to[c] = page;
     }
     if (lane == 0) a.lengths_out[i] = length;
   }
@@ -371,27 +375,36 @@ __device__ void compact_count(const CompactArgs &a) {
 // Phase 1: with U used pages, the r-th used page from U on goes to the r-th free
 // page below U.  Both sides of the moves, and every page's rank r among its kind.
 __device__ void compact_rank(const CompactArgs &a) {
-  const Tiles tiles = share(pages_tiles(a.pages));
-  const int64_t U = block_total(a.w.counts, pages_tiles(a.pages));
+  const int64_t all_tiles = pages_tiles(a.pages);
+  const Tiles tiles = share(all_tiles);
+  // All used pages, and those before this workgroup's tiles.
+  int64_t U, before;
+  {
+    int64_t sum = 0, some = 0;
+    for (int64_t i = threadIdx.x; i < all_tiles; i += kBig) {
+      const int n = a.w.counts[i];
+      sum += n;
+      if (i < tiles.begin) some += n;
+    }
+    block_sum_before(sum, &U);
+    block_sum_before(some, &before);
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.used = (int)U;
-  int64_t before = block_total(a.w.counts, tiles.begin);  // used pages before the tile
   // Used pages below U: those that the ranks from U on do not count.
-  __shared__ int in_tile;
-  int64_t below = 0;
+  int64_t below;
   {
     const int64_t tu = U / kPagesTile;  // the tile that U lies in, or the one past the last
-    below = block_total(a.w.counts, tu);
-    if (tu < pages_tiles(a.pages)) {
+    int64_t some = 0;
+    for (int64_t i = threadIdx.x; i < tu; i += kBig) some += a.w.counts[i];
+    if (tu < all_tiles) {
       int64_t first;
-      int in, all;
+      int in;
       int used = used_bits(a.refs, a.pages, tu, &first, &in);
       for (int k = 0; k < 4; ++k)
         if (first + k >= U) used &= ~(1 << k);
-      block_sum_before((int)__popc(used), &all);
-      if (threadIdx.x == 0) in_tile = all;
-      __syncthreads();
-      below += in_tile;
+      some += __popc(used);
     }
+    block_sum_before(some, &below);
   }
   for (int64_t t = tiles.begin; t < tiles.end; ++t) {
     int64_t first;
@@ -434,21 +447,17 @@ __device__ void compact_apply(const CompactArgs &a) {
     }
     a.refs_out[p] = r;
   }
-  const int lane = threadIdx.x & 63;
-  for (int64_t b = me >> 6; b < a.to.seqs; b += threads >> 6) {
+  // A thread per entry of the table: its page, then that page's count and rank, then
+  // its place, are three loads that wait for each other.
+  const int64_t columns = a.to.max_pages, entries = columns * a.to.seqs;
+  for (int64_t i = me; i < entries; i += threads) {
+    const int64_t b = i / columns, c = i - b * columns;
     const int length = a.lengths[b];
-    const int held = fits(length, a.from) ? pages_of(length, a.page_shift) : 0;
-    for (int c = lane; c < a.to.max_pages; c += 64) {
-      int page = -1;
-      if (c < held) {
-        page = a.from.table[b * a.from.stride + c];
-        if (!is_page(page, a.pages) || a.refs[page] <= 0)
-          page = -1;
-        else if (page >= U)
-          page = a.moves[2 * (int64_t)a.w.list[page] + 1];
-      }
-      a.to.table[b * a.to.stride + c] = page;
-    }
+    const int from = a.from.table[b * a.from.stride + c];
+    int page = -1;
+    if (fits(length, a.from) && c < pages_of(length, a.page_shift) && is_page(from, a.pages) && a.refs[from] > 0)
+      page = from < U ? from : a.moves[2 * (int64_t)a.w.list[from] + 1];
+    a.to.table[b * a.to.stride + c] = page;
   }
 }
 
