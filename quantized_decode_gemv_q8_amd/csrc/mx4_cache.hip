@@ -10,8 +10,12 @@
 // of two, so every step but the rounding to a code is exact.
 //
 // All three are bound by memory: they touch each byte once.  A row of dim
-// channels belongs to 16 lanes; lane j holds channel pair j of every block, whose
-// two codes share a byte.
+// channels belongs to 16 lanes.  In the cache a lane's bytes are channel pair j of
+// every block, which keep and read take as they are; write takes dim / 16 channels of one
+// block per lane, so that a block's maximum needs few exchanges and its scale is found
+// few times, and swaps the codes' bytes between lanes at the end (19600 tokens of prompts
+// of 8 heads of 128, bf16, written and read: 46 us, 49 from pairs; f32 rows are as fast
+// either way).
 #include <algorithm>
 
 #include "cache_rows.h"
@@ -47,37 +51,109 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return (uint32_t)min(max(e, kMx4Least), kMx4Most);
 }
 
-constexpr int kRowsPerGroup = 2;
-constexpr int kRowsPerWave = kRowsPerGroup * 4;
+// (head, K or V) rows per 16-lane group.  19600 tokens of prompts of 8 heads are written
+// and read back in 49.8, 45.7 and 44.9 us with one, two and four (bf16, dim 128), 43, 34.9
+// and 31.9 (dim 64), 94, 96.8 and 87.9 (dim 256); f32 rows in 88, 91 and 82 (dim 128), but
+// 136 and 139.5 with two and four at dim 256.  A step of 1536 drafts takes 17.1 and 17.6.
+template <RowType T, int DIM>
+constexpr int kRowsPerGroup = T == kRowF32 && DIM == 256 ? 2 : 4;
 
-// A wave takes one token's rows r = kRowsPerWave * blockIdx.y ..: row r is
+template <typename E, int N>
+struct __attribute__((packed, aligned(sizeof(E)))) Run {
+  E x[N];
+};
+
+// The value of lane l ^ D, for D = 1, 2, 4 and 8.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+  if constexpr (D == 4) return across<1>(across<2>(__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true)));  // l ^ 7 first
+  constexpr int ctrl = D == 1 ? 0xb1 : D == 2 ? 0x4e : 0x128;
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xf, 0xf, true);
+}
+
+// Which lanes of a row's 16 are block `block` of it, and which part of that.
+template <int NB>
+struct Piece {
+  int block, part;
+  __device__ __forceinline__ explicit Piece(int j) {
+    if constexpr (NB == 8) {
+      block = (j & 3) | (j >> 1 & 4);
+      part = j >> 2 & 1;
+    } else {
+      block = j & (NB - 1);
+      part = j / NB;
+    }
+  }
+};
+
+// Largest of a block's 16 / NB lanes.
+template <int NB>
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  if constexpr (NB == 2) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xf, 0xf, true));  // row_ror:2, 4, 8
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, true));
+    m = max(m, across<8>(m));
+  } else if constexpr (NB == 4) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, true));
+    m = max(m, across<8>(m));
+  } else {
+    m = max(m, across<4>(m));
+  }
+  return m;
+}
+
+// Byte i of the lane of block b, to byte b of that block's i-th lane: for every part
+// of the row, NB lanes that hold NB bytes each.
+template <int NB>
+__device__ __forceinline__ void turn_bytes(uint32_t (&w)[(NB + 3) / 4], int block) {
+  if constexpr (NB == 8) {
+    const bool high = block & 4;
+    const uint32_t other = across<8>(high ? w[0] : w[1]);
+    if (high)
+      w[0] = other;
+    else
+      w[1] = other;
+  }
+#pragma unroll
+  for (int k = 0; k < (NB + 3) / 4; ++k) {
+    w[k] = __builtin_amdgcn_perm(across<1>(w[k]), w[k], block & 1 ? 0x03070105u : 0x06020400u);
+    if constexpr (NB > 2) w[k] = __builtin_amdgcn_perm(across<2>(w[k]), w[k], block & 2 ? 0x03020706u : 0x05040100u);
+  }
+}
+
+// A wave takes one token's rows r = 4 * kRowsPerGroup * blockIdx.y ..: row r is
 // head r / 2, K for even r and V for odd.
 template <RowType T, int DIM>
 __global__ __launch_bounds__(kThreads) void mx4_write_kernel(CacheRowsArgs p) {
   typedef typename Elem<T>::type E;
   typedef typename PairBytes<DIM>::type Word;
-  constexpr int NB = DIM / 32;
+  constexpr int ROWS = kRowsPerGroup<T, DIM>;
+  constexpr int NB = DIM / 32, N = 2 * NB, NW = (NB + 3) / 4;  // channels of a lane; words of its codes
+  // A lane's channels come in runs of at most 16 bytes, and those of a block's lanes lie
+  // side by side (f32 rows of dim 256, written and read: 135.6 us, 136.7 with a lane's runs
+  // side by side).
+  constexpr int RUN = N * sizeof(E) <= 16 ? N : 16 / (int)sizeof(E), RUNS = N / RUN;
   const int lane = threadIdx.x & 63;
   const uint32_t row = __builtin_amdgcn_readfirstlane(p.row0 + blockIdx.x * kWaves + (threadIdx.x >> 6));
   if (row >= (uint32_t)p.s.rows) return;  // unsigned: the last workgroup may pass 2^31
   const int t = (int)row;
   const int group = lane >> 4, j = lane & 15;
+  const Piece<NB> piece(j);
   const int nrows = 2 * p.c.heads;
-  const int r0 = blockIdx.y * kRowsPerWave + group;
+  const int r0 = blockIdx.y * 4 * ROWS + group;
+  // The pair whose codes the lane holds in the end: the block-th of its part's.
+  const int pair = 16 / RUNS * (piece.block / (RUN / 2)) + RUN / 2 * piece.part + piece.block % (RUN / 2);
 
-  float x[kRowsPerGroup][NB][2];
+  Run<E, RUN> x[ROWS][RUNS];
 #pragma unroll
-  for (int q = 0; q < kRowsPerGroup; ++q) {
+  for (int q = 0; q < ROWS; ++q) {
     const int r = r0 + 4 * q;
     const int rr = r < nrows ? r : 0;
     const E *from = static_cast<const E *>((rr & 1) ? p.v : p.k) + (int64_t)t * ((rr & 1) ? p.v_stride : p.k_stride) +
                    (int64_t)(rr >> 1) * DIM;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const Pair<E> v = *reinterpret_cast<const Pair<E> *>(from + 32 * b + 2 * j);
-      x[q][b][0] = Elem<T>::to_float(v.x);
-      x[q][b][1] = Elem<T>::to_float(v.y);
-    }
+    for (int k = 0; k < RUNS; ++k)
+      x[q][k] = *reinterpret_cast<const Run<E, RUN> *>(from + 32 * piece.block + 32 / RUNS * k + RUN * piece.part);
   }
   const Place at = find_row(p.s, t, lane);
   if (!at.found || at.seq.bad) return;
@@ -85,25 +161,50 @@ __global__ __launch_bounds__(kThreads) void mx4_write_kernel(CacheRowsArgs p) {
   if (base < 0) return;
   const int inside = (int)(base & ((1 << p.c.page_shift) - 1));
 #pragma unroll
-  for (int q = 0; q < kRowsPerGroup; ++q) {
+  for (int q = 0; q < ROWS; ++q) {
     const int r = r0 + 4 * q;
-    Word codes = 0, scales = 0;
+    float y[N];
+    uint32_t top = 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float x0 = x[q][b][0], x1 = x[q][b][1];
-      const uint32_t top = group_max(max(__float_as_uint(x0) & 0x7fffffffu, __float_as_uint(x1) & 0x7fffffffu));
-      const uint32_t e = scale_byte(top);
-      // Only the scale's exponent counts; values past 6 s become 6 s.
-      const uint32_t pair =
-          __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x0, x1, __uint_as_float(e << 23), 0) & 0xffu;
-      codes |= (Word)(e == 255 ? 0u : pair) << (8 * b);
-      scales |= (Word)e << (8 * b);
+    for (int i = 0; i < N; ++i) {
+      y[i] = Elem<T>::to_float(x[q][i / RUN].x[i % RUN]);
+      top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
+    }
+    const uint32_t e = scale_byte(block_max<NB>(top));
+    uint32_t w[NW];
+    // Only the scale's exponent counts; values past 6 s become 6 s.
+    const float s = __uint_as_float(e << 23);
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float *z = y + 8 * k;
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, z[0], z[1], s, 0);
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], z[2], z[3], s, 1);
+      if constexpr (NB > 2) {
+        w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], z[4], z[5], s, 2);
+        w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], z[6], z[7], s, 3);
+      }
+      if (e == 255) w[k] = 0;
+    }
+    turn_bytes<NB>(w, piece.block);
+    // The scales of all blocks, in every lane of a part.
+    uint32_t es[NW];
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      es[k] = piece.block >> 2 == k ? e << (8 * (piece.block & 3)) : 0u;
+      es[k] |= across<1>(es[k]);
+      if constexpr (NB > 2) es[k] |= across<2>(es[k]);
+      if constexpr (NB > 4) es[k] |= across<8>(es[k]);
     }
     if (r < nrows) {
       const int64_t page = (base - inside) + ((int64_t)(r >> 1) << p.c.page_shift);  // its first token, of this head
       uint8_t *to = reinterpret_cast<uint8_t *>((r & 1) ? p.c.V : p.c.K) + page * (DIM / 2);
       uint8_t *st = reinterpret_cast<uint8_t *>((r & 1) ? p.c.VS : p.c.KS) + (page + inside) * NB;
-      *reinterpret_cast<Word *>(to + pair_place<DIM>(r & 1, inside, j)) = codes;
+      Word codes = (Word)w[0], scales = (Word)es[0];
+      if constexpr (NW == 2) {
+        codes |= (Word)w[1] << 32;
+        scales |= (Word)es[1] << 32;
+      }
+      *reinterpret_cast<Word *>(to + pair_place<DIM>(r & 1, inside, pair)) = codes;
       if (j == 0) *reinterpret_cast<Word *>(st) = scales;
     }
   }
@@ -124,21 +225,21 @@ template <RowType T, int DIM, bool PAST>
 __global__ __launch_bounds__(kThreads) void mx4_read_kernel(CacheRowsArgs p) {
   typedef typename Elem<T>::type E;
   typedef typename PairBytes<DIM>::type Word;
-  constexpr int NB = DIM / 32;
+  constexpr int NB = DIM / 32, ROWS = kRowsPerGroup<T, DIM>;
   const int lane = threadIdx.x & 63;
   const uint32_t row = __builtin_amdgcn_readfirstlane(p.row0 + blockIdx.x * kWaves + (threadIdx.x >> 6));
   if (row >= (uint32_t)p.s.rows) return;  // unsigned: the last workgroup may pass 2^31
   const int t = (int)row;
   const int group = lane >> 4, j = lane & 15;
   const int nrows = 2 * p.c.heads;
-  const int r0 = blockIdx.y * kRowsPerWave + group;
+  const int r0 = blockIdx.y * 4 * ROWS + group;
   const Place at = find_row(p.s, t, lane);
   if (!at.found) return;  // no sequence's row: left as it was
   int64_t base = -1;
   if (!at.seq.bad) base = token_row(p.c, p.s, at.b, at.seq.length - at.seq.n + at.index);
   const int inside = (int)(base & ((1 << p.c.page_shift) - 1));
 #pragma unroll
-  for (int q = 0; q < kRowsPerGroup; ++q) {
+  for (int q = 0; q < ROWS; ++q) {
     const int r = r0 + 4 * q;
     if (r >= nrows) continue;
     Word codes = 0, scales = (Word)~0ull;  // no such token: NaN, never a wrong value
@@ -240,17 +341,19 @@ __global__ __launch_bounds__(kThreads) void mx4_keep_kernel(CacheKeepArgs p) {
 
 template <RowType T>
 hipError_t launch_rows(const CacheRowsArgs &a, int rows, bool write, hipStream_t stream) {
-  const dim3 grid((unsigned)((rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kRowsPerWave - 1) / kRowsPerWave));
   const bool past = 2 * (int64_t)sizeof(typename Elem<T>::type) * a.s.rows * a.c.heads * a.c.dim > kPastCachesBytes;
 #define Q8_LAUNCH(DIM)                                                                                 \
-  case DIM:                                                                                            \
+  case DIM: {                                                                                          \
+    constexpr int kPerWave = 4 * kRowsPerGroup<T, DIM>;                                                \
+    const dim3 grid((unsigned)((rows + kWaves - 1) / kWaves), (unsigned)((2 * a.c.heads + kPerWave - 1) / kPerWave)); \
     if (write)                                                                                         \
       hipLaunchKernelGGL((mx4_write_kernel<T, DIM>), grid, dim3(kThreads), 0, stream, a);              \
     else if (past)                                                                                     \
       hipLaunchKernelGGL((mx4_read_kernel<T, DIM, true>), grid, dim3(kThreads), 0, stream, a);         \
     else                                                                                               \
       hipLaunchKernelGGL((mx4_read_kernel<T, DIM, false>), grid, dim3(kThreads), 0, stream, a);        \
-    return hipGetLastError();
+    return hipGetLastError();                                                                          \
+  }
   switch (a.c.dim) {
     Q8_LAUNCH(64)
     Q8_LAUNCH(128)
