@@ -66,20 +66,37 @@ __device__ __forceinline__ int64_t block_total(const X *x, int64_t n) {
   return all;
 }
 
-// The four neighbouring pages of this thread in tile t: bit k of the result is set
-// where refs[first + k] > 0; pages past the pool are left out of `in`.
-__device__ __forceinline__ int used_bits(const int *refs, int pages, int64_t t, int64_t *first, int *in) {
-  const int64_t p = t * kPagesTile + 4 * (int64_t)threadIdx.x;
-  *first = p;
-  int used = 0;
-  *in = 0;
+// The counts of a thread's four neighbouring pages in tile t.  Bit k of `in` is set where
+// the pool has page first + k, of used() where an owner has it.
+struct Quad {
+  int64_t first;
+  int in, refs[4];
+  __device__ __forceinline__ int used() const {
+    int bits = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (p + k < pages) {
-      *in |= 1 << k;
-      if (refs[p + k] > 0) used |= 1 << k;
+    for (int k = 0; k < 4; ++k) bits |= (refs[k] > 0) << k;
+    return bits & in;
+  }
+};
+__device__ __forceinline__ Quad load_quad(const int *refs, int pages, int64_t t) {
+  Quad q;
+  q.first = t * kPagesTile + 4 * (int64_t)threadIdx.x;
+  if (q.first + 4 <= pages) {
+    typedef int Four __attribute__((ext_vector_type(4), aligned(4)));
+    const Four x = *reinterpret_cast<const Four *>(refs + q.first);
+    q.in = 15;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q.refs[k] = x[k];
+  } else {
+    q.in = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool is = q.first + k < pages;
+      q.refs[k] = is ? refs[q.first + k] : 0;
+      q.in |= is << k;
     }
-  return used;
+  }
+  return q;
 }
 
 // A workgroup's share of `tiles` tiles.
@@ -142,20 +159,33 @@ __device__ __forceinline__ Change change_of(const ResizeArgs &a, int64_t b) {
   return c;
 }
 
-// Phase 0: pages past what is wanted are released, one wave per sequence.
+// Phase 0: pages past what is wanted are released.  A lane takes its sequence's first
+// ones, its wave the rest of one sequence after another (1000 sequences that take or
+// give back one page each: 5.3 us, 20 with all by waves).
+constexpr int kOwn = 4;
 __device__ void resize_release(const ResizeArgs &a) {
   const int lane = threadIdx.x & 63;
   const int64_t waves = (int64_t)gridDim.x * kBigWaves;
-  // A wave looks at up to 64 sequences at a time and takes those that shrink one by one.
+  // A wave looks at up to 64 sequences at a time.
   const int64_t each = min((a.t.seqs + waves - 1) / waves, (int64_t)64);
   for (int64_t b0 = ((int64_t)blockIdx.x * kBigWaves + (threadIdx.x >> 6)) * each; b0 < a.t.seqs; b0 += waves * each) {
     Change c{};
     if (lane < each && b0 + lane < a.t.seqs) c = change_of(a, b0 + lane);
-    uint64_t shrink = __ballot(c.want < c.held);
-    while (shrink != 0) {
-      const int s = __builtin_ctzll(shrink);
-      shrink &= shrink - 1;
-      const int held = __shfl(c.held, s), want = __shfl(c.want, s);
+    int *own = a.t.table + (c.want < c.held ? b0 + lane : 0) * a.t.stride;
+    int page[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) page[i] = c.want + i < c.held ? own[c.want + i] : -1;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (c.want + i < c.held) {
+        if (is_page(page[i], a.pages)) atomicAdd(a.refs + page[i], -1);
+        own[c.want + i] = -1;
+      }
+    uint64_t more = __ballot(c.want + kOwn < c.held);
+    while (more != 0) {
+      const int s = __builtin_ctzll(more);
+      more &= more - 1;
+      const int held = __shfl(c.held, s), want = __shfl(c.want, s) + kOwn;
       int *row = a.t.table + (b0 + s) * a.t.stride;
       for (int i = want + lane; i < held; i += 64) {
         const int page = row[i];
@@ -173,10 +203,9 @@ constexpr int64_t kReplaced = (int64_t)1 << 62;
 __device__ void resize_count(const ResizeArgs &a) {
   const Tiles tiles = share(pages_tiles(a.pages));
   for (int64_t t = tiles.begin; t < tiles.end; ++t) {
-    int64_t first;
-    int in, all;
-    const int used = used_bits(a.refs, a.pages, t, &first, &in);
-    block_sum_before((int)__popc(in & ~used), &all);
+    const Quad q = load_quad(a.refs, a.pages, t);
+    int all;
+    block_sum_before((int)__popc(q.in & ~q.used()), &all);
     if (threadIdx.x == 0) a.w.counts[t] = all;
   }
   const Tiles seqs = share(seqs_tiles(a.t.seqs));
@@ -205,20 +234,17 @@ __device__ void resize_list(const ResizeArgs &a) {
   const int64_t wanted = block_total(a.w.totals, seqs_tiles(a.t.seqs));
   int64_t rank = block_total(a.w.counts, tiles.begin);
   for (int64_t t = tiles.begin; t < tiles.end && rank < wanted; ++t) {
-    int64_t first;
-    int in, all;
-    const int used = used_bits(a.refs, a.pages, t, &first, &in);
-    int free = in & ~used;
+    const Quad q = load_quad(a.refs, a.pages, t);
+    int all, free = q.in & ~q.used();
     int64_t r = rank + block_sum_before((int)__popc(free), &all);
     for (; free != 0; free &= free - 1, ++r)
-      if (r < wanted) a.w.list[r] = (int)(first + __builtin_ctz(free));
+      if (r < wanted) a.w.list[r] = (int)(q.first + __builtin_ctz(free));
     rank += all;
   }
 }
 
 // Phase 3: a thread gives a sequence its first pages, its wave the rest.
 __device__ void resize_give(const ResizeArgs &a) {
-  constexpr int kOwn = 4;
   const Tiles seqs = share(seqs_tiles(a.t.seqs));
   if (seqs.begin >= seqs.end) return;
   const int lane = threadIdx.x & 63;
@@ -290,7 +316,7 @@ __global__ __launch_bounds__(kBig) void resize_kernel(ResizeArgs a) {
 constexpr int kSmallSeqs = kBig;
 template <bool RELEASE>
 __global__ __launch_bounds__(kBig) void resize_small_kernel(ResizeArgs a) {
-  constexpr int kOwn = 4, kListed = 4096;
+  constexpr int kListed = 4096;
   __shared__ int listed[kListed];  // the first ones; the others go through memory
   const int b = threadIdx.x, lane = b & 63;
   const bool in = b < a.t.seqs;
@@ -310,20 +336,21 @@ __global__ __launch_bounds__(kBig) void resize_small_kernel(ResizeArgs a) {
   int64_t wanted;
   const int64_t start = block_sum_before((int64_t)need, &wanted);
   int64_t found = 0;
+  Quad q;
+  if (wanted > 0) q = load_quad(a.refs, a.pages, 0);
   for (int64_t t = 0; t < pages_tiles(a.pages) && found < wanted; ++t) {
-    int64_t first;
-    int used_in, all;
-    const int used = used_bits(a.refs, a.pages, t, &first, &used_in);
-    int free = used_in & ~used;
+    const Quad next = load_quad(a.refs, a.pages, t + 1);
+    int all, free = q.in & ~q.used();
     int64_t r = found + block_sum_before((int)__popc(free), &all);
     for (; free != 0; free &= free - 1, ++r) {
-      const int page = (int)(first + __builtin_ctz(free));
+      const int page = (int)(q.first + __builtin_ctz(free));
       if (r < kListed)
         listed[r] = page;
       else if (r < wanted)
         a.w.list[r] = page;
     }
     found += all;
+    q = next;
   }
   __syncthreads();
   const bool served = start + need <= found;
@@ -364,10 +391,8 @@ __global__ __launch_bounds__(kBig) void resize_small_kernel(ResizeArgs a) {
 __device__ void compact_count(const CompactArgs &a) {
   const Tiles tiles = share(pages_tiles(a.pages));
   for (int64_t t = tiles.begin; t < tiles.end; ++t) {
-    int64_t first;
-    int in, all;
-    const int used = used_bits(a.refs, a.pages, t, &first, &in);
-    block_sum_before((int)__popc(used), &all);
+    int all;
+    block_sum_before((int)__popc(load_quad(a.refs, a.pages, t).used()), &all);
     if (threadIdx.x == 0) a.w.counts[t] = all;
   }
 }
@@ -397,24 +422,23 @@ __device__ void compact_rank(const CompactArgs &a) {
     int64_t some = 0;
     for (int64_t i = threadIdx.x; i < tu; i += kBig) some += a.w.counts[i];
     if (tu < all_tiles) {
-      int64_t first;
-      int in;
-      int used = used_bits(a.refs, a.pages, tu, &first, &in);
+      const Quad q = load_quad(a.refs, a.pages, tu);
+      int used = q.used();
       for (int k = 0; k < 4; ++k)
-        if (first + k >= U) used &= ~(1 << k);
+        if (q.first + k >= U) used &= ~(1 << k);
       some += __popc(used);
     }
     block_sum_before(some, &below);
   }
   for (int64_t t = tiles.begin; t < tiles.end; ++t) {
-    int64_t first;
-    int in, all;
-    const int used = used_bits(a.refs, a.pages, t, &first, &in);
+    const Quad q = load_quad(a.refs, a.pages, t);
+    const int used = q.used();
+    int all;
     int64_t u = before + block_sum_before((int)__popc(used), &all);  // used pages before this thread's
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (!(in >> k & 1)) continue;
-      const int64_t p = first + k;
+      if (!(q.in >> k & 1)) continue;
+      const int64_t p = q.first + k;
       const bool is = used >> k & 1;
       if (is && p >= U) {
         const int64_t r = u - below;
@@ -541,8 +565,15 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
   }
 }
 
-// Pools and tables up to these sizes are done by one workgroup.
-constexpr int64_t kOnePages = 32768, kOneEntries = 32768;
+// Up to these sizes one workgroup does all of it.
+// Resize, pages: 64 sequences that take one page each take 5 us where free pages come early,
+// 0.1 us more per 1024 pages before them (65536: 12.1), and by launches of their own 14 from
+// any pool.  Table entries: where all leave 64 x 256 take 8.4 us, 1000 x 32 25.7; with
+// the release in a launch of its own 7, but 5.5 instead of 4.0 where nothing changes.
+constexpr int64_t kResizePages = 131072, kResizeEntries = 16384;
+// Compact, pages: 2048 take 9.9 us, by three launches 11.6; 4096 13.0 and 13.4, 8192 17.7 and
+// 14.  Entries: 64 x 64 11.2 and 11.6, 128 x 128 19.4 and 11.9.
+constexpr int64_t kCompactPages = 4096, kCompactEntries = 4096;
 
 }  // namespace
 
@@ -553,9 +584,8 @@ hipError_t launch_pages_fork(const ForkArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_pages_resize(const ResizeArgs &a, int cus, hipStream_t stream) {
-  const bool small = a.pages <= kOnePages && a.t.seqs <= kSmallSeqs;
-  // Releasing many entries takes the whole device.
-  if (small && (int64_t)a.t.seqs * a.t.max_pages <= kOneEntries) {
+  const bool small = a.pages <= kResizePages && a.t.seqs <= kSmallSeqs;
+  if (small && (int64_t)a.t.seqs * a.t.max_pages <= kResizeEntries) {
     hipLaunchKernelGGL((resize_small_kernel<true>), dim3(1), dim3(kBig), 0, stream, a);
     return hipGetLastError();
   }
@@ -573,7 +603,7 @@ hipError_t launch_pages_resize(const ResizeArgs &a, int cus, hipStream_t stream)
 }
 
 hipError_t launch_pages_compact(const CompactArgs &a, int cus, hipStream_t stream) {
-  if (a.pages <= kOnePages && (int64_t)a.to.seqs * a.to.max_pages <= kOneEntries) {
+  if (a.pages <= kCompactPages && (int64_t)a.to.seqs * a.to.max_pages <= kCompactEntries) {
     hipLaunchKernelGGL((compact_kernel<-1>), dim3(1), dim3(kBig), 0, stream, a);
     return hipGetLastError();
   }

@@ -38,7 +38,10 @@ __device__ __forceinline__ void angle_of(uint64_t turns, int position, float &co
   if (quarter & 2) sine = -sine;            // quarters 2 and 3
 }
 
-// Below this many rows a workgroup takes one, from there on each of its waves.
+// A workgroup takes a row, where there are fewer than this many rows and a wave would not have
+// all heads of one in flight at once; otherwise each of its waves does.  40 heads of 128,
+// bf16: 256 rows 4.2 us, a wave each 5.5; 1024 6.1 and 6.7; 2048 10.4 and 10.2; 8192 31.9
+// and 29.2.  4 heads: 256 rows 3.5 both ways, 2048 6.0 and 3.8.
 constexpr int kFewRows = 2048;
 // Heads that a thread has in flight at a time.
 constexpr int kRopeHeads = 4;
@@ -173,7 +176,7 @@ hipError_t launch_rows(RopeArgs a, hipStream_t stream) {
 
 template <RowType T, bool INTERLEAVED, int P>
 hipError_t launch_pairs(const RopeArgs &a, hipStream_t stream) {
-  if (a.s.rows < kFewRows) return launch_rows<T, INTERLEAVED, P, kThreads>(a, stream);
+  if (a.s.rows < kFewRows && a.heads * (a.rot / 2 / P) > 64 * kRopeHeads) return launch_rows<T, INTERLEAVED, P, kThreads>(a, stream);
   return launch_rows<T, INTERLEAVED, P, 64>(a, stream);
 }
 

@@ -116,6 +116,22 @@ def test_wrong_descriptions_are_left_alone():
         check_resize(refs, table, before, after, page)
 
 
+@pytest.mark.parametrize("n_pages,takes,columns", [(9000, [4095], 5000), (9000, [4096, 3], 5000), (9000, [1, 5000, 2], 5001),
+                                                   (9000, [3000, 3000], 9000), (131072, [5, 70], 90), (131073, [5, 70], 90)])
+def test_many_pages_at_once(n_pages, takes, columns):
+    """More pages than one workgroup lists on the chip, and the borders of what one workgroup does."""
+    page = 16
+    _, refs, table = pool((9, n_pages, len(takes)), n_pages, [0] * len(takes), page, columns)
+    rng = np.random.default_rng((10, n_pages))
+    for p in rng.choice(n_pages, n_pages // 3, replace=False):
+        refs[p] = 1                                     # owned by rows of another table
+    after = [n * page - 3 for n in takes]
+    print(f"[pages] {takes} of {n_pages}", flush=True)
+    refs, table, _, missing = check_resize(refs, table, [0] * len(takes), after, page)
+    assert missing == [0] * len(takes)
+    check_resize(refs, table, after, [0, 4 * page] + [0] * (len(takes) - 2) if len(takes) > 1 else [20], page)
+
+
 def test_pools_and_tables_of_nothing():
     none = torch.zeros((0, 3), dtype=torch.int32, device=DEV)
     refs = ints([1, 0])
@@ -151,7 +167,8 @@ def test_fork(seqs, children, columns):
         assert got is t and got.tolist() == want[1] and n.tolist() == want[2] and r.tolist() == want[0]
 
 
-@pytest.mark.parametrize("n_pages,seqs,columns", [(1, 1, 1), (7, 2, 2), (300, 20, 9), (4096, 100, 30), (40001, 700, 33)])
+@pytest.mark.parametrize("n_pages,seqs,columns", [(1, 1, 1), (7, 2, 2), (300, 20, 9), (4096, 100, 30), (40001, 700, 33),
+                                                   (4096, 64, 64), (4096, 64, 65), (4097, 10, 300)])
 @pytest.mark.parametrize("fill", [0.1, 0.5, 0.97, 1.0])
 def test_compact(n_pages, seqs, columns, fill):
     rng = np.random.default_rng((5, n_pages, int(100 * fill)))
