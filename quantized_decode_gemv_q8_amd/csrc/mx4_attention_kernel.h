@@ -1063,17 +1063,18 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
 template <RowType T, int DIM>
 hipError_t launch_rows(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
   if (rows == 16) return launch_instance<T, DIM, 16>(a, wgs, stream);
-  if constexpr (attn_direct_rows(DIM) == 32)
+  if constexpr (DIM <= 128)
     if (rows == 32) return launch_instance<T, DIM, 32>(a, wgs, stream);
-  if (rows == 64) return launch_instance<T, DIM, 64>(a, wgs, stream);
-  if constexpr (mx4_max_rows(T, DIM) == 128)
+  if constexpr (mx4_deep(T, DIM)) {
     if (rows == 128) return launch_instance<T, DIM, 128>(a, wgs, stream);
-  if constexpr (mx4_has_deep(T, DIM))
     if (rows == kMx4DeepRows) return launch_instance<T, DIM, kMx4DeepRows>(a, wgs, stream);
+  } else {
+    if (rows == 64) return launch_instance<T, DIM, 64>(a, wgs, stream);
+  }
   return hipErrorInvalidValue;
 }
 
-// rows: of an item, a power of two from 16 to 256.
+// rows: of an item (mx4_tile).
 template <RowType T>
 hipError_t launch_attention(const AttnArgs &a, int rows, int wgs, hipStream_t stream) {
   switch (a.c.dim) {

@@ -42,12 +42,28 @@ constexpr int mx4_direct_wgs(RowType type, int dim) { return dim > 64 ? kAttnWgs
 // Rows of an item of the kernels whose waves share keys: 64 or 128, as far as half of a
 // SIMD's registers hold, or 256 where all of them do.
 constexpr int kMx4DeepRows = 256;
-constexpr bool mx4_has_deep(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32); }
-constexpr int mx4_max_rows(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32) ? 128 : 64; }
-// For a mean of more than 64 rows.  At 128 rows of dim 128 the two are alike (f16 78 and 77
-// us over 8 x 8192 keys, bf16 70 and 74), below it items of 128 are faster (68 rows 70 and 75).
-constexpr int mx4_many_rows(RowType type, int dim, int64_t mean) {
-  return mean > 128 && mx4_has_deep(type, dim) ? kMx4DeepRows : mx4_max_rows(type, dim);
+constexpr bool mx4_deep(RowType type, int dim) { return dim <= 64 || (dim == 128 && type != kRowF32); }
+
+// Rows of an item, for `mean` rows of an average sequence's head.  us by the rows of an
+// item, trees of drafts over 8 x 8192 keys (32 heads, 8 of keys), then 32 sequences of up to
+// 32768 keys (4 heads of keys):
+//   20 rows, dim 128, bf16   16: 36.9  32: 35.7  64: 46.2         16: 113  32:  88  64: 146
+//   20 rows, dim 128, f32    16: 41.0  32: 45.3  64: 54.4         16: 127  32: 117  64: 180
+//   20 rows, dim 256, bf16   16: 53.6            64: 68.7         16: 236           64: 235
+//   20 rows, dim 256, f32    16: 86.4            64: 91.5         16: 359           64: 332
+//   48 rows, dim 128, bf16   32: 47.8  64: 49.0  128: 51.7        32: 151  64: 154  128: 151
+//   48 rows, dim 128, f32    16: 54.7  32: 63.8  64: 58.6         16: 197  32: 210  64: 189
+//   48 rows, dim 256, bf16   16: 81.6            64: 73.7         16: 348           64: 253
+//   96 rows, dim  64, f32    32: 57.4  64: 66.3  128: 63.7        32: 188  64: 234  128: 197
+//   96 rows, dim 128, f16    32: 67.8  64: 78.9  128: 71.8
+//   96 rows, dim 128, bf16   32: 63.9  64: 76.3  128: 67.3        32: 223  64: 272  128: 223
+//  128 rows, dim 128, bf16   32: 72.9  64: 78.6  128: 71.5
+// From 129 on 256: at 128 rows of dim 128 the two are alike (f16 78 us in items of 128, 77
+// in those of 256, bf16 70 and 74).
+constexpr int mx4_tile(RowType type, int dim, int64_t mean) {
+  if (mean <= 16 || (mean <= 32 && dim == 256 && type != kRowF32)) return 16;
+  if (!mx4_deep(type, dim)) return mean <= 32 && dim == 128 ? 32 : 64;
+  return mean <= 96 ? 32 : mean <= 128 ? 128 : kMx4DeepRows;
 }
 
 constexpr int mx4_wgs(RowType type, int dim, int tile) {

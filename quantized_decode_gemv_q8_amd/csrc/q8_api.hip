@@ -809,22 +809,46 @@ q8_status cache_rows_impl(const C *c, const void *k, const void *v, q8_type type
   return hip_status(launch(a, (q8::RowType)type, (hipStream_t)stream_v));
 }
 
+// The smallest items that hold an average sequence's rows of a head (mean); past 32,
+// the kernel whose waves share keys.  24 sequences of 4096 keys, us by the rows
+// of an item:
+//    4 rows, dim  64, f32     4: 41.6    8: 42.9   16: 45.1
+//    4 rows, dim 128, f32     4: 47.0    8: 46.0   16: 45.8
+//    4 rows, dim 128, bf16    4: 43.9    8: 43.5   16: 43.4
+//    8 rows, dim  64, f32     8: 43.6   16: 45.4   32: 66.5
+//   16 rows, dim 128, f32     8: 75.3   16: 48.0   32: 65.4
+//   32 rows, dim 128, bf16   16: 76.9   32: 56.9   64: 84.2
+//   40 rows, dim 128, bf16   16: 99.2   32: 90.8   64: 85.9   128: 90.7
+//   72 rows, dim 128, bf16   32: 130.2  64: 154.1  128: 117.8
+//  128 rows, dim 128, f16    32: 162.7  64: 161.4  128: 143.7
+// At 4 rows of dim 128 the three are within 3% over such batches; 4 is the
+// fastest for one short sequence (15.9 us, 16.6 with 16).  Two borders could be
+// drawn better: 17 to 32 rows of dim 256 take 81 us of bf16 and 96 of f32 in
+// 16-row items, 87 and 107 in the 64-row ones that the rule gives them.
+// The instances for 4 and 8 rows do not fit the registers at dim 256.
+int cache_attention_tile(q8::RowType type, int dim, int64_t mean) {
+  return mean <= 4 && dim <= 128             ? 4
+         : mean <= 8 && dim <= 128           ? 8
+         : mean <= 16                        ? 16
+         : mean <= q8::attn_direct_rows(dim) ? 32
+         : mean <= 64                        ? 64
+                                             : q8::attn_max_rows(type, dim);
+}
+
 // What the attentions over the two caches differ in.
 struct AttnFormat {
   const char *name;
-  bool few;        // has kernels for items of 4 and 8 rows
-  bool any_alpha;  // takes a scale of the scores that is not finite
-  double channel_bytes;  // of codes and scales, per channel of a key or value
-  int (*many_rows)(q8::RowType type, int dim, int64_t mean);  // of an item, for a mean of more than 64
-  int (*per_cu)(q8::RowType type, int dim, int tile);         // workgroups
+  bool any_alpha;                                        // takes a scale of the scores that is not finite
+  double channel_bytes;                                  // of codes and scales, per channel of a key or value
+  int (*tile)(q8::RowType type, int dim, int64_t mean);  // rows of an item, by those of an average sequence's head
+  int (*per_cu)(q8::RowType type, int dim, int tile);    // workgroups
   hipError_t (*launch[3])(const q8::AttnArgs &, int, int, hipStream_t);  // by the rows' type
 };
 constexpr double kCachesBytes = 256.0 * (1 << 20);  // the Infinity Cache
-const AttnFormat kQ8Attention = {"cache_attention", true, true, 1.125,
-                                 [](q8::RowType type, int dim, int64_t) { return q8::attn_max_rows(type, dim); },
+const AttnFormat kQ8Attention = {"cache_attention", true, 1.125, cache_attention_tile,
                                  [](q8::RowType, int, int) { return q8::kAttnWgsPerCu; },
                                  {q8::launch_attention_f32, q8::launch_attention_bf16, q8::launch_attention_f16}};
-const AttnFormat kMx4Attention = {"mx4_attention", false, false, 17. / 32, q8::mx4_many_rows, q8::mx4_wgs,
+const AttnFormat kMx4Attention = {"mx4_attention", false, 17. / 32, q8::mx4_tile, q8::mx4_wgs,
                                   {q8::launch_mx4_attention_f32, q8::launch_mx4_attention_bf16, q8::launch_mx4_attention_f16}};
 
 // How the rows of an attention call are cut: items of up to `tile` rows
@@ -861,29 +885,7 @@ constexpr int kAttnItemCost = 2;
 AttnPlan attn_plan(const AttnFormat &format, q8::RowType type, int heads, int group, int dim, int64_t rows, int64_t seqs, int64_t max_tokens) {
   AttnPlan p = {};
   const int64_t mean = ceil_div(rows, seqs) * group;  // rows of an average sequence and head
-  // The smallest items that hold an average sequence's rows of a head; past 32,
-  // the kernel whose waves share keys.  24 sequences of 4096 keys, us by the rows
-  // of an item:
-  //    4 rows, dim  64, f32     4: 41.6    8: 42.9   16: 45.1
-  //    4 rows, dim 128, f32     4: 47.0    8: 46.0   16: 45.8
-  //    4 rows, dim 128, bf16    4: 43.9    8: 43.5   16: 43.4
-  //    8 rows, dim  64, f32     8: 43.6   16: 45.4   32: 66.5
-  //   16 rows, dim 128, f32     8: 75.3   16: 48.0   32: 65.4
-  //   32 rows, dim 128, bf16   16: 76.9   32: 56.9   64: 84.2
-  //   40 rows, dim 128, bf16   16: 99.2   32: 90.8   64: 85.9   128: 90.7
-  //   72 rows, dim 128, bf16   32: 130.2  64: 154.1  128: 117.8
-  //  128 rows, dim 128, f16    32: 162.7  64: 161.4  128: 143.7
-  // At 4 rows of dim 128 the three are within 3% over such batches; 4 is the
-  // fastest for one short sequence (15.9 us, 16.6 with 16).  Two borders could be
-  // drawn better: 17 to 32 rows of dim 256 take 81 us of bf16 and 96 of f32 in
-  // 16-row items, 87 and 107 in the 64-row ones that the rule gives them.
-  // The instances for 4 and 8 rows do not fit the registers at dim 256.
-  p.tile = mean <= 4 && dim <= 128 && format.few   ? 4
-           : mean <= 8 && dim <= 128 && format.few ? 8
-           : mean <= 16                            ? 16
-           : mean <= q8::attn_direct_rows(dim)     ? 32
-           : mean <= 64                            ? 64
-                                                   : format.many_rows(type, dim, mean);
+  p.tile = format.tile(type, dim, mean);
   const int tile = p.tile;
   p.subs = (int)ceil_div(group, tile);
   p.sub_heads = (int)ceil_div(group, p.subs);

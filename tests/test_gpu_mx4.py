@@ -224,6 +224,19 @@ def test_groups(group):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tree", [False, True])
+def test_items_of_all_sizes(tree, dim, dtype):
+    """On both sides of every number of rows at which an item's size or kernel changes."""
+    for n in (16, 17, 32, 33, 64, 65, 96, 97, 128, 129, 257):
+        c = Case((48, n, dim), [n + 75, 2 * n], [n, n], 2 if n < 100 else 1, 1, dim, 32, dtype, tree=tree)
+        c.check(c.run())
+    for group, news in ((7, [14, 13]), (24, [4, 4]), (100, [1, 1]), (130, [1, 1])):
+        c = Case((49, group, dim), [190, 33], news, 1, group, dim, 16, dtype, tree=tree)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_many_sequences_and_long_ones(dtype):
     """More sequences than a workgroup has threads; few rows split over many workgroups; a wide tree."""
     rng = np.random.default_rng(23)
@@ -259,7 +272,7 @@ def mark_lost(c, name, seq, pos, block, page_size):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("news", [[4, 6], [40, 60]])
+@pytest.mark.parametrize("news", [[4, 6], [40, 60], [25, 30]])
 def test_lost_values_and_keys(news, dtype):
     """A value scale of 255 loses its block of the rows that see it, a key scale the rows, and no others."""
     c = Case((46, news[0]), [300, 30 + news[1]], news, 1, 4, 128, 64, dtype, tree=True)
@@ -278,7 +291,7 @@ def test_lost_values_and_keys(news, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_what_is_not_seen_changes_nothing(dtype):
     """Behind the last token, and of a draft that no row sees: any bits."""
-    for news in ([2, 3], [40, 60]):
+    for news in ([2, 3], [40, 60], [25, 30]):
         c = Case((45, news[0]), [300, 90], news, 1, 4, 128, 64, dtype, tree=True)
         c.trees[1] = [b & ~(1 << 1) for b in c.trees[1]]
         want = c.run()
@@ -330,7 +343,7 @@ def test_alpha(alpha, news):
 
 
 def test_large_scores_and_queries():
-    for news in ([1, 2], [60, 2]):
+    for news in ([1, 2], [60, 2], [120, 2], [150, 2]):
         c = Case(31, [500, 77], news, 2, 2, 64, 16, torch.float32, q_scale=60.0)
         c.check(c.run())
         c = Case(32, [500], [news[0]], 2, 2, 64, 16, torch.float32, q_scale=1e30, alpha=1e-31)
@@ -342,7 +355,7 @@ def test_large_scores_and_queries():
 @pytest.mark.parametrize("dtype", TYPES)
 def test_infinite_and_nan_queries(dtype):
     """A row whose query is not finite gives NaN; its neighbours are as without it."""
-    for news in ([4, 1], [70, 1]):
+    for news in ([4, 1], [70, 1], [60, 1]):
         c = Case(33, [80, 40], news, 1, 4, 128, 16, dtype)
         cache = handle(c.c)
         want = c.run(cache)
@@ -355,7 +368,7 @@ def test_infinite_and_nan_queries(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("news", [[2, 3, 1], [70, 130, 1]])
+@pytest.mark.parametrize("news", [[2, 3, 1], [70, 130, 1], [60, 110, 1]])
 def test_attention_over_bad_descriptions(news, dtype):
     c = Case((44, news[0]), [90, 300, 64], news, 2, 2, 64, 16, dtype)
     cache, q = handle(c.c), c.q.to(DEV)
