@@ -14,14 +14,20 @@
  *              C[m,n] = sum_k A[m,k] * W[n,k], i8 operands, i32 result.
  *   q8_cache_* a paged cache of keys and values in Q8_0 and the attention over
  *              it (declared and described below).
+ *   q8_mx4_*   the same in 4-bit floats.
+ *   q8_pages_* the pages of these caches: shared by forks, given and taken
+ *              back as sequences grow and leave, moved together.
+ *   q8_rope    rotary positions of queries and keys.
  *
  * Conventions shared by every entry point:
  *   - All tensor pointers are DEVICE pointers (memory of the current HIP
  *     device) to dense row-major arrays; there are no leading-dimension
- *     arguments (but for the rows and the page table that q8_cache_* take, which
- *     may be apart).  The caller owns them; the library only reads the inputs
- *     and overwrites the output.  It reads C only through an epilogue with
- *     row factors (corr != NULL, below).  C must not alias an input.
+ *     arguments (but for the rows and the page tables that q8_cache_*, q8_mx4_*,
+ *     q8_pages_* and q8_rope take, which may be apart).  The caller owns them;
+ *     the library only reads the inputs and overwrites the output (a cache, and
+ *     a pool and its table, change in place where their operations say so).  It
+ *     reads C only through an epilogue with row factors (corr != NULL, below).
+ *     C must not alias an input.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).
  *     Calls are asynchronous on that stream: a status of Q8_OK means the work
  *     was enqueued; faults surface at the caller's next synchronisation.
@@ -32,8 +38,9 @@
  *     below 2^31 (otherwise Q8_ERR_TOO_LARGE).
  *   - Thread safety: concurrent calls are safe on distinct streams.  Host
  *     threads that share one stream must serialise their calls.
- *   - Workspace (q8_cache_attention takes its own from the caller, the other
- *     q8_cache_* need none): the split-K workspace (partial sums and arrival
+ *   - Workspace (the attentions, q8_pages_resize and q8_pages_compact take
+ *     theirs from the caller; the other operations on caches, pages and
+ *     positions need none): the split-K workspace (partial sums and arrival
  *     counters) is owned by the library, one per (device, stream).  It is allocated by
  *     the first call that needs it on that stream and grown by a later call
  *     that needs more; buffers it grows out of stay allocated (a graph
