@@ -289,7 +289,7 @@ __device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float
 }
 
 // The same for items of more rows (trees, prompts), up to 64 * RT: all four waves
-// take the same keys.  Per step of 64 keys each wave loads 16 keys' codes, converts
+// take the same keys.  Bound by the issue of vector instructions.  Per step of 64 keys each wave loads 16 keys' codes, converts
 // them and lays them into LDS as the matrix operands that all waves read (16 bytes
 // per lane, conflict-free); the next step's codes are in flight meanwhile.  Row
 // tiles are dealt to the waves in turn, so a short item still uses all four.
@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
           if constexpr (n < 4 * NB) a[n % (kAhead + 1)] = lds.k[buf][n % 4][n / 4][lane];
         };
         // Products first: what another wave of the SIMD does meanwhile fits between them
-        // (trees of bf16 124 us, 129 without).
+        // (256 rows of bf16 a sequence over 8 x 8192 keys 124 us, 129 without).
         __builtin_amdgcn_s_setprio(1);
         static_for<0, kAhead>(fetch);
         auto products = [&](auto lays_) {
@@ -654,6 +654,11 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
 //   slot 2 t + 1:  first group weights(t), K(t + 1)  second group PV(t - 1), S(t)
 // Two buffers of each are enough: K(t + 1) replaces K(t - 1), last read in slot 2 t - 1, V(t)
 // replaces V(t - 2), last read there too.
+// Trees of 64 drafts over 8 x 8192 keys (32 heads, 8 of keys, of 128): bf16 103 us, 124 by the
+// kernel above; f16 116, 133.  A slot takes some 3100 cycles, 1660 of matrix instructions
+// (bf16): the wave that makes weights issues an instruction in five cycles, and loses about
+// six to each product of the SIMD's other wave.  Products of 32 x 32 x 16, half as many, made
+// dim 64 5 % faster and dim 128 4 % slower.
 template <int DIM>
 struct Mx4DeepLds {
   static constexpr int NB = DIM / 32;
