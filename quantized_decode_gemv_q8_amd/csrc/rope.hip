@@ -176,7 +176,8 @@ hipError_t launch_rows(RopeArgs a, hipStream_t stream) {
 
 template <RowType T, bool INTERLEAVED, int P>
 hipError_t launch_pairs(const RopeArgs &a, hipStream_t stream) {
-  if (a.s.rows < kFewRows && a.heads * (a.rot / 2 / P) > 64 * kRopeHeads) return launch_rows<T, INTERLEAVED, P, kThreads>(a, stream);
+  const bool many_heads = (int64_t)a.heads * (a.rot / 2 / P) > 64 * kRopeHeads;
+  if (a.s.rows < kFewRows && many_heads) return launch_rows<T, INTERLEAVED, P, kThreads>(a, stream);
   return launch_rows<T, INTERLEAVED, P, 64>(a, stream);
 }
 

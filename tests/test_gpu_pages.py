@@ -132,6 +132,53 @@ def test_many_pages_at_once(n_pages, takes, columns):
     check_resize(refs, table, after, [0, 4 * page] + [0] * (len(takes) - 2) if len(takes) > 1 else [20], page)
 
 
+def test_more_tiles_than_workgroups():
+    """Pools and batches of which a workgroup takes several tiles, and more children than a grid has waves."""
+    n_pages, seqs, columns, page = 2_200_000, 530_000, 4, 16
+    rng = np.random.default_rng(12)
+    before = rng.integers(0, 3 * page, seqs)
+    after = np.maximum(before + rng.integers(-20, 21, seqs), 0).tolist()
+    before = before.tolist()
+    _, refs, table = pool(13, n_pages, before, page, columns)
+    print("[pages] large resize", flush=True)
+    refs, table, _, missing = check_resize(refs, table, before, after, page)
+    assert missing == [-1 if n > columns * page else 0 for n in after]
+    print("[pages] large compact", flush=True)
+    want = pages.compact(refs, table, after, page)
+    got = binding.q8_pages_compact(ints(refs), ints(table), ints(after), page)
+    for g, w, name in zip(got, (want[0], want[1], want[2], [want[3]]), ("refs", "table", "moves", "used")):
+        assert torch.equal(g.cpu(), torch.tensor(w, dtype=torch.int32)), name
+    children = (1 << 22) + 9
+    parent = torch.arange(children, dtype=torch.int32, device=DEV) % 3
+    count = ints([0] * 5)
+    print("[pages] many children", flush=True)
+    t, n = binding.q8_pages_fork(count, ints([[4], [-1], [2]]), ints([3, 0, 16]), parent, page)
+    assert torch.equal(t[:, 0], ints([4, -1, 2])[parent.long()]) and torch.equal(n, ints([3, 0, 16])[parent.long()])
+    assert count.tolist() == [0, 0, int((parent == 2).sum()), 0, int((parent == 0).sum())]
+
+
+def test_table_rows_past_32_bits():
+    """Rows of a table whose bytes lie past 2^33."""
+    page, wide = 16, (1 << 30) + 16
+    room = torch.empty(2 * wide + 8, dtype=torch.int32, device=DEV)
+    far = room.as_strided((3, 4), (wide, 1))
+    table = [[5, 1, -1, -1], [3, -1, -1, -1], [0, 2, -1, -1]]
+    refs = [1, 1, 1, 1, 0, 1, 0, 0, 0, 0]
+    before, after = [20, 16, 32], [50, 0, 40]
+    far.copy_(ints(table))
+    r = ints(refs)
+    print("[pages] rows far apart", flush=True)
+    moves, missing = binding.q8_pages_resize(r, far, ints(before), ints(after), page)
+    want = pages.resize(refs, table, before, after, page)
+    for got, w in zip((r, far, moves, missing), want):
+        assert got.tolist() == w
+    got = binding.q8_pages_compact(r, far, ints(after), page)
+    assert got[1].tolist() == pages.compact(want[0], want[1], after, page)[1]
+    children = pages.fork(want[0], want[1], after, [2, 0, 2], page, 4)
+    t, n = binding.q8_pages_fork(r, far, ints(after), ints([2, 0, 2]), page)
+    assert t.tolist() == children[1] and n.tolist() == children[2] and r.tolist() == children[0]
+
+
 def test_pools_and_tables_of_nothing():
     none = torch.zeros((0, 3), dtype=torch.int32, device=DEV)
     refs = ints([1, 0])

@@ -185,6 +185,37 @@ def test_refusals():
         binding.Rope([float("nan")], device=DEV)
 
 
+def test_rows_past_32_bits_and_past_one_launch():
+    """Rows whose elements lie past 2^32, and more of them than a grid holds."""
+    rng = np.random.default_rng(11)
+    freq = binding.Rope.frequencies(64)
+    r = binding.Rope(freq, device=DEV)
+    x, xf = cc.rows_of(rng, (3, 2, 64), torch.bfloat16)
+    wide = (1 << 31) + 64
+    room = torch.empty(2 * wide + 128, dtype=torch.bfloat16, device=DEV)
+    far, out = room.as_strided((3, 2, 64), (wide, 64, 1)), torch.empty((3, 2, 64), dtype=torch.bfloat16, device=DEV)
+    far.copy_(x)
+    print("[rope] rows far apart", flush=True)
+    binding.q8_rope(far, r, positions=ints([5, -7, 90000]), out=out)
+    check(xf, out, [5, -7, 90000], r, freq)
+    binding.q8_rope(far, r, positions=ints([5, -7, 90000]), out=far)
+    assert torch.equal(far, out)
+    del room, far
+
+    rows, few = (1 << 24) + 7, torch.tensor([0, 1, 77, (1 << 24) - 1, 1 << 24, (1 << 24) + 6], device=DEV)
+    r = binding.Rope([0.7], device=DEV)
+    x = torch.randn((rows, 1, 2), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    p = torch.arange(rows, dtype=torch.int32, device=DEV) - 9
+    print("[rope] rows past one launch", flush=True)
+    out = binding.q8_rope(x, r, positions=p)
+    check(x[few].double().cpu().numpy(), out[few], p[few].tolist(), r, [0.7])
+    a = (p.double() * 0.7)[:, None]
+    want = torch.cat([x[:, 0, :1] * a.cos() - x[:, 0, 1:] * a.sin(), x[:, 0, :1] * a.sin() + x[:, 0, 1:] * a.cos()], 1)
+    # in f64 the angles, up to 2^24, are off by 2^-29 before their sines are taken
+    size = x.abs().sum(2).double()
+    assert bool(((out[:, 0] - want).abs() <= size * (7 * 2.0 ** -24 + 2.0 ** -28)).all())
+
+
 def test_captured_and_replayed():
     r = binding.Rope.scaled(128, device=DEV)
     q, k, n = torch.randn((6, 8, 128), device=DEV), torch.randn((6, 2, 128), device=DEV), ints([5, 70, 9])
