@@ -1039,11 +1039,14 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
   });
 }
 
-template <class A, RowType T, int DIM, int ROWS, int WAVES>
+template <class A, RowType T, int DIM, int ROWS>
 void launch_direct(const AttnArgs &a, int wgs, hipStream_t stream) {
-  hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, WAVES>), dim3((unsigned)wgs), dim3(64 * WAVES), 0, stream, a);
+  hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, kWaves>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
 }
 
+// Four waves a workgroup also where it takes all keys of its items (tables of up to 1024
+// tokens): of single tokens 16 sequences of 1023 keys take 12.2 us, 11.5 with eight waves, but
+// 32 of them 16.3 and 21.4, 128 of 200 keys 15.7 and 25.1 (bf16, 8 heads of keys of 128).
 template <RowType T, int DIM, int ROWS>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
   if constexpr (ROWS == kMx4DeepRows)
@@ -1051,13 +1054,11 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
   else if constexpr (ROWS >= 64)
     hipLaunchKernelGGL((mx4_wide_kernel<T, DIM, ROWS / 64>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   else if constexpr (ROWS > 16)
-    launch_direct<Mx4Attn<T, DIM, ROWS / 16, false>, T, DIM, ROWS, 4>(a, wgs, stream);
-  else if (a.items == nullptr)
-    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS, 8>(a, wgs, stream);
+    launch_direct<Mx4Attn<T, DIM, ROWS / 16, false>, T, DIM, ROWS>(a, wgs, stream);
   else if (a.past_caches)
-    launch_direct<Mx4Attn<T, DIM, 1, true>, T, DIM, ROWS, 4>(a, wgs, stream);
+    launch_direct<Mx4Attn<T, DIM, 1, true>, T, DIM, ROWS>(a, wgs, stream);
   else
-    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS, 4>(a, wgs, stream);
+    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS>(a, wgs, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.items == nullptr) return e;  // without items none is split
   hipLaunchKernelGGL((attention_join_kernel<T, DIM>), dim3((ROWS + kWaves * join_rows(DIM) - 1) / (kWaves * join_rows(DIM)), (unsigned)wgs),

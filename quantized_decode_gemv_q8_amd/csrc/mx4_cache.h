@@ -34,10 +34,14 @@ hipError_t launch_mx4_read(const CacheRowsArgs &a, RowType type, hipStream_t str
 hipError_t launch_mx4_keep(const CacheKeepArgs &a, hipStream_t stream);
 
 // Workgroups per CU of the kernel for 16 rows: as many as fit its registers, where more of
-// them have more bytes in flight (32 sequences of up to 32768 keys of dim 64: bf16 74 us
-// with 4, 84 with 2; f32 81 with 3, 91 with 2; at dim 128 3 are no faster for bf16 and spill
-// for f32).
-constexpr int mx4_direct_wgs(RowType type, int dim) { return dim > 64 ? kAttnWgsPerCu : type == kRowF32 ? 3 : 4; }
+// them have more bytes in flight.  32 sequences of up to 32768 keys: dim 64 bf16 74 us with 4,
+// 84 with 2; f32 81 with 3, 91 with 2.  At dim 128 3 are no faster for bf16 and spill for
+// f32.  At dim 256 2 spill: f32 357 us, 303 with 1; f16 294 and 265; bf16 (4 registers) 228 and
+// 256.
+constexpr int mx4_direct_wgs(RowType type, int dim) {
+  if (dim == 64) return type == kRowF32 ? 3 : 4;
+  return dim == 128 || type == kRowBf16 ? kAttnWgsPerCu : 1;
+}
 
 // Rows of an item of the kernels whose waves share keys: 64 or 128, as far as half of a
 // SIMD's registers hold, or 256 where all of them do.
@@ -50,7 +54,7 @@ constexpr bool mx4_deep(RowType type, int dim) { return dim <= 64 || (dim == 128
 //   20 rows, dim 128, bf16   16: 36.9  32: 35.7  64: 46.2         16: 113  32:  88  64: 146
 //   20 rows, dim 128, f32    16: 41.0  32: 45.3  64: 54.4         16: 127  32: 117  64: 180
 //   20 rows, dim 256, bf16   16: 53.6            64: 68.7         16: 236           64: 235
-//   20 rows, dim 256, f32    16: 86.4            64: 91.5         16: 359           64: 332
+//   20 rows, dim 256, f32    16: 76.9            64: 91.5         16: 319           64: 332
 //   48 rows, dim 128, bf16   32: 47.8  64: 49.0  128: 51.7        32: 151  64: 154  128: 151
 //   48 rows, dim 128, f32    16: 54.7  32: 63.8  64: 58.6         16: 197  32: 210  64: 189
 //   48 rows, dim 256, bf16   16: 81.6            64: 73.7         16: 348           64: 253
@@ -61,8 +65,8 @@ constexpr bool mx4_deep(RowType type, int dim) { return dim <= 64 || (dim == 128
 // From 129 on 256: at 128 rows of dim 128 the two are alike (f16 78 us in items of 128, 77
 // in those of 256, bf16 70 and 74).
 constexpr int mx4_tile(RowType type, int dim, int64_t mean) {
-  if (mean <= 16 || (mean <= 32 && dim == 256 && type != kRowF32)) return 16;
-  if (!mx4_deep(type, dim)) return mean <= 32 && dim == 128 ? 32 : 64;
+  if (mean <= 16 || (mean <= 32 && dim == 256)) return 16;
+  if (!mx4_deep(type, dim)) return mean <= 32 ? 32 : 64;
   return mean <= 96 ? 32 : mean <= 128 ? 128 : kMx4DeepRows;
 }
 
