@@ -1039,14 +1039,16 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
   });
 }
 
-template <class A, RowType T, int DIM, int ROWS>
+template <class A, RowType T, int DIM, int ROWS, int WAVES = kWaves>
 void launch_direct(const AttnArgs &a, int wgs, hipStream_t stream) {
-  hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, kWaves>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_kernel<A, T, DIM, ROWS, WAVES>), dim3((unsigned)wgs), dim3(64 * WAVES), 0, stream, a);
 }
 
-// Four waves a workgroup also where it takes all keys of its items (tables of up to 1024
-// tokens): of single tokens 16 sequences of 1023 keys take 12.2 us, 11.5 with eight waves, but
-// 32 of them 16.3 and 21.4, 128 of 200 keys 15.7 and 25.1 (bf16, 8 heads of keys of 128).
+// Workgroups of eight waves where each takes all keys of its items (tables of up to 1024 tokens)
+// and there are few of them: 1 and 8 sequences of 1023 keys take 11.2 and 11.5 us, 11.8 and
+// 12.0 with four waves; but 32 of them 21.4 and 16.3, 128 of 200 keys 25.1 and 15.7 (bf16, 8 heads
+// of keys of 128).  At dim 256 they spill or are no faster.
+constexpr int kFewWorkgroups = 128;
 template <RowType T, int DIM, int ROWS>
 hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
   if constexpr (ROWS == kMx4DeepRows)
@@ -1055,6 +1057,8 @@ hipError_t launch_instance(const AttnArgs &a, int wgs, hipStream_t stream) {
     hipLaunchKernelGGL((mx4_wide_kernel<T, DIM, ROWS / 64>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a);
   else if constexpr (ROWS > 16)
     launch_direct<Mx4Attn<T, DIM, ROWS / 16, false>, T, DIM, ROWS>(a, wgs, stream);
+  else if (DIM <= 128 && a.items == nullptr && wgs <= kFewWorkgroups)
+    launch_direct<Mx4Attn<T, DIM, 1, false>, T, DIM, ROWS, DIM <= 128 ? 2 * kWaves : kWaves>(a, wgs, stream);
   else if (a.past_caches)
     launch_direct<Mx4Attn<T, DIM, 1, true>, T, DIM, ROWS>(a, wgs, stream);
   else
