@@ -883,19 +883,20 @@ def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengt
         raise TypeError("parent must be a torch.Tensor of rank 1")
     n = parent.shape[0]
     written = [("refs", refs)]      # what is new overlaps nothing
+    _ints(device, lengths=(lengths, (table.shape[0],)), parent=(parent, (n,)))
+    if lengths_out is not None:
+        _ints(device, lengths_out=(lengths_out, (n,)))
+        written.append(("lengths_out", lengths_out))
     if table_out is None:
         table_out = _empty_on(stream, (n, table.shape[1]), torch.int32, device)
     else:
         written.append(("table_out", table_out))
-    if lengths_out is None:
-        lengths_out = _empty_on(stream, (n,), torch.int32, device)
-    else:
-        written.append(("lengths_out", lengths_out))
     to = _table("table_out", table_out, device)
     if table_out.shape[0] != n:
         raise ValueError(f"{n} parents need {n} rows of table_out, got {table_out.shape[0]}")
-    _ints(device, lengths=(lengths, (table.shape[0],)), parent=(parent, (n,)), lengths_out=(lengths_out, (n,)))
     _all_apart(written, [("table", table), ("lengths", lengths), ("parent", parent)])
+    if lengths_out is None:
+        lengths_out = _empty_on(stream, (n,), torch.int32, device)
     _call(refs, stream, "q8_pages_fork", load().q8_pages_fork, pool, source, lengths.data_ptr(), parent.data_ptr(), to,
           lengths_out.data_ptr())
     return table_out, lengths_out
@@ -915,16 +916,18 @@ def q8_pages_resize(refs, table, before, after, page_size, moves=None, missing=N
     rows = _table("table", table, device)
     n = table.shape[0]
     written = [("refs", refs), ("table", table)]
+    _ints(device, before=(before, (n,)), after=(after, (n,)))
+    if moves is not None:
+        _ints(device, moves=(moves, (n, 2)))
+        written.append(("moves", moves))
+    if missing is not None:
+        _ints(device, missing=(missing, (n,)))
+        written.append(("missing", missing))
+    _all_apart(written, [("before", before), ("after", after)])
     if moves is None:
         moves = _empty_on(stream, (n, 2), torch.int32, device)
-    else:
-        written.append(("moves", moves))
     if missing is None:
         missing = _empty_on(stream, (n,), torch.int32, device)
-    else:
-        written.append(("missing", missing))
-    _ints(device, before=(before, (n,)), after=(after, (n,)), moves=(moves, (n, 2)), missing=(missing, (n,)))
-    _all_apart(written, [("before", before), ("after", after)])
     work, need = _pages_workspace(pool, n, stream, device)
     _call(refs, stream, "q8_pages_resize", load().q8_pages_resize, pool, rows, before.data_ptr(), after.data_ptr(),
           moves.data_ptr(), missing.data_ptr(), work.data_ptr(), need)
@@ -941,17 +944,20 @@ def q8_pages_compact(refs, table, lengths, page_size, refs_out=None, table_out=N
     device = refs.device
     source = _table("table", table, device)
     pages, n = refs.shape[0], table.shape[0]
-    written = [(name, t) for name, t in (("refs_out", refs_out), ("table_out", table_out), ("moves", moves), ("used", used))
-               if t is not None]
+    given = {name: (t, shape) for name, t, shape in (("refs_out", refs_out, (pages,)), ("moves", moves, (pages // 2, 2)),
+                                                     ("used", used, (1,))) if t is not None}
+    _ints(device, lengths=(lengths, (n,)), **given)
+    written = [(name, t) for name, (t, _) in given.items()]
+    if table_out is not None:
+        written.append(("table_out", table_out))
     new = lambda t, *shape: _empty_on(stream, shape, torch.int32, device) if t is None else t  # noqa: E731
-    refs_out, table_out = new(refs_out, pages), new(table_out, *table.shape)
-    moves, used = new(moves, pages // 2, 2), new(used, 1)
+    table_out = new(table_out, *table.shape)
     to = _table("table_out", table_out, device)
     if table_out.shape != table.shape:
         raise ValueError(f"table_out must have shape {tuple(table.shape)}, got {tuple(table_out.shape)}")
-    _ints(device, lengths=(lengths, (n,)), refs_out=(refs_out, (pages,)), moves=(moves, (pages // 2, 2)), used=(used, (1,)))
     if written:
         _all_apart(written, [("refs", refs), ("table", table), ("lengths", lengths)])
+    refs_out, moves, used = new(refs_out, pages), new(moves, pages // 2, 2), new(used, 1)
     work, need = _pages_workspace(pool, n, stream, device)
     _call(refs, stream, "q8_pages_compact", load().q8_pages_compact, pool, source, lengths.data_ptr(), refs_out.data_ptr(),
           to, moves.data_ptr(), used.data_ptr(), work.data_ptr(), need)
