@@ -599,7 +599,7 @@ def _empty_on(stream, shape, dtype, device):
 def _call(cache, stream, what, fn, *args):
     """fn(*args, stream) on the cache's device; an error status raises."""
     device = cache.device
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
@@ -805,7 +805,8 @@ def _pool(refs, page_size, stream):
         raise TypeError("refs must be a torch.Tensor")
     if refs.dim() != 1:
         raise ValueError(f"refs must be rank 1, got {refs.dim()} dimensions")
-    _check_tensor("refs", refs, torch.int32, refs.shape)
+    if refs.dtype is not torch.int32 or not refs.is_cuda or not refs.is_contiguous():
+        _check_tensor("refs", refs, torch.int32, refs.shape)
     if page_size not in _PAGE_SIZES:
         raise ValueError(f"page_size must be a power of two from 16 to 1024, got {page_size}")
     if stream is not None and stream.device != refs.device:
@@ -835,27 +836,40 @@ def _table(name, t, device):
 
 
 def _all_apart(written, read):
-    """Refuses calls whose written tensors overlap each other or a read one."""
-    spans = [(*_span(t), name) for name, t in written + read]
+    """Refuses calls whose written i32 tensors overlap each other or a read one."""
+    spans = []
+    for _, t in written + read:
+        a = t.data_ptr()
+        spans.append((a, a + 4 * t.numel()) if t.is_contiguous() else _span(t))
     edge = 0
-    for a, b, _ in sorted(spans):
+    for a, b in sorted(spans):
         if a < edge and a < b:
             break
-        edge = max(edge, b)
+        if b > edge:
+            edge = b
     else:
         return
     # Some do: refused unless both are only read.
-    for i, (a, b, name) in enumerate(spans[:len(written)]):
-        for c, d, other in spans[i + 1:]:
+    named = [name for name, _ in written + read]
+    for i, (a, b) in enumerate(spans[:len(written)]):
+        for (c, d), other in zip(spans[i + 1:], named[i + 1:]):
             if a < d and c < b:
-                raise ValueError(f"{name} overlaps {other}")
+                raise ValueError(f"{named[i]} overlaps {other}")
+
+
+def _new(like, stream, shape):
+    """A new tensor of like's type and device, its memory ordered with the work of `stream`."""
+    if stream is None:
+        return like.new_empty(shape)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape)
 
 
 #: Workspace sizes by pages and sequences.
 _PAGES_WORKSPACE = {}
 
 
-def _pages_workspace(pool, seqs, stream, device):
+def _pages_workspace(refs, pool, seqs, stream):
     need = _PAGES_WORKSPACE.get((pool.pages, seqs))
     if need is None:
         size = ctypes.c_int64(0)
@@ -866,7 +880,7 @@ def _pages_workspace(pool, seqs, stream, device):
             _PAGES_WORKSPACE.clear()
         need = _PAGES_WORKSPACE[pool.pages, seqs] = size.value
     # held by the caller until the call has returned, as the attention's is
-    return _empty_on(stream, (max(need, 16),), torch.uint8, device), need
+    return _new(refs, stream, max(need, 16) // 4), need
 
 
 def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengths_out=None, stream=None):
@@ -888,7 +902,7 @@ def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengt
         _ints(device, lengths_out=(lengths_out, (n,)))
         written.append(("lengths_out", lengths_out))
     if table_out is None:
-        table_out = _empty_on(stream, (n, table.shape[1]), torch.int32, device)
+        table_out = _new(refs, stream, (n, table.shape[1]))
     else:
         written.append(("table_out", table_out))
     to = _table("table_out", table_out, device)
@@ -896,7 +910,7 @@ def q8_pages_fork(refs, table, lengths, parent, page_size, table_out=None, lengt
         raise ValueError(f"{n} parents need {n} rows of table_out, got {table_out.shape[0]}")
     _all_apart(written, [("table", table), ("lengths", lengths), ("parent", parent)])
     if lengths_out is None:
-        lengths_out = _empty_on(stream, (n,), torch.int32, device)
+        lengths_out = _new(refs, stream, n)
     _call(refs, stream, "q8_pages_fork", load().q8_pages_fork, pool, source, lengths.data_ptr(), parent.data_ptr(), to,
           lengths_out.data_ptr())
     return table_out, lengths_out
@@ -925,10 +939,10 @@ def q8_pages_resize(refs, table, before, after, page_size, moves=None, missing=N
         written.append(("missing", missing))
     _all_apart(written, [("before", before), ("after", after)])
     if moves is None:
-        moves = _empty_on(stream, (n, 2), torch.int32, device)
+        moves = _new(refs, stream, (n, 2))
     if missing is None:
-        missing = _empty_on(stream, (n,), torch.int32, device)
-    work, need = _pages_workspace(pool, n, stream, device)
+        missing = _new(refs, stream, n)
+    work, need = _pages_workspace(refs, pool, n, stream)
     _call(refs, stream, "q8_pages_resize", load().q8_pages_resize, pool, rows, before.data_ptr(), after.data_ptr(),
           moves.data_ptr(), missing.data_ptr(), work.data_ptr(), need)
     return moves, missing
@@ -950,15 +964,20 @@ def q8_pages_compact(refs, table, lengths, page_size, refs_out=None, table_out=N
     written = [(name, t) for name, (t, _) in given.items()]
     if table_out is not None:
         written.append(("table_out", table_out))
-    new = lambda t, *shape: _empty_on(stream, shape, torch.int32, device) if t is None else t  # noqa: E731
-    table_out = new(table_out, *table.shape)
+    if table_out is None:
+        table_out = _new(refs, stream, table.shape)
     to = _table("table_out", table_out, device)
     if table_out.shape != table.shape:
         raise ValueError(f"table_out must have shape {tuple(table.shape)}, got {tuple(table_out.shape)}")
     if written:
         _all_apart(written, [("refs", refs), ("table", table), ("lengths", lengths)])
-    refs_out, moves, used = new(refs_out, pages), new(moves, pages // 2, 2), new(used, 1)
-    work, need = _pages_workspace(pool, n, stream, device)
+    if refs_out is None:
+        refs_out = _new(refs, stream, pages)
+    if moves is None:
+        moves = _new(refs, stream, (pages // 2, 2))
+    if used is None:
+        used = _new(refs, stream, 1)
+    work, need = _pages_workspace(refs, pool, n, stream)
     _call(refs, stream, "q8_pages_compact", load().q8_pages_compact, pool, source, lengths.data_ptr(), refs_out.data_ptr(),
           to, moves.data_ptr(), used.data_ptr(), work.data_ptr(), need)
     return refs_out, table_out, moves, used
@@ -993,6 +1012,7 @@ def q8_mx4_copy(cache, moves, stream=None):
 
 # ------------------------------------------------------------------ rotary positions
 
+_ROPE_ROWS = [_RopeRowsStruct * n for n in range(5)]
 _SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
 
 
@@ -1120,8 +1140,8 @@ def q8_rope(x, rope, positions=None, lengths=None, offsets=None, inverse=False, 
         n = lengths.shape[0]
         _ints(device, lengths=(lengths, (n,)), offsets=(offsets, (n + 1,)))
         seqs = _SeqsStruct(None, lengths.data_ptr(), offsets.data_ptr(), n, 0, 0)
-    tensors = (_RopeRowsStruct * len(xs))(*((t.data_ptr(), o.data_ptr(), t.shape[1], a, b)
-                                            for t, o, a, b in zip(xs, outs, strides, out_strides)))
+    tensors = _ROPE_ROWS[len(xs)](*[(t.data_ptr(), o.data_ptr(), t.shape[1], a, b)
+                                    for t, o, a, b in zip(xs, outs, strides, out_strides)])
     _call(rope, stream, "q8_rope", load().q8_rope, rope._struct, tensors, len(xs), _ROW_TYPES[dtype], rows, dim,
           None if positions is None else positions.data_ptr(), seqs, int(inverse))
     return outs[0] if one else outs
