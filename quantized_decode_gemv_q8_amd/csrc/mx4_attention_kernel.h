@@ -257,34 +257,37 @@ struct Mx4Attn {
 // ---------------------------------------------------------------- many rows
 
 // Scores to the exponents of their weights, against the row's kept maximum, which is
-// raised where one passes it by kMaxSlack (as in settle; looked for in the exponents,
-// which the scores become anyway).  What grows with the weights, sums and l, is scaled down.
+// raised first where one passes it by kMaxSlack (as in settle).  What grows with the
+// weights, sums and l, is scaled down.  A score is rounded once, against the new maximum:
+// against the one before, a row whose first keys score far below the others would lose
+// what those differ by.
 template <int NRT, int NK, int NSUMS>
 __device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float *m, v4f (*sums)[NSUMS], float *l = nullptr) {
-  float from[NRT], top[NRT];
+  float top[NRT];
   bool above = false;
 #pragma unroll
   for (int rt = 0; rt < NRT; ++rt) {
-    from[rt] = base_of(m[rt]);
-#pragma unroll
-    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from[rt]);
     top[rt] = s[rt][0];
 #pragma unroll
     for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
-    above |= top[rt] > (m[rt] == -INFINITY ? -INFINITY : kMaxSlack);  // the first key that is seen, too
+    above |= top[rt] * undo > m[rt] + kMaxSlack;  // the first key that is seen, too
   }
   if (__ballot(above) != 0) {
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
-      const float to = fmaxf(m[rt], from[rt] + row_max<1>(top[rt])), down = base_of(to) - from[rt];
+      const float to = fmaxf(m[rt], row_max<1>(top[rt]) * undo);
       const float f = __builtin_amdgcn_exp2f(m[rt] - base_of(to));
       m[rt] = to;
-#pragma unroll
-      for (int k = 0; k < NK; ++k) s[rt][k] -= down;
 #pragma unroll
       for (int n = 0; n < NSUMS; ++n) sums[rt][n] *= f;
       if (l != nullptr) l[rt] *= f;
     }
+  }
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    const float from = base_of(m[rt]);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from);
   }
 }
 

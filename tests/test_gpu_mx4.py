@@ -471,6 +471,49 @@ def test_one_visible_key_gives_its_value(news, dim):
         assert ((got - want).abs() <= (6 * 2.0 ** -24 if dtype == torch.float32 else 0) * want.abs()).all()
 
 
+# ------------------------------------------------------------------ scores far apart
+
+def far_keys(seed, news, dim, dtype, far, alpha=None):
+    """A call whose context's first 64 keys of every 128 score far below the others: q is 1 in channel 0, where
+    those keys hold -4 * 2^(far - 127) and zeros elsewhere, and the others 0."""
+    c = Case((61, seed, dim, news), [300 + news], [news], 1, 4, dim, 16, dtype, alpha=alpha)
+    q = c.q.float()
+    q[..., 0] = 1
+    c.q = q.to(dtype)
+    c.qf = c.q.float().numpy()
+    c.far = np.arange(300 + news) % 128 < 64
+    c.far[300:] = False
+    c.c["k"].reshape(-1, dim // 2)[:, 0] &= 0xf0       # channel 0: the low half of byte 0 of a key's row
+    for pos in np.flatnonzero(c.far):
+        page, at = oc.slot_of(c.table, 16, 0, int(pos))
+        c.c["k"][page, :, at] = 0
+        c.c["k"][page, :, at, 0] = 14
+        c.c["k_scale"][page, :, at] = far
+    return c
+
+
+def want_of_near(c):
+    """(out, spread, size) over the other keys alone."""
+    def near(cache, name, table, b, length):
+        return mx4.sequence(cache, name, table, b, length + int(c.far.sum()))[:, ~c.far]
+    return oc.attention(c.qf, c.c, c.table, c.lengths - int(c.far.sum()), c.offsets, c.alpha, sequence=near)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 10, 30, 40])
+def test_keys_that_score_far_below_the_others(news, dim, dtype):
+    """Keys at -10^3 to -10^7 have no weight in f32 or in 64 bits (exp(-750) is none), so what is
+    lost must not grow with them: the bound is that of the other keys alone."""
+    for far in (139, 147, 152):
+        c = far_keys(far, news, dim, dtype, far)
+        ref, spread, size = want_of_near(c)
+        assert np.abs(c.want()[0] - ref).max() <= 1e-12
+        got = c.run().float().cpu().numpy()
+        off = np.abs(got - ref) / bound(ref, spread, size, dtype)
+        assert off.max() <= 1, f"far {far}: {off.max():.3f} of the bound"
+
+
 # ------------------------------------------------------------------ large offsets, graphs, streams
 
 def test_offsets_past_32_bits():
