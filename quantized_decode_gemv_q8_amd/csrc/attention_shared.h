@@ -380,7 +380,8 @@ __device__ __forceinline__ void settle(const float (&s)[NRT][NK], const float *u
 // are exp2(-inf) = 0.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Scores, up to the row's factor undo[rt], to weights against the rows' kept maxima.
+// Scores, up to the row's factor undo[rt], a power of two, to weights against the rows'
+// kept maxima.
 template <int NRT, int NK, int NB, int PACK>
 __device__ __forceinline__ void weigh(float (&s)[NRT][NK], const float *undo, float *m, float *l, v4f (*acc)[NB][2]) {
   settle<NRT, NK, NB, PACK>(s, undo, m, l, acc);
@@ -538,7 +539,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs &p, const Share &h, in
 }
 
 // A: how a wave takes a tile of 32 keys from a cache's codes to scores and sums
-// (loads, scores, masks, values).  WAVES: 4, or 8 where a workgroup takes all
+// (loads, scores, masks, weights, values).  WAVES: 4, or 8 where a workgroup takes all
 // keys of its items.
 template <class A, RowType T, int DIM, int ROWS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? A::WGS : 1) void attention_kernel(AttnArgs p) {
@@ -594,7 +595,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? A::WGS : 1) void attention
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       a.cut(rt, q[rt], in[rt]);
-      a.m[rt] = -INFINITY;
+      a.no_top(rt);
       a.l[rt] = 0.f;
 #pragma unroll
       for (int bb = 0; bb < NB; ++bb) a.acc[rt][bb][0] = a.acc[rt][bb][1] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -619,7 +620,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? A::WGS : 1) void attention
           sees[rt] = seen_bits(p, at, h.context, h.seq.length, index[rt], h.seq.start + index[rt]);
         some_lost = a.mask(t, s, sees, lost);
       }
-      weigh<RT, A::NK, NB, A::PACK>(s, a.undo, a.m, a.l, a.acc);
+      a.weights(s);
       a.values(t, s);
       if (some_lost) {
 #pragma unroll
@@ -637,7 +638,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? A::WGS : 1) void attention
       const float l = row_sum<A::PACK>(a.l[rt]);
       if (!a.holds_row()) continue;
       if (a.c == 0) {
-        tops[wave][a.row_of(rt)] = a.m[rt];
+        tops[wave][a.row_of(rt)] = a.top(rt);
         weights[wave][a.row_of(rt)] = l;
       }
 #pragma unroll

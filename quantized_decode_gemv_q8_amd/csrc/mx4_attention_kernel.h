@@ -84,6 +84,69 @@ __device__ __forceinline__ void cut_bf16(const QueryRow<T, DIM> &from, bool in, 
   }
 }
 
+// A row's kept maximum, as its scores meet it: what they are taken against, 0 before any
+// is seen, and from where on a score raises it: everything does before any is seen.
+struct Top {
+  float from, limit;
+  __device__ __forceinline__ void none() {
+    from = 0.f;
+    limit = -INFINITY;
+  }
+  __device__ __forceinline__ float value() const { return limit == -INFINITY ? -INFINITY : from; }
+};
+
+// Scores, up to the factor undo, to the exponents of their weights, against the row's
+// kept maximum, which is raised first where one passes it by kMaxSlack (as in settle).
+// scale_sums(rt, f) scales what grows with the weights.  A score is rounded once, against
+// the new maximum: against the one before, a row whose first keys score far below the
+// others would lose what those differ by.
+// undo is no power of two, so a maximum is rounded where a score is not, and its own weight
+// is 2^r with r up to half a step of the maximum.  That cancels, but where the step is large
+// 2^r passes f32.  For maxima from kCoarse on (r up to a half) every step's scores pass the
+// limit, and are rounded as the maximum is.
+constexpr float kCoarse = 1 << 24, kLeast = -3.4028234663852886e38f;
+// Scores times undo must keep the order of their sizes, and masked ones -inf; the sign is
+// the query's.
+__device__ __forceinline__ float undo_of(float scale) { return scale == 0.f ? 1.f : fabsf(scale); }
+template <int NRT, int NK, typename F>
+__device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, Top *m, F scale_sums) {
+  float top[NRT], factor = undo;
+  bool above = false;
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    top[rt] = s[rt][0];
+#pragma unroll
+    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
+    above |= top[rt] * undo > m[rt].limit;
+  }
+  if (__ballot(above) != 0) {
+    bool coarse = false;
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
+      const float before = m[rt].value(), to = fmaxf(before, row_max<1>(top[rt]) * undo);
+      const bool far = finite(to) && fabsf(to) >= kCoarse;
+      m[rt].from = base_of(to);
+      m[rt].limit = far ? kLeast : to + kMaxSlack;
+      scale_sums(rt, __builtin_amdgcn_exp2f(before - m[rt].from));
+      coarse |= far;
+    }
+    if (__ballot(coarse) != 0) {
+      factor = 1.f;
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          s[rt][k] *= undo;
+          pin(s[rt][k]);  // a branch, no selection among both in every step
+        }
+    }
+  }
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], factor, -m[rt].from);
+}
+
 // Cache policy of loads that are not to stay in the caches (nt).
 constexpr int kPastCaches = 2;
 
@@ -112,7 +175,8 @@ struct Mx4Attn {
   };
   v4u qf[RT][NB][QP];
   v4f acc[RT][NB][2];
-  float m[RT], l[RT], undo[RT];
+  Top m[RT];
+  float l[RT];
 
   const AttnArgs *p;
   float scale;       // alpha log2 e
@@ -121,8 +185,6 @@ struct Mx4Attn {
   __device__ __forceinline__ int row_of(int rt) const { return 16 * rt + row; }  // of the item
   __device__ __forceinline__ bool holds_row() const { return true; }             // in its sums
   __device__ __forceinline__ void cut(int rt, const QueryRow<T, DIM> &from, bool in) {
-    // Scores times `undo` must keep the order of their sizes, and masked ones -inf.
-    undo[rt] = scale == 0.f ? 1.f : fabsf(scale);
     cut_bf16<T, DIM>(from, in, scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f, qf[rt]);
   }
   __device__ __forceinline__ void start() {}
@@ -226,6 +288,28 @@ struct Mx4Attn {
     return true;
   }
 
+  __device__ __forceinline__ void no_top(int rt) { m[rt].none(); }
+  __device__ __forceinline__ float top(int rt) const { return m[rt].value(); }
+  __device__ __forceinline__ void weights(float (&s)[RT][8]) {
+    exponents<RT, 8>(s, undo_of(scale), m, [&](int rt, float f) {
+      l[rt] *= f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[rt][b][i] *= f;
+    });
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[rt][k] = __builtin_amdgcn_exp2f(s[rt][k]);
+        sum += s[rt][k];
+      }
+      l[rt] += sum;
+    }
+  }
+
   __device__ __forceinline__ void values(const Tile &t, const float (&s)[RT][8]) {
     v4u parts[RT][PP];
 #pragma unroll
@@ -255,41 +339,6 @@ struct Mx4Attn {
 };
 
 // ---------------------------------------------------------------- many rows
-
-// Scores to the exponents of their weights, against the row's kept maximum, which is
-// raised first where one passes it by kMaxSlack (as in settle).  What grows with the
-// weights, sums and l, is scaled down.  A score is rounded once, against the new maximum:
-// against the one before, a row whose first keys score far below the others would lose
-// what those differ by.
-template <int NRT, int NK, int NSUMS>
-__device__ __forceinline__ void exponents(float (&s)[NRT][NK], float undo, float *m, v4f (*sums)[NSUMS], float *l = nullptr) {
-  float top[NRT];
-  bool above = false;
-#pragma unroll
-  for (int rt = 0; rt < NRT; ++rt) {
-    top[rt] = s[rt][0];
-#pragma unroll
-    for (int k = 1; k < NK; ++k) top[rt] = fmaxf(top[rt], s[rt][k]);
-    above |= top[rt] * undo > m[rt] + kMaxSlack;  // the first key that is seen, too
-  }
-  if (__ballot(above) != 0) {
-#pragma unroll
-    for (int rt = 0; rt < NRT; ++rt) {
-      const float to = fmaxf(m[rt], row_max<1>(top[rt]) * undo);
-      const float f = __builtin_amdgcn_exp2f(m[rt] - base_of(to));
-      m[rt] = to;
-#pragma unroll
-      for (int n = 0; n < NSUMS; ++n) sums[rt][n] *= f;
-      if (l != nullptr) l[rt] *= f;
-    }
-  }
-#pragma unroll
-  for (int rt = 0; rt < NRT; ++rt) {
-    const float from = base_of(m[rt]);
-#pragma unroll
-    for (int k = 0; k < NK; ++k) s[rt][k] = fmaf(s[rt][k], undo, -from);
-  }
-}
 
 // The same for items of more rows (trees, prompts), up to 64 * RT: all four waves
 // take the same keys.  Bound by the issue of vector instructions.  Per step of 64 keys each wave loads 16 keys' codes, converts
@@ -337,7 +386,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
   const uint8_t *Kc = reinterpret_cast<const uint8_t *>(p.c.K), *Ks = reinterpret_cast<const uint8_t *>(p.c.KS);
   const uint8_t *Vc = reinterpret_cast<const uint8_t *>(p.c.V), *Vs = reinterpret_cast<const uint8_t *>(p.c.VS);
   const float scale = p.alpha * 1.4426950408889634f;
-  const float undo = scale == 0.f ? 1.f : fabsf(scale);
+  const float undo = undo_of(scale);
 
   // This wave's 16 keys of a step, on their way to LDS.
   uint32_t kw[NB], ksw[KS], vw[NB], vsw[NB];
@@ -415,7 +464,8 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
     // Row tile rt of this wave: rows 16 (4 rt + wave) .. of the item.
     v4u qf[RT][NB][QP];
     v4f acc[RT][2 * NB];
-    float m[RT], l[RT];
+    Top m[RT];
+  float l[RT];
     int index[RT];
     bool in[RT];
     QueryRow<T, DIM> q[RT];
@@ -434,7 +484,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       cut_bf16<T, DIM>(q[rt], in[rt], scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f, qf[rt]);
-      m[rt] = -INFINITY;
+      m[rt].none();
       l[rt] = 0.f;
 #pragma unroll
       for (int n = 0; n < 2 * NB; ++n) acc[rt][n] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -504,7 +554,11 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
             if (!((sees[rt] >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
         }
       }
-      exponents<NRT, 16, 2 * NB>(s, undo, m, acc, l);
+      exponents<NRT, 16>(s, undo, m, [&](int rt, float f) {
+        l[rt] *= f;
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n) acc[rt][n] *= f;
+      });
       {
         constexpr int RING = kAhead + 1;
         v4u a[RING][2];
@@ -637,7 +691,7 @@ __global__ __launch_bounds__(kThreads, kAttnWgsPerCu) void mx4_wide_kernel(AttnA
         }
       }
       if (!h.whole && c == 0) {
-        h.slot[(int64_t)ROWS * DIM + rho] = m[rt];
+        h.slot[(int64_t)ROWS * DIM + rho] = m[rt].value();
         h.slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
       }
     }
@@ -684,7 +738,7 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
   const int group = wave >> 2, quarter = wave & 3;  // of the keys of a step
   const int lane = tid & 63, row = lane & 15, c = lane >> 4;
   const float scale = p.alpha * 1.4426950408889634f;
-  const float undo = scale == 0.f ? 1.f : fabsf(scale);
+  const float undo = undo_of(scale);
   const v4u ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 
   // 16 keys of a step, on their way to LDS: keys in the first group, values in the second.
@@ -780,7 +834,7 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
     v4u qf[RT][NB][QP];
     // Sums over a row tile: of block b's channels at 2 b, 2 b + 1, of the weights at 2 NB.
     v4f acc[RT][2 * NB + 1];
-    float m[RT];
+    Top m[RT];
     {
       QueryRow<T, DIM> q[RT];
       bool in[RT];
@@ -794,7 +848,7 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         cut_bf16<T, DIM>(q[rt], in[rt], scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f, qf[rt]);
-        m[rt] = -INFINITY;
+        m[rt].none();
 #pragma unroll
         for (int n = 0; n <= 2 * NB; ++n) acc[rt][n] = v4f{0.f, 0.f, 0.f, 0.f};
       }
@@ -922,7 +976,10 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
                 if (!((sees >> (16 * (k / 4) + k % 4)) & 1)) s[rt][k] = -INFINITY;
             }
           }
-          exponents<NRT, 16, 2 * NB + 1>(s, undo, m, acc);
+          exponents<NRT, 16>(s, undo, m, [&](int rt, float f) {
+#pragma unroll
+            for (int n = 0; n <= 2 * NB; ++n) acc[rt][n] *= f;
+          });
 #pragma unroll
           for (int rt = 0; rt < NRT; ++rt) {
 #pragma unroll
@@ -1035,7 +1092,7 @@ __global__ __launch_bounds__(2 * kThreads, 1) void mx4_deep_kernel(AttnArgs p) {
         }
       }
       if (!h.whole && c == 0) {
-        h.slot[(int64_t)ROWS * DIM + rho] = m[rt];
+        h.slot[(int64_t)ROWS * DIM + rho] = m[rt].value();
         h.slot[(int64_t)ROWS * (DIM + 1) + rho] = weight;
       }
     }

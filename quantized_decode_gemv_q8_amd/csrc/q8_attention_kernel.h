@@ -262,6 +262,10 @@ struct Attn {
     return true;
   }
 
+  __device__ __forceinline__ void no_top(int rt) { m[rt] = -INFINITY; }
+  __device__ __forceinline__ float top(int rt) const { return m[rt]; }
+  __device__ __forceinline__ void weights(float (&s)[RT][NK]) { weigh<RT, NK, NB, PACK>(s, undo, m, l, acc); }
+
   __device__ __forceinline__ void values(const Tile &t, const float (&s)[RT][8]) {
     static_for<0, NB>([&](auto b_) {
       constexpr int b = decltype(b_)::value;
@@ -459,6 +463,10 @@ struct AttnFew {
     lost[0] = gone;
     return true;
   }
+
+  __device__ __forceinline__ void no_top(int rt) { m[rt] = -INFINITY; }
+  __device__ __forceinline__ float top(int rt) const { return m[rt]; }
+  __device__ __forceinline__ void weights(float (&s)[1][NK]) { weigh<1, NK, NB, PACK>(s, undo, m, l, acc); }
 
   __device__ __forceinline__ void values(const Tile &t, const float (&s)[1][NK]) {
     static_for<0, NB>([&](auto b_) {

@@ -514,6 +514,47 @@ def test_keys_that_score_far_below_the_others(news, dim, dtype):
         assert off.max() <= 1, f"far {far}: {off.max():.3f} of the bound"
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 10, 30, 40])
+def test_keys_that_score_further_below(news, dim, dtype):
+    """The same at -10^9 and -10^37, where a step of f32 is more than what two weights may differ by."""
+    for far in (160, 252):
+        c = far_keys(far, news, dim, dtype, far)
+        ref, spread, size = want_of_near(c)
+        off = np.abs(c.run().float().cpu().numpy() - ref) / bound(ref, spread, size, dtype)
+        assert off.max() <= 1, f"far {far}: {off.max():.3f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 10, 30, 40])
+def test_scores_further_apart_than_the_largest_number(news, dim, dtype):
+    """Keys at -2^127 and, after them, at 2^127 (alpha is 1): all the weight is on the latter, the same for each,
+    since what their other channels add is less than half a step of such a score."""
+    c = far_keys(1, news, dim, dtype, 252, alpha=1.0)
+    for pos in np.flatnonzero(~c.far):
+        page, at = oc.slot_of(c.table, 16, 0, int(pos))
+        c.c["k"][page, :, at, ::dim // 32] = 0         # block 0
+        c.c["k"][page, :, at, 0] = 6
+        c.c["k_scale"][page, :, at, 0] = 252
+    ref, spread, size = want_of_near(c)
+    got = c.run().float().cpu().numpy()
+    off = np.abs(got - ref) / bound(ref, spread, 0 * size, dtype)
+    assert off.max() <= 1, f"{off.max():.3f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news", [1, 10, 30, 40])
+@pytest.mark.parametrize("size", [1e6, 1e11, 1e30])
+def test_all_scores_far_apart(size, news, dtype):
+    """Every row's largest score is far above its next one, so its key's value is the output: the two are
+    2^-13 of the terms' size apart or more, what they are rounded by is 16 * 2^-24 of it at most."""
+    c = Case((63, news), [300 + news], [news], 1, 4, 128, 16, dtype, alpha=size)
+    ref, got = c.want()[0], c.run().float().cpu().numpy()
+    assert (np.abs(got - ref) <= bound(ref, np.abs(ref), np.zeros(ref.shape[:2]), dtype)).all()
+
+
 # ------------------------------------------------------------------ large offsets, graphs, streams
 
 def test_offsets_past_32_bits():
