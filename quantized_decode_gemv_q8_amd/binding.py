@@ -1111,6 +1111,19 @@ def q8_rope(x, rope, positions=None, lengths=None, offsets=None, inverse=False, 
     if rope.rot > dim:
         raise ValueError(f"the rope turns {rope.rot} channels, x has {dim}")
     strides = [_rope_rows("x", t, rows, dim, dtype, device) for t in xs]
+    if positions is not None:
+        if lengths is not None or offsets is not None:
+            raise ValueError("pass positions, or lengths and offsets")
+        _ints(device, positions=(positions, (rows,)))
+        seqs = None
+    else:
+        if not isinstance(lengths, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+            raise TypeError("pass positions, or lengths and offsets")
+        if lengths.dim() != 1:
+            raise ValueError(f"lengths must be rank 1, got {lengths.dim()} dimensions")
+        n = lengths.shape[0]
+        _ints(device, lengths=(lengths, (n,)), offsets=(offsets, (n + 1,)))
+        seqs = _SeqsStruct(None, lengths.data_ptr(), offsets.data_ptr(), n, 0, 0)
     if out is None:
         outs = tuple(_empty_on(stream, t.shape, dtype, device) for t in xs)
         out_strides = [t.shape[1] * dim for t in xs]
@@ -1127,19 +1140,6 @@ def q8_rope(x, rope, positions=None, lengths=None, offsets=None, inverse=False, 
             others += [("another out", u) for u in outs[:i]]
             _check_apart("out", o, others + [("positions", positions), ("lengths", lengths), ("offsets", offsets),
                                              ("the rope", rope.turns)])
-    if positions is not None:
-        if lengths is not None or offsets is not None:
-            raise ValueError("pass positions, or lengths and offsets")
-        _ints(device, positions=(positions, (rows,)))
-        seqs = None
-    else:
-        if not isinstance(lengths, torch.Tensor) or not isinstance(offsets, torch.Tensor):
-            raise TypeError("pass positions, or lengths and offsets")
-        if lengths.dim() != 1:
-            raise ValueError(f"lengths must be rank 1, got {lengths.dim()} dimensions")
-        n = lengths.shape[0]
-        _ints(device, lengths=(lengths, (n,)), offsets=(offsets, (n + 1,)))
-        seqs = _SeqsStruct(None, lengths.data_ptr(), offsets.data_ptr(), n, 0, 0)
     tensors = _ROPE_ROWS[len(xs)](*[(t.data_ptr(), o.data_ptr(), t.shape[1], a, b)
                                     for t, o, a, b in zip(xs, outs, strides, out_strides)])
     _call(rope, stream, "q8_rope", load().q8_rope, rope._struct, tensors, len(xs), _ROW_TYPES[dtype], rows, dim,

@@ -329,3 +329,19 @@ def test_rope_rows_are_checked():
             binding._rope_rows("x", bad, 5, 64, f32, cpu)
     with pytest.raises(TypeError):
         binding._rope_rows("x", 1, 5, 64, f32, cpu)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_rope_positions_are_checked_before_they_are_used(given):
+    """Whether or not there is an output to keep apart from them."""
+    x, one = torch.zeros((4, 2, 64)), torch.zeros(4, dtype=torch.int32)
+    r = binding.Rope([1.0] * 32, device="cpu")
+    kw = dict(out=torch.zeros((4, 2, 64))) if given else {}
+    for bad in (dict(positions=[0, 1, 2, 3]), dict(positions=3), dict(lengths=[4], offsets=[0, 4]), dict(lengths=one, offsets=[0, 4]),
+                dict()):
+        with pytest.raises(TypeError):
+            binding.q8_rope(x, r, **bad, **kw)
+    for bad in (dict(positions=one, lengths=one), dict(positions=one.long()), dict(positions=one), dict(lengths=one, offsets=one),
+                dict(lengths=one[None], offsets=one)):
+        with pytest.raises(ValueError):
+            binding.q8_rope(x, r, **bad, **kw)
