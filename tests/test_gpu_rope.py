@@ -65,6 +65,67 @@ def test_rotation(shape, interleaved, dtype):
     assert torch.equal(y, out)
 
 
+# A workgroup per row (more heads than a wave has in flight at once, fewer than 2048 rows) and a wave per row, for
+# runs of 8 (of 4 for f32), 4 and 1 pairs; all of the head, and part of it with what is left whole or ragged.
+MANY_HEADS = [(3, 40, 128, 128), (5, 33, 128, 128), (2, 90, 24, 24), (3, 90, 96, 24), (2, 90, 97, 40), (2, 9, 80, 40), (3, 90, 6, 6),
+              (2, 300, 7, 2), (3, 70, 130, 64)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", range(len(MANY_HEADS)))
+def test_rotation_of_many_heads(shape, interleaved, dtype):
+    rows, heads, dim, rot = MANY_HEADS[shape]
+    rng = np.random.default_rng((12, shape))
+    freq = binding.Rope.frequencies(rot)
+    r = binding.Rope(freq, interleaved, 1.0, DEV)
+    positions = rng.integers(-10, 200000, rows).tolist()
+    x, xf = cc.rows_of(rng, (rows, heads, dim), dtype)
+    print(f"[rope] {MANY_HEADS[shape]} {interleaved} {dtype}", flush=True)
+    for inverse in (False, True):
+        out = binding.q8_rope(x.to(DEV), r, positions=ints(positions), inverse=inverse)
+        check(xf, out, positions, r, freq, inverse)
+    y = x.to(DEV)
+    assert binding.q8_rope(y, r, positions=ints(positions), inverse=True, out=y) is y      # in place
+    assert torch.equal(y, out)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("place", [False, True])
+def test_a_step_of_many_heads_by_sequences(place, dtype):
+    """Queries and keys of a decode step with rows of no sequence, a workgroup per row."""
+    rng = np.random.default_rng(13)
+    lengths, news = [40, 0, 33, 7, 100000], [3, 0, 33, 1, 2]
+    offsets = cc.offsets_of(news, 2)
+    rows = int(offsets[-1]) + 3
+    positions = [n - m + i for n, m in zip(lengths, news) for i in range(m)]
+    freq = binding.Rope.frequencies(96)
+    r = binding.Rope(freq, True, device=DEV)
+    (q, qf), (k, kf) = cc.rows_of(rng, (rows, 64, 128), dtype), cc.rows_of(rng, (rows, 8, 128), dtype)
+    xs = q.to(DEV), k.to(DEV)
+    outs = xs if place else tuple(torch.full(x.shape, 9.0, dtype=x.dtype, device=DEV) for x in xs)
+    got = binding.q8_rope(xs, r, lengths=ints(lengths), offsets=torch.from_numpy(offsets).to(DEV), out=outs)
+    own = slice(2, rows - 3)
+    for x, x0, out in ((qf, q, got[0]), (kf, k, got[1])):
+        check(x[own], out[own], positions, r, freq)
+        for part in (slice(0, 2), slice(rows - 3, rows)):
+            assert torch.equal(out[part].cpu(), x0[part] if place else torch.full_like(x0[part], 9.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_both_sides_of_few_rows(dtype):
+    """2047 rows by a workgroup each, 2048 by a wave each: the same bits."""
+    rng = np.random.default_rng(14)
+    freq = binding.Rope.frequencies(128)
+    r = binding.Rope(freq, device=DEV)
+    x = torch.randn((2048, 33, 128), generator=torch.Generator(device=DEV).manual_seed(5), device=DEV).to(dtype)
+    p = ints(rng.integers(0, 100000, 2048).tolist())
+    many, few = binding.q8_rope(x, r, positions=p), binding.q8_rope(x[:2047], r, positions=p[:2047])
+    assert torch.equal(many[:2047], few)
+    at = [0, 1, 1000, 2046, 2047]
+    check(x[at].float().cpu().numpy(), many[at], p[at].tolist(), r, freq)
+
+
 @pytest.mark.parametrize("scaling", ["none", "linear", "base", "turns", "index"])
 def test_far_positions_and_scalings(scaling):
     """Positions up to the ends of 32 bits; frequencies from whole turns to almost none."""
