@@ -555,6 +555,102 @@ def test_all_scores_far_apart(size, news, dtype):
     assert (np.abs(got - ref) <= bound(ref, np.abs(ref), np.zeros(ref.shape[:2]), dtype)).all()
 
 
+# ------------------------------------------------------------------ large caches
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_loads_past_the_caches(dim, dtype):
+    """A table and a cache that may hold more than the Infinity Cache (256 MB), which a call with a narrow table
+    over few pages does not.  What the sequences do not own is NaN."""
+    page, heads, columns = 64, 4, 40
+    c = Case((71, dim), [2049, 300, 1], [1, 2, 1], heads, 4, dim, page, dtype)
+    c.table = np.pad(c.table, ((0, 0), (0, columns)), constant_values=-1)[:, :columns]
+    want = c.run()
+    c.check(want)
+    # 3 sequences of `wide` columns and as many pages: tokens x heads x dim x 17 / 16 bytes
+    wide = 1 + (256 << 20) * 16 // (17 * 3 * page * heads * dim)
+    cache = binding.Mx4Cache.empty(3 * wide, heads, page, dim, DEV)
+    for n in NAMES:
+        getattr(cache, n).fill_(255)
+        getattr(cache, n)[:len(c.c["k"])] = dev(c.c[n])
+    assert 2 * sum(getattr(cache, n).numel() for n in ("k", "k_scale")) > 256 << 20
+    c.table = np.pad(c.table, ((0, 0), (0, wide - columns)), constant_values=-1)
+    out = c.run(cache)
+    c.check(out)
+    assert torch.equal(out[-1], want[-1])       # one key; the others' items may be cut elsewhere
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_reads_past_the_caches(dtype):
+    """Rows of more than 256 MB read back past the caches: the same bits as in smaller reads."""
+    dim, heads, page = 128, 8, 64
+    rows = (256 << 20) // (2 * heads * dim * (torch.finfo(dtype).bits // 8)) + 37
+    pages = -(-rows // page)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    cache = binding.Mx4Cache(*(torch.randint(*((0, 256) if n in "kv" else (100, 130)), (pages, heads, page, dim // 2 if n in "kv" else dim // 32),
+                                             generator=g, device=DEV, dtype=torch.uint8) for n in NAMES))
+    table = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)[None]
+    k, v = binding.q8_mx4_read(cache, table, ints([rows]), ints([0, rows]), rows, dtype=dtype)
+    half = rows // 2 + 5
+    for first, n in ((0, half), (half, rows - half)):       # the newest n tokens of the first ones
+        a, b = binding.q8_mx4_read(cache, table, ints([first + n]), ints([0, n]), n, dtype=dtype)
+        assert torch.equal(a, k[first:first + n]) and torch.equal(b, v[first:first + n])
+    few = np.array([0, 1, 63, 64, half, rows - 1])
+    own = table[0].cpu().numpy()[few // page]
+    c = {n: getattr(cache, n)[torch.from_numpy(own).long().to(DEV)].cpu().numpy() for n in NAMES}
+    for i, t in enumerate(few):
+        for name, got in (("k", k), ("v", v)):
+            for h in (0, heads - 1):
+                want = mx4.values(*mx4.get(c, name, i, h, int(t) % page))
+                assert torch.equal(got[t, h].cpu(), torch.from_numpy(want).to(dtype))
+
+
+def test_offsets_past_2_to_the_32():
+    """Codes whose bytes lie past 2^32: written, read, kept, copied and attended to.  The pages that offsets
+    without their 32nd or 33rd bit would reach are watched."""
+    pages, heads, page, dim = 132000, 8, 64, 128      # 4.3 GB of codes a side
+    size = heads * page * dim // 2
+    assert (pages - 300) * size > 1 << 32
+    cache = binding.Mx4Cache.empty(pages, heads, page, dim, DEV)
+    for n in NAMES:
+        getattr(cache, n).zero_()
+    rng = np.random.default_rng(16)
+    own = np.array([[pages - 1, 1, pages - 200, pages - 300]], np.int32)
+    near = sorted({int(p) - b * (1 << 31) // size for p in own[0] if p > 1 for b in (1, 2)})
+    copies = [near[0] + 7, near[-1] + 7, pages - 100, 77]
+    assert all(0 <= p < pages and p not in own[0] for p in near) and not set(copies) & (set(near) | set(own[0].tolist()))
+    k, kf = cc.rows_of(rng, (220, heads, dim), torch.bfloat16)
+    v, vf = cc.rows_of(rng, (220, heads, dim), torch.bfloat16)
+    q, qf = cc.rows_of(rng, (220, heads, dim), torch.bfloat16)
+    held, offsets = (dev(own), ints([220]), ints([0, 220])), np.array([0, 220], np.int32)
+    small = np.arange(4, dtype=np.int32)[None]
+    c = {n: np.zeros((4, heads, page, dim // 2 if len(n) == 1 else dim // 32), np.uint8) for n in NAMES}
+
+    def check(places):
+        for n in NAMES:
+            for i, p in enumerate(places):
+                assert np.array_equal(getattr(cache, n)[int(p)].cpu().numpy(), c[n][i]), (n, p)
+            assert not getattr(cache, n)[near].any(), n
+
+    print("[mx4] write past 2^32", flush=True)
+    binding.q8_mx4_write(cache, k.to(DEV), v.to(DEV), *held)
+    mx4.write(c, kf, vf, small, [220], offsets)
+    check(own[0])
+    for got, want in zip(binding.q8_mx4_read(cache, *held, 220), mx4.read(c, small, [220], offsets)):
+        assert torch.equal(got.cpu().double(), torch.from_numpy(want))
+    kept = [3, 40, 64, 100, 150, 219]
+    binding.q8_mx4_keep(cache, *held, ints([kept]))
+    mx4.keep(c, small, [220], offsets, [kept])
+    check(own[0])
+    out = binding.q8_mx4_attention(q.to(DEV), cache, *held)
+    ref, spread, size = mx4.attention(qf, c, small, [220], offsets, dim ** -0.5)
+    assert (np.abs(out.float().cpu().numpy() - ref) <= bound(ref, spread, size, torch.bfloat16)).all()
+    binding.q8_mx4_copy(cache, ints([[a, b] for a, b in zip(own[0].tolist(), copies)]))
+    check(copies)
+    check(own[0])
+    assert torch.equal(binding.q8_mx4_attention(q.to(DEV), cache, ints([copies]), *held[1:]), out)
+
+
 # ------------------------------------------------------------------ large offsets, graphs, streams
 
 def test_offsets_past_32_bits():
