@@ -522,9 +522,11 @@ q8_status q8_pages_fork(const q8_pool *pool, const q8_page_table *from, const in
  *            every layer's cache (q8_cache_copy, q8_mx4_copy) before the new tokens are
  *            written
  *   missing  i32 [seqs]: 0, or the pages that the sequence lacks (nothing of it has
- *            changed: call again with the same lengths once pages are free, and do not
- *            write its new tokens), or -1 where before[b] or after[b] is negative or
- *            past the table (it is left alone)
+ *            changed: give it the same lengths again once pages are free, the others
+ *            after[b] as their before[b]), or -1 where before[b] or after[b] is negative or
+ *            past the table (it is left alone).  New tokens of a sequence with anything
+ *            but 0 must not be written: its last page may still be others' too.  With a
+ *            length of -1 in that step the cache's calls write none and give NaN
  *   workspace  q8_pages_workspace bytes of device memory, 16-byte aligned; needs no preparation, and
  *            one call at a time may use it
  * Entries that are no page are released as nothing and never replaced.

@@ -924,7 +924,9 @@ def q8_pages_resize(refs, table, before, after, page_size, moves=None, missing=N
     (moves, missing): i32 [seqs, 2] pages to copy in every cache (q8_cache_copy,
     q8_mx4_copy; -1 where there are none), and i32 [seqs] pages that a sequence could
     not be given (nothing of it has changed then), or -1 for lengths that the table
-    cannot hold."""
+    cannot hold.  What is written for a sequence with anything but 0 may land in a page
+    that others share: give it a length of -1 in that step, torch.where(missing == 0,
+    after, -1), and its old length in the next one's before."""
     pool = _pool(refs, page_size, stream)
     device = refs.device
     rows = _table("table", table, device)

@@ -410,3 +410,81 @@ def test_a_search_over_a_cache(dtype):
                 x[b] = x[a]
     assert any(a >= 0 for a, _ in m)
     step([1, 1, 1])
+
+
+@pytest.mark.parametrize("dtype", mc.TYPES)
+def test_a_captured_step_that_runs_out_of_pages(dtype):
+    """Sequences that get no page get a length of -1 for the step, on the device: nothing of theirs is written,
+    least of all into the last page that they share with others, and their rows are NaN."""
+    heads, group, dim, page, columns, seqs, n_pages = 2, 2, 64, 16, 4, 4, 4
+    cache = binding.Mx4Cache.empty(n_pages, heads, page, dim, DEV)
+    for x in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        x.fill_(120)
+    c = {n: getattr(cache, n).cpu().numpy() for n in ("k", "k_scale", "v", "v_scale")}
+    # all share 24 tokens in pages 2 and 0; pages 1 and 3 are free
+    refs, table, lengths, news = [4, 0, 4, 0], [[2, 0, -1, -1] for _ in range(seqs)], [24] * seqs, [1] * seqs
+    r, t, before, new, offsets = ints(refs), ints(table), ints(lengths), ints(news), ints(list(range(seqs + 1)))
+    q, k, v = (torch.zeros((seqs, h, dim), dtype=dtype, device=DEV) for h in (heads * group, heads, heads))
+    rope = binding.Rope.scaled(dim, device=DEV)
+    now = {}
+
+    def step():
+        after = before + new
+        moves, missing = binding.q8_pages_resize(r, t, before, after, page)
+        binding.q8_mx4_copy(cache, moves)
+        now["held"] = torch.where(missing == 0, after, -1)
+        now["q"], now["k"] = binding.q8_rope((q, k), rope, lengths=now["held"], offsets=offsets)
+        binding.q8_mx4_write(cache, now["k"], v, t, now["held"], offsets)
+        now["out"] = binding.q8_mx4_attention(now["q"], cache, t, now["held"], offsets)
+        before.copy_(torch.where(missing == 0, after, before))
+
+    def fresh():
+        for x in (q, k, v):
+            x.normal_()
+
+    def follow():
+        nonlocal refs, table, lengths
+        after = [a + b for a, b in zip(lengths, news)]
+        refs, table, moves, missing = pages.resize(refs, table, lengths, after, page)
+        for a, b in moves:
+            if a >= 0:
+                for x in c.values():
+                    x[b] = x[a]
+        served = [b for b in range(seqs) if missing[b] == 0 and news[b]]
+        assert now["held"].tolist() == [a if m == 0 else -1 for a, m in zip(after, missing)]
+        lengths = [a if m == 0 else b for a, b, m in zip(after, lengths, missing)]
+        rows, only = np.array(served), np.arange(len(served) + 1)
+        host = {n: now[n].float().cpu().numpy() for n in ("q", "k", "out")}
+        own = np.array(table)[rows], [lengths[b] for b in served], only
+        mx4.write(c, host["k"][rows], v.float().cpu().numpy()[rows], *own)
+        for name, x in c.items():
+            assert np.array_equal(getattr(cache, name).cpu().numpy(), x), name
+        ref, spread, size = mx4.attention(host["q"][rows], c, *own, dim ** -0.5)
+        assert (np.abs(host["out"][rows] - ref) <= mc.bound(ref, spread, size, dtype)).all()
+        assert np.isnan(host["out"][[b for b in range(seqs) if b not in served]]).all()
+        assert r.tolist() == refs and t.tolist() == table and before.tolist() == lengths
+        return served
+
+    def leave(b):
+        nonlocal refs, table, lengths
+        after = [0 if i == b else n for i, n in enumerate(lengths)]
+        binding.q8_pages_resize(r, t, before, ints(after), page)
+        refs, table, _, _ = pages.resize(refs, table, lengths, after, page)
+        lengths, news[b] = after, 0
+        before.copy_(ints(after))
+        new.copy_(ints(news))
+
+    fresh()
+    step()
+    assert follow() == [0, 1]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for gone, want in ((None, [0, 1]), (None, [0, 1]), (0, [1, 2]), (None, [1, 2, 3]), (1, [2, 3])):
+        if gone is not None:
+            leave(gone)
+        fresh()
+        g.replay()
+        torch.cuda.synchronize()
+        assert follow() == want
