@@ -566,11 +566,16 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
 }
 
 // Up to these sizes one workgroup does all of it.
-// Resize, pages: 64 sequences that take one page each take 5 us where free pages come early,
-// 0.1 us more per 1024 pages before them (65536: 12.1), and by launches of their own 14 from
-// any pool.  Table entries: where all leave 64 x 256 take 8.4 us, 1000 x 32 25.7; with
+// Resize, pages: it looks at those in front of the last free one that it gives, 0.24 us per
+// 1024.  16 to 1000 sequences that take one page each, us, by launches of their own in
+// brackets: free pages early in the pool 4.5 to 5.5 (14 to 15) at any size, none wanted 4 (13);
+// free ones last 7.2 (13.8) in a pool of 16384, 10.8 (13.8) of 32768, 18.5 (13.9) of
+// 65536, 22.4 (14) of 81920, 34 (14.2) of 131072.  Where the free pages lie is known
+// on the device only.  At the border the one side loses 8.5 where they come last, the other 9.5
+// where they come early.
+// Table entries: where all leave 64 x 256 take 8.4 us, 1000 x 32 25.7; with
 // the release in a launch of its own 7, but 5.5 instead of 4.0 where nothing changes.
-constexpr int64_t kResizePages = 131072, kResizeEntries = 16384;
+constexpr int64_t kResizePages = 81920, kResizeEntries = 16384;
 // Compact, pages: 2048 take 9.9 us, by three launches 11.6; 4096 13.0 and 13.4, 8192 17.7 and
 // 14.  Entries: 64 x 64 11.2 and 11.6, 128 x 128 19.4 and 11.9.
 constexpr int64_t kCompactPages = 4096, kCompactEntries = 4096;

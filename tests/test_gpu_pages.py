@@ -132,6 +132,18 @@ def test_many_pages_at_once(n_pages, takes, columns):
     check_resize(refs, table, after, [0, 4 * page] + [0] * (len(takes) - 2) if len(takes) > 1 else [20], page)
 
 
+@pytest.mark.parametrize("n_pages", [81920, 81921])
+def test_free_pages_that_come_last(n_pages):
+    """On both sides of what one workgroup looks through; all pages but the last 80 have owners."""
+    page, lengths = 16, [24, 16, 24, 0, 160]
+    _, refs, table = pool((15, n_pages), n_pages - 80, lengths, page, 60, share=0.5)
+    refs = [max(x, 1) for x in refs] + [0] * 80
+    refs, table, _, missing = check_resize(refs, table, lengths, [40, 100, 25, 900, 0], page)
+    assert missing == [0, 0, 0, 0, 0]
+    _, _, _, missing = check_resize(refs, table, [40, 100, 25, 900, 0], [60, 120, 0, 940, 500], page)
+    assert missing[-1] > 0
+
+
 def test_more_tiles_than_workgroups():
     """Pools and batches of which a workgroup takes several tiles, and more children than a grid has waves."""
     n_pages, seqs, columns, page = 2_200_000, 530_000, 4, 16
