@@ -34,10 +34,10 @@ hipError_t launch_mx4_read(const CacheRowsArgs &a, RowType type, hipStream_t str
 hipError_t launch_mx4_keep(const CacheKeepArgs &a, hipStream_t stream);
 
 // Workgroups per CU of the kernel for 16 rows: as many as fit its registers, where more of
-// them have more bytes in flight.  32 sequences of up to 32768 keys: dim 64 bf16 74 us with 4,
-// 84 with 2; f32 81 with 3, 91 with 2.  At dim 128 3 are no faster for bf16 and spill for
-// f32.  At dim 256 2 spill: f32 357 us, 303 with 1; f16 294 and 265; bf16 (4 registers) 228 and
-// 256.
+// them have more bytes in flight.  32 sequences of up to 32768 keys: dim 64 bf16 69 us with 4,
+// 81 with 2; f16 71 and 84; f32 79 with 3, 89 with 2.  At dim 128 3 are no faster for bf16 and
+// spill for f32.  At dim 256 2 spill: f32 420 us, 304 with 1; f16 265 and 268; bf16 (6 registers)
+// 230, 256 with 1.
 constexpr int mx4_direct_wgs(RowType type, int dim) {
   if (dim == 64) return type == kRowF32 ? 3 : 4;
   return dim == 128 || type == kRowBf16 ? kAttnWgsPerCu : 1;

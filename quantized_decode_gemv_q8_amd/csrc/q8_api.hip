@@ -810,21 +810,21 @@ q8_status cache_rows_impl(const C *c, const void *k, const void *v, q8_type type
 }
 
 // The smallest items that hold an average sequence's rows of a head (mean); past 32,
-// the kernel whose waves share keys.  24 sequences of 4096 keys, us by the rows
-// of an item:
-//    4 rows, dim  64, f32     4: 41.6    8: 42.9   16: 45.1
-//    4 rows, dim 128, f32     4: 47.0    8: 46.0   16: 45.8
-//    4 rows, dim 128, bf16    4: 43.9    8: 43.5   16: 43.4
-//    8 rows, dim  64, f32     8: 43.6   16: 45.4   32: 66.5
-//   16 rows, dim 128, f32     8: 75.3   16: 48.0   32: 65.4
-//   32 rows, dim 128, bf16   16: 76.9   32: 56.9   64: 84.2
-//   40 rows, dim 128, bf16   16: 99.2   32: 90.8   64: 85.9   128: 90.7
-//   72 rows, dim 128, bf16   32: 130.2  64: 154.1  128: 117.8
-//  128 rows, dim 128, f16    32: 162.7  64: 161.4  128: 143.7
+// the kernel whose waves share keys.  24 sequences of 4096 keys, 8 heads of keys, us by the
+// rows of an item:
+//    4 rows, dim  64, f32     4: 27.9    8: 28.3   16: 28.9
+//    4 rows, dim 128, f32     4: 46.6    8: 45.4   16: 45.5
+//    4 rows, dim 128, bf16    4: 43.2    8: 43.6   16: 43.6
+//    8 rows, dim  64, f32     8: 28.7   16: 29.4   32: 39.2
+//   16 rows, dim 128, f32     8: 75.4   16: 48.2   32: 63.5
+//   32 rows, dim 128, bf16   16: 78.0   32: 56.3   64: 82.2
+//   40 rows, dim 128, bf16   16: 99.5   32: 89.3   64: 84.3   128: 89.4
+//   72 rows, dim 128, bf16   32: 127.9  64: 149.9  128: 115.3
+//  128 rows, dim 128, f16    32: 160.5  64: 160.1  128: 140.7
 // At 4 rows of dim 128 the three are within 3% over such batches; 4 is the
-// fastest for one short sequence (15.9 us, 16.6 with 16).  Two borders could be
-// drawn better: 17 to 32 rows of dim 256 take 81 us of bf16 and 96 of f32 in
-// 16-row items, 87 and 107 in the 64-row ones that the rule gives them.
+// fastest for one short sequence (16.7 us, 17.5 with 16).  Two borders could be
+// drawn better: 32 rows of dim 256 take 161 us of bf16 and 191 of f32 in
+// 16-row items, 169 and 200 in the 64-row ones that the rule gives them.
 // The instances for 4 and 8 rows do not fit the registers at dim 256.
 int cache_attention_tile(q8::RowType type, int dim, int64_t mean) {
   return mean <= 4 && dim <= 128             ? 4

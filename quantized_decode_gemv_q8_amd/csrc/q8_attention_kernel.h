@@ -42,14 +42,14 @@
 // What bounds it.  Few rows: memory.  With 4 rows of f32 per head, dim 128, time
 // grows by 1 us per 5.85 MB of cache.  A large copy moves 4.9 TB/s; a large read
 // of contiguous runs 6.1, 7.1 with loads that leave no trace in the caches, which
-// are not used here.  A batch of 32 ragged sequences (316 MB) takes 64 us and its
+// are not used here.  A batch of 32 ragged sequences (316 MB) takes 62 to 67 us and its
 // join 5, two sequences of 131072 keys (604 MB) 112 and 7.  From 16 rows on:
 // vector instructions, for the codes' conversion, the exponentials and the
-// weights' parts.  68 GFLOP of bf16 trees take 169 us (0.40 PFLOP/s); of the 160
+// weights' parts.  68 GFLOP of bf16 trees take 167 us (0.41 PFLOP/s); of the 156
 // of the main kernel vector instructions issue for 107 on every SIMD and the
-// matrix cores are busy for 43, 9 of them at the same time.  16 GFLOP of f32
-// pieces of prompts take 81 us (0.2 PFLOP/s, two parts of q and three of the
-// weights): 42, 17 and 4 of 68.
+// matrix cores are busy for 43, 11 of them at the same time.  16 GFLOP of f32
+// pieces of prompts take 78 us (0.2 PFLOP/s, two parts of q and three of the
+// weights): 41, 17 and 4 of 66.
 #pragma once
 
 #include "attention_shared.h"
@@ -304,8 +304,8 @@ struct Attn {
 };
 
 // The same for items of at most 16 / PACK rows (one new token of a small group;
-// 24 sequences of 4096 keys, dim 64, 4 rows of f32: 41.6 us, 45.1 with 16-row
-// items; one sequence of 1000 keys, dim 128: 15.9 and 16.6):
+// 24 sequences of 4096 keys, dim 64, 4 rows of f32: 27.9 us, 28.9 with 16-row
+// items; one sequence of 1000 keys, dim 128: 16.7 and 17.5):
 // the query's columns repeat PACK times across the matrix operand, so that the
 // lanes of a row's repeats hold the same scores, and each keeps a PACK-th of the
 // keys (KPL).  Exponentials, weights and their parts, most of the other
@@ -536,7 +536,7 @@ struct AttnOf<T, DIM, 8> {
 // ---------------------------------------------------------------- many rows
 
 // The same for items of more rows (trees, prompts; 24 sequences of 4096 keys, 72
-// rows of bf16, dim 128: 118 us, 130 with 32-row items): up to 64 * RT rows, 16 * RT
+// rows of bf16, dim 128: 115 us, 128 with 32-row items): up to 64 * RT rows, 16 * RT
 // for each wave, and all four waves take the same keys.  Converting the codes
 // costs as much as the rest of the work on 32 rows, so a workgroup does it
 // once: per step of 64 keys each wave loads 16 keys' codes, converts them and
